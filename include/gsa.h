@@ -318,6 +318,65 @@ gsa_status grouped_scaled_act_bwd_graph_safe(const void *dy_bf16, const void *x_
                                              int64_t *padded_row_offsets_opt, void *workspace, size_t workspace_bytes,
                                              gsa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Tokens into expert order and back.
+ *
+ * Around the expert FFN: the routed tokens are sorted by expert (permute), run
+ * through the grouped steps, and come back as weighted sums (unpermute).  A
+ * slot is one of a token's topk routed copies; n = tokens * topk < 2^31.
+ * expert_idx [tokens, topk] holds each slot's expert; a value outside
+ * [0, experts) drops the slot (capacity limits; -1 by convention).
+ *   row_of_slot [tokens, topk] int32: the slot's row in expert order, slots of
+ *     one expert in slot order (a stable sort).  Dropped slots follow the last
+ *     expert's rows; their entry is ~row (negative).
+ *   split_sizes [experts + 1] int64, device: rows per expert, then the dropped
+ *     rows.  The whole array is a split of n rows over experts + 1 groups for
+ *     the graph-safe calls; its first `experts` entries are the split of the
+ *     grouped products.
+ * Rows have `hidden` elements of one element type (GSA_BF16, GSA_FP16,
+ * GSA_FP32), any hidden >= 1; probs, weights and their gradients are FP32.
+ * Sums run in FP32 in slot order and are rounded once.  Nothing synchronizes or
+ * allocates: every call can be captured in a CUDA graph.  Tensors of rows,
+ * expert_idx and row_of_slot (as an output) start on 16 bytes.  With tokens = 0
+ * pointers may be NULL.  A plan entry outside [-n, n) is skipped.
+ * Errors: INVALID_ARG, UNSUPPORTED (experts > 256, n or hidden >= 2^31),
+ * ALIGNMENT, WORKSPACE (the sort), CUDA. */
+typedef enum { GSA_BF16 = 0, GSA_FP16 = 1, GSA_FP32 = 2 } gsa_dtype;
+
+/* Workspace bytes of gsa_moe_sort, 16-byte aligned.  0 where none is needed (it
+ * may then be NULL) and on invalid arguments. */
+size_t gsa_moe_sort_workspace_size(int64_t tokens, int64_t topk, int64_t experts);
+
+/* The plan.  idx_bytes: 4 (int32) or 8 (int64) per expert index. */
+gsa_status gsa_moe_sort(const void *expert_idx, int32_t idx_bytes, int64_t tokens, int64_t topk, int64_t experts,
+                        int32_t *row_of_slot, int64_t *split_sizes, void *workspace, size_t workspace_bytes,
+                        gsa_stream_t stream);
+
+/* xs[row(t, j)] = x[t] and, with probs [tokens, topk], ps[row(t, j)] = probs[t, j]
+ * (both or neither).  x [tokens, hidden], xs [n, hidden], ps [n]; dropped rows
+ * are zero. */
+gsa_status gsa_moe_permute(const void *x, const float *probs, const int32_t *row_of_slot, int64_t tokens, int64_t topk,
+                           int64_t hidden, int32_t dtype, void *xs, float *ps, gsa_stream_t stream);
+
+/* Gradient of gsa_moe_permute: dx[t] = sum_j dxs[row(t, j)], dprobs[t, j] =
+ * dps[row(t, j)]; dropped slots give nothing (dprobs 0). */
+gsa_status gsa_moe_permute_bwd(const void *dxs, const float *dps, const int32_t *row_of_slot, int64_t tokens,
+                               int64_t topk, int64_t hidden, int32_t dtype, void *dx, float *dprobs,
+                               gsa_stream_t stream);
+
+/* out[t] = sum_j weights[t, j] ys[row(t, j)] over the slots that were not
+ * dropped (weights NULL: 1, for rows already scaled by the activation step).
+ * A token without a slot gets zeros. */
+gsa_status gsa_moe_unpermute(const void *ys, const float *weights, const int32_t *row_of_slot, int64_t tokens,
+                             int64_t topk, int64_t hidden, int32_t dtype, void *out, gsa_stream_t stream);
+
+/* Gradient of gsa_moe_unpermute: dys[row(t, j)] = weights[t, j] dout[t] (zeros
+ * in dropped rows), dweights[t, j] = <dout[t], ys[row(t, j)]> (0 where dropped).
+ * Either output may be NULL; ys is read for dweights alone. */
+gsa_status gsa_moe_unpermute_bwd(const void *dout, const void *ys, const float *weights, const int32_t *row_of_slot,
+                                 int64_t tokens, int64_t topk, int64_t hidden, int32_t dtype, void *dys,
+                                 float *dweights, gsa_stream_t stream);
+
 /* Failure-detection self-test.  Enqueues a one-thread kernel that runs one of
  * the library's bounded waits on something nothing signals -- which = 0: the
  * wait for a workspace counter (the encode pass's wait for its expert's amax

@@ -1,0 +1,533 @@
+// moe_route.cu -- tokens into expert order and back, for sm_103a: the sort plan
+// of the routed expert indices, the gather of the token rows (permute), the
+// weighted way back (unpermute) and both gradients, with their C entry points.
+//
+// With slot s = (t, j) of token t, e(s) its expert and n = tokens * topk:
+//   row(s)  = #{s' : e(s') < e(s)} + #{s' < s : e(s') = e(s)}    (a stable counting sort)
+//   permute            xs[row(t, j)] = x[t],  ps[row(t, j)] = p[t, j]
+//   its gradient       dx[t] = sum_j dxs[row(t, j)],  dp[t, j] = dps[row(t, j)]
+//   unpermute          out[t] = sum_j w[t, j] ys[row(t, j)]
+//   its gradient       dys[row(t, j)] = w[t, j] dout[t],  dw[t, j] = <dout[t], ys[row(t, j)]>
+// A dropped slot (no expert in [0, E)) sorts behind every expert; the plan holds
+// ~row for it, its rows are written as zeros and never read back.
+//
+// Everything after the plan moves each byte once and is bound by memory.  All
+// four kernels go by token: a token's own row is read (or written) once whatever
+// topk is, and only the expert side moves topk rows.  Sums run in FP32 in slot
+// order, so results do not depend on the launch shape (dw: see unpermute_bwd).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "gsa.h"
+#include "launches.h"
+
+namespace {
+
+constexpr int kMaxBins = 257;        // 256 experts and the dropped slots
+constexpr int kSortWarps = 32;
+constexpr int kGroup = 8;            // expert rows in flight per thread
+
+// ------------------------------------------------------------------- sort
+
+__device__ __forceinline__ int bin_of(const void *idx, int idx_bytes, int64_t s, int E) {
+    const int64_t e = idx_bytes == 8 ? static_cast<const int64_t *>(idx)[s]
+                                     : static_cast<int64_t>(static_cast<const int32_t *>(idx)[s]);
+    return e >= 0 && e < E ? static_cast<int>(e) : E;
+}
+
+// Slots [s0, s1) of one warp, 32 at a time in slot order, each counted into the
+// warp's own bins; lanes of the same bin find one another with match_any, so no
+// atomics are needed and the order is the slots' own.  kRank: the bins hold the
+// next free row of each expert and every slot's row is written.
+template <bool kRank>
+__device__ __forceinline__ void walk(const void *idx, int idx_bytes, int64_t s0, int64_t s1, int E, int *bins,
+                                     int32_t *row_of_slot) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t s = s0; s < s1; s += 32) {
+        const bool in = s + lane < s1;
+        const int b = in ? bin_of(idx, idx_bytes, s + lane, E) : kMaxBins;
+        const uint32_t same = __match_any_sync(0xFFFFFFFFu, b);
+        const int before = __popc(same & ((1u << lane) - 1u));
+        const int base = in ? bins[b] : 0;
+        __syncwarp();
+        if (in && before == 0) bins[b] = base + __popc(same);
+        __syncwarp();
+        if (kRank && in) {
+            const int32_t row = base + before;
+            row_of_slot[s + lane] = b == E ? ~row : row;
+        }
+    }
+}
+
+// Block b counts slots [b * seg, (b + 1) * seg) into counts[b][bin].
+__global__ void __launch_bounds__(1024) sort_count(const void *idx, int idx_bytes, int64_t n, int E, int64_t seg,
+                                                   int *counts) {
+    __shared__ int bins[kSortWarps][kMaxBins];
+    const int w = threadIdx.x >> 5, nw = blockDim.x >> 5, nb = E + 1;
+    for (int i = threadIdx.x; i < nw * kMaxBins; i += blockDim.x) (&bins[0][0])[i] = 0;
+    __syncthreads();
+    const int64_t b0 = blockIdx.x * seg, b1 = min(n, b0 + seg);
+    const int64_t per = ((seg + nw - 1) / nw + 31) / 32 * 32;
+    walk<false>(idx, idx_bytes, b0 + w * per, min(b1, b0 + (w + 1) * per), E, bins[w], nullptr);
+    __syncthreads();
+    for (int b = threadIdx.x; b < nb; b += blockDim.x) {
+        int c = 0;
+        for (int k = 0; k < nw; ++k) c += bins[k][b];
+        counts[static_cast<int64_t>(blockIdx.x) * nb + b] = c;
+    }
+}
+
+// Ranks of the slots of one block.  counts: the blocks' counts (sort_count), or
+// nullptr when one block holds every slot and counts them itself.
+__global__ void __launch_bounds__(1024) sort_rank(const void *idx, int idx_bytes, int64_t n, int E, int64_t seg,
+                                                  const int *counts, int32_t *row_of_slot, int64_t *split) {
+    __shared__ int bins[kSortWarps][kMaxBins];
+    __shared__ int before[kMaxBins];   // rows of this expert in earlier blocks
+    __shared__ int total[kMaxBins];    // rows of this expert, then the expert's first row
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5, nb = E + 1;
+    for (int i = threadIdx.x; i < nw * kMaxBins; i += blockDim.x) (&bins[0][0])[i] = 0;
+    __syncthreads();
+    const int64_t b0 = blockIdx.x * seg, b1 = min(n, b0 + seg);
+    const int64_t per = ((seg + nw - 1) / nw + 31) / 32 * 32;
+    const int64_t w0 = b0 + w * per, w1 = min(b1, b0 + (w + 1) * per);
+    walk<false>(idx, idx_bytes, w0, w1, E, bins[w], nullptr);
+    __syncthreads();
+    for (int b = threadIdx.x; b < nb; b += blockDim.x) {
+        int mine = 0, first = 0, all = 0;
+        if (counts) {
+#pragma unroll 8
+            for (int k = 0; k < static_cast<int>(gridDim.x); ++k) {
+                const int c = counts[static_cast<int64_t>(k) * nb + b];
+                all += c;
+                if (k < static_cast<int>(blockIdx.x)) first += c;
+            }
+        }
+        for (int k = 0; k < nw; ++k) {   // warp prefixes within the block
+            const int c = bins[k][b];
+            bins[k][b] = mine;
+            mine += c;
+        }
+        before[b] = first;
+        total[b] = counts ? all : mine;
+    }
+    __syncthreads();
+    if (w == 0) {   // exclusive scan over the bins; block 0 also writes the split
+        int carry = 0;
+        for (int b = lane; b < (nb + 31) / 32 * 32; b += 32) {
+            const int c = b < nb ? total[b] : 0;
+            int inc = c;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+                if (lane >= d) inc += v;
+            }
+            if (b < nb) {
+                total[b] = carry + inc - c + before[b];
+                if (blockIdx.x == 0) split[b] = c;
+            }
+            carry += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        }
+    }
+    __syncthreads();
+    for (int b = lane; b < nb; b += 32) bins[w][b] += total[b];
+    __syncwarp();
+    walk<true>(idx, idx_bytes, w0, w1, E, bins[w], row_of_slot);
+}
+
+// One block up to kOneBlockSlots slots, else blocks of `seg` slots and two launches.
+constexpr int64_t kOneBlockSlots = 8192;
+constexpr int kSegThreads = 256;
+
+int64_t sort_segment(int64_t n) {
+    if (n <= kOneBlockSlots) return n;
+    const int64_t seg = (n + 255) / 256;   // at most 256 blocks: each reads every block's counts
+    return seg < 2048 ? 2048 : (seg + 31) / 32 * 32;
+}
+
+// ------------------------------------------------------- rows and vectors
+
+template <int V> struct Raw;
+template <> struct Raw<16> { using T = uint4; };
+template <> struct Raw<8> { using T = uint2; };
+template <> struct Raw<4> { using T = uint32_t; };
+template <> struct Raw<2> { using T = uint16_t; };
+
+// Rows are read once: past L1, whose lines nothing would hit.
+template <int V> __device__ __forceinline__ typename Raw<V>::T load_once(const void *p) {
+    return __ldcs(static_cast<const typename Raw<V>::T *>(p));
+}
+
+__device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float as_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ void put(__nv_bfloat16 &d, float v) { d = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half &d, float v) { d = __float2half_rn(v); }
+__device__ __forceinline__ void put(float &d, float v) { d = v; }
+
+template <typename T, int V> union Vec {
+    typename Raw<V>::T raw;
+    T e[V / sizeof(T)];
+    __device__ Vec() {}
+};
+
+// Row index of a plan entry, -1 where the slot is dropped (or out of range).
+__device__ __forceinline__ int live_row(int32_t r, int n) {
+    return static_cast<uint32_t>(r) < static_cast<uint32_t>(n) ? r : -1;
+}
+
+// The blocks are (columns, tokens): threadIdx.x walks a row's vectors, blockDim.y tokens per block.
+
+template <int V>
+__global__ void __launch_bounds__(256) permute_fwd(const uint8_t *x, const float *probs, const int32_t *row_of_slot,
+                                                   int tokens, int topk, int64_t nv, uint8_t *xs, float *ps) {
+    using R = typename Raw<V>::T;
+    const int t = blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= tokens) return;
+    const int n = tokens * topk;
+    const int32_t *rows = row_of_slot + static_cast<int64_t>(t) * topk;
+    if (ps && blockIdx.y == 0) {
+        for (int j = threadIdx.x; j < topk; j += blockDim.x) {
+            const int32_t r = rows[j];
+            const int at = r < 0 ? ~r : r;
+            if (at < n) ps[at] = r < 0 ? 0.0f : probs[static_cast<int64_t>(t) * topk + j];
+        }
+    }
+    for (int64_t c = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; c < nv;
+         c += static_cast<int64_t>(gridDim.y) * blockDim.x) {
+        const R v = load_once<V>(x + (t * nv + c) * V);
+        const R zero{};
+        for (int j = 0; j < topk; ++j) {
+            const int32_t r = rows[j];
+            const int at = r < 0 ? ~r : r;
+            if (at < n) *reinterpret_cast<R *>(xs + (at * nv + c) * V) = r < 0 ? zero : v;
+        }
+    }
+}
+
+// out[t] = sum_j w_j rows[row(t, j)] (w = 1 without weights): unpermute, and the
+// gradient of permute (which also brings the probabilities' gradients back).
+// kGroup rows are loaded before the first is used.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) combine(const uint8_t *ys, const float *weights, const int32_t *row_of_slot,
+                                               int tokens, int topk, int64_t nv, uint8_t *out, const float *dps,
+                                               float *dprobs) {
+    constexpr int N = V / sizeof(T);
+    const int t = blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= tokens) return;
+    const int n = tokens * topk;
+    const int32_t *rows = row_of_slot + static_cast<int64_t>(t) * topk;
+    if (dprobs && blockIdx.y == 0) {
+        for (int j = threadIdx.x; j < topk; j += blockDim.x) {
+            const int r = live_row(rows[j], n);
+            dprobs[static_cast<int64_t>(t) * topk + j] = r < 0 ? 0.0f : dps[r];
+        }
+    }
+    for (int64_t c = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; c < nv;
+         c += static_cast<int64_t>(gridDim.y) * blockDim.x) {
+        float acc[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+        for (int j0 = 0; j0 < topk; j0 += kGroup) {
+            Vec<T, V> v[kGroup];
+            float w[kGroup];
+            bool live[kGroup];
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g) {
+                const int r = j0 + g < topk ? live_row(rows[j0 + g], n) : -1;
+                live[g] = r >= 0;
+                if (live[g]) {
+                    v[g].raw = load_once<V>(ys + (r * nv + c) * V);
+                    w[g] = weights ? weights[static_cast<int64_t>(t) * topk + j0 + g] : 1.0f;
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g) {
+                if (live[g]) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i] = __fmaf_rn(w[g], as_f32(v[g].e[i]), acc[i]);
+                }
+            }
+        }
+        Vec<T, V> o;
+#pragma unroll
+        for (int i = 0; i < N; ++i) put(o.e[i], acc[i]);
+        *reinterpret_cast<typename Raw<V>::T *>(out + (t * nv + c) * V) = o.raw;
+    }
+}
+
+// dys[row] = w dout[t] and dw = <dout[t], ys[row]> in one pass.  blockDim.y
+// groups of `wpt` warps take a token each; a thread keeps kGroup partial dot
+// products, summed over its columns in order, then over the lanes by halving
+// distances and over the token's warps in order: the sum's order depends on
+// wpt alone, which the launch takes from tokens and width.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) unpermute_bwd(const uint8_t *dout, const uint8_t *ys, const float *weights,
+                                                     const int32_t *row_of_slot, int tokens, int topk, int64_t nv,
+                                                     uint8_t *dys, float *dw) {
+    constexpr int N = V / sizeof(T);
+    __shared__ float part[8][kGroup];
+    const int t = blockIdx.x * blockDim.y + threadIdx.y;
+    const int n = tokens * topk;
+    const int lane = threadIdx.x & 31, wpt = blockDim.x >> 5, warp = threadIdx.y * wpt + (threadIdx.x >> 5);
+    const bool on = t < tokens;
+    const int32_t *rows = row_of_slot + static_cast<int64_t>(on ? t : 0) * topk;
+    for (int j0 = 0; j0 < topk; j0 += kGroup) {
+        int32_t r[kGroup];
+        float w[kGroup], acc[kGroup];
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) {
+            const bool has = on && j0 + g < topk;
+            r[g] = has ? rows[j0 + g] : n;   // n: nothing to do
+            w[g] = has && weights ? weights[static_cast<int64_t>(t) * topk + j0 + g] : 1.0f;
+            acc[g] = 0.0f;
+        }
+        if (on) {
+            for (int64_t c = threadIdx.x; c < nv; c += blockDim.x) {
+                Vec<T, V> d, y[kGroup];
+                d.raw = *reinterpret_cast<const typename Raw<V>::T *>(dout + (t * nv + c) * V);
+                if (dw) {
+#pragma unroll
+                    for (int g = 0; g < kGroup; ++g)
+                        if (live_row(r[g], n) >= 0) y[g].raw = load_once<V>(ys + (r[g] * nv + c) * V);
+                }
+#pragma unroll
+                for (int g = 0; g < kGroup; ++g) {
+                    const bool live = live_row(r[g], n) >= 0;
+                    const int at = r[g] < 0 ? ~r[g] : r[g];
+                    if (dw && live) {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) acc[g] = __fmaf_rn(as_f32(d.e[i]), as_f32(y[g].e[i]), acc[g]);
+                    }
+                    if (dys && at < n) {
+                        Vec<T, V> o;
+#pragma unroll
+                        for (int i = 0; i < N; ++i) put(o.e[i], live ? w[g] * as_f32(d.e[i]) : 0.0f);
+                        *reinterpret_cast<typename Raw<V>::T *>(dys + (at * nv + c) * V) = o.raw;
+                    }
+                }
+            }
+        }
+        if (dw) {
+#pragma unroll
+            for (int g = 0; g < kGroup; ++g) {
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1) acc[g] += __shfl_xor_sync(0xFFFFFFFFu, acc[g], s);
+            }
+            if (wpt > 1) {
+                __syncthreads();
+                if (lane == 0) {
+#pragma unroll
+                    for (int g = 0; g < kGroup; ++g) part[warp][g] = acc[g];
+                }
+                __syncthreads();
+            }
+            if (on && static_cast<int>(threadIdx.x) < kGroup && j0 + static_cast<int>(threadIdx.x) < topk) {
+                const int g = threadIdx.x;
+                float s = 0.0f;
+                if (wpt > 1) {
+                    for (int k = 0; k < wpt; ++k) s += part[threadIdx.y * wpt + k][g];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k)
+                        if (k == g) s = acc[k];
+                }
+                dw[static_cast<int64_t>(t) * topk + j0 + g] = s;
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------- launch
+
+int elem_bytes(int dtype) { return dtype == GSA_FP32 ? 4 : 2; }
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Widest access that every row start allows (the tensors start on 16 bytes).
+int vector_bytes(int64_t row_bytes) {
+    for (int v = 16; v > 2; v /= 2)
+        if (row_bytes % v == 0) return v;
+    return 2;
+}
+
+struct Shape {
+    dim3 grid, block;
+};
+
+// Columns x tokens of a block of 256 threads; columns beyond one pass of a block
+// go to further blocks along grid.y.
+Shape row_shape(int64_t tokens, int64_t nv) {
+    int x = 1;
+    while (x < 256 && x < nv) x *= 2;
+    const int y = 256 / x;
+    int64_t gy = (nv + x - 1) / x;
+    if (gy > 64) gy = 64;
+    return {dim3(static_cast<unsigned>((tokens + y - 1) / y), static_cast<unsigned>(gy)), dim3(x, y)};
+}
+
+gsa_status check_shape(int64_t tokens, int64_t topk, int64_t hidden, int32_t dtype) {
+    if (tokens < 0 || topk <= 0 || hidden <= 0) return GSA_ERR_INVALID_ARG;
+    if (dtype != GSA_BF16 && dtype != GSA_FP16 && dtype != GSA_FP32) return GSA_ERR_INVALID_ARG;
+    if (topk >= (int64_t(1) << 31) || tokens >= (int64_t(1) << 31) || tokens * topk >= (int64_t(1) << 31) ||
+        hidden >= (int64_t(1) << 31))
+        return GSA_ERR_UNSUPPORTED;
+    return GSA_OK;
+}
+
+gsa_status done(int launches) {
+    if (cudaGetLastError() != cudaSuccess) return GSA_ERR_CUDA;
+    gsa::set_last_launches(launches);
+    return GSA_OK;
+}
+
+// Calls f<T, V>() for the element type and access width.
+template <typename T, typename F> void with_vector(int v, F &&f) {
+    switch (v) {
+    case 16: f(T(), std::integral_constant<int, 16>()); break;
+    case 8: f(T(), std::integral_constant<int, 8>()); break;
+    case 4: f(T(), std::integral_constant<int, 4>()); break;
+    default:
+        if constexpr (sizeof(T) == 2) f(T(), std::integral_constant<int, 2>());
+    }
+}
+
+template <typename F> void with_type(int dtype, int v, F &&f) {
+    if (dtype == GSA_BF16) with_vector<__nv_bfloat16>(v, f);
+    else if (dtype == GSA_FP16) with_vector<__half>(v, f);
+    else with_vector<float>(v, f);
+}
+
+gsa_status run_combine(const void *ys, const float *weights, const int32_t *row_of_slot, int64_t tokens, int64_t topk,
+                       int64_t hidden, int32_t dtype, void *out, const float *dps, float *dprobs,
+                       gsa_stream_t stream) {
+    const int v = vector_bytes(hidden * elem_bytes(dtype));
+    const int64_t nv = hidden * elem_bytes(dtype) / v;
+    const Shape s = row_shape(tokens, nv);
+    with_type(dtype, v, [&](auto tag, auto width) {
+        combine<decltype(tag), decltype(width)::value><<<s.grid, s.block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+            static_cast<const uint8_t *>(ys), weights, row_of_slot, static_cast<int>(tokens), static_cast<int>(topk),
+            nv, static_cast<uint8_t *>(out), dps, dprobs);
+    });
+    return done(1);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gsa_moe_sort_workspace_size(int64_t tokens, int64_t topk, int64_t experts) {
+    if (tokens < 0 || topk <= 0 || experts <= 0 || experts >= kMaxBins || tokens >= (int64_t(1) << 31) ||
+        topk >= (int64_t(1) << 31) || tokens * topk >= (int64_t(1) << 31))
+        return 0;
+    const int64_t n = tokens * topk;
+    if (n <= kOneBlockSlots) return 0;
+    const int64_t seg = sort_segment(n);
+    return static_cast<size_t>((n + seg - 1) / seg * (experts + 1) * 4 + 15) / 16 * 16;
+}
+
+gsa_status gsa_moe_sort(const void *expert_idx, int32_t idx_bytes, int64_t tokens, int64_t topk, int64_t experts,
+                        int32_t *row_of_slot, int64_t *split_sizes, void *workspace, size_t workspace_bytes,
+                        gsa_stream_t stream) {
+    if (tokens < 0 || topk <= 0 || experts <= 0 || (idx_bytes != 4 && idx_bytes != 8)) return GSA_ERR_INVALID_ARG;
+    if (experts >= kMaxBins || tokens >= (int64_t(1) << 31) || topk >= (int64_t(1) << 31) ||
+        tokens * topk >= (int64_t(1) << 31))
+        return GSA_ERR_UNSUPPORTED;
+    const int64_t n = tokens * topk;
+    if (!split_sizes || (n > 0 && (!expert_idx || !row_of_slot))) return GSA_ERR_INVALID_ARG;
+    if (!aligned(expert_idx, 16) || !aligned(row_of_slot, 16) || !aligned(split_sizes, 8) || !aligned(workspace, 16))
+        return GSA_ERR_ALIGNMENT;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int E = static_cast<int>(experts);
+    const int64_t seg = sort_segment(n);
+    if (n <= kOneBlockSlots) {
+        int threads = 32;
+        while (threads < 1024 && threads * 4 < n) threads *= 2;
+        sort_rank<<<1, threads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, nullptr, row_of_slot, split_sizes);
+        return done(1);
+    }
+    if (!workspace || workspace_bytes < gsa_moe_sort_workspace_size(tokens, topk, experts)) return GSA_ERR_WORKSPACE;
+    const unsigned blocks = static_cast<unsigned>((n + seg - 1) / seg);
+    sort_count<<<blocks, kSegThreads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, static_cast<int *>(workspace));
+    sort_rank<<<blocks, kSegThreads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, static_cast<const int *>(workspace),
+                                             row_of_slot, split_sizes);
+    return done(2);
+}
+
+gsa_status gsa_moe_permute(const void *x, const float *probs, const int32_t *row_of_slot, int64_t tokens, int64_t topk,
+                           int64_t hidden, int32_t dtype, void *xs, float *ps, gsa_stream_t stream) {
+    gsa_status st = check_shape(tokens, topk, hidden, dtype);
+    if (st != GSA_OK) return st;
+    if ((probs == nullptr) != (ps == nullptr) && tokens > 0) return GSA_ERR_INVALID_ARG;
+    if (tokens > 0 && (!x || !xs || !row_of_slot)) return GSA_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(row_of_slot, 4) || !aligned(probs, 4) || !aligned(ps, 4))
+        return GSA_ERR_ALIGNMENT;
+    if (tokens == 0) return done(0);
+    const int v = vector_bytes(hidden * elem_bytes(dtype));
+    const int64_t nv = hidden * elem_bytes(dtype) / v;
+    const Shape s = row_shape(tokens, nv);
+    auto go = [&](auto width) {
+        permute_fwd<decltype(width)::value><<<s.grid, s.block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+            static_cast<const uint8_t *>(x), probs, row_of_slot, static_cast<int>(tokens), static_cast<int>(topk), nv,
+            static_cast<uint8_t *>(xs), ps);
+    };
+    switch (v) {
+    case 16: go(std::integral_constant<int, 16>()); break;
+    case 8: go(std::integral_constant<int, 8>()); break;
+    case 4: go(std::integral_constant<int, 4>()); break;
+    default: go(std::integral_constant<int, 2>());
+    }
+    return done(1);
+}
+
+gsa_status gsa_moe_permute_bwd(const void *dxs, const float *dps, const int32_t *row_of_slot, int64_t tokens,
+                               int64_t topk, int64_t hidden, int32_t dtype, void *dx, float *dprobs,
+                               gsa_stream_t stream) {
+    gsa_status st = check_shape(tokens, topk, hidden, dtype);
+    if (st != GSA_OK) return st;
+    if ((dps == nullptr) != (dprobs == nullptr) && tokens > 0) return GSA_ERR_INVALID_ARG;
+    if (tokens > 0 && (!dxs || !dx || !row_of_slot)) return GSA_ERR_INVALID_ARG;
+    if (!aligned(dxs, 16) || !aligned(dx, 16) || !aligned(row_of_slot, 4) || !aligned(dps, 4) || !aligned(dprobs, 4))
+        return GSA_ERR_ALIGNMENT;
+    if (tokens == 0) return done(0);
+    return run_combine(dxs, nullptr, row_of_slot, tokens, topk, hidden, dtype, dx, dps, dprobs, stream);
+}
+
+gsa_status gsa_moe_unpermute(const void *ys, const float *weights, const int32_t *row_of_slot, int64_t tokens,
+                             int64_t topk, int64_t hidden, int32_t dtype, void *out, gsa_stream_t stream) {
+    gsa_status st = check_shape(tokens, topk, hidden, dtype);
+    if (st != GSA_OK) return st;
+    if (tokens > 0 && (!ys || !out || !row_of_slot)) return GSA_ERR_INVALID_ARG;
+    if (!aligned(ys, 16) || !aligned(out, 16) || !aligned(row_of_slot, 4) || !aligned(weights, 4))
+        return GSA_ERR_ALIGNMENT;
+    if (tokens == 0) return done(0);
+    return run_combine(ys, weights, row_of_slot, tokens, topk, hidden, dtype, out, nullptr, nullptr, stream);
+}
+
+gsa_status gsa_moe_unpermute_bwd(const void *dout, const void *ys, const float *weights, const int32_t *row_of_slot,
+                                 int64_t tokens, int64_t topk, int64_t hidden, int32_t dtype, void *dys,
+                                 float *dweights, gsa_stream_t stream) {
+    gsa_status st = check_shape(tokens, topk, hidden, dtype);
+    if (st != GSA_OK) return st;
+    if (tokens > 0 && (!dout || !row_of_slot || (!dys && !dweights) || (dweights && !ys))) return GSA_ERR_INVALID_ARG;
+    if (!aligned(dout, 16) || !aligned(ys, 16) || !aligned(dys, 16) || !aligned(row_of_slot, 4) ||
+        !aligned(weights, 4) || !aligned(dweights, 4))
+        return GSA_ERR_ALIGNMENT;
+    if (tokens == 0) return done(0);
+    const int v = vector_bytes(hidden * elem_bytes(dtype));
+    const int64_t nv = hidden * elem_bytes(dtype) / v;
+    // warps per token: one while the tokens alone fill the machine
+    int wpt = 1;
+    while (wpt < 8 && tokens * wpt < 152 * 32 && wpt * 32 < nv) wpt *= 2;
+    const dim3 block(32 * wpt, 8 / wpt), grid(static_cast<unsigned>((tokens + block.y - 1) / block.y));
+    with_type(dtype, v, [&](auto tag, auto width) {
+        unpermute_bwd<decltype(tag), decltype(width)::value>
+            <<<grid, block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+                static_cast<const uint8_t *>(dout), static_cast<const uint8_t *>(ys), weights, row_of_slot,
+                static_cast<int>(tokens), static_cast<int>(topk), nv, static_cast<uint8_t *>(dys), dweights);
+    });
+    return done(1);
+}
+
+}  // extern "C"

@@ -27,7 +27,8 @@ EXPORTED = ["gsa_layout", "gsa_workspace_size", "grouped_scaled_act_fwd", "group
             "gsa_workspace_status", "gsa_last_launch_count", "gsa_status_string", "gsa_version",
             "gsa_fwd_noalloc", "gsa_fwd_noalloc_status", "gsa_layout_bound", "gsa_workspace_size_graph_safe",
             "grouped_scaled_act_fwd_graph_safe", "grouped_scaled_act_bwd_graph_safe", "gsa_selftest_wait_timeout",
-            "gsa_layout_ex", "gsa_layout_bound_ex"]
+            "gsa_layout_ex", "gsa_layout_bound_ex", "gsa_moe_sort_workspace_size", "gsa_moe_sort", "gsa_moe_permute",
+            "gsa_moe_permute_bwd", "gsa_moe_unpermute", "gsa_moe_unpermute_bwd"]
 
 
 class GsaError(RuntimeError):
@@ -111,6 +112,16 @@ def load():
         L.gsa_last_launch_count.argtypes = []
         L.gsa_status_string.restype = ctypes.c_char_p
         L.gsa_status_string.argtypes = [ctypes.c_int]
+        route = [_I64, _I64, _I64, ctypes.c_int32]   # tokens, topk, hidden, dtype
+        for name, args in (("gsa_moe_sort", [_P, ctypes.c_int32, _I64, _I64, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
+                           ("gsa_moe_permute", [_P, _P, _P, *route, _P, _P, _P]),
+                           ("gsa_moe_permute_bwd", [_P, _P, _P, *route, _P, _P, _P]),
+                           ("gsa_moe_unpermute", [_P, _P, _P, *route, _P, _P]),
+                           ("gsa_moe_unpermute_bwd", [_P, _P, _P, _P, *route, _P, _P, _P])):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = args
+        L.gsa_moe_sort_workspace_size.restype = ctypes.c_size_t
+        L.gsa_moe_sort_workspace_size.argtypes = [_I64, _I64, _I64]
         L.gsa_version.restype = ctypes.c_int32
         L.gsa_version.argtypes = []
         _lib = L
@@ -467,3 +478,172 @@ def bwd_graph_safe(dy, x, probs, split_dev, act: str, recipe_kind: int, rht: boo
                                            _stream_ptr(stream))
     _check(st, "grouped_scaled_act_bwd_graph_safe")
     return out
+
+
+# ------------------------------------------- tokens into expert order and back
+
+BF16, FP16, FP32 = 0, 1, 2
+_DTYPE_NAMES = {"torch.bfloat16": BF16, "torch.float16": FP16, "torch.float32": FP32}
+_DTYPES: dict = {}
+
+
+def _dtype_code(t, what):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        code = _DTYPE_NAMES.get(str(t.dtype))
+        if code is None:
+            raise GsaError(1, f"{what}: element type {t.dtype} (bfloat16, float16 or float32 expected)")
+        _DTYPES[t.dtype] = code
+    return code
+
+
+def _require(t, what, shape, dtype, device=None):
+    """A contiguous CUDA tensor of this shape and type (on `device`)."""
+    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
+        raise GsaError(1, f"{what}: contiguous CUDA {dtype} {list(shape)} expected, got {t.device} {t.dtype} "
+                          f"{list(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'}")
+    if device is not None and t.device != device:
+        raise GsaError(1, f"{what}: on {t.device}, expected {device}")
+
+
+class _On:
+    """The stream of a call.  With `stream` given, new tensors are allocated for that stream and the inputs are
+    recorded on it, so that the caching allocator keeps both until the stream is done with them."""
+
+    def __init__(self, stream, device, *inputs):
+        import torch
+        if stream is None:
+            self.ctx, self.ptr = None, torch.cuda.current_stream(device).cuda_stream
+        else:
+            self.ctx, self.ptr = torch.cuda.stream(stream), stream.cuda_stream
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def empty(self, shape, dtype, device):
+        import torch
+        if self.ctx is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with self.ctx:
+            return torch.empty(shape, dtype=dtype, device=device)
+
+    def out(self, given, what, shape, dtype, device):
+        if given is None:
+            return self.empty(shape, dtype, device)
+        _require(given, what, shape, dtype, device)
+        return given
+
+
+def moe_sort(expert_idx, experts: int, out: tuple | None = None, stream=None):
+    """Sort plan of expert_idx [tokens, topk] (int32 / int64; a value outside [0, experts) drops the slot):
+    -> (row_of_slot [tokens, topk] int32, split_sizes [experts + 1] int64), both on the device."""
+    import torch
+    if expert_idx.dim() != 2 or expert_idx.dtype not in (torch.int32, torch.int64):
+        raise GsaError(1, "moe_sort: expert_idx must be int32 or int64 [tokens, topk]")
+    _require(expert_idx, "moe_sort: expert_idx", tuple(expert_idx.shape), expert_idx.dtype)
+    L, dev = load(), expert_idx.device
+    tokens, topk = expert_idx.shape
+    on = _On(stream, dev, expert_idx)
+    row, split = out or (None, None)
+    row = on.out(row, "moe_sort: row_of_slot", (tokens, topk), torch.int32, dev)
+    split = on.out(split, "moe_sort: split_sizes", (max(0, experts) + 1,), torch.int64, dev)
+    nbytes = L.gsa_moe_sort_workspace_size(tokens, topk, experts)
+    ws = on.empty((nbytes,), torch.uint8, dev) if nbytes else None
+    _check(L.gsa_moe_sort(expert_idx.data_ptr(), expert_idx.element_size(), tokens, topk, experts, row.data_ptr(),
+                          split.data_ptr(), ws.data_ptr() if nbytes else None, nbytes, on.ptr), "gsa_moe_sort")
+    return row, split
+
+
+def _plan_shape(row_of_slot, what):
+    import torch
+    if row_of_slot.dim() != 2:
+        raise GsaError(1, f"{what}: row_of_slot must be [tokens, topk]")
+    _require(row_of_slot, f"{what}: row_of_slot", tuple(row_of_slot.shape), torch.int32)
+    return row_of_slot.shape
+
+
+def _rows(t, n, what):
+    """(hidden, dtype code) of a [n, hidden] row tensor."""
+    if t.dim() != 2:
+        raise GsaError(1, f"{what} must be [{n}, hidden]")
+    code = _dtype_code(t, what)
+    _require(t, what, (n, t.shape[1]), t.dtype)
+    return t.shape[1], code
+
+
+def moe_permute(x, row_of_slot, probs=None, out: tuple | None = None, stream=None):
+    """Token rows x [tokens, hidden] into expert order: xs [tokens * topk, hidden], and with probs
+    [tokens, topk] (FP32) -> (xs, ps [tokens * topk])."""
+    import torch
+    tokens, topk = _plan_shape(row_of_slot, "moe_permute")
+    hidden, code = _rows(x, tokens, "moe_permute: x")
+    dev = x.device
+    on = _On(stream, dev, x, row_of_slot, probs)
+    xs, ps = (out if probs is not None else (out, None)) if out is not None else (None, None)
+    xs = on.out(xs, "moe_permute: xs", (tokens * topk, hidden), x.dtype, dev)
+    if probs is not None:
+        _require(probs, "moe_permute: probs", (tokens, topk), torch.float32, dev)
+        ps = on.out(ps, "moe_permute: ps", (tokens * topk,), torch.float32, dev)
+    _check(load().gsa_moe_permute(x.data_ptr(), None if probs is None else probs.data_ptr(), row_of_slot.data_ptr(),
+                                  tokens, topk, hidden, code, xs.data_ptr(), None if ps is None else ps.data_ptr(),
+                                  on.ptr), "gsa_moe_permute")
+    return xs if probs is None else (xs, ps)
+
+
+def moe_permute_bwd(dxs, row_of_slot, dps=None, out: tuple | None = None, stream=None):
+    """Gradient of moe_permute: dx [tokens, hidden], and with dps [tokens * topk] -> (dx, dprobs)."""
+    import torch
+    tokens, topk = _plan_shape(row_of_slot, "moe_permute_bwd")
+    hidden, code = _rows(dxs, tokens * topk, "moe_permute_bwd: dxs")
+    dev = dxs.device
+    on = _On(stream, dev, dxs, row_of_slot, dps)
+    dx, dprobs = (out if dps is not None else (out, None)) if out is not None else (None, None)
+    dx = on.out(dx, "moe_permute_bwd: dx", (tokens, hidden), dxs.dtype, dev)
+    if dps is not None:
+        _require(dps, "moe_permute_bwd: dps", (tokens * topk,), torch.float32, dev)
+        dprobs = on.out(dprobs, "moe_permute_bwd: dprobs", (tokens, topk), torch.float32, dev)
+    _check(load().gsa_moe_permute_bwd(dxs.data_ptr(), None if dps is None else dps.data_ptr(), row_of_slot.data_ptr(),
+                                      tokens, topk, hidden, code, dx.data_ptr(),
+                                      None if dprobs is None else dprobs.data_ptr(), on.ptr), "gsa_moe_permute_bwd")
+    return dx if dps is None else (dx, dprobs)
+
+
+def moe_unpermute(ys, row_of_slot, weights=None, out=None, stream=None):
+    """Expert rows ys [tokens * topk, hidden] back to tokens: out [tokens, hidden], the sum over a token's slots
+    weighted by weights [tokens, topk] (FP32; None: 1)."""
+    import torch
+    tokens, topk = _plan_shape(row_of_slot, "moe_unpermute")
+    hidden, code = _rows(ys, tokens * topk, "moe_unpermute: ys")
+    dev = ys.device
+    on = _On(stream, dev, ys, row_of_slot, weights)
+    if weights is not None:
+        _require(weights, "moe_unpermute: weights", (tokens, topk), torch.float32, dev)
+    out = on.out(out, "moe_unpermute: out", (tokens, hidden), ys.dtype, dev)
+    _check(load().gsa_moe_unpermute(ys.data_ptr(), None if weights is None else weights.data_ptr(),
+                                    row_of_slot.data_ptr(), tokens, topk, hidden, code, out.data_ptr(), on.ptr),
+           "gsa_moe_unpermute")
+    return out
+
+
+def moe_unpermute_bwd(dout, ys, row_of_slot, weights=None, want_dys: bool = True, out: tuple | None = None,
+                      stream=None):
+    """Gradient of moe_unpermute for dout [tokens, hidden]: (dys [tokens * topk, hidden], dweights [tokens, topk]
+    FP32).  ys = None skips dweights, want_dys = False skips dys (None in its place)."""
+    import torch
+    tokens, topk = _plan_shape(row_of_slot, "moe_unpermute_bwd")
+    hidden, code = _rows(dout, tokens, "moe_unpermute_bwd: dout")
+    dev = dout.device
+    on = _On(stream, dev, dout, ys, row_of_slot, weights)
+    if weights is not None:
+        _require(weights, "moe_unpermute_bwd: weights", (tokens, topk), torch.float32, dev)
+    dys, dw = out if out is not None else (None, None)
+    if want_dys:
+        dys = on.out(dys, "moe_unpermute_bwd: dys", (tokens * topk, hidden), dout.dtype, dev)
+    if ys is not None:
+        _require(ys, "moe_unpermute_bwd: ys", (tokens * topk, hidden), dout.dtype, dev)
+        dw = on.out(dw, "moe_unpermute_bwd: dweights", (tokens, topk), torch.float32, dev)
+    _check(load().gsa_moe_unpermute_bwd(dout.data_ptr(), None if ys is None else ys.data_ptr(),
+                                        None if weights is None else weights.data_ptr(), row_of_slot.data_ptr(),
+                                        tokens, topk, hidden, code, dys.data_ptr() if want_dys else None,
+                                        None if ys is None else dw.data_ptr(), on.ptr), "gsa_moe_unpermute_bwd")
+    return dys if want_dys else None, dw if ys is not None else None
