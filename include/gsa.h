@@ -377,6 +377,49 @@ gsa_status gsa_moe_unpermute_bwd(const void *dout, const void *ys, const float *
                                  int64_t tokens, int64_t topk, int64_t hidden, int32_t dtype, void *dys,
                                  float *dweights, gsa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Grouped products of quantized operands.
+ *
+ * The GEMMs on both sides of the activation step, on the quantized copies that
+ * the calls above write, with GSA_SCALES_TILED scales and per-expert weights.
+ * The split is in device memory, as for the graph-safe calls: nothing depends on
+ * the host knowing it, nothing synchronizes or allocates, one launch per call. */
+
+/* One quantized operand: a copy's codes, its tiled scales and (NVFP4) its
+ * amax [E].  The byte counts are the buffers' sizes; the calls check them. */
+typedef struct {
+    const void *data;
+    const void *scale;
+    const float *amax;
+    int64_t data_bytes;
+    int64_t scale_bytes;
+} gsa_qin;
+
+/* out[r, n] = sum_k A[r, k] B_e[n, k] for the rows r of expert e.
+ *   a    rowwise copy of a [M, K] tensor grouped by split_sizes_dev.
+ *   b    E matrices [N, K]: the rowwise copy of [E * N, K] grouped in E times N
+ *        rows (forward, weights [N, K]), or the columnwise copy (without RHT) of
+ *        [E * K, N] in E times K rows (input gradient: b is the transpose of
+ *        weights [K, N]; needs K % 32 = 0 there).  Both have the same layout.
+ *   split_sizes_dev  [E] int64, device: rows per expert, the sum at most M.  Rows
+ *        of out past the sum are zero (dropped rows of a sort).
+ *   out  [M, N] row-major, out_dtype GSA_BF16 or GSA_FP32 (sums in FP32).
+ * K is a multiple of 64, N and the row counts are arbitrary.  A device split with
+ * a negative entry, a sum above M or more row tiles than a->scale_bytes holds is
+ * not processed: nothing is written and gsa_grouped_gemm_status returns
+ * GSA_ERR_INVALID_ARG.
+ * Errors: INVALID_ARG, UNSUPPORTED (E > 256, K % 64, sizes past 2^31), ALIGNMENT
+ * (16 bytes; split 8), CUDA. */
+gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *split_sizes_dev, int64_t E, int64_t M,
+                            int64_t N, int64_t K, int32_t recipe_kind, void *out, int32_t out_dtype,
+                            gsa_stream_t stream);
+
+/* Synchronizes `stream`; then what grouped products on the current device have
+ * reported since the last query, which it clears: GSA_OK, GSA_ERR_INVALID_ARG
+ * (a device split), GSA_ERR_DEVICE_TIMEOUT (a bounded wait ran out).  Errors:
+ * CUDA. */
+gsa_status gsa_grouped_gemm_status(gsa_stream_t stream);
+
 /* Failure-detection self-test.  Enqueues a one-thread kernel that runs one of
  * the library's bounded waits on something nothing signals -- which = 0: the
  * wait for a workspace counter (the encode pass's wait for its expert's amax

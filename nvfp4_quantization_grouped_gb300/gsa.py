@@ -28,7 +28,8 @@ EXPORTED = ["gsa_layout", "gsa_workspace_size", "grouped_scaled_act_fwd", "group
             "gsa_fwd_noalloc", "gsa_fwd_noalloc_status", "gsa_layout_bound", "gsa_workspace_size_graph_safe",
             "grouped_scaled_act_fwd_graph_safe", "grouped_scaled_act_bwd_graph_safe", "gsa_selftest_wait_timeout",
             "gsa_layout_ex", "gsa_layout_bound_ex", "gsa_moe_sort_workspace_size", "gsa_moe_sort", "gsa_moe_permute",
-            "gsa_moe_permute_bwd", "gsa_moe_unpermute", "gsa_moe_unpermute_bwd"]
+            "gsa_moe_permute_bwd", "gsa_moe_unpermute", "gsa_moe_unpermute_bwd", "gsa_grouped_gemm",
+            "gsa_grouped_gemm_status"]
 
 
 class GsaError(RuntimeError):
@@ -50,6 +51,11 @@ class Recipe(ctypes.Structure):
 class QOut(ctypes.Structure):
     _fields_ = [("row_data", ctypes.c_void_p), ("row_scale", ctypes.c_void_p), ("col_data", ctypes.c_void_p),
                 ("col_scale", ctypes.c_void_p), ("amax_row", ctypes.c_void_p), ("amax_col", ctypes.c_void_p)]
+
+
+class QIn(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("amax", ctypes.c_void_p),
+                ("data_bytes", ctypes.c_int64), ("scale_bytes", ctypes.c_int64)]
 
 
 class LayoutInfo(ctypes.Structure):
@@ -122,6 +128,11 @@ def load():
             getattr(L, name).argtypes = args
         L.gsa_moe_sort_workspace_size.restype = ctypes.c_size_t
         L.gsa_moe_sort_workspace_size.argtypes = [_I64, _I64, _I64]
+        L.gsa_grouped_gemm.restype = ctypes.c_int
+        L.gsa_grouped_gemm.argtypes = [ctypes.POINTER(QIn), ctypes.POINTER(QIn), _P, _I64, _I64, _I64, _I64,
+                                       ctypes.c_int32, _P, ctypes.c_int32, _P]
+        L.gsa_grouped_gemm_status.restype = ctypes.c_int
+        L.gsa_grouped_gemm_status.argtypes = [_P]
         L.gsa_version.restype = ctypes.c_int32
         L.gsa_version.argtypes = []
         _lib = L
@@ -647,3 +658,56 @@ def moe_unpermute_bwd(dout, ys, row_of_slot, weights=None, want_dys: bool = True
                                         tokens, topk, hidden, code, dys.data_ptr() if want_dys else None,
                                         None if ys is None else dw.data_ptr(), on.ptr), "gsa_moe_unpermute_bwd")
     return dys if want_dys else None, dw if ys is not None else None
+
+
+# ---------------------------------------- grouped products of quantized operands
+
+def _operand(q: dict, side: str, recipe_kind: int, experts: int, what: str, dev):
+    """QIn of one copy of a quantized tensor (side 'row' or 'col'), and its tensors."""
+    import torch
+    t = [q.get(side + "_data"), q.get(side + "_scale"), q.get("amax_" + side) if recipe_kind == NVFP4 else None]
+    for name, v in zip((side + "_data", side + "_scale"), t):
+        if v is None:
+            raise GsaError(1, f"{what}: no {name} (a {side} copy with tiled scales is needed)")
+        _require(v, f"{what}: {name}", tuple(v.shape), torch.uint8, dev)
+    if recipe_kind == NVFP4:
+        if t[2] is None:
+            raise GsaError(1, f"{what}: no amax_{side}")
+        _require(t[2], f"{what}: amax_{side}", (t[2].numel(),), torch.float32, dev)
+        if t[2].numel() < experts:
+            raise GsaError(1, f"{what}: amax_{side} has {t[2].numel()} entries for {experts} experts")
+    return QIn(t[0].data_ptr(), t[1].data_ptr(), t[2].data_ptr() if t[2] is not None else None, t[0].numel(),
+               t[1].numel()), t
+
+
+def _out_code(out_dtype):
+    code = _DTYPE_NAMES.get(str(out_dtype))
+    if code not in (BF16, FP32):
+        raise GsaError(1, f"output type {out_dtype} (bfloat16 or float32 expected)")
+    return code
+
+
+def grouped_gemm(a: dict, b: dict, split, m: int, n: int, k: int, recipe_kind: int, out_dtype=None,
+                 b_columnwise: bool = False, out=None, stream=None):
+    """out [m, n] = A B_e^T over the rows of each expert, on the quantized copies that fwd / bwd write with
+    scale_layout=SCALES_TILED.  a: the rowwise copy of the [m, k] rows.  b: the experts' weights, the rowwise copy
+    of [E * n, k] split into E times n rows, or with b_columnwise the columnwise copy of [E * k, n] split into E
+    times k rows (the input gradient's product with weights [k, n]).  split: [E] int64 on the device, sum at most
+    m (rows past it become zero).  out_dtype: torch.bfloat16 (default) or torch.float32."""
+    import torch
+    out_dtype = out_dtype or torch.bfloat16
+    code = _out_code(out_dtype)
+    _require(split, "grouped_gemm: split", (split.numel(),), torch.int64)
+    dev, experts = split.device, split.numel()
+    qa, ta = _operand(a, "row", recipe_kind, experts, "grouped_gemm: a", dev)
+    qb, tb = _operand(b, "col" if b_columnwise else "row", recipe_kind, experts, "grouped_gemm: b", dev)
+    on = _On(stream, dev, split, *ta, *tb)
+    out = on.out(out, "grouped_gemm: out", (m, n), out_dtype, dev)
+    _check(load().gsa_grouped_gemm(qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, out.data_ptr(), code,
+                                   on.ptr), "gsa_grouped_gemm")
+    return out
+
+
+def grouped_gemm_status(stream=None) -> int:
+    """What the grouped products on this device have reported since the last query (synchronizes the stream)."""
+    return load().gsa_grouped_gemm_status(_stream_ptr(stream))
