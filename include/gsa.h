@@ -414,6 +414,17 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
                             int64_t N, int64_t K, int32_t recipe_kind, void *out, int32_t out_dtype,
                             gsa_stream_t stream);
 
+/* dw[e] [N, K] = sum over the rows r of expert e of A[r, :]^T B[r, :].
+ *   a, b  columnwise copies of [M, N] and [M, K] tensors grouped by the split
+ *         (NVFP4 with the RHT: the same sign mask in both, it cancels).
+ *   dw    [E, N, K] row-major, GSA_BF16 or GSA_FP32; zeros for an expert without
+ *         rows.  accumulate != 0: added to what dw holds (one rounding of the sum).
+ * N and K are even (NVFP4) or arbitrary (MXFP8); the split and errors as for
+ * gsa_grouped_gemm, the buffers checked against all four byte counts. */
+gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int64_t *split_sizes_dev, int64_t E,
+                                  int64_t M, int64_t N, int64_t K, int32_t recipe_kind, void *dw, int32_t out_dtype,
+                                  int32_t accumulate, gsa_stream_t stream);
+
 /* Synchronizes `stream`; then what grouped products on the current device have
  * reported since the last query, which it clears: GSA_OK, GSA_ERR_INVALID_ARG
  * (a device split), GSA_ERR_DEVICE_TIMEOUT (a bounded wait ran out).  Errors:

@@ -143,8 +143,9 @@ __device__ __forceinline__ Tile tile_at(const GemmParams &P, const Shared &sh, i
     return t;
 }
 
-__device__ __forceinline__ void store_row(__nv_bfloat16 *o, const float *v, int n, bool wide) {
-    if (wide && n == 8) {
+// Up to 8 results to o (wide: o is on 16 bytes), rounded once; add: onto what is there.
+__device__ __forceinline__ void store_row(__nv_bfloat16 *o, const float *v, int n, bool wide, bool add) {
+    if (wide && n == 8 && !add) {
         uint4 w;
         __nv_bfloat162 h[4];
 #pragma unroll
@@ -154,19 +155,135 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *o, const float *v, int 
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) o[i] = __float2bfloat16_rn(v[i]);
+            if (i < n) o[i] = __float2bfloat16_rn(add ? __bfloat162float(o[i]) + v[i] : v[i]);
     }
 }
 
-__device__ __forceinline__ void store_row(float *o, const float *v, int n, bool wide) {
+__device__ __forceinline__ void store_row(float *o, const float *v, int n, bool wide, bool add) {
     if (wide && n == 8) {
-        *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4 *>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        float4 x = make_float4(v[0], v[1], v[2], v[3]), y = make_float4(v[4], v[5], v[6], v[7]);
+        if (add) {
+            const float4 p = *reinterpret_cast<const float4 *>(o), q = *reinterpret_cast<const float4 *>(o + 4);
+            x.x += p.x, x.y += p.y, x.z += p.z, x.w += p.w;
+            y.x += q.x, y.y += q.y, y.z += q.z, y.w += q.w;
+        }
+        *reinterpret_cast<float4 *>(o) = x;
+        *reinterpret_cast<float4 *>(o + 4) = y;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) o[i] = v[i];
+            if (i < n) o[i] = add ? o[i] + v[i] : v[i];
     }
+}
+
+// Where a stage's parts lie in shared memory.
+template <bool NV, int BN> struct Stages {
+    using C = Cfg<NV, BN>;
+    uint32_t base;   // a multiple of 1024: the swizzle pattern repeats every 1024 bytes
+    __device__ explicit Stages(const void *dyn) : base((tc::smem_u32(dyn) + 1023u) & ~1023u) {}
+    __device__ uint32_t a(int s) const { return base + s * C::kStride; }
+    __device__ uint32_t b(int s) const { return a(s) + C::kBytesA; }
+    __device__ uint32_t sa(int s) const { return b(s) + C::kBytesB; }
+    __device__ uint32_t sb(int s) const { return sa(s) + C::kBytesSA; }
+};
+
+// The products of one stage: scales to their columns of tensor memory, then
+// `steps` steps of 32 bytes of k.  The scale columns are the stage's own, so the
+// barrier that frees the stage frees them too.
+template <bool NV, int BN>
+__device__ __forceinline__ void multiply_stage(const Stages<NV, BN> &st, int s, uint32_t tmem, uint32_t d, int steps,
+                                               bool first) {
+    using C = Cfg<NV, BN>;
+    constexpr uint32_t idesc = tc::idesc_block_scaled(NV, kRowsT, BN);
+    constexpr int kSc = C::kSc;
+    const uint32_t sfa = tmem + C::kAcc * BN + s * C::kScCols, sfb = sfa + 4 * kSc;
+#pragma unroll
+    for (int j = 0; j < kSc; ++j) {
+        tc::copy_scales(sfa + 4 * j, tc::desc_scales(st.sa(s) + j * kScaleTile));
+#pragma unroll
+        for (int b = 0; b < C::kGroupsB; ++b)
+            tc::copy_scales(sfb + 4 * (j * C::kGroupsB + b), tc::desc_scales(st.sb(s) + (b * kSc + j) * kScaleTile));
+    }
+    for (int j = 0; j < steps; ++j) {
+        const uint64_t da = tc::desc_sw128(st.a(s) + 32 * j), db = tc::desc_sw128(st.b(s) + 32 * j);
+        const bool add = !first || j > 0;
+        if (NV) tc::mma_nvf4(d, da, db, idesc, sfa + 4 * j, sfb + 4 * C::kGroupsB * j, add);
+        else tc::mma_mxf8(d, da, db, idesc | tc::idesc_scale_id(j), sfa, sfb, add);
+    }
+}
+
+// After a wait that ran out: waits (bounded) for the last stages' barriers, so
+// that no copy or product is in flight when the block leaves.
+template <int kStages> __device__ __forceinline__ void settle(uint64_t *bars, int it) {
+    uint32_t none = 0;
+    for (int j = it < kStages ? 0 : it - kStages; j < it; ++j)
+        tc::bar_wait(tc::smem_u32(&bars[j % kStages]), (j / kStages) & 1, &none);
+}
+
+// Barriers, tensor memory, and the block's start and end.
+template <int kStages> __device__ __forceinline__ void open_block(Shared &sh, int warp, uint32_t full_count, uint32_t cols) {
+    if (threadIdx.x == 0) {
+        sh.dead = 0;
+        for (int s = 0; s < kStages; ++s) {
+            tc::bar_init(tc::smem_u32(&sh.full[s]), full_count);
+            tc::bar_init(tc::smem_u32(&sh.empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            tc::bar_init(tc::smem_u32(&sh.acc_full[a]), 1);
+            tc::bar_init(tc::smem_u32(&sh.acc_empty[a]), kEpiWarps);
+        }
+        tc::bar_init_fence();
+    }
+    if (warp == 1) tc::tmem_alloc(tc::smem_u32(&sh.tmem), cols);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+}
+
+__device__ __forceinline__ void close_block(Shared &sh, int warp, uint32_t cols) {
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after();
+        tc::tmem_free(sh.tmem, cols);
+    }
+    if (threadIdx.x == 0 && sh.dead) atomicOr(&g_status, ERR_TIMEOUT);
+}
+
+// One accumulator to memory: this thread's lane and kHalf columns from tensor
+// memory, times ua and ub, to o[0 .. cols).  on: the lane holds a row of the
+// result.  add: onto what is there.  The accumulator is handed back as soon as
+// its last columns are in registers.
+template <int kHalf, typename T>
+__device__ __forceinline__ void drain(uint32_t src, uint64_t *acc_empty, float ua, float ub, T *o, int64_t cols,
+                                      bool on, bool wide, bool add) {
+#pragma unroll
+    for (int c = 0; c < kHalf; c += 64) {
+        uint32_t v[64];
+        tc::tmem_ld64(src + c, v);
+        if (c + 64 == kHalf) {
+            tc::fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) tc::bar_arrive(tc::smem_u32(acc_empty));
+        }
+        if (on) {
+#pragma unroll
+            for (int j = 0; j < 64; j += 8) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[j + e]) * ua * ub;
+                const int64_t left = cols - c - j;
+                if (left > 0) store_row(o + c + j, f, static_cast<int>(left < 8 ? left : 8), wide, add);
+            }
+        }
+    }
+}
+
+template <typename T> __device__ __forceinline__ void zeros(T *o, int half, int64_t cols, bool wide) {
+    const float zero[8] = {};
+    for (int c = 0; c < half && c < cols; c += 8)
+        store_row(o + c, zero, static_cast<int>(cols - c < 8 ? cols - c : 8), wide, false);
 }
 
 template <bool NV, int BN, typename T>
@@ -182,27 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
     }
     const int64_t total = static_cast<int64_t>(sh.tile0[P.E + 1]) * P.n_tiles;
     if (static_cast<int64_t>(blockIdx.x) >= total) return;
-    const uint32_t base = (tc::smem_u32(dyn) + 1023u) & ~1023u;   // the swizzle pattern repeats every 1024 bytes
-    auto sA = [&](int s) { return base + s * C::kStride; };
-    auto sB = [&](int s) { return sA(s) + C::kBytesA; };
-    auto sSA = [&](int s) { return sB(s) + C::kBytesB; };
-    auto sSB = [&](int s) { return sSA(s) + C::kBytesSA; };
-    if (threadIdx.x == 0) {
-        sh.dead = 0;
-        for (int s = 0; s < C::kStages; ++s) {
-            tc::bar_init(tc::smem_u32(&sh.full[s]), 1);
-            tc::bar_init(tc::smem_u32(&sh.empty[s]), 1);
-        }
-        for (int a = 0; a < 2; ++a) {
-            tc::bar_init(tc::smem_u32(&sh.acc_full[a]), 1);
-            tc::bar_init(tc::smem_u32(&sh.acc_empty[a]), kEpiWarps);
-        }
-        tc::bar_init_fence();
-    }
-    if (warp == 1) tc::tmem_alloc(tc::smem_u32(&sh.tmem), C::kCols);
-    tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
+    const Stages<NV, BN> st(dyn);
+    open_block<C::kStages>(sh, warp, 1, C::kCols);
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *dead = &sh.dead;
     constexpr int kSc = C::kSc;
@@ -225,23 +323,17 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
                 }
                 const uint32_t bar = tc::smem_u32(&sh.full[s]);
                 tc::bar_expect(bar, C::kStageBytes);
-                tc::load_2d(sA(s), &P.tm_a, k * kStageK, static_cast<int>(t.row), bar);
-                tc::load_2d(sB(s), &P.tm_b, k * kStageK, static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN), bar);
-                tc::load_2d(sSA(s), &P.tm_sa, 0, a_tile + k * kSc, bar);
+                tc::load_2d(st.a(s), &P.tm_a, k * kStageK, static_cast<int>(t.row), bar);
+                tc::load_2d(st.b(s), &P.tm_b, k * kStageK, static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN), bar);
+                tc::load_2d(st.sa(s), &P.tm_sa, 0, a_tile + k * kSc, bar);
 #pragma unroll
                 for (int b = 0; b < C::kGroupsB; ++b)
-                    tc::load_2d(sSB(s) + b * kSc * kScaleTile, &P.tm_sb, 0,
+                    tc::load_2d(st.sb(s) + b * kSc * kScaleTile, &P.tm_sb, 0,
                                 (g * P.b_scale_rows + t.nt * C::kGroupsB + b) * P.scale_cols + k * kSc, bar);
             }
         }
-        // a block that gives up waits for its copies in flight before it leaves
-        if (!ok) {
-            uint32_t none = 0;
-            const int first = it < C::kStages ? 0 : it - C::kStages;
-            for (int j = first; j < it; ++j) tc::bar_wait(tc::smem_u32(&sh.full[j % C::kStages]), (j / C::kStages) & 1, &none);
-        }
+        if (!ok) settle<C::kStages>(sh.full, it);
     } else if (warp == 1 && lane == 0) {
-        constexpr uint32_t idesc = tc::idesc_block_scaled(NV, kRowsT, BN);
         int g = 0, it = 0, n = 0;
         bool ok = true;
         for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x, ++n) {
@@ -259,31 +351,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
                     break;
                 }
                 tc::fence_after();
-                const uint32_t sfa = tmem + C::kAcc * BN + s * C::kScCols, sfb = sfa + 4 * kSc;
-#pragma unroll
-                for (int j = 0; j < kSc; ++j) {
-                    tc::copy_scales(sfa + 4 * j, tc::desc_scales(sSA(s) + j * kScaleTile));
-#pragma unroll
-                    for (int b = 0; b < C::kGroupsB; ++b)
-                        tc::copy_scales(sfb + 4 * (j * C::kGroupsB + b), tc::desc_scales(sSB(s) + (b * kSc + j) * kScaleTile));
-                }
-                // steps of 32 bytes of k; the last stage holds only what is left
-                const int steps = min(4, (P.k_bytes - k * kStageK) / 32);
-                for (int j = 0; j < steps; ++j) {
-                    const uint64_t da = tc::desc_sw128(sA(s) + 32 * j), db = tc::desc_sw128(sB(s) + 32 * j);
-                    const bool add = k > 0 || j > 0;
-                    if (NV) tc::mma_nvf4(d, da, db, idesc, sfa + 4 * j, sfb + 4 * C::kGroupsB * j, add);
-                    else tc::mma_mxf8(d, da, db, idesc | tc::idesc_scale_id(j), sfa, sfb, add);
-                }
+                // the last stage holds only what is left of k
+                multiply_stage(st, s, tmem, d, min(4, (P.k_bytes - k * kStageK) / 32), k == 0);
                 tc::commit(tc::smem_u32(&sh.empty[s]));
             }
             if (ok) tc::commit(tc::smem_u32(&sh.acc_full[a]));
         }
-        if (!ok || *dead) {   // the products issued so far end before the memory they read goes
-            uint32_t none = 0;
-            const int first = it < C::kStages ? 0 : it - C::kStages;
-            for (int j = first; j < it; ++j) tc::bar_wait(tc::smem_u32(&sh.empty[j % C::kStages]), (j / C::kStages) & 1, &none);
-        }
+        if (!ok || *dead) settle<C::kStages>(sh.empty, it);
     } else if (warp >= 4) {
         const int q = warp & 3, h = (warp - 4) >> 2;   // lanes 32 q .., column half h
         constexpr int kHalf = BN / 2;
@@ -298,10 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
             T *o = out + (t.row + r) * P.N + c0;
             const int64_t cols = P.N - c0;   // columns from c0 on
             if (g == P.E) {
-                const float zero[8] = {};
-                if (r < t.rows)
-                    for (int c = 0; c < kHalf && c < cols; c += 8)
-                        store_row(o + c, zero, static_cast<int>(cols - c < 8 ? cols - c : 8), wide);
+                if (r < t.rows) zeros(o, kHalf, cols, wide);
                 continue;
             }
             const int a = n % C::kAcc;
@@ -314,36 +385,239 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
                 ua = __fdiv_rn(1.0f, tensor_scale(P.amax_a[g]));
                 ub = __fdiv_rn(1.0f, tensor_scale(P.amax_b[g]));
             }
+            drain<kHalf>(tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16), &sh.acc_empty[a], ua, ub, o,
+                         cols, r < t.rows, wide, false);
+        }
+    }
+    close_block(sh, warp, C::kCols);
+}
+
+// ---------------------------------------------------------- weight gradient
+//
+//   dw_e[n, k] = u_e sum_r A[r, n] B[r, k] over the rows r of expert e,
+// from columnwise copies: per expert [N, Mp_e] and [K, Mp_e], Mp_e the rows padded
+// to whole scale blocks, so that the sum runs along the contiguous axis again.
+// An expert's pitch is Mp_e codes: a multiple of 8 bytes only (NVFP4), which TMA
+// does not take, so four warps bring the stages in with 16- or 8-byte
+// asynchronous copies, zeros past the matrices.  Scales past Mp_e are padding that
+// nobody wrote: they are masked to zero, since a zero code times a NaN scale would
+// still be NaN.
+
+struct WgradParams {
+    const uint8_t *a, *b, *sa, *sb;
+    const int64_t *split;
+    const float *amax_a, *amax_b;
+    void *out;
+    int64_t M;
+    int N, K, E;
+    int n_tiles, k_tiles;              // tiles along N (128) and K (BN)
+    int64_t a_bytes, b_bytes, sa_bytes, sb_bytes;
+    int accumulate;
+};
+
+constexpr int kWgradThreads = 512;   // as above, and warps 12-15 load
+constexpr int kLoaders = 128;
+
+struct WgradShared : Shared {
+    int64_t pad0[kMaxE + 1];    // padded rows before each expert
+    int wide0[kMaxE + 1];       // scale tiles along the rows before each expert
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Writes to shared memory so far become visible to the tensor core's reads.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Rows [r0, r0 + rows) x 128 bytes at k0 of a matrix [n, pitch bytes] into a
+// swizzled stage: 16-byte chunk c of row r at chunk c ^ (r mod 8).
+template <int kRows>
+__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t *m, int64_t pitch, int n, int r0, int64_t k0,
+                                           int thread) {
+    if (pitch % 16 == 0) {
+#pragma unroll 4
+        for (int i = thread; i < kRows * 8; i += kLoaders) {
+            const int r = i >> 3, c = i & 7;
+            const int64_t left = r0 + r < n ? pitch - k0 - 16 * c : 0;
+            const int bytes = left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0;
+            cp_async16(dst + r * 128 + ((c ^ (r & 7)) << 4), bytes ? m + (r0 + r) * pitch + k0 + 16 * c : m, bytes);
+        }
+    } else {
+#pragma unroll 4
+        for (int i = thread; i < kRows * 16; i += kLoaders) {
+            const int r = i >> 4, c = i & 15;
+            const int64_t left = r0 + r < n ? pitch - k0 - 8 * c : 0;
+            const int bytes = left >= 8 ? 8 : 0;
+            cp_async8(dst + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1), bytes ? m + (r0 + r) * pitch + k0 + 8 * c : m,
+                      bytes);
+        }
+    }
+}
+
+// The scale tiles of a stage for 128-row groups g0 .. of a matrix: tiles
+// [c0, c0 + kSc) of each row of tiles, entries from `cols` on as zero.
+template <int kSc, int kGroups>
+__device__ __forceinline__ void load_scales(uint32_t dst, uint8_t *dst_p, const uint8_t *m, int groups, int g0, int wide,
+                                            int c0, int cols, int thread) {
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 64) {
-                uint32_t v[64];
-                tc::tmem_ld64(tmem + a * BN + h * kHalf + c + (static_cast<uint32_t>(32 * q) << 16), v);
-                if (c + 64 == kHalf) {
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::bar_arrive(tc::smem_u32(&sh.acc_empty[a]));
+    for (int i = thread; i < kGroups * kSc * (kScaleTile / 16); i += kLoaders) {
+        const int tile = i >> 5, g = tile / kSc, j = tile % kSc;
+        const bool in = g0 + g < groups && c0 + j < wide;
+        const uint8_t *src = in ? m + ((static_cast<int64_t>(g0 + g) * wide + c0 + j) * kScaleTile + (i & 31) * 16) : m;
+        const int left = cols - 4 * (c0 + j);
+        if (!in || left >= 4) {
+            cp_async16(dst + i * 16, src, in ? 16 : 0);
+        } else {
+            const uint32_t keep = left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+            uint4 v = *reinterpret_cast<const uint4 *>(src);
+            v.x &= keep, v.y &= keep, v.z &= keep, v.w &= keep;
+            *reinterpret_cast<uint4 *>(dst_p + i * 16) = v;
+        }
+    }
+}
+
+template <bool NV, int BN, typename T>
+__global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_constant__ WgradParams P) {
+    using C = Cfg<NV, BN>;
+    extern __shared__ uint8_t dyn[];
+    __shared__ WgradShared sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kBlock = NV ? 16 : 32, kSc = C::kSc, kDepth = C::kStages - 2;
+    // group bounds: padded rows and scale tiles before each expert
+    {
+        const int t = threadIdx.x;
+        int64_t m = t < P.E ? P.split[t] : 0;
+        const bool neg = m < 0 || m > P.M;
+        if (neg) m = 0;
+        int64_t rows = m, pad = (m + kBlock - 1) / kBlock * kBlock, wide = (m + 4 * kBlock - 1) / (4 * kBlock);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, d), q = __shfl_up_sync(0xFFFFFFFFu, pad, d),
+                          u = __shfl_up_sync(0xFFFFFFFFu, wide, d);
+            if (lane >= d) rows += r, pad += q, wide += u;
+        }
+        __shared__ int64_t scan[kMaxE / 32][3];
+        if (warp < kMaxE / 32 && lane == 31) scan[warp][0] = rows, scan[warp][1] = pad, scan[warp][2] = wide;
+        const bool any_neg = __syncthreads_or(neg);
+        for (int k = 0; k < warp && k < kMaxE / 32; ++k) rows += scan[k][0], pad += scan[k][1], wide += scan[k][2];
+        if (t < P.E) sh.pad0[t + 1] = pad, sh.wide0[t + 1] = static_cast<int>(wide);
+        if (t == 0) sh.pad0[0] = 0, sh.wide0[0] = 0;
+        if (t == P.E - 1) {
+            const int64_t codes = NV ? pad / 2 : pad, tiles = wide * kScaleTile;
+            sh.bad = any_neg || rows > P.M || codes * P.N > P.a_bytes || codes * P.K > P.b_bytes ||
+                     tiles * ((P.N + 127) / 128) > P.sa_bytes || tiles * ((P.K + 127) / 128) > P.sb_bytes;
+        }
+        __syncthreads();
+    }
+    if (sh.bad) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_status, ERR_SPLIT);
+        return;
+    }
+    const int per = P.n_tiles * P.k_tiles;
+    const int64_t total = static_cast<int64_t>(P.E) * per;
+    const Stages<NV, BN> st(dyn);
+    open_block<C::kStages>(sh, warp, kLoaders, C::kCols);
+    const uint32_t tmem = sh.tmem;
+    volatile uint32_t *dead = &sh.dead;
+
+    if (warp == 1 && lane == 0) {
+        int it = 0, n = 0;
+        bool ok = true;
+        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+            const int e = static_cast<int>(i / per);
+            const int64_t len = (sh.pad0[e + 1] - sh.pad0[e]) / (NV ? 2 : 1);
+            if (len == 0) continue;
+            const int a = n % C::kAcc, kt = static_cast<int>((len + kStageK - 1) / kStageK);
+            if (n >= C::kAcc && !tc::bar_wait(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) break;
+            ++n;
+            tc::fence_after();
+            for (int k = 0; k < kt; ++k, ++it) {
+                const int s = it % C::kStages;
+                if (!tc::bar_wait(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) {
+                    ok = false;
+                    break;
                 }
-                if (r < t.rows) {
-#pragma unroll
-                    for (int j = 0; j < 64; j += 8) {
-                        float f[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[j + e]) * ua * ub;
-                        const int64_t left = cols - c - j;
-                        if (left > 0) store_row(o + c + j, f, static_cast<int>(left < 8 ? left : 8), wide);
-                    }
+                tc::fence_after();
+                const int64_t left = len - static_cast<int64_t>(k) * kStageK;
+                multiply_stage(st, s, tmem, tmem + a * BN, left >= kStageK ? 4 : static_cast<int>((left + 31) / 32), k == 0);
+                tc::commit(tc::smem_u32(&sh.empty[s]));
+            }
+            if (ok) tc::commit(tc::smem_u32(&sh.acc_full[a]));
+        }
+        if (!ok || *dead) settle<C::kStages>(sh.empty, it);
+    } else if (warp >= 12) {
+        const int thread = threadIdx.x - 12 * 32;
+        int it = 0;
+        bool ok = true;
+        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+            const int e = static_cast<int>(i / per), j = static_cast<int>(i - static_cast<int64_t>(e) * per);
+            const int64_t pad0 = sh.pad0[e], mp = sh.pad0[e + 1] - pad0;
+            const int64_t pitch = NV ? mp / 2 : mp, first = NV ? pad0 / 2 : pad0;
+            const int wide = sh.wide0[e + 1] - sh.wide0[e], cols = static_cast<int>(mp / kBlock);
+            const int nt = j / P.k_tiles, kt = j - nt * P.k_tiles;
+            const int n128 = (P.N + 127) / 128, k128 = (P.K + 127) / 128;
+            const uint8_t *a = P.a + first * P.N, *b = P.b + first * P.K;
+            const uint8_t *sa = P.sa + static_cast<int64_t>(sh.wide0[e]) * n128 * kScaleTile;
+            const uint8_t *sb = P.sb + static_cast<int64_t>(sh.wide0[e]) * k128 * kScaleTile;
+            for (int64_t k = 0; k < pitch; k += kStageK, ++it) {
+                const int s = it % C::kStages;
+                if (it >= C::kStages && !tc::bar_wait(tc::smem_u32(&sh.empty[s]), (it / C::kStages - 1) & 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                load_codes<kRowsT>(st.a(s), a, pitch, P.N, nt * kRowsT, k, thread);
+                load_codes<BN>(st.b(s), b, pitch, P.K, kt * BN, k, thread);
+                const int c0 = static_cast<int>(k / kStageK) * kSc;
+                uint8_t *p = dyn + (st.sa(s) - tc::smem_u32(dyn));
+                load_scales<kSc, 1>(st.sa(s), p, sa, n128, nt, wide, c0, cols, thread);
+                load_scales<kSc, C::kGroupsB>(st.sb(s), p + C::kBytesSA, sb, k128, kt * C::kGroupsB, wide, c0, cols, thread);
+                cp_commit();
+                if (it >= kDepth) {   // the stage kDepth before this one has arrived
+                    cp_wait<kDepth>();
+                    fence_async();
+                    tc::bar_arrive(tc::smem_u32(&sh.full[(it - kDepth) % C::kStages]));
                 }
             }
         }
+        cp_wait<0>();
+        fence_async();
+        if (ok)
+            for (int j = it < kDepth ? 0 : it - kDepth; j < it; ++j) tc::bar_arrive(tc::smem_u32(&sh.full[j % C::kStages]));
+    } else if (warp >= 4 && warp < 12) {
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        constexpr int kHalf = BN / 2;
+        T *out = static_cast<T *>(P.out);
+        const bool wide = (P.K * sizeof(T)) % 16 == 0, add = P.accumulate != 0;
+        int n = 0;
+        for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
+            const int e = static_cast<int>(i / per), j = static_cast<int>(i - static_cast<int64_t>(e) * per);
+            const int nt = j / P.k_tiles, kt = j - nt * P.k_tiles;
+            const int row = nt * kRowsT + 32 * q + lane, c0 = kt * BN + h * kHalf;
+            T *o = out + (static_cast<int64_t>(e) * P.N + row) * P.K + c0;
+            if (sh.pad0[e + 1] == sh.pad0[e]) {   // no rows: a zero gradient
+                if (row < P.N && !add) zeros(o, kHalf, P.K - c0, wide);
+                continue;
+            }
+            const int a = n % C::kAcc;
+            if (!tc::bar_wait(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, dead)) break;
+            ++n;
+            __syncwarp();
+            tc::fence_after();
+            float ua = 1.0f, ub = 1.0f;
+            if (NV) {
+                ua = __fdiv_rn(1.0f, tensor_scale(P.amax_a[e]));
+                ub = __fdiv_rn(1.0f, tensor_scale(P.amax_b[e]));
+            }
+            drain<kHalf>(tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16), &sh.acc_empty[a], ua, ub, o,
+                         static_cast<int64_t>(P.K) - c0, row < P.N, wide, add);
+        }
     }
-    __syncwarp();
-    tc::fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc::fence_after();
-        tc::tmem_free(tmem, C::kCols);
-    }
-    if (threadIdx.x == 0 && sh.dead) atomicOr(&g_status, ERR_TIMEOUT);
+    close_block(sh, warp, C::kCols);
 }
 
 // -------------------------------------------------------------------- host
@@ -408,6 +682,17 @@ gsa_status launch(const GemmParams &P, int64_t tiles, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
 }
 
+template <bool NV, int BN, typename T> gsa_status launch_wgrad(const WgradParams &P, cudaStream_t s) {
+    const int sms = sm_count();
+    if (!sms) return GSA_ERR_CUDA;
+    auto k = grouped_wgrad<NV, BN, T>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NV, BN>::kSmem) != cudaSuccess)
+        return GSA_ERR_CUDA;
+    const int64_t tiles = static_cast<int64_t>(P.E) * P.n_tiles * P.k_tiles;
+    k<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kWgradThreads, Cfg<NV, BN>::kSmem, s>>>(P);
+    return cudaGetLastError() == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
+}
+
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
@@ -467,6 +752,54 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     gsa_status st;
     if (nv) st = out_dtype == GSA_BF16 ? launch<true, 256, __nv_bfloat16>(P, tiles, s) : launch<true, 256, float>(P, tiles, s);
     else st = out_dtype == GSA_BF16 ? launch<false, 256, __nv_bfloat16>(P, tiles, s) : launch<false, 256, float>(P, tiles, s);
+    if (st == GSA_OK) gsa::set_last_launches(1);
+    return st;
+}
+
+gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int64_t *split_sizes_dev, int64_t E,
+                                  int64_t M, int64_t N, int64_t K, int32_t recipe_kind, void *out, int32_t out_dtype,
+                                  int32_t accumulate, gsa_stream_t stream) {
+    if (!a || !b || E <= 0 || M < 0 || N <= 0 || K <= 0) return GSA_ERR_INVALID_ARG;
+    if (recipe_kind != GSA_MXFP8 && recipe_kind != GSA_NVFP4) return GSA_ERR_INVALID_ARG;
+    if (out_dtype != GSA_BF16 && out_dtype != GSA_FP32) return GSA_ERR_INVALID_ARG;
+    const bool nv = recipe_kind == GSA_NVFP4;
+    if (E > kMaxE || M >= (int64_t(1) << 31) - 256 * 64 || N >= (int64_t(1) << 30) || K >= (int64_t(1) << 30))
+        return GSA_ERR_UNSUPPORTED;
+    if (!a->data || !a->scale || !b->data || !b->scale || !split_sizes_dev || !out) return GSA_ERR_INVALID_ARG;
+    if (nv && (!a->amax || !b->amax)) return GSA_ERR_INVALID_ARG;
+    if (!aligned(a->data, 16) || !aligned(a->scale, 16) || !aligned(b->data, 16) || !aligned(b->scale, 16) ||
+        !aligned(out, 16) || !aligned(split_sizes_dev, 8) || !aligned(a->amax, 4) || !aligned(b->amax, 4))
+        return GSA_ERR_ALIGNMENT;
+    // an expert's codes start on 16 bytes: its padded rows (a multiple of the block) times the width
+    if ((nv ? N * 8 : N * 32) % 16 != 0 || (nv ? K * 8 : K * 32) % 16 != 0) return GSA_ERR_UNSUPPORTED;
+
+    WgradParams P;
+    std::memset(&P, 0, sizeof(P));
+    P.a = static_cast<const uint8_t *>(a->data);
+    P.b = static_cast<const uint8_t *>(b->data);
+    P.sa = static_cast<const uint8_t *>(a->scale);
+    P.sb = static_cast<const uint8_t *>(b->scale);
+    P.split = split_sizes_dev;
+    P.amax_a = a->amax;
+    P.amax_b = b->amax;
+    P.out = out;
+    P.M = M;
+    P.N = static_cast<int>(N);
+    P.K = static_cast<int>(K);
+    P.E = static_cast<int>(E);
+    const int BN = 128;
+    P.n_tiles = static_cast<int>((N + kRowsT - 1) / kRowsT);
+    P.k_tiles = static_cast<int>((K + BN - 1) / BN);
+    P.a_bytes = a->data_bytes;
+    P.b_bytes = b->data_bytes;
+    P.sa_bytes = a->scale_bytes;
+    P.sb_bytes = b->scale_bytes;
+    P.accumulate = accumulate != 0;
+    if (static_cast<int64_t>(P.n_tiles) * P.k_tiles >= (int64_t(1) << 31)) return GSA_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    gsa_status st;
+    if (nv) st = out_dtype == GSA_BF16 ? launch_wgrad<true, BN, __nv_bfloat16>(P, s) : launch_wgrad<true, BN, float>(P, s);
+    else st = out_dtype == GSA_BF16 ? launch_wgrad<false, BN, __nv_bfloat16>(P, s) : launch_wgrad<false, BN, float>(P, s);
     if (st == GSA_OK) gsa::set_last_launches(1);
     return st;
 }

@@ -29,7 +29,7 @@ EXPORTED = ["gsa_layout", "gsa_workspace_size", "grouped_scaled_act_fwd", "group
             "grouped_scaled_act_fwd_graph_safe", "grouped_scaled_act_bwd_graph_safe", "gsa_selftest_wait_timeout",
             "gsa_layout_ex", "gsa_layout_bound_ex", "gsa_moe_sort_workspace_size", "gsa_moe_sort", "gsa_moe_permute",
             "gsa_moe_permute_bwd", "gsa_moe_unpermute", "gsa_moe_unpermute_bwd", "gsa_grouped_gemm",
-            "gsa_grouped_gemm_status"]
+            "gsa_grouped_gemm_wgrad", "gsa_grouped_gemm_status"]
 
 
 class GsaError(RuntimeError):
@@ -131,6 +131,9 @@ def load():
         L.gsa_grouped_gemm.restype = ctypes.c_int
         L.gsa_grouped_gemm.argtypes = [ctypes.POINTER(QIn), ctypes.POINTER(QIn), _P, _I64, _I64, _I64, _I64,
                                        ctypes.c_int32, _P, ctypes.c_int32, _P]
+        L.gsa_grouped_gemm_wgrad.restype = ctypes.c_int
+        L.gsa_grouped_gemm_wgrad.argtypes = [ctypes.POINTER(QIn), ctypes.POINTER(QIn), _P, _I64, _I64, _I64, _I64,
+                                             ctypes.c_int32, _P, ctypes.c_int32, ctypes.c_int32, _P]
         L.gsa_grouped_gemm_status.restype = ctypes.c_int
         L.gsa_grouped_gemm_status.argtypes = [_P]
         L.gsa_version.restype = ctypes.c_int32
@@ -705,6 +708,27 @@ def grouped_gemm(a: dict, b: dict, split, m: int, n: int, k: int, recipe_kind: i
     out = on.out(out, "grouped_gemm: out", (m, n), out_dtype, dev)
     _check(load().gsa_grouped_gemm(qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, out.data_ptr(), code,
                                    on.ptr), "gsa_grouped_gemm")
+    return out
+
+
+def grouped_gemm_wgrad(a: dict, b: dict, split, m: int, n: int, k: int, recipe_kind: int, out_dtype=None,
+                       out=None, accumulate: bool = False, stream=None):
+    """dw [experts, n, k]: for each expert the product A^T B over its rows, from the columnwise copies (tiled scales)
+    of the [m, n] and [m, k] tensors.  out_dtype: torch.float32 (default) or torch.bfloat16.  accumulate adds to
+    `out`.  NVFP4 copies made with the RHT need the same sign mask on both sides."""
+    import torch
+    out_dtype = out_dtype or (out.dtype if out is not None else torch.float32)
+    code = _out_code(out_dtype)
+    if accumulate and out is None:
+        raise GsaError(1, "grouped_gemm_wgrad: accumulate needs out")
+    _require(split, "grouped_gemm_wgrad: split", (split.numel(),), torch.int64)
+    dev, experts = split.device, split.numel()
+    qa, ta = _operand(a, "col", recipe_kind, experts, "grouped_gemm_wgrad: a", dev)
+    qb, tb = _operand(b, "col", recipe_kind, experts, "grouped_gemm_wgrad: b", dev)
+    on = _On(stream, dev, split, *ta, *tb)
+    out = on.out(out, "grouped_gemm_wgrad: out", (experts, n, k), out_dtype, dev)
+    _check(load().gsa_grouped_gemm_wgrad(qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, out.data_ptr(),
+                                         code, int(bool(accumulate)), on.ptr), "gsa_grouped_gemm_wgrad")
     return out
 
 

@@ -103,3 +103,28 @@ def test_product_exact(recipe, out, split, n, k):
     assert gsa.grouped_gemm_status() == 0
     ref = np.concatenate([x @ w.T for x, w in zip(a.values, b.values)] + [np.zeros((tail, n))])
     assert np.array_equal(got.double().cpu().numpy(), rounded(ref, out))
+
+
+def padded(split, recipe):
+    b = BLOCK[recipe]
+    return [-(-s // b) * b for s in split]
+
+
+@pytest.mark.parametrize("recipe", [MX, NV])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("split", SPLITS + [[1, 15, 16, 17, 31, 33, 47, 63, 65, 255, 257, 1000]], ids=str)
+@pytest.mark.parametrize("n,k", [(2, 64), (64, 2), (128, 130), (200, 256), (320, 512)])
+def test_wgrad_exact(recipe, out, split, n, k):
+    rng = np.random.default_rng(n * 5 + k + len(split))
+    mp = padded(split, recipe)
+    a, b = Matrices(rng, [n] * len(split), mp, recipe), Matrices(rng, [k] * len(split), mp, recipe)
+    got = gsa.grouped_gemm_wgrad(a.dev("col"), b.dev("col"), dev_split(split), sum(split), n, k, recipe, out_dtype=out,
+                                 out=torch.full((len(split), n, k), float("nan"), dtype=out, device="cuda"))
+    assert gsa.grouped_gemm_status() == 0
+    ref = np.stack([x @ w.T for x, w in zip(a.values, b.values)])
+    assert np.array_equal(got.double().cpu().numpy(), rounded(ref, out))
+    first = rng.integers(-8, 9, size=ref.shape).astype(np.float64)
+    acc = torch.from_numpy(first.astype(np.float32)).to("cuda", out)
+    gsa.grouped_gemm_wgrad(a.dev("col"), b.dev("col"), dev_split(split), sum(split), n, k, recipe, out=acc,
+                           accumulate=True)
+    assert np.array_equal(acc.double().cpu().numpy(), rounded(ref + first, out))
