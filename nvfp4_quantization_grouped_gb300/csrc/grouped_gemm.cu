@@ -84,6 +84,9 @@ struct Shared {
     int64_t scan[kThreads / 32][2];
 };
 
+// A value that is the same in all lanes, as the compiler cannot tell.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
 // Group bounds from the device split: rows and row tiles before each group.  Every thread of the block.
 // A negative size, a sum above M or more scale tiles than A's buffer holds sets sh.bad.
 __device__ void scan_split(const GemmParams &P, Shared &sh) {
@@ -187,9 +190,9 @@ template <bool NV, int BN> struct Stages {
     __device__ uint32_t sb(int s) const { return sa(s) + C::kBytesSA; }
 };
 
-// The products of one stage: scales to their columns of tensor memory, then
-// `steps` steps of 32 bytes of k.  The scale columns are the stage's own, so the
-// barrier that frees the stage frees them too.
+// The products of one stage (one elected lane): scales to their columns of
+// tensor memory, then `steps` steps of 32 bytes of k.  The scale columns are the
+// stage's own, so the barrier that frees the stage frees them too.
 template <bool NV, int BN>
 __device__ __forceinline__ void multiply_stage(const Stages<NV, BN> &st, int s, uint32_t tmem, uint32_t d, int steps,
                                                bool first) {
@@ -291,71 +294,76 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
     using C = Cfg<NV, BN>;
     extern __shared__ uint8_t dyn[];
     __shared__ Shared sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     scan_split(P, sh);
     if (sh.bad) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_status, ERR_SPLIT);
         return;
     }
     const int64_t total = static_cast<int64_t>(sh.tile0[P.E + 1]) * P.n_tiles;
+    const int64_t used = static_cast<int64_t>(sh.tile0[P.E]) * P.n_tiles;   // the rest is zeros
     if (static_cast<int64_t>(blockIdx.x) >= total) return;
     const Stages<NV, BN> st(dyn);
     open_block<C::kStages>(sh, warp, 1, C::kCols);
-    const uint32_t tmem = sh.tmem;
+    constexpr uint32_t tmem = 0;   // the block holds all columns
     volatile uint32_t *dead = &sh.dead;
     constexpr int kSc = C::kSc;
 
-    if (warp == 0 && lane == 0) {
-        tc::prefetch_map(&P.tm_a);
-        tc::prefetch_map(&P.tm_b);
+    if (warp == 0) {
+        if (tc::elect()) {
+            tc::prefetch_map(&P.tm_a);
+            tc::prefetch_map(&P.tm_b);
+        }
         int g = 0, it = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
+        for (int64_t i = blockIdx.x; i < used && ok; i += gridDim.x) {
             const Tile t = tile_at(P, sh, i, g);
             g = t.g;
-            if (g == P.E) break;   // only zeros from here on
-            const int a_tile = (sh.tile0[g] + t.mt) * P.scale_cols;
+            const int row = uniform(static_cast<int>(t.row)), a_tile = uniform((sh.tile0[g] + t.mt) * P.scale_cols);
+            const int b_row = uniform(static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN));
+            const int b_tile = uniform((g * P.b_scale_rows + t.nt * C::kGroupsB) * P.scale_cols);
             for (int k = 0; k < P.kt; ++k, ++it) {
                 const int s = it % C::kStages;
-                if (it >= C::kStages && !tc::bar_wait(tc::smem_u32(&sh.empty[s]), (it / C::kStages - 1) & 1, dead)) {
+                if (it >= C::kStages && !tc::bar_wait_warp(tc::smem_u32(&sh.empty[s]), (it / C::kStages - 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
                 const uint32_t bar = tc::smem_u32(&sh.full[s]);
-                tc::bar_expect(bar, C::kStageBytes);
-                tc::load_2d(st.a(s), &P.tm_a, k * kStageK, static_cast<int>(t.row), bar);
-                tc::load_2d(st.b(s), &P.tm_b, k * kStageK, static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN), bar);
-                tc::load_2d(st.sa(s), &P.tm_sa, 0, a_tile + k * kSc, bar);
+                if (tc::elect()) {
+                    tc::bar_expect(bar, C::kStageBytes);
+                    tc::load_2d(st.a(s), &P.tm_a, k * kStageK, row, bar);
+                    tc::load_2d(st.b(s), &P.tm_b, k * kStageK, b_row, bar);
+                    tc::load_2d(st.sa(s), &P.tm_sa, 0, a_tile + k * kSc, bar);
 #pragma unroll
-                for (int b = 0; b < C::kGroupsB; ++b)
-                    tc::load_2d(st.sb(s) + b * kSc * kScaleTile, &P.tm_sb, 0,
-                                (g * P.b_scale_rows + t.nt * C::kGroupsB + b) * P.scale_cols + k * kSc, bar);
+                    for (int b = 0; b < C::kGroupsB; ++b)
+                        tc::load_2d(st.sb(s) + b * kSc * kScaleTile, &P.tm_sb, 0, b_tile + b * P.scale_cols + k * kSc, bar);
+                }
             }
         }
         if (!ok) settle<C::kStages>(sh.full, it);
-    } else if (warp == 1 && lane == 0) {
-        int g = 0, it = 0, n = 0;
-        bool ok = true;
-        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x, ++n) {
-            const Tile t = tile_at(P, sh, i, g);
-            g = t.g;
-            if (g == P.E) break;
+    } else if (warp == 1) {
+        const int mine = uniform(static_cast<int>((used - blockIdx.x + gridDim.x - 1) / gridDim.x));
+        int it = 0;
+        bool ok = static_cast<int64_t>(blockIdx.x) < used;
+        for (int n = 0; n < mine && ok; ++n) {
             const int a = n % C::kAcc;
-            if (n >= C::kAcc && !tc::bar_wait(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) break;
+            if (n >= C::kAcc && !tc::bar_wait_warp(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) break;
             tc::fence_after();
-            const uint32_t d = tmem + a * BN;
             for (int k = 0; k < P.kt; ++k, ++it) {
                 const int s = it % C::kStages;
-                if (!tc::bar_wait(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) {
+                if (!tc::bar_wait_warp(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after();
-                // the last stage holds only what is left of k
-                multiply_stage(st, s, tmem, d, min(4, (P.k_bytes - k * kStageK) / 32), k == 0);
-                tc::commit(tc::smem_u32(&sh.empty[s]));
+                if (tc::elect()) {
+                    // the last stage holds only what is left of k
+                    multiply_stage(st, s, tmem, tmem + a * BN, min(4, (P.k_bytes - k * kStageK) / 32), k == 0);
+                    tc::commit(tc::smem_u32(&sh.empty[s]));
+                    if (k == P.kt - 1) tc::commit(tc::smem_u32(&sh.acc_full[a]));
+                }
+                __syncwarp();
             }
-            if (ok) tc::commit(tc::smem_u32(&sh.acc_full[a]));
         }
         if (!ok || *dead) settle<C::kStages>(sh.empty, it);
     } else if (warp >= 4) {
@@ -486,7 +494,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_c
     using C = Cfg<NV, BN>;
     extern __shared__ uint8_t dyn[];
     __shared__ WgradShared sh;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kBlock = NV ? 16 : 32, kSc = C::kSc, kDepth = C::kStages - 2;
     // group bounds: padded rows and scale tiles before each expert
     {
@@ -522,32 +530,34 @@ __global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_c
     const int64_t total = static_cast<int64_t>(P.E) * per;
     const Stages<NV, BN> st(dyn);
     open_block<C::kStages>(sh, warp, kLoaders, C::kCols);
-    const uint32_t tmem = sh.tmem;
+    constexpr uint32_t tmem = 0;   // the block holds all columns
     volatile uint32_t *dead = &sh.dead;
 
-    if (warp == 1 && lane == 0) {
+    if (warp == 1) {
         int it = 0, n = 0;
         bool ok = true;
         for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
             const int e = static_cast<int>(i / per);
-            const int64_t len = (sh.pad0[e + 1] - sh.pad0[e]) / (NV ? 2 : 1);
+            const int len = uniform(static_cast<int>((sh.pad0[e + 1] - sh.pad0[e]) / (NV ? 2 : 1)));
             if (len == 0) continue;
-            const int a = n % C::kAcc, kt = static_cast<int>((len + kStageK - 1) / kStageK);
-            if (n >= C::kAcc && !tc::bar_wait(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) break;
+            const int a = n % C::kAcc, kt = (len + kStageK - 1) / kStageK;
+            if (n >= C::kAcc && !tc::bar_wait_warp(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) break;
             ++n;
             tc::fence_after();
             for (int k = 0; k < kt; ++k, ++it) {
                 const int s = it % C::kStages;
-                if (!tc::bar_wait(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) {
+                if (!tc::bar_wait_warp(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after();
-                const int64_t left = len - static_cast<int64_t>(k) * kStageK;
-                multiply_stage(st, s, tmem, tmem + a * BN, left >= kStageK ? 4 : static_cast<int>((left + 31) / 32), k == 0);
-                tc::commit(tc::smem_u32(&sh.empty[s]));
+                if (tc::elect()) {
+                    multiply_stage(st, s, tmem, tmem + a * BN, min(4, (len - k * kStageK + 31) / 32), k == 0);
+                    tc::commit(tc::smem_u32(&sh.empty[s]));
+                    if (k == kt - 1) tc::commit(tc::smem_u32(&sh.acc_full[a]));
+                }
+                __syncwarp();
             }
-            if (ok) tc::commit(tc::smem_u32(&sh.acc_full[a]));
         }
         if (!ok || *dead) settle<C::kStages>(sh.empty, it);
     } else if (warp >= 12) {
