@@ -60,59 +60,68 @@ template <bool NV> struct Fmt;
 template <> struct Fmt<false> { static constexpr int kScaleTiles = 1; };   // scale tiles per stage and 128 rows
 template <> struct Fmt<true> { static constexpr int kScaleTiles = 4; };
 
-template <bool NV, int BN> struct Cfg {
+// A block's tile is 128 rows (its lanes of tensor memory) x BN columns.  kPair: two
+// blocks of a cluster share a tile of 256 rows; each brings its own rows and half
+// of the columns' operand, and the pair's products read both halves.
+template <bool NV, int BN, bool kPair> struct Cfg {
     static constexpr int kSc = Fmt<NV>::kScaleTiles;
-    static constexpr int kBytesA = kRowsT * kStageK, kBytesB = BN * kStageK;
+    static constexpr int kRowsB = kPair ? BN / 2 : BN;
+    static constexpr int kBytesA = kRowsT * kStageK, kBytesB = kRowsB * kStageK;
     static constexpr int kGroupsB = BN / 128;
     static constexpr int kBytesSA = kSc * kScaleTile, kBytesSB = kGroupsB * kSc * kScaleTile;
     static constexpr int kStageBytes = kBytesA + kBytesB + kBytesSA + kBytesSB;
     static constexpr int kStride = (kStageBytes + 1023) / 1024 * 1024;   // stages start on the swizzle's period
-    static constexpr int kStages = BN == 256 ? 4 : 6;
     static constexpr int kAcc = BN == 256 ? 1 : 2;       // accumulators in tensor memory
     static constexpr int kScCols = 4 * kSc * (1 + kGroupsB);   // scale columns of a stage
     static constexpr int kCols = 512;
-    static_assert(kAcc * BN + kStages * kScCols <= kCols, "tensor memory");
+    static constexpr int kBySmem = (227 * 1024 - 8192 - 1024) / kStride, kByCols = (kCols - kAcc * BN) / kScCols;
+    static constexpr int kFit = kBySmem < kByCols ? kBySmem : kByCols;
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr int kSmem = kStages * kStride + 1024;
 };
 
 struct Shared {
     int64_t row0[kMaxE + 2];    // first row of each group; group E: rows that no expert has
-    int tile0[kMaxE + 2];       // first row tile of each group (in tiles of all column tiles: times n_tiles)
+    int tile0[kMaxE + 2];       // first row tile of each group
+    int scale0[kMaxE + 1];      // first 128-row scale tile of each expert
     uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
     uint32_t tmem;
     uint32_t dead, bad;
-    int64_t scan[kThreads / 32][2];
+    int64_t scan[kThreads / 32][3];
 };
 
 // A value that is the same in all lanes, as the compiler cannot tell.
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
-// Group bounds from the device split: rows and row tiles before each group.  Every thread of the block.
-// A negative size, a sum above M or more scale tiles than A's buffer holds sets sh.bad.
-__device__ void scan_split(const GemmParams &P, Shared &sh) {
+// Group bounds from the device split: rows, scale tiles and row tiles of kRows before each group.  Every thread
+// of the block.  A negative size, a sum above M or more scale tiles than A's buffer holds sets sh.bad.
+template <int kRows> __device__ void scan_split(const GemmParams &P, Shared &sh) {
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     int64_t m = t < P.E ? P.split[t] : 0;
     const bool neg = m < 0 || m > P.M;
     if (neg) m = 0;
-    int64_t rows = m, tiles = (m + kRowsT - 1) / kRowsT;
+    int64_t rows = m, scales = (m + 127) / 128, tiles = (m + kRows - 1) / kRows;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, d), q = __shfl_up_sync(0xFFFFFFFFu, tiles, d);
-        if (lane >= d) rows += r, tiles += q;
+        const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, d), q = __shfl_up_sync(0xFFFFFFFFu, scales, d),
+                      u = __shfl_up_sync(0xFFFFFFFFu, tiles, d);
+        if (lane >= d) rows += r, scales += q, tiles += u;
     }
-    if (lane == 31) sh.scan[w][0] = rows, sh.scan[w][1] = tiles;
+    if (lane == 31) sh.scan[w][0] = rows, sh.scan[w][1] = scales, sh.scan[w][2] = tiles;
     const bool any_neg = __syncthreads_or(neg);
-    int64_t r0 = 0, q0 = 0;
-    for (int k = 0; k < w; ++k) r0 += sh.scan[k][0], q0 += sh.scan[k][1];
-    rows += r0, tiles += q0;
-    if (t < P.E) sh.row0[t + 1] = rows, sh.tile0[t + 1] = static_cast<int>(tiles);
-    if (t == 0) sh.row0[0] = 0, sh.tile0[0] = 0;
+    for (int k = 0; k < w; ++k) rows += sh.scan[k][0], scales += sh.scan[k][1], tiles += sh.scan[k][2];
+    if (t < P.E) {
+        sh.row0[t + 1] = rows;
+        sh.scale0[t + 1] = static_cast<int>(scales);
+        sh.tile0[t + 1] = static_cast<int>(tiles);
+    }
+    if (t == 0) sh.row0[0] = 0, sh.scale0[0] = 0, sh.tile0[0] = 0;
     __syncthreads();
     if (t == 0) {
         const int64_t sum = sh.row0[P.E];
-        sh.bad = any_neg || sum > P.M || sh.tile0[P.E] > P.a_scale_tiles;
+        sh.bad = any_neg || sum > P.M || sh.scale0[P.E] > P.a_scale_tiles;
         sh.row0[P.E + 1] = P.M;
-        sh.tile0[P.E + 1] = sh.tile0[P.E] + static_cast<int>((P.M - (sum > P.M ? P.M : sum) + kRowsT - 1) / kRowsT);
+        sh.tile0[P.E + 1] = sh.tile0[P.E] + static_cast<int>((P.M - (sum > P.M ? P.M : sum) + kRows - 1) / kRows);
     }
     __syncthreads();
 }
@@ -132,56 +141,62 @@ struct Tile {
     int nt;         // column tile
 };
 
-// Tile number i, searching from group g on (tile numbers only grow).
-__device__ __forceinline__ Tile tile_at(const GemmParams &P, const Shared &sh, int64_t i, int g) {
+// Tile number i of kRows rows, searching from group g on (tile numbers only grow).
+template <int kRows> __device__ __forceinline__ Tile tile_at(const GemmParams &P, const Shared &sh, int64_t i, int g) {
     const int q = static_cast<int>(i / P.n_tiles);
     while (q >= sh.tile0[g + 1]) ++g;
     Tile t;
     t.g = g;
     t.nt = static_cast<int>(i - static_cast<int64_t>(q) * P.n_tiles);
     t.mt = q - sh.tile0[g];
-    t.row = sh.row0[g] + static_cast<int64_t>(t.mt) * kRowsT;
+    t.row = sh.row0[g] + static_cast<int64_t>(t.mt) * kRows;
     const int64_t left = sh.row0[g + 1] - t.row;
-    t.rows = left < kRowsT ? static_cast<int>(left) : kRowsT;
+    t.rows = left < kRows ? static_cast<int>(left) : kRows;
     return t;
 }
 
-// Up to 8 results to o (wide: o is on 16 bytes), rounded once; add: onto what is there.
-__device__ __forceinline__ void store_row(__nv_bfloat16 *o, const float *v, int n, bool wide, bool add) {
-    if (wide && n == 8 && !add) {
-        uint4 w;
-        __nv_bfloat162 h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        memcpy(&w, h, 16);
-        *reinterpret_cast<uint4 *>(o) = w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) o[i] = __float2bfloat16_rn(add ? __bfloat162float(o[i]) + v[i] : v[i]);
+// 32 bytes of results at o.  align: the bytes that o is aligned to (32, 16 or less); n: how many of the results
+// there are (at most 32 bytes of them).
+__device__ __forceinline__ void store_raw(uint8_t *o, const uint32_t *w, int align) {
+    if (align == 32)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    else {
+        *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(o + 16) = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
 
-__device__ __forceinline__ void store_row(float *o, const float *v, int n, bool wide, bool add) {
-    if (wide && n == 8) {
-        float4 x = make_float4(v[0], v[1], v[2], v[3]), y = make_float4(v[4], v[5], v[6], v[7]);
-        if (add) {
-            const float4 p = *reinterpret_cast<const float4 *>(o), q = *reinterpret_cast<const float4 *>(o + 4);
-            x.x += p.x, x.y += p.y, x.z += p.z, x.w += p.w;
-            y.x += q.x, y.y += q.y, y.z += q.z, y.w += q.w;
-        }
-        *reinterpret_cast<float4 *>(o) = x;
-        *reinterpret_cast<float4 *>(o + 4) = y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) o[i] = add ? o[i] + v[i] : v[i];
+__device__ __forceinline__ void store_some(__nv_bfloat16 *o, const uint32_t *w, int n, int align) {
+    if (n >= 16 && align >= 16) {
+        store_raw(reinterpret_cast<uint8_t *>(o), w, align);
+        return;
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n) reinterpret_cast<uint16_t *>(o)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+}
+
+__device__ __forceinline__ void store_some(float *o, const uint32_t *w, int n, int align) {
+    if (n >= 8 && align >= 16) {
+        store_raw(reinterpret_cast<uint8_t *>(o), w, align);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) o[i] = __uint_as_float(w[i]);
+}
+
+// Largest of 32, 16 and 1 that every row start of out [.., n] is aligned to.
+template <typename T> __device__ __forceinline__ int row_align(const T *out, int64_t n) {
+    const uint64_t x = reinterpret_cast<uint64_t>(out) | static_cast<uint64_t>(n * static_cast<int64_t>(sizeof(T)));
+    return x % 32 == 0 ? 32 : x % 16 == 0 ? 16 : 1;
 }
 
 // Where a stage's parts lie in shared memory.
-template <bool NV, int BN> struct Stages {
-    using C = Cfg<NV, BN>;
+template <bool NV, int BN, bool kPair> struct Stages {
+    using C = Cfg<NV, BN, kPair>;
     uint32_t base;   // a multiple of 1024: the swizzle pattern repeats every 1024 bytes
     __device__ explicit Stages(const void *dyn) : base((tc::smem_u32(dyn) + 1023u) & ~1023u) {}
     __device__ uint32_t a(int s) const { return base + s * C::kStride; }
@@ -193,25 +208,25 @@ template <bool NV, int BN> struct Stages {
 // The products of one stage (one elected lane): scales to their columns of
 // tensor memory, then `steps` steps of 32 bytes of k.  The scale columns are the
 // stage's own, so the barrier that frees the stage frees them too.
-template <bool NV, int BN>
-__device__ __forceinline__ void multiply_stage(const Stages<NV, BN> &st, int s, uint32_t tmem, uint32_t d, int steps,
+template <bool NV, int BN, bool kPair>
+__device__ __forceinline__ void multiply_stage(const Stages<NV, BN, kPair> &st, int s, uint32_t tmem, uint32_t d, int steps,
                                                bool first) {
-    using C = Cfg<NV, BN>;
-    constexpr uint32_t idesc = tc::idesc_block_scaled(NV, kRowsT, BN);
+    using C = Cfg<NV, BN, kPair>;
+    constexpr uint32_t idesc = tc::idesc_block_scaled(NV, kPair ? 2 * kRowsT : kRowsT, BN);
     constexpr int kSc = C::kSc;
     const uint32_t sfa = tmem + C::kAcc * BN + s * C::kScCols, sfb = sfa + 4 * kSc;
 #pragma unroll
     for (int j = 0; j < kSc; ++j) {
-        tc::copy_scales(sfa + 4 * j, tc::desc_scales(st.sa(s) + j * kScaleTile));
+        tc::copy_scales<kPair>(sfa + 4 * j, tc::desc_scales(st.sa(s) + j * kScaleTile));
 #pragma unroll
         for (int b = 0; b < C::kGroupsB; ++b)
-            tc::copy_scales(sfb + 4 * (j * C::kGroupsB + b), tc::desc_scales(st.sb(s) + (b * kSc + j) * kScaleTile));
+            tc::copy_scales<kPair>(sfb + 4 * (j * C::kGroupsB + b), tc::desc_scales(st.sb(s) + (b * kSc + j) * kScaleTile));
     }
     for (int j = 0; j < steps; ++j) {
         const uint64_t da = tc::desc_sw128(st.a(s) + 32 * j), db = tc::desc_sw128(st.b(s) + 32 * j);
         const bool add = !first || j > 0;
-        if (NV) tc::mma_nvf4(d, da, db, idesc, sfa + 4 * j, sfb + 4 * C::kGroupsB * j, add);
-        else tc::mma_mxf8(d, da, db, idesc | tc::idesc_scale_id(j), sfa, sfb, add);
+        if (NV) tc::mma_nvf4<kPair>(d, da, db, idesc, sfa + 4 * j, sfb + 4 * C::kGroupsB * j, add);
+        else tc::mma_mxf8<kPair>(d, da, db, idesc | tc::idesc_scale_id(j), sfa, sfb, add);
     }
 }
 
@@ -223,8 +238,9 @@ template <int kStages> __device__ __forceinline__ void settle(uint64_t *bars, in
         tc::bar_wait(tc::smem_u32(&bars[j % kStages]), (j / kStages) & 1, &none);
 }
 
-// Barriers, tensor memory, and the block's start and end.
-template <int kStages> __device__ __forceinline__ void open_block(Shared &sh, int warp, uint32_t full_count, uint32_t cols) {
+// Barriers, tensor memory, and the block's (the pair's) start and end.
+template <int kStages, bool kPair>
+__device__ __forceinline__ void open_block(Shared &sh, int warp, uint32_t full_count, uint32_t cols) {
     if (threadIdx.x == 0) {
         sh.dead = 0;
         for (int s = 0; s < kStages; ++s) {
@@ -233,81 +249,138 @@ template <int kStages> __device__ __forceinline__ void open_block(Shared &sh, in
         }
         for (int a = 0; a < 2; ++a) {
             tc::bar_init(tc::smem_u32(&sh.acc_full[a]), 1);
-            tc::bar_init(tc::smem_u32(&sh.acc_empty[a]), kEpiWarps);
+            tc::bar_init(tc::smem_u32(&sh.acc_empty[a]), kPair ? 2 * kEpiWarps : kEpiWarps);
         }
         tc::bar_init_fence();
     }
-    if (warp == 1) tc::tmem_alloc(tc::smem_u32(&sh.tmem), cols);
+    if (warp == 1) tc::tmem_alloc<kPair>(tc::smem_u32(&sh.tmem), cols);
     tc::fence_before();
-    __syncthreads();
+    if (kPair) tc::cluster_sync();
+    else __syncthreads();
     tc::fence_after();
 }
 
-__device__ __forceinline__ void close_block(Shared &sh, int warp, uint32_t cols) {
+template <bool kPair> __device__ __forceinline__ void close_block(Shared &sh, int warp, uint32_t cols) {
     __syncwarp();
     tc::fence_before();
-    __syncthreads();
+    if (kPair) tc::cluster_sync();   // neither block leaves while the other may read its memory or signal it
+    else __syncthreads();
     if (warp == 1) {
         tc::fence_after();
-        tc::tmem_free(sh.tmem, cols);
+        tc::tmem_free<kPair>(0, cols);
     }
     if (threadIdx.x == 0 && sh.dead) atomicOr(&g_status, ERR_TIMEOUT);
 }
 
-// One accumulator to memory: this thread's lane and kHalf columns from tensor
-// memory, times ua and ub, to o[0 .. cols).  on: the lane holds a row of the
-// result.  add: onto what is there.  The accumulator is handed back as soon as
-// its last columns are in registers.
-template <int kHalf, typename T>
-__device__ __forceinline__ void drain(uint32_t src, uint64_t *acc_empty, float ua, float ub, T *o, int64_t cols,
-                                      bool on, bool wide, bool add) {
+// 64 accumulators of a lane times ua and ub, rounded to T and packed.
+template <typename T> __device__ __forceinline__ void finish(const uint32_t (&v)[64], bool scale, float ua, float ub, uint32_t *w) {
+    float f[64];
 #pragma unroll
-    for (int c = 0; c < kHalf; c += 64) {
-        uint32_t v[64];
-        tc::tmem_ld64(src + c, v);
-        if (c + 64 == kHalf) {
-            tc::fence_before();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) tc::bar_arrive(tc::smem_u32(acc_empty));
-        }
-        if (on) {
+    for (int i = 0; i < 64; ++i) f[i] = scale ? __uint_as_float(v[i]) * ua * ub : __uint_as_float(v[i]);
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int j = 0; j < 64; j += 8) {
-                float f[8];
+        for (int i = 0; i < 64; ++i) w[i] = __float_as_uint(f[i]);
+    } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[j + e]) * ua * ub;
-                const int64_t left = cols - c - j;
-                if (left > 0) store_row(o + c + j, f, static_cast<int>(left < 8 ? left : 8), wide, add);
-            }
+        for (int i = 0; i < 32; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            memcpy(&w[i], &h, 4);
         }
     }
 }
 
-template <typename T> __device__ __forceinline__ void zeros(T *o, int half, int64_t cols, bool wide) {
-    const float zero[8] = {};
-    for (int c = 0; c < half && c < cols; c += 8)
-        store_row(o + c, zero, static_cast<int>(cols - c < 8 ? cols - c : 8), wide, false);
+// What is at o added to `n` packed results before they are stored.
+__device__ __forceinline__ void add_some(const __nv_bfloat16 *o, const uint32_t (&v)[64], int at, float ua, float ub, int n,
+                                         uint32_t *w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = 2 * i < n ? __bfloat162float(o[2 * i]) : 0.0f, y = 2 * i + 1 < n ? __bfloat162float(o[2 * i + 1]) : 0.0f;
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x + __uint_as_float(v[at + 2 * i]) * ua * ub,
+                                                       y + __uint_as_float(v[at + 2 * i + 1]) * ua * ub);
+        memcpy(&w[i], &h, 4);
+    }
+}
+__device__ __forceinline__ void add_some(const float *o, const uint32_t (&v)[64], int at, float ua, float ub, int n,
+                                         uint32_t *w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint((i < n ? o[i] : 0.0f) + __uint_as_float(v[at + i]) * ua * ub);
 }
 
-template <bool NV, int BN, typename T>
+// One accumulator to memory: this thread's lane and kHalf columns from tensor
+// memory, times ua and ub (kScale), to o[0 .. cols).  on: the lane holds a row of
+// the result.  The accumulator is handed back (`release`) once all its columns are
+// in registers, rounded: the stores run while the next tile is multiplied.
+template <int kHalf, bool kScale, typename T, typename F>
+__device__ __forceinline__ void drain(uint32_t src, float ua, float ub, T *o, int64_t cols, bool on, int align, F &&release) {
+    constexpr int kPer = 32 / sizeof(T), kWords = 64 * sizeof(T) / 4;
+    uint32_t w[kHalf / 64][kWords];
+#pragma unroll
+    for (int c = 0; c < kHalf / 64; ++c) {
+        uint32_t v[64];
+        tc::tmem_ld64(src + 64 * c, v);
+        finish<T>(v, kScale, ua, ub, w[c]);
+    }
+    release();
+    if (!on) return;
+#pragma unroll
+    for (int c = 0; c < kHalf / 64; ++c)
+#pragma unroll
+        for (int j = 0; j < 64; j += kPer) {
+            const int64_t left = cols - 64 * c - j;
+            if (left > 0) store_some(o + 64 * c + j, w[c] + j * sizeof(T) / 4, left < kPer ? static_cast<int>(left) : kPer, align);
+        }
+}
+
+// The same onto what memory holds.
+template <int kHalf, typename T, typename F>
+__device__ __forceinline__ void drain_add(uint32_t src, float ua, float ub, T *o, int64_t cols, bool on, int align, F &&release) {
+    constexpr int kPer = 32 / sizeof(T);
+#pragma unroll
+    for (int c = 0; c < kHalf / 64; ++c) {
+        uint32_t v[64];
+        tc::tmem_ld64(src + 64 * c, v);
+        if (c == kHalf / 64 - 1) release();
+        if (!on) continue;
+#pragma unroll
+        for (int j = 0; j < 64; j += kPer) {
+            const int64_t left = cols - 64 * c - j;
+            const int n = left < kPer ? static_cast<int>(left) : kPer;
+            if (left <= 0) continue;
+            uint32_t w[8];
+            add_some(o + 64 * c + j, v, j, ua, ub, n, w);
+            store_some(o + 64 * c + j, w, n, align);
+        }
+    }
+}
+
+template <typename T> __device__ __forceinline__ void zeros(T *o, int half, int64_t cols, int align) {
+    constexpr int kPer = 32 / sizeof(T);
+    const uint32_t zero[8] = {};
+    for (int c = 0; c < half && c < cols; c += kPer)
+        store_some(o + c, zero, cols - c < kPer ? static_cast<int>(cols - c) : kPer, align);
+}
+
+template <bool NV, int BN, bool kPair, typename T>
 __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constant__ GemmParams P) {
-    using C = Cfg<NV, BN>;
+    using C = Cfg<NV, BN, kPair>;
     extern __shared__ uint8_t dyn[];
     __shared__ Shared sh;
+    constexpr int kRows = kPair ? 2 * kRowsT : kRowsT, kSc = C::kSc;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    scan_split(P, sh);
+    scan_split<kRows>(P, sh);
+    const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x, units = kPair ? gridDim.x >> 1 : gridDim.x;
+    const int half = kPair ? blockIdx.x & 1 : 0;   // the block's 128 rows of the tile (and its rank in the cluster)
     if (sh.bad) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_status, ERR_SPLIT);
         return;
     }
     const int64_t total = static_cast<int64_t>(sh.tile0[P.E + 1]) * P.n_tiles;
     const int64_t used = static_cast<int64_t>(sh.tile0[P.E]) * P.n_tiles;   // the rest is zeros
-    if (static_cast<int64_t>(blockIdx.x) >= total) return;
-    const Stages<NV, BN> st(dyn);
-    open_block<C::kStages>(sh, warp, 1, C::kCols);
+    if (unit >= total) return;
+    const Stages<NV, BN, kPair> st(dyn);
+    open_block<C::kStages, kPair>(sh, warp, 1, C::kCols);
     constexpr uint32_t tmem = 0;   // the block holds all columns
     volatile uint32_t *dead = &sh.dead;
-    constexpr int kSc = C::kSc;
 
     if (warp == 0) {
         if (tc::elect()) {
@@ -316,11 +389,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
         }
         int g = 0, it = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; i < used && ok; i += gridDim.x) {
-            const Tile t = tile_at(P, sh, i, g);
+        for (int64_t i = unit; i < used && ok; i += units) {
+            const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
-            const int row = uniform(static_cast<int>(t.row)), a_tile = uniform((sh.tile0[g] + t.mt) * P.scale_cols);
-            const int b_row = uniform(static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN));
+            const int row = uniform(static_cast<int>(t.row)) + half * kRowsT;
+            const int a_tile = uniform((sh.scale0[g] + t.mt * (kRows / 128) + half) * P.scale_cols);
+            const int b_row = uniform(static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN)) + half * C::kRowsB;
             const int b_tile = uniform((g * P.b_scale_rows + t.nt * C::kGroupsB) * P.scale_cols);
             for (int k = 0; k < P.kt; ++k, ++it) {
                 const int s = it % C::kStages;
@@ -328,23 +402,31 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
                     ok = false;
                     break;
                 }
-                const uint32_t bar = tc::smem_u32(&sh.full[s]);
+                const uint32_t own = tc::smem_u32(&sh.full[s]), bar = kPair ? tc::map_to(own, 0) : own;
+                auto load = [&](uint32_t dst, const CUtensorMap *tm, int x, int y) {
+                    if (kPair) tc::load_2d_pair(dst, tm, x, y, bar);
+                    else tc::load_2d(dst, tm, x, y, bar);
+                };
                 if (tc::elect()) {
-                    tc::bar_expect(bar, C::kStageBytes);
-                    tc::load_2d(st.a(s), &P.tm_a, k * kStageK, row, bar);
-                    tc::load_2d(st.b(s), &P.tm_b, k * kStageK, b_row, bar);
-                    tc::load_2d(st.sa(s), &P.tm_sa, 0, a_tile + k * kSc, bar);
+                    if (half == 0) tc::bar_expect(own, kPair ? 2 * C::kStageBytes : C::kStageBytes);
+                    load(st.a(s), &P.tm_a, k * kStageK, row);
+                    load(st.b(s), &P.tm_b, k * kStageK, b_row);
+                    load(st.sa(s), &P.tm_sa, 0, a_tile + k * kSc);
 #pragma unroll
                     for (int b = 0; b < C::kGroupsB; ++b)
-                        tc::load_2d(st.sb(s) + b * kSc * kScaleTile, &P.tm_sb, 0, b_tile + b * P.scale_cols + k * kSc, bar);
+                        load(st.sb(s) + b * kSc * kScaleTile, &P.tm_sb, 0, b_tile + b * P.scale_cols + k * kSc);
                 }
+                __syncwarp();
             }
         }
-        if (!ok) settle<C::kStages>(sh.full, it);
-    } else if (warp == 1) {
-        const int mine = uniform(static_cast<int>((used - blockIdx.x + gridDim.x - 1) / gridDim.x));
+        if (!ok) {
+            if (half == 0) settle<C::kStages>(sh.full, it);
+            else tc::pause(1000000);   // its copies count on the other block's barriers: time for them to land
+        }
+    } else if (warp == 1 && half == 0) {
+        const int mine = unit < used ? uniform(static_cast<int>((used - unit + units - 1) / units)) : 0;
         int it = 0;
-        bool ok = static_cast<int64_t>(blockIdx.x) < used;
+        bool ok = true;
         for (int n = 0; n < mine && ok; ++n) {
             const int a = n % C::kAcc;
             if (n >= C::kAcc && !tc::bar_wait_warp(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) break;
@@ -359,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
                 if (tc::elect()) {
                     // the last stage holds only what is left of k
                     multiply_stage(st, s, tmem, tmem + a * BN, min(4, (P.k_bytes - k * kStageK) / 32), k == 0);
-                    tc::commit(tc::smem_u32(&sh.empty[s]));
-                    if (k == P.kt - 1) tc::commit(tc::smem_u32(&sh.acc_full[a]));
+                    tc::commit<kPair>(tc::smem_u32(&sh.empty[s]));
+                    if (k == P.kt - 1) tc::commit<kPair>(tc::smem_u32(&sh.acc_full[a]));
                 }
                 __syncwarp();
             }
@@ -370,34 +452,41 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
         const int q = warp & 3, h = (warp - 4) >> 2;   // lanes 32 q .., column half h
         constexpr int kHalf = BN / 2;
         T *out = static_cast<T *>(P.out);
-        const bool wide = (P.N * sizeof(T)) % 16 == 0;
+        const int align = row_align(out, P.N);
         int g = 0, n = 0;
-        for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-            const Tile t = tile_at(P, sh, i, g);
+        for (int64_t i = unit; i < total; i += units) {
+            const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
-            const int r = 32 * q + lane;
+            const int r = half * kRowsT + 32 * q + lane;
             const int64_t c0 = static_cast<int64_t>(t.nt) * BN + h * kHalf;
             T *o = out + (t.row + r) * P.N + c0;
             const int64_t cols = P.N - c0;   // columns from c0 on
             if (g == P.E) {
-                if (r < t.rows) zeros(o, kHalf, cols, wide);
+                if (r < t.rows) zeros(o, kHalf, cols, align);
                 continue;
             }
             const int a = n % C::kAcc;
-            if (!tc::bar_wait(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, dead)) break;
-            ++n;
-            __syncwarp();
-            tc::fence_after();
             float ua = 1.0f, ub = 1.0f;
             if (NV) {
                 ua = __fdiv_rn(1.0f, tensor_scale(P.amax_a[g]));
                 ub = __fdiv_rn(1.0f, tensor_scale(P.amax_b[g]));
             }
-            drain<kHalf>(tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16), &sh.acc_empty[a], ua, ub, o,
-                         cols, r < t.rows, wide, false);
+            if (!tc::bar_wait_warp(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, dead)) break;
+            ++n;
+            tc::fence_after();
+            drain<kHalf, NV>(tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16), ua, ub, o, cols, r < t.rows,
+                             align, [&] {
+                                 tc::fence_before();
+                                 __syncwarp();
+                                 if (lane == 0) {
+                                     const uint32_t bar = tc::smem_u32(&sh.acc_empty[a]);
+                                     if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
+                                     else tc::bar_arrive(bar);
+                                 }
+                             });
         }
     }
-    close_block(sh, warp, C::kCols);
+    close_block<kPair>(sh, warp, C::kCols);
 }
 
 // ---------------------------------------------------------- weight gradient
@@ -491,7 +580,7 @@ __device__ __forceinline__ void load_scales(uint32_t dst, uint8_t *dst_p, const 
 
 template <bool NV, int BN, typename T>
 __global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_constant__ WgradParams P) {
-    using C = Cfg<NV, BN>;
+    using C = Cfg<NV, BN, false>;
     extern __shared__ uint8_t dyn[];
     __shared__ WgradShared sh;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -528,8 +617,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_c
     }
     const int per = P.n_tiles * P.k_tiles;
     const int64_t total = static_cast<int64_t>(P.E) * per;
-    const Stages<NV, BN> st(dyn);
-    open_block<C::kStages>(sh, warp, kLoaders, C::kCols);
+    const Stages<NV, BN, false> st(dyn);
+    open_block<C::kStages, false>(sh, warp, kLoaders, C::kCols);
     constexpr uint32_t tmem = 0;   // the block holds all columns
     volatile uint32_t *dead = &sh.dead;
 
@@ -553,8 +642,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_c
                 tc::fence_after();
                 if (tc::elect()) {
                     multiply_stage(st, s, tmem, tmem + a * BN, min(4, (len - k * kStageK + 31) / 32), k == 0);
-                    tc::commit(tc::smem_u32(&sh.empty[s]));
-                    if (k == kt - 1) tc::commit(tc::smem_u32(&sh.acc_full[a]));
+                    tc::commit<false>(tc::smem_u32(&sh.empty[s]));
+                    if (k == kt - 1) tc::commit<false>(tc::smem_u32(&sh.acc_full[a]));
                 }
                 __syncwarp();
             }
@@ -602,7 +691,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_c
         const int q = warp & 3, h = (warp - 4) >> 2;
         constexpr int kHalf = BN / 2;
         T *out = static_cast<T *>(P.out);
-        const bool wide = (P.K * sizeof(T)) % 16 == 0, add = P.accumulate != 0;
+        const int align = row_align(out, P.K);
+        const bool add = P.accumulate != 0;
         int n = 0;
         for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
             const int e = static_cast<int>(i / per), j = static_cast<int>(i - static_cast<int64_t>(e) * per);
@@ -610,7 +700,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_c
             const int row = nt * kRowsT + 32 * q + lane, c0 = kt * BN + h * kHalf;
             T *o = out + (static_cast<int64_t>(e) * P.N + row) * P.K + c0;
             if (sh.pad0[e + 1] == sh.pad0[e]) {   // no rows: a zero gradient
-                if (row < P.N && !add) zeros(o, kHalf, P.K - c0, wide);
+                if (row < P.N && !add) zeros(o, kHalf, P.K - c0, align);
                 continue;
             }
             const int a = n % C::kAcc;
@@ -623,11 +713,18 @@ __global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_c
                 ua = __fdiv_rn(1.0f, tensor_scale(P.amax_a[e]));
                 ub = __fdiv_rn(1.0f, tensor_scale(P.amax_b[e]));
             }
-            drain<kHalf>(tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16), &sh.acc_empty[a], ua, ub, o,
-                         static_cast<int64_t>(P.K) - c0, row < P.N, wide, add);
+            const uint32_t src = tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16);
+            const int64_t left = static_cast<int64_t>(P.K) - c0;
+            auto release = [&] {
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(tc::smem_u32(&sh.acc_empty[a]));
+            };
+            if (add) drain_add<kHalf>(src, ua, ub, o, left, row < P.N, align, release);
+            else drain<kHalf, NV>(src, ua, ub, o, left, row < P.N, align, release);
         }
     }
-    close_block(sh, warp, C::kCols);
+    close_block<false>(sh, warp, C::kCols);
 }
 
 // -------------------------------------------------------------------- host
@@ -680,26 +777,54 @@ int sm_count() {
     return n[dev];
 }
 
-template <bool NV, int BN, typename T>
+template <bool NV, int BN, bool kPair, typename T>
 gsa_status launch(const GemmParams &P, int64_t tiles, cudaStream_t s) {
     const int sms = sm_count();
     if (!sms) return GSA_ERR_CUDA;
-    auto k = grouped_gemm<NV, BN, T>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NV, BN>::kSmem) != cudaSuccess)
+    auto k = grouped_gemm<NV, BN, kPair, T>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NV, BN, kPair>::kSmem) != cudaSuccess)
         return GSA_ERR_CUDA;
-    const int64_t grid = tiles * P.n_tiles < sms ? tiles * P.n_tiles : sms;
-    k<<<static_cast<unsigned>(grid), kThreads, Cfg<NV, BN>::kSmem, s>>>(P);
-    return cudaGetLastError() == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
+    static std::once_flag once;
+    static int pairs = 0;   // pairs that fit the machine at once (its clusters may not fill every SM)
+    const int64_t smem = Cfg<NV, BN, kPair>::kSmem;
+    if (kPair)
+        std::call_once(once, [&] {
+            cudaLaunchConfig_t c = {};
+            c.gridDim = dim3(2 * (sms / 2));
+            c.blockDim = dim3(kThreads);
+            c.dynamicSmemBytes = smem;
+            cudaLaunchAttribute a;
+            a.id = cudaLaunchAttributeClusterDimension;
+            a.val.clusterDim.x = 2;
+            a.val.clusterDim.y = a.val.clusterDim.z = 1;
+            c.attrs = &a;
+            c.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&pairs, k, &c) != cudaSuccess) pairs = 0;
+        });
+    if (kPair && pairs <= 0) return GSA_ERR_CUDA;
+    const int64_t units = kPair ? pairs : sms, want = tiles * P.n_tiles, n = want < units ? want : units;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * n : n));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = kPair ? 2 : 1;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, P) == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
 }
 
 template <bool NV, int BN, typename T> gsa_status launch_wgrad(const WgradParams &P, cudaStream_t s) {
     const int sms = sm_count();
     if (!sms) return GSA_ERR_CUDA;
     auto k = grouped_wgrad<NV, BN, T>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NV, BN>::kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NV, BN, false>::kSmem) != cudaSuccess)
         return GSA_ERR_CUDA;
     const int64_t tiles = static_cast<int64_t>(P.E) * P.n_tiles * P.k_tiles;
-    k<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kWgradThreads, Cfg<NV, BN>::kSmem, s>>>(P);
+    k<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kWgradThreads, Cfg<NV, BN, false>::kSmem, s>>>(P);
     return cudaGetLastError() == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
 }
 
@@ -739,8 +864,9 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     GemmParams P;
     std::memset(&P, 0, sizeof(P));
     const int BN = 256;
+    const bool pair = M >= 64 * E;
     const int sc = nv ? 4 : 1;
-    if (!map_codes(&P.tm_a, a->data, M, k_bytes, kRowsT) || !map_codes(&P.tm_b, b->data, E * N, k_bytes, BN) ||
+    if (!map_codes(&P.tm_a, a->data, M, k_bytes, kRowsT) || !map_codes(&P.tm_b, b->data, E * N, k_bytes, pair ? BN / 2 : BN) ||
         !map_scales(&P.tm_sa, a->scale, a_rows * cols, sc) || !map_scales(&P.tm_sb, b->scale, E * n128 * cols, sc))
         return GSA_ERR_CUDA;
     P.split = split_sizes_dev;
@@ -760,8 +886,12 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     const int64_t tiles = (M + kRowsT - 1) / kRowsT + (E < M ? E : M);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     gsa_status st;
-    if (nv) st = out_dtype == GSA_BF16 ? launch<true, 256, __nv_bfloat16>(P, tiles, s) : launch<true, 256, float>(P, tiles, s);
-    else st = out_dtype == GSA_BF16 ? launch<false, 256, __nv_bfloat16>(P, tiles, s) : launch<false, 256, float>(P, tiles, s);
+    auto go = [&](auto fmt, auto two, auto type) {
+        return launch<decltype(fmt)::value, BN, decltype(two)::value, decltype(type)>(P, tiles, s);
+    };
+    auto typed = [&](auto fmt, auto two) { return out_dtype == GSA_BF16 ? go(fmt, two, __nv_bfloat16()) : go(fmt, two, float()); };
+    auto sized = [&](auto fmt) { return pair ? typed(fmt, std::true_type()) : typed(fmt, std::false_type()); };
+    st = nv ? sized(std::true_type()) : sized(std::false_type());
     if (st == GSA_OK) gsa::set_last_launches(1);
     return st;
 }
