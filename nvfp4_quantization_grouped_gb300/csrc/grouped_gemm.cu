@@ -272,84 +272,58 @@ template <bool kPair> __device__ __forceinline__ void close_block(Shared &sh, in
     if (threadIdx.x == 0 && sh.dead) atomicOr(&g_status, ERR_TIMEOUT);
 }
 
-// 64 accumulators of a lane times ua and ub, rounded to T and packed.
-template <typename T> __device__ __forceinline__ void finish(const uint32_t (&v)[64], bool scale, float ua, float ub, uint32_t *w) {
-    float f[64];
+// 32 bytes of results: accumulators times ua and ub (kScale), rounded to T.
+template <bool kScale> __device__ __forceinline__ void finish(const uint32_t *v, float ua, float ub, uint32_t (&w)[8], float) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i) f[i] = scale ? __uint_as_float(v[i]) * ua * ub : __uint_as_float(v[i]);
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 64; ++i) w[i] = __float_as_uint(f[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            memcpy(&w[i], &h, 4);
-        }
-    }
+    for (int i = 0; i < 8; ++i) w[i] = kScale ? __float_as_uint(__uint_as_float(v[i]) * ua * ub) : v[i];
 }
-
-// What is at o added to `n` packed results before they are stored.
-__device__ __forceinline__ void add_some(const __nv_bfloat16 *o, const uint32_t (&v)[64], int at, float ua, float ub, int n,
-                                         uint32_t *w) {
+template <bool kScale>
+__device__ __forceinline__ void finish(const uint32_t *v, float ua, float ub, uint32_t (&w)[8], __nv_bfloat16) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float x = 2 * i < n ? __bfloat162float(o[2 * i]) : 0.0f, y = 2 * i + 1 < n ? __bfloat162float(o[2 * i + 1]) : 0.0f;
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x + __uint_as_float(v[at + 2 * i]) * ua * ub,
-                                                       y + __uint_as_float(v[at + 2 * i + 1]) * ua * ub);
+        const float x = __uint_as_float(v[2 * i]), y = __uint_as_float(v[2 * i + 1]);
+        const __nv_bfloat162 h = kScale ? __floats2bfloat162_rn(x * ua * ub, y * ua * ub) : __floats2bfloat162_rn(x, y);
         memcpy(&w[i], &h, 4);
     }
 }
-__device__ __forceinline__ void add_some(const float *o, const uint32_t (&v)[64], int at, float ua, float ub, int n,
-                                         uint32_t *w) {
+
+// The same onto the n values at o.
+__device__ __forceinline__ void finish_add(const float *o, const uint32_t *v, float ua, float ub, int n, uint32_t (&w)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint((i < n ? o[i] : 0.0f) + __uint_as_float(v[at + i]) * ua * ub);
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint((i < n ? o[i] : 0.0f) + __uint_as_float(v[i]) * ua * ub);
+}
+__device__ __forceinline__ void finish_add(const __nv_bfloat16 *o, const uint32_t *v, float ua, float ub, int n,
+                                           uint32_t (&w)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = 2 * i < n ? __bfloat162float(o[2 * i]) : 0.0f, y = 2 * i + 1 < n ? __bfloat162float(o[2 * i + 1]) : 0.0f;
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x + __uint_as_float(v[2 * i]) * ua * ub,
+                                                       y + __uint_as_float(v[2 * i + 1]) * ua * ub);
+        memcpy(&w[i], &h, 4);
+    }
 }
 
 // One accumulator to memory: this thread's lane and kHalf columns from tensor
-// memory, times ua and ub (kScale), to o[0 .. cols).  on: the lane holds a row of
-// the result.  The accumulator is handed back (`release`) once all its columns are
-// in registers, rounded: the stores run while the next tile is multiplied.
+// memory, times ua and ub (kScale), to o[0 .. cols), or onto what is there (add).
+// on: the lane holds a row of the result.  The accumulator is handed back
+// (`release`) as soon as it is in registers: scaling, rounding and stores run while
+// the next tile is multiplied.
 template <int kHalf, bool kScale, typename T, typename F>
-__device__ __forceinline__ void drain(uint32_t src, float ua, float ub, T *o, int64_t cols, bool on, int align, F &&release) {
-    constexpr int kPer = 32 / sizeof(T), kWords = 64 * sizeof(T) / 4;
-    uint32_t w[kHalf / 64][kWords];
-#pragma unroll
-    for (int c = 0; c < kHalf / 64; ++c) {
-        uint32_t v[64];
-        tc::tmem_ld64(src + 64 * c, v);
-        finish<T>(v, kScale, ua, ub, w[c]);
-    }
+__device__ __forceinline__ void drain(uint32_t src, float ua, float ub, T *o, int64_t cols, bool on, int align, bool add,
+                                      F &&release) {
+    constexpr int kPer = 32 / sizeof(T);
+    uint32_t v[kHalf];
+    tc::tmem_ld(src, v);
     release();
     if (!on) return;
 #pragma unroll
-    for (int c = 0; c < kHalf / 64; ++c)
-#pragma unroll
-        for (int j = 0; j < 64; j += kPer) {
-            const int64_t left = cols - 64 * c - j;
-            if (left > 0) store_some(o + 64 * c + j, w[c] + j * sizeof(T) / 4, left < kPer ? static_cast<int>(left) : kPer, align);
-        }
-}
-
-// The same onto what memory holds.
-template <int kHalf, typename T, typename F>
-__device__ __forceinline__ void drain_add(uint32_t src, float ua, float ub, T *o, int64_t cols, bool on, int align, F &&release) {
-    constexpr int kPer = 32 / sizeof(T);
-#pragma unroll
-    for (int c = 0; c < kHalf / 64; ++c) {
-        uint32_t v[64];
-        tc::tmem_ld64(src + 64 * c, v);
-        if (c == kHalf / 64 - 1) release();
-        if (!on) continue;
-#pragma unroll
-        for (int j = 0; j < 64; j += kPer) {
-            const int64_t left = cols - 64 * c - j;
-            const int n = left < kPer ? static_cast<int>(left) : kPer;
-            if (left <= 0) continue;
-            uint32_t w[8];
-            add_some(o + 64 * c + j, v, j, ua, ub, n, w);
-            store_some(o + 64 * c + j, w, n, align);
-        }
+    for (int j = 0; j < kHalf; j += kPer) {
+        if (j >= cols) break;
+        const int n = cols - j < kPer ? static_cast<int>(cols - j) : kPer;
+        uint32_t w[8];
+        if (add) finish_add(o + j, v + j, ua, ub, n, w);
+        else finish<kScale>(v + j, ua, ub, w, T());
+        store_some(o + j, w, n, align);
     }
 }
 
@@ -475,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
             ++n;
             tc::fence_after();
             drain<kHalf, NV>(tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16), ua, ub, o, cols, r < t.rows,
-                             align, [&] {
+                             align, false, [&] {
                                  tc::fence_before();
                                  __syncwarp();
                                  if (lane == 0) {
@@ -720,8 +694,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_c
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem_u32(&sh.acc_empty[a]));
             };
-            if (add) drain_add<kHalf>(src, ua, ub, o, left, row < P.N, align, release);
-            else drain<kHalf, NV>(src, ua, ub, o, left, row < P.N, align, release);
+            drain<kHalf, NV>(src, ua, ub, o, left, row < P.N, align, add, release);
         }
     }
     close_block<false>(sh, warp, C::kCols);
