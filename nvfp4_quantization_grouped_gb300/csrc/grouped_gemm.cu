@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
 // from columnwise copies: per expert [N, Mp_e] and [K, Mp_e], Mp_e the rows padded
 // to whole scale blocks, so that the sum runs along the contiguous axis again.
 // An expert's pitch is Mp_e codes: a multiple of 8 bytes only (NVFP4), which TMA
-// does not take, so four warps bring the stages in with 16- or 8-byte
+// does not take, so three warps bring the stages in with 16- or 8-byte
 // asynchronous copies, zeros past the matrices.  Scales past Mp_e are padding that
 // nobody wrote: they are masked to zero, since a zero code times a NaN scale would
 // still be NaN.
@@ -486,12 +486,13 @@ struct WgradParams {
     int accumulate;
 };
 
-constexpr int kWgradThreads = 512;   // as above, and warps 12-15 load
-constexpr int kLoaders = 128;
+constexpr int kLoadWarps = 3;        // warps 0, 2 and 3; warp 1 multiplies, warps 4-11 drain
+constexpr int kLoaders = 32 * kLoadWarps;
 
 struct WgradShared : Shared {
     int64_t pad0[kMaxE + 1];    // padded rows before each expert
     int wide0[kMaxE + 1];       // scale tiles along the rows before each expert
+    int order[kMaxE];           // experts by descending size
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
@@ -503,43 +504,61 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, int byt
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 // Writes to shared memory so far become visible to the tensor core's reads.
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-// Rows [r0, r0 + rows) x 128 bytes at k0 of a matrix [n, pitch bytes] into a
-// swizzled stage: 16-byte chunk c of row r at chunk c ^ (r mod 8).
-template <int kRows>
-__device__ __forceinline__ void load_codes(uint32_t dst, const uint8_t *m, int64_t pitch, int n, int r0, int64_t k0,
-                                           int thread) {
-    if (pitch % 16 == 0) {
-#pragma unroll 4
-        for (int i = thread; i < kRows * 8; i += kLoaders) {
-            const int r = i >> 3, c = i & 7;
-            const int64_t left = r0 + r < n ? pitch - k0 - 16 * c : 0;
-            const int bytes = left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0;
-            cp_async16(dst + r * 128 + ((c ^ (r & 7)) << 4), bytes ? m + (r0 + r) * pitch + k0 + 16 * c : m, bytes);
-        }
-    } else {
-#pragma unroll 4
-        for (int i = thread; i < kRows * 16; i += kLoaders) {
-            const int r = i >> 4, c = i & 15;
-            const int64_t left = r0 + r < n ? pitch - k0 - 8 * c : 0;
-            const int bytes = left >= 8 ? 8 : 0;
-            cp_async8(dst + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1), bytes ? m + (r0 + r) * pitch + k0 + 8 * c : m,
-                      bytes);
+// 128 rows of a matrix [n, pitch bytes] from row r0 on, as one loader thread sees
+// them.  A warp's copy takes 4 rows in chunks of 16 bytes, or 2 in chunks of 8
+// where the pitch is no multiple of 16; the warps take every kLoadWarps-th such
+// group.  Chunk c of row r lies at c ^ (r mod 8) of the swizzled stage.
+struct CodeLoad {
+    const uint8_t *p;   // the thread's chunk of its first row, at k = 0
+    int64_t step;       // bytes from a row of the thread to its next
+    int row, rows;      // its first row within the 128, and how many rows the matrix has from r0 on
+    int c;              // its chunk
+    bool wide;          // chunks of 16 bytes
+    __device__ CodeLoad(const uint8_t *m, int64_t pitch, int n, int r0, int warp, int lane) {
+        wide = pitch % 16 == 0;
+        c = wide ? lane & 7 : lane & 15;
+        row = wide ? 4 * warp + (lane >> 3) : 2 * warp + (lane >> 4);
+        rows = n - r0;
+        step = (wide ? 4 : 2) * kLoadWarps * pitch;
+        p = m + static_cast<int64_t>(r0 + row) * pitch + c * (wide ? 16 : 8);
+    }
+    // 128 bytes of k from k0 on (pitch: the matrix' bytes of k), zeros past the matrix.
+    __device__ __forceinline__ void operator()(uint32_t stage, int64_t k0, int64_t pitch) const {
+        const uint8_t *src = p + k0;
+        if (wide) {
+            const int left = k0 + 16 * c < pitch ? rows : 0;
+#pragma unroll
+            for (int j = 0; j < (32 + kLoadWarps - 1) / kLoadWarps; ++j) {
+                const int r = row + 4 * kLoadWarps * j;
+                if (r < kRowsT) cp_async16(stage + r * 128 + ((c ^ (r & 7)) << 4), r < left ? src : p, r < left ? 16 : 0);
+                src += step;
+            }
+        } else {
+            const int left = k0 + 8 * c < pitch ? rows : 0;
+#pragma unroll
+            for (int j = 0; j < (64 + kLoadWarps - 1) / kLoadWarps; ++j) {
+                const int r = row + 2 * kLoadWarps * j;
+                if (r < kRowsT)
+                    cp_async8(stage + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1), r < left ? src : p, r < left ? 8 : 0);
+                src += step;
+            }
         }
     }
-}
+};
 
 // The scale tiles of a stage for 128-row groups g0 .. of a matrix: tiles
 // [c0, c0 + kSc) of each row of tiles, entries from `cols` on as zero.
 template <int kSc, int kGroups>
 __device__ __forceinline__ void load_scales(uint32_t dst, uint8_t *dst_p, const uint8_t *m, int groups, int g0, int wide,
                                             int c0, int cols, int thread) {
+    constexpr int kChunks = kSc * (kScaleTile / 16);   // of a group: contiguous in memory and in the stage
 #pragma unroll
-    for (int i = thread; i < kGroups * kSc * (kScaleTile / 16); i += kLoaders) {
-        const int tile = i >> 5, g = tile / kSc, j = tile % kSc;
+    for (int i = thread; i < kGroups * kChunks; i += kLoaders) {
+        const int g = i / kChunks, j = (i % kChunks) >> 5;
         const bool in = g0 + g < groups && c0 + j < wide;
-        const uint8_t *src = in ? m + ((static_cast<int64_t>(g0 + g) * wide + c0 + j) * kScaleTile + (i & 31) * 16) : m;
+        const uint8_t *src = in ? m + (static_cast<int64_t>(g0 + g) * wide + c0) * kScaleTile + (i % kChunks) * 16 : m;
         const int left = cols - 4 * (c0 + j);
         if (!in || left >= 4) {
             cp_async16(dst + i * 16, src, in ? 16 : 0);
@@ -552,152 +571,209 @@ __device__ __forceinline__ void load_scales(uint32_t dst, uint8_t *dst_p, const 
     }
 }
 
-template <bool NV, int BN, typename T>
-__global__ void __launch_bounds__(kWgradThreads, 1) grouped_wgrad(const __grid_constant__ WgradParams P) {
-    using C = Cfg<NV, BN, false>;
+// Padded rows and scale tiles before each expert, and the experts by descending size.  Every thread of the block.
+template <int kBlock> __device__ void scan_wgrad(const WgradParams &P, WgradShared &sh, bool nv) {
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    int64_t m = t < P.E ? P.split[t] : 0;
+    const bool neg = m < 0 || m > P.M;
+    if (neg) m = 0;
+    if (t < P.E) sh.row0[t] = m;   // sizes, until sorted
+    int64_t rows = m, pad = (m + kBlock - 1) / kBlock * kBlock, wide = (m + 4 * kBlock - 1) / (4 * kBlock);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, d), q = __shfl_up_sync(0xFFFFFFFFu, pad, d),
+                      u = __shfl_up_sync(0xFFFFFFFFu, wide, d);
+        if (lane >= d) rows += r, pad += q, wide += u;
+    }
+    if (w < kThreads / 32 && lane == 31) sh.scan[w][0] = rows, sh.scan[w][1] = pad, sh.scan[w][2] = wide;
+    const bool any_neg = __syncthreads_or(neg);
+    for (int k = 0; k < w && k < kThreads / 32; ++k) rows += sh.scan[k][0], pad += sh.scan[k][1], wide += sh.scan[k][2];
+    if (t < P.E) {
+        sh.pad0[t + 1] = pad;
+        sh.wide0[t + 1] = static_cast<int>(wide);
+        int rank = 0;
+        for (int k = 0; k < P.E; ++k) rank += sh.row0[k] > m || (sh.row0[k] == m && k < t);
+        sh.order[rank] = t;
+    }
+    if (t == 0) sh.pad0[0] = 0, sh.wide0[0] = 0;
+    if (t == P.E - 1) {
+        const int64_t codes = nv ? pad / 2 : pad, tiles = wide * kScaleTile;
+        sh.bad = any_neg || rows > P.M || codes * P.N > P.a_bytes || codes * P.K > P.b_bytes ||
+                 tiles * ((P.N + 127) / 128) > P.sa_bytes || tiles * ((P.K + 127) / 128) > P.sb_bytes;
+    }
+    __syncthreads();
+}
+
+// A tile of the weight gradients.  A unit's r-th tile goes back and forth over the
+// units (u, then units - 1 - u, ..) in the order of descending experts, so that
+// long and short sums even out.
+struct WTile {
+    int e, nt, kt;
+    int64_t pad0, rows;   // padded rows before the expert, and its own
+};
+__device__ __forceinline__ int64_t wgrad_tile(int64_t r, int unit, int units) {
+    return r * units + ((r & 1) ? units - 1 - unit : unit);
+}
+__device__ __forceinline__ WTile wtile_at(const WgradParams &P, const WgradShared &sh, int64_t i) {
+    const int per = P.n_tiles * P.k_tiles;
+    WTile t;
+    const int x = static_cast<int>(i / per), j = static_cast<int>(i - static_cast<int64_t>(x) * per);
+    t.e = sh.order[x];
+    t.nt = j / P.k_tiles;
+    t.kt = j - t.nt * P.k_tiles;
+    t.pad0 = sh.pad0[t.e];
+    t.rows = sh.pad0[t.e + 1] - t.pad0;
+    return t;
+}
+
+template <bool NV, int BN, bool kPair, typename T>
+__global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_constant__ WgradParams P) {
+    using C = Cfg<NV, BN, kPair>;
     extern __shared__ uint8_t dyn[];
     __shared__ WgradShared sh;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     constexpr int kBlock = NV ? 16 : 32, kSc = C::kSc, kDepth = C::kStages - 2;
-    // group bounds: padded rows and scale tiles before each expert
-    {
-        const int t = threadIdx.x;
-        int64_t m = t < P.E ? P.split[t] : 0;
-        const bool neg = m < 0 || m > P.M;
-        if (neg) m = 0;
-        int64_t rows = m, pad = (m + kBlock - 1) / kBlock * kBlock, wide = (m + 4 * kBlock - 1) / (4 * kBlock);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, d), q = __shfl_up_sync(0xFFFFFFFFu, pad, d),
-                          u = __shfl_up_sync(0xFFFFFFFFu, wide, d);
-            if (lane >= d) rows += r, pad += q, wide += u;
-        }
-        __shared__ int64_t scan[kMaxE / 32][3];
-        if (warp < kMaxE / 32 && lane == 31) scan[warp][0] = rows, scan[warp][1] = pad, scan[warp][2] = wide;
-        const bool any_neg = __syncthreads_or(neg);
-        for (int k = 0; k < warp && k < kMaxE / 32; ++k) rows += scan[k][0], pad += scan[k][1], wide += scan[k][2];
-        if (t < P.E) sh.pad0[t + 1] = pad, sh.wide0[t + 1] = static_cast<int>(wide);
-        if (t == 0) sh.pad0[0] = 0, sh.wide0[0] = 0;
-        if (t == P.E - 1) {
-            const int64_t codes = NV ? pad / 2 : pad, tiles = wide * kScaleTile;
-            sh.bad = any_neg || rows > P.M || codes * P.N > P.a_bytes || codes * P.K > P.b_bytes ||
-                     tiles * ((P.N + 127) / 128) > P.sa_bytes || tiles * ((P.K + 127) / 128) > P.sb_bytes;
-        }
-        __syncthreads();
-    }
+    constexpr int kRows = kPair ? 2 * kRowsT : kRowsT;
+    scan_wgrad<kBlock>(P, sh, NV);
     if (sh.bad) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_status, ERR_SPLIT);
         return;
     }
-    const int per = P.n_tiles * P.k_tiles;
-    const int64_t total = static_cast<int64_t>(P.E) * per;
-    const Stages<NV, BN, false> st(dyn);
-    open_block<C::kStages, false>(sh, warp, kLoaders, C::kCols);
+    const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x, units = kPair ? gridDim.x >> 1 : gridDim.x;
+    const int half = kPair ? blockIdx.x & 1 : 0;
+    const int64_t total = static_cast<int64_t>(P.E) * P.n_tiles * P.k_tiles;
+    const Stages<NV, BN, kPair> st(dyn);
+    open_block<C::kStages, kPair>(sh, warp, (kPair ? 2 : 1) * kLoadWarps, C::kCols);
     constexpr uint32_t tmem = 0;   // the block holds all columns
     volatile uint32_t *dead = &sh.dead;
 
     if (warp == 1) {
-        int it = 0, n = 0;
-        bool ok = true;
-        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
-            const int e = static_cast<int>(i / per);
-            const int len = uniform(static_cast<int>((sh.pad0[e + 1] - sh.pad0[e]) / (NV ? 2 : 1)));
-            if (len == 0) continue;
-            const int a = n % C::kAcc, kt = (len + kStageK - 1) / kStageK;
-            if (n >= C::kAcc && !tc::bar_wait_warp(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) break;
-            ++n;
-            tc::fence_after();
-            for (int k = 0; k < kt; ++k, ++it) {
-                const int s = it % C::kStages;
-                if (!tc::bar_wait_warp(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) {
-                    ok = false;
-                    break;
+        if (half == 0) {
+            int it = 0, n = 0;
+            bool ok = true;
+            for (int64_t r = 0;; ++r) {
+                const int64_t i = wgrad_tile(r, unit, units);
+                if (i >= total) {
+                    if (r * units >= total) break;
+                    continue;
                 }
+                const WTile t = wtile_at(P, sh, i);
+                const int len = uniform(static_cast<int>(NV ? t.rows / 2 : t.rows));
+                if (len == 0) continue;
+                const int a = n % C::kAcc, kt = (len + kStageK - 1) / kStageK;
+                if (n >= C::kAcc && !tc::bar_wait_warp(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) break;
+                ++n;
                 tc::fence_after();
-                if (tc::elect()) {
-                    multiply_stage(st, s, tmem, tmem + a * BN, min(4, (len - k * kStageK + 31) / 32), k == 0);
-                    tc::commit<false>(tc::smem_u32(&sh.empty[s]));
-                    if (k == kt - 1) tc::commit<false>(tc::smem_u32(&sh.acc_full[a]));
+                for (int k = 0; k < kt; ++k, ++it) {
+                    const int s = it % C::kStages;
+                    if (!tc::bar_wait_warp(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    if (tc::elect()) {
+                        multiply_stage(st, s, tmem, tmem + a * BN, min(4, (len - k * kStageK + 31) / 32), k == 0);
+                        tc::commit<kPair>(tc::smem_u32(&sh.empty[s]));
+                        if (k == kt - 1) tc::commit<kPair>(tc::smem_u32(&sh.acc_full[a]));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
             }
+            if (!ok || *dead) settle<C::kStages>(sh.empty, it);
         }
-        if (!ok || *dead) settle<C::kStages>(sh.empty, it);
-    } else if (warp >= 12) {
-        const int thread = threadIdx.x - 12 * 32;
+    } else if (warp < 4) {
+        const int loader = warp == 0 ? 0 : warp - 1, thread = 32 * loader + lane;
+        const int n128 = (P.N + 127) / 128, k128 = (P.K + 127) / 128;
+        auto arrive = [&](int j) {   // stage j's copies of this warp have landed
+            fence_async();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t bar = tc::smem_u32(&sh.full[j % C::kStages]);
+                if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
+                else tc::bar_arrive(bar);
+            }
+        };
         int it = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; i < total && ok; i += gridDim.x) {
-            const int e = static_cast<int>(i / per), j = static_cast<int>(i - static_cast<int64_t>(e) * per);
-            const int64_t pad0 = sh.pad0[e], mp = sh.pad0[e + 1] - pad0;
-            const int64_t pitch = NV ? mp / 2 : mp, first = NV ? pad0 / 2 : pad0;
-            const int wide = sh.wide0[e + 1] - sh.wide0[e], cols = static_cast<int>(mp / kBlock);
-            const int nt = j / P.k_tiles, kt = j - nt * P.k_tiles;
-            const int n128 = (P.N + 127) / 128, k128 = (P.K + 127) / 128;
-            const uint8_t *a = P.a + first * P.N, *b = P.b + first * P.K;
-            const uint8_t *sa = P.sa + static_cast<int64_t>(sh.wide0[e]) * n128 * kScaleTile;
-            const uint8_t *sb = P.sb + static_cast<int64_t>(sh.wide0[e]) * k128 * kScaleTile;
+        for (int64_t r = 0; ok; ++r) {
+            const int64_t i = wgrad_tile(r, unit, units);
+            if (i >= total) {
+                if (r * units >= total) break;
+                continue;
+            }
+            const WTile t = wtile_at(P, sh, i);
+            const int64_t pitch = NV ? t.rows / 2 : t.rows, first = NV ? t.pad0 / 2 : t.pad0;
+            const int wide = sh.wide0[t.e + 1] - sh.wide0[t.e], cols = static_cast<int>(t.rows / kBlock);
+            const uint8_t *sa = P.sa + static_cast<int64_t>(sh.wide0[t.e]) * n128 * kScaleTile;
+            const uint8_t *sb = P.sb + static_cast<int64_t>(sh.wide0[t.e]) * k128 * kScaleTile;
+            const CodeLoad load_a(P.a + first * P.N, pitch, P.N, t.nt * kRows + half * kRowsT, loader, lane);
+            const CodeLoad load_b(P.b + first * P.K, pitch, P.K, t.kt * BN + half * C::kRowsB, loader, lane);
             for (int64_t k = 0; k < pitch; k += kStageK, ++it) {
                 const int s = it % C::kStages;
-                if (it >= C::kStages && !tc::bar_wait(tc::smem_u32(&sh.empty[s]), (it / C::kStages - 1) & 1, dead)) {
+                if (it >= C::kStages && !tc::bar_wait_warp(tc::smem_u32(&sh.empty[s]), (it / C::kStages - 1) & 1, dead)) {
                     ok = false;
                     break;
                 }
-                load_codes<kRowsT>(st.a(s), a, pitch, P.N, nt * kRowsT, k, thread);
-                load_codes<BN>(st.b(s), b, pitch, P.K, kt * BN, k, thread);
+                load_a(st.a(s), k, pitch);
+                load_b(st.b(s), k, pitch);
                 const int c0 = static_cast<int>(k / kStageK) * kSc;
                 uint8_t *p = dyn + (st.sa(s) - tc::smem_u32(dyn));
-                load_scales<kSc, 1>(st.sa(s), p, sa, n128, nt, wide, c0, cols, thread);
-                load_scales<kSc, C::kGroupsB>(st.sb(s), p + C::kBytesSA, sb, k128, kt * C::kGroupsB, wide, c0, cols, thread);
+                load_scales<kSc, 1>(st.sa(s), p, sa, n128, t.nt * (kRows / 128) + half, wide, c0, cols, thread);
+                load_scales<kSc, C::kGroupsB>(st.sb(s), p + C::kBytesSA, sb, k128, t.kt * C::kGroupsB, wide, c0, cols, thread);
                 cp_commit();
                 if (it >= kDepth) {   // the stage kDepth before this one has arrived
                     cp_wait<kDepth>();
-                    fence_async();
-                    tc::bar_arrive(tc::smem_u32(&sh.full[(it - kDepth) % C::kStages]));
+                    arrive(it - kDepth);
                 }
             }
         }
         cp_wait<0>();
-        fence_async();
         if (ok)
-            for (int j = it < kDepth ? 0 : it - kDepth; j < it; ++j) tc::bar_arrive(tc::smem_u32(&sh.full[j % C::kStages]));
-    } else if (warp >= 4 && warp < 12) {
+            for (int j = it < kDepth ? 0 : it - kDepth; j < it; ++j) arrive(j);
+    } else {
         const int q = warp & 3, h = (warp - 4) >> 2;
         constexpr int kHalf = BN / 2;
         T *out = static_cast<T *>(P.out);
         const int align = row_align(out, P.K);
         const bool add = P.accumulate != 0;
         int n = 0;
-        for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
-            const int e = static_cast<int>(i / per), j = static_cast<int>(i - static_cast<int64_t>(e) * per);
-            const int nt = j / P.k_tiles, kt = j - nt * P.k_tiles;
-            const int row = nt * kRowsT + 32 * q + lane, c0 = kt * BN + h * kHalf;
-            T *o = out + (static_cast<int64_t>(e) * P.N + row) * P.K + c0;
-            if (sh.pad0[e + 1] == sh.pad0[e]) {   // no rows: a zero gradient
-                if (row < P.N && !add) zeros(o, kHalf, P.K - c0, align);
+        for (int64_t r = 0;; ++r) {
+            const int64_t i = wgrad_tile(r, unit, units);
+            if (i >= total) {
+                if (r * units >= total) break;
+                continue;
+            }
+            const WTile t = wtile_at(P, sh, i);
+            const int row = t.nt * kRows + half * kRowsT + 32 * q + lane, c0 = t.kt * BN + h * kHalf;
+            T *o = out + (static_cast<int64_t>(t.e) * P.N + row) * P.K + c0;
+            const int64_t left = static_cast<int64_t>(P.K) - c0;
+            if (t.rows == 0) {   // no rows: a zero gradient
+                if (row < P.N && !add) zeros(o, kHalf, left, align);
                 continue;
             }
             const int a = n % C::kAcc;
-            if (!tc::bar_wait(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, dead)) break;
-            ++n;
-            __syncwarp();
-            tc::fence_after();
             float ua = 1.0f, ub = 1.0f;
             if (NV) {
-                ua = __fdiv_rn(1.0f, tensor_scale(P.amax_a[e]));
-                ub = __fdiv_rn(1.0f, tensor_scale(P.amax_b[e]));
+                ua = __fdiv_rn(1.0f, tensor_scale(P.amax_a[t.e]));
+                ub = __fdiv_rn(1.0f, tensor_scale(P.amax_b[t.e]));
             }
-            const uint32_t src = tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16);
-            const int64_t left = static_cast<int64_t>(P.K) - c0;
-            auto release = [&] {
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::bar_arrive(tc::smem_u32(&sh.acc_empty[a]));
-            };
-            drain<kHalf, NV>(src, ua, ub, o, left, row < P.N, align, add, release);
+            if (!tc::bar_wait_warp(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, dead)) break;
+            ++n;
+            tc::fence_after();
+            drain<kHalf, NV>(tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16), ua, ub, o, left, row < P.N,
+                             align, add, [&] {
+                                 tc::fence_before();
+                                 __syncwarp();
+                                 if (lane == 0) {
+                                     const uint32_t bar = tc::smem_u32(&sh.acc_empty[a]);
+                                     if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
+                                     else tc::bar_arrive(bar);
+                                 }
+                             });
         }
     }
-    close_block<false>(sh, warp, C::kCols);
+    close_block<kPair>(sh, warp, C::kCols);
 }
 
 // -------------------------------------------------------------------- host
@@ -750,35 +826,16 @@ int sm_count() {
     return n[dev];
 }
 
-template <bool NV, int BN, bool kPair, typename T>
-gsa_status launch(const GemmParams &P, int64_t tiles, cudaStream_t s) {
+// A persistent launch of at most `want` blocks (kPair: pairs of blocks), as many as run at once.
+template <bool kPair, typename P>
+gsa_status launch(void (*kernel)(P), const P &params, int threads, size_t smem, int64_t want, cudaStream_t s, int &pairs,
+                  std::once_flag &once) {
     const int sms = sm_count();
     if (!sms) return GSA_ERR_CUDA;
-    auto k = grouped_gemm<NV, BN, kPair, T>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NV, BN, kPair>::kSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return GSA_ERR_CUDA;
-    static std::once_flag once;
-    static int pairs = 0;   // pairs that fit the machine at once (its clusters may not fill every SM)
-    const int64_t smem = Cfg<NV, BN, kPair>::kSmem;
-    if (kPair)
-        std::call_once(once, [&] {
-            cudaLaunchConfig_t c = {};
-            c.gridDim = dim3(2 * (sms / 2));
-            c.blockDim = dim3(kThreads);
-            c.dynamicSmemBytes = smem;
-            cudaLaunchAttribute a;
-            a.id = cudaLaunchAttributeClusterDimension;
-            a.val.clusterDim.x = 2;
-            a.val.clusterDim.y = a.val.clusterDim.z = 1;
-            c.attrs = &a;
-            c.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&pairs, k, &c) != cudaSuccess) pairs = 0;
-        });
-    if (kPair && pairs <= 0) return GSA_ERR_CUDA;
-    const int64_t units = kPair ? pairs : sms, want = tiles * P.n_tiles, n = want < units ? want : units;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * n : n));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at;
@@ -787,18 +844,30 @@ gsa_status launch(const GemmParams &P, int64_t tiles, cudaStream_t s) {
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, P) == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
+    if (kPair)   // the machine's clusters may not fill every SM
+        std::call_once(once, [&] {
+            cfg.gridDim = dim3(2 * (sms / 2));
+            if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess) pairs = 0;
+        });
+    if (kPair && pairs <= 0) return GSA_ERR_CUDA;
+    const int64_t units = kPair ? pairs : sms, n = want < units ? want : units;
+    cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * n : n));
+    return cudaLaunchKernelEx(&cfg, kernel, params) == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
 }
 
-template <bool NV, int BN, typename T> gsa_status launch_wgrad(const WgradParams &P, cudaStream_t s) {
-    const int sms = sm_count();
-    if (!sms) return GSA_ERR_CUDA;
-    auto k = grouped_wgrad<NV, BN, T>;
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NV, BN, false>::kSmem) != cudaSuccess)
-        return GSA_ERR_CUDA;
-    const int64_t tiles = static_cast<int64_t>(P.E) * P.n_tiles * P.k_tiles;
-    k<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kWgradThreads, Cfg<NV, BN, false>::kSmem, s>>>(P);
-    return cudaGetLastError() == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
+template <bool NV, int BN, bool kPair, typename T>
+gsa_status launch_gemm(const GemmParams &P, int64_t tiles, cudaStream_t s) {
+    static std::once_flag once;
+    static int pairs = 0;
+    return launch<kPair, GemmParams>(grouped_gemm<NV, BN, kPair, T>, P, kThreads, Cfg<NV, BN, kPair>::kSmem, tiles * P.n_tiles,
+                                     s, pairs, once);
+}
+
+template <bool NV, int BN, bool kPair, typename T> gsa_status launch_wgrad(const WgradParams &P, cudaStream_t s) {
+    static std::once_flag once;
+    static int pairs = 0;
+    return launch<kPair, WgradParams>(grouped_wgrad<NV, BN, kPair, T>, P, kThreads, Cfg<NV, BN, kPair>::kSmem,
+                                      static_cast<int64_t>(P.E) * P.n_tiles * P.k_tiles, s, pairs, once);
 }
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -860,7 +929,7 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     gsa_status st;
     auto go = [&](auto fmt, auto two, auto type) {
-        return launch<decltype(fmt)::value, BN, decltype(two)::value, decltype(type)>(P, tiles, s);
+        return launch_gemm<decltype(fmt)::value, BN, decltype(two)::value, decltype(type)>(P, tiles, s);
     };
     auto typed = [&](auto fmt, auto two) { return out_dtype == GSA_BF16 ? go(fmt, two, __nv_bfloat16()) : go(fmt, two, float()); };
     auto sized = [&](auto fmt) { return pair ? typed(fmt, std::true_type()) : typed(fmt, std::false_type()); };
@@ -900,9 +969,10 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     P.N = static_cast<int>(N);
     P.K = static_cast<int>(K);
     P.E = static_cast<int>(E);
-    const int BN = 128;
-    P.n_tiles = static_cast<int>((N + kRowsT - 1) / kRowsT);
-    P.k_tiles = static_cast<int>((K + BN - 1) / BN);
+    const bool pair = N > 128 && K > 128;
+    const int tile = pair ? 256 : 128;
+    P.n_tiles = static_cast<int>((N + tile - 1) / tile);
+    P.k_tiles = static_cast<int>((K + tile - 1) / tile);
     P.a_bytes = a->data_bytes;
     P.b_bytes = b->data_bytes;
     P.sa_bytes = a->scale_bytes;
@@ -911,8 +981,12 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     if (static_cast<int64_t>(P.n_tiles) * P.k_tiles >= (int64_t(1) << 31)) return GSA_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     gsa_status st;
-    if (nv) st = out_dtype == GSA_BF16 ? launch_wgrad<true, BN, __nv_bfloat16>(P, s) : launch_wgrad<true, BN, float>(P, s);
-    else st = out_dtype == GSA_BF16 ? launch_wgrad<false, BN, __nv_bfloat16>(P, s) : launch_wgrad<false, BN, float>(P, s);
+    auto typed = [&](auto fmt, auto type) {
+        return pair ? launch_wgrad<decltype(fmt)::value, 256, true, decltype(type)>(P, s)
+                    : launch_wgrad<decltype(fmt)::value, 128, false, decltype(type)>(P, s);
+    };
+    auto sized = [&](auto fmt) { return out_dtype == GSA_BF16 ? typed(fmt, __nv_bfloat16()) : typed(fmt, float()); };
+    st = nv ? sized(std::true_type()) : sized(std::false_type());
     if (st == GSA_OK) gsa::set_last_launches(1);
     return st;
 }
