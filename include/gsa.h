@@ -383,7 +383,7 @@ gsa_status gsa_moe_unpermute_bwd(const void *dout, const void *ys, const float *
  * The GEMMs on both sides of the activation step, on the quantized copies that
  * the calls above write, with GSA_SCALES_TILED scales and per-expert weights.
  * The split is in device memory, as for the graph-safe calls: nothing depends on
- * the host knowing it, nothing synchronizes or allocates, one launch per call. */
+ * the host knowing it, nothing synchronizes or allocates. */
 
 /* One quantized operand: a copy's codes, its tiled scales and (NVFP4) its
  * amax [E].  The byte counts are the buffers' sizes; the calls check them. */
@@ -414,16 +414,22 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
                             int64_t N, int64_t K, int32_t recipe_kind, void *out, int32_t out_dtype,
                             gsa_stream_t stream);
 
+/* Workspace bytes of gsa_grouped_gemm_wgrad (256-byte aligned; any content).
+ * 0 on invalid arguments.  NVFP4 keeps copies of the experts there whose padded
+ * rows are an odd multiple of 16, so it takes about the operands' own size. */
+size_t gsa_grouped_gemm_wgrad_workspace_size(int64_t E, int64_t M, int64_t N, int64_t K, int32_t recipe_kind);
+
 /* dw[e] [N, K] = sum over the rows r of expert e of A[r, :]^T B[r, :].
  *   a, b  columnwise copies of [M, N] and [M, K] tensors grouped by the split
  *         (NVFP4 with the RHT: the same sign mask in both, it cancels).
  *   dw    [E, N, K] row-major, GSA_BF16 or GSA_FP32; zeros for an expert without
  *         rows.  accumulate != 0: added to what dw holds (one rounding of the sum).
- * N and K are even (NVFP4) or arbitrary (MXFP8); the split and errors as for
- * gsa_grouped_gemm, the buffers checked against all four byte counts. */
+ * N and K are even (NVFP4) or arbitrary (MXFP8), both below 2^30.  The split as
+ * for gsa_grouped_gemm, the buffers checked against all four byte counts.  Two
+ * launches.  Errors: as gsa_grouped_gemm, and WORKSPACE. */
 gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int64_t *split_sizes_dev, int64_t E,
                                   int64_t M, int64_t N, int64_t K, int32_t recipe_kind, void *dw, int32_t out_dtype,
-                                  int32_t accumulate, gsa_stream_t stream);
+                                  int32_t accumulate, void *workspace, size_t workspace_bytes, gsa_stream_t stream);
 
 /* Synchronizes `stream`; then what grouped products on the current device have
  * reported since the last query, which it clears: GSA_OK, GSA_ERR_INVALID_ARG

@@ -80,14 +80,17 @@ template <bool NV, int BN, bool kPair> struct Cfg {
     static constexpr int kSmem = kStages * kStride + 1024;
 };
 
-struct Shared {
+struct Barriers {
+    uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
+    uint32_t tmem, dead;
+};
+
+struct GemmShared : Barriers {
     int64_t row0[kMaxE + 2];    // first row of each group; group E: rows that no expert has
     int tile0[kMaxE + 2];       // first row tile of each group
     int scale0[kMaxE + 1];      // first 128-row scale tile of each expert
-    uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
-    uint32_t tmem;
-    uint32_t dead, bad;
     int64_t scan[kThreads / 32][3];
+    uint32_t bad;
 };
 
 // A value that is the same in all lanes, as the compiler cannot tell.
@@ -95,7 +98,7 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, 
 
 // Group bounds from the device split: rows, scale tiles and row tiles of kRows before each group.  Every thread
 // of the block.  A negative size, a sum above M or more scale tiles than A's buffer holds sets sh.bad.
-template <int kRows> __device__ void scan_split(const GemmParams &P, Shared &sh) {
+template <int kRows> __device__ void scan_split(const GemmParams &P, GemmShared &sh) {
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     int64_t m = t < P.E ? P.split[t] : 0;
     const bool neg = m < 0 || m > P.M;
@@ -142,7 +145,7 @@ struct Tile {
 };
 
 // Tile number i of kRows rows, searching from group g on (tile numbers only grow).
-template <int kRows> __device__ __forceinline__ Tile tile_at(const GemmParams &P, const Shared &sh, int64_t i, int g) {
+template <int kRows> __device__ __forceinline__ Tile tile_at(const GemmParams &P, const GemmShared &sh, int64_t i, int g) {
     const int q = static_cast<int>(i / P.n_tiles);
     while (q >= sh.tile0[g + 1]) ++g;
     Tile t;
@@ -209,12 +212,11 @@ template <bool NV, int BN, bool kPair> struct Stages {
 // tensor memory, then `steps` steps of 32 bytes of k.  The scale columns are the
 // stage's own, so the barrier that frees the stage frees them too.
 template <bool NV, int BN, bool kPair>
-__device__ __forceinline__ void multiply_stage(const Stages<NV, BN, kPair> &st, int s, uint32_t tmem, uint32_t d, int steps,
-                                               bool first) {
+__device__ __forceinline__ void multiply_stage(const Stages<NV, BN, kPair> &st, int s, uint32_t d, int steps, bool first) {
     using C = Cfg<NV, BN, kPair>;
     constexpr uint32_t idesc = tc::idesc_block_scaled(NV, kPair ? 2 * kRowsT : kRowsT, BN);
     constexpr int kSc = C::kSc;
-    const uint32_t sfa = tmem + C::kAcc * BN + s * C::kScCols, sfb = sfa + 4 * kSc;
+    const uint32_t sfa = C::kAcc * BN + s * C::kScCols, sfb = sfa + 4 * kSc;   // the block holds all columns: they start at 0
 #pragma unroll
     for (int j = 0; j < kSc; ++j) {
         tc::copy_scales<kPair>(sfa + 4 * j, tc::desc_scales(st.sa(s) + j * kScaleTile));
@@ -240,7 +242,7 @@ template <int kStages> __device__ __forceinline__ void settle(uint64_t *bars, in
 
 // Barriers, tensor memory, and the block's (the pair's) start and end.
 template <int kStages, bool kPair>
-__device__ __forceinline__ void open_block(Shared &sh, int warp, uint32_t full_count, uint32_t cols) {
+__device__ __forceinline__ void open_block(Barriers &sh, int warp, uint32_t full_count, uint32_t cols) {
     if (threadIdx.x == 0) {
         sh.dead = 0;
         for (int s = 0; s < kStages; ++s) {
@@ -260,7 +262,7 @@ __device__ __forceinline__ void open_block(Shared &sh, int warp, uint32_t full_c
     tc::fence_after();
 }
 
-template <bool kPair> __device__ __forceinline__ void close_block(Shared &sh, int warp, uint32_t cols) {
+template <bool kPair> __device__ __forceinline__ void close_block(Barriers &sh, int warp, uint32_t cols) {
     __syncwarp();
     tc::fence_before();
     if (kPair) tc::cluster_sync();   // neither block leaves while the other may read its memory or signal it
@@ -334,12 +336,96 @@ template <typename T> __device__ __forceinline__ void zeros(T *o, int half, int6
         store_some(o + c, zero, cols - c < kPer ? static_cast<int>(cols - c) : kPer, align);
 }
 
+// The products of one output tile, `len` bytes of k, by the (converged) issuing warp.  n: tiles so far of this unit;
+// it: stages so far.  False: a wait ran out.
+template <bool NV, int BN, bool kPair>
+__device__ __forceinline__ bool multiply_tile(Barriers &sh, const Stages<NV, BN, kPair> &st, int n, int &it, int len) {
+    using C = Cfg<NV, BN, kPair>;
+    volatile uint32_t *dead = &sh.dead;
+    const int a = n % C::kAcc, kt = (len + kStageK - 1) / kStageK;
+    if (n >= C::kAcc && !tc::bar_wait_warp(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) return false;
+    tc::fence_after();
+    for (int k = 0; k < kt; ++k, ++it) {
+        const int s = it % C::kStages;
+        if (!tc::bar_wait_warp(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) return false;
+        tc::fence_after();
+        if (tc::elect()) {
+            // the last stage holds only what is left of k
+            multiply_stage(st, s, a * BN, min(4, (len - k * kStageK + 31) / 32), k == 0);
+            tc::commit<kPair>(tc::smem_u32(&sh.empty[s]));
+            if (k == kt - 1) tc::commit<kPair>(tc::smem_u32(&sh.acc_full[a]));
+        }
+        __syncwarp();
+    }
+    return true;
+}
+
+// One stage's copies by the (converged) loading warp: 128 rows of A's codes, the
+// block's rows of B's, and the scale tiles, at (x, row) and (0, tile) of their
+// maps.  False: a wait ran out.
+struct StageAt {
+    const CUtensorMap *a, *b, *sa, *sb;
+    int x, a_row, b_row, a_tile, b_tile, b_tile_step;   // step: between the 128-row groups of B's scales
+};
+template <bool NV, int BN, bool kPair>
+__device__ __forceinline__ bool load_stage(Barriers &sh, const Stages<NV, BN, kPair> &st, int half, int it, const StageAt &w) {
+    using C = Cfg<NV, BN, kPair>;
+    const int s = it % C::kStages;
+    if (it >= C::kStages && !tc::bar_wait_warp(tc::smem_u32(&sh.empty[s]), (it / C::kStages - 1) & 1, &sh.dead)) return false;
+    const uint32_t own = tc::smem_u32(&sh.full[s]), bar = kPair ? tc::map_to(own, 0) : own;
+    auto load = [&](uint32_t dst, const CUtensorMap *tm, int x, int y) {
+        if (kPair) tc::load_2d_pair(dst, tm, x, y, bar);
+        else tc::load_2d(dst, tm, x, y, bar);
+    };
+    if (tc::elect()) {
+        if (half == 0) tc::bar_expect(own, kPair ? 2 * C::kStageBytes : C::kStageBytes);
+        load(st.a(s), w.a, w.x, w.a_row);
+        load(st.b(s), w.b, w.x, w.b_row);
+        load(st.sa(s), w.sa, 0, w.a_tile);
+#pragma unroll
+        for (int b = 0; b < C::kGroupsB; ++b) load(st.sb(s) + b * C::kSc * kScaleTile, w.sb, 0, w.b_tile + b * w.b_tile_step);
+    }
+    __syncwarp();
+    return true;
+}
+
+// After a wait of the loading warp ran out.
+template <int kStages> __device__ __forceinline__ void settle_loads(Barriers &sh, int half, int it) {
+    if (half == 0) settle<kStages>(sh.full, it);
+    else tc::pause(1000000);   // these copies count on the other block's barriers: time for them to land
+}
+
+// The finished accumulator of the unit's n-th tile to memory by one draining warp.  False: a wait ran out.
+template <bool NV, int BN, bool kPair, typename T>
+__device__ __forceinline__ bool drain_tile(Barriers &sh, int n, int warp, int lane, const float *amax_a, const float *amax_b,
+                                           int g, T *o, int64_t cols, bool on, int align, bool add) {
+    using C = Cfg<NV, BN, kPair>;
+    const int a = n % C::kAcc, q = warp & 3, h = (warp - 4) >> 2;
+    float ua = 1.0f, ub = 1.0f;
+    if (NV) {
+        ua = __fdiv_rn(1.0f, tensor_scale(amax_a[g]));
+        ub = __fdiv_rn(1.0f, tensor_scale(amax_b[g]));
+    }
+    if (!tc::bar_wait_warp(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, &sh.dead)) return false;
+    tc::fence_after();
+    drain<BN / 2, NV>(a * BN + h * (BN / 2) + (static_cast<uint32_t>(32 * q) << 16), ua, ub, o, cols, on, align, add, [&] {
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            const uint32_t bar = tc::smem_u32(&sh.acc_empty[a]);
+            if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
+            else tc::bar_arrive(bar);
+        }
+    });
+    return true;
+}
+
 template <bool NV, int BN, bool kPair, typename T>
 __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constant__ GemmParams P) {
     using C = Cfg<NV, BN, kPair>;
     extern __shared__ uint8_t dyn[];
-    __shared__ Shared sh;
-    constexpr int kRows = kPair ? 2 * kRowsT : kRowsT, kSc = C::kSc;
+    __shared__ GemmShared sh;
+    constexpr int kRows = kPair ? 2 * kRowsT : kRowsT;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     scan_split<kRows>(P, sh);
     const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x, units = kPair ? gridDim.x >> 1 : gridDim.x;
@@ -353,8 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
     if (unit >= total) return;
     const Stages<NV, BN, kPair> st(dyn);
     open_block<C::kStages, kPair>(sh, warp, 1, C::kCols);
-    constexpr uint32_t tmem = 0;   // the block holds all columns
-    volatile uint32_t *dead = &sh.dead;
 
     if (warp == 0) {
         if (tc::elect()) {
@@ -366,98 +450,41 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
         for (int64_t i = unit; i < used && ok; i += units) {
             const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
-            const int row = uniform(static_cast<int>(t.row)) + half * kRowsT;
-            const int a_tile = uniform((sh.scale0[g] + t.mt * (kRows / 128) + half) * P.scale_cols);
-            const int b_row = uniform(static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN)) + half * C::kRowsB;
-            const int b_tile = uniform((g * P.b_scale_rows + t.nt * C::kGroupsB) * P.scale_cols);
-            for (int k = 0; k < P.kt; ++k, ++it) {
-                const int s = it % C::kStages;
-                if (it >= C::kStages && !tc::bar_wait_warp(tc::smem_u32(&sh.empty[s]), (it / C::kStages - 1) & 1, dead)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t own = tc::smem_u32(&sh.full[s]), bar = kPair ? tc::map_to(own, 0) : own;
-                auto load = [&](uint32_t dst, const CUtensorMap *tm, int x, int y) {
-                    if (kPair) tc::load_2d_pair(dst, tm, x, y, bar);
-                    else tc::load_2d(dst, tm, x, y, bar);
-                };
-                if (tc::elect()) {
-                    if (half == 0) tc::bar_expect(own, kPair ? 2 * C::kStageBytes : C::kStageBytes);
-                    load(st.a(s), &P.tm_a, k * kStageK, row);
-                    load(st.b(s), &P.tm_b, k * kStageK, b_row);
-                    load(st.sa(s), &P.tm_sa, 0, a_tile + k * kSc);
-#pragma unroll
-                    for (int b = 0; b < C::kGroupsB; ++b)
-                        load(st.sb(s) + b * kSc * kScaleTile, &P.tm_sb, 0, b_tile + b * P.scale_cols + k * kSc);
-                }
-                __syncwarp();
+            StageAt w{&P.tm_a, &P.tm_b, &P.tm_sa, &P.tm_sb, 0};
+            w.a_row = uniform(static_cast<int>(t.row)) + half * kRowsT;
+            w.a_tile = uniform((sh.scale0[g] + t.mt * (kRows / 128) + half) * P.scale_cols);
+            w.b_row = uniform(static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN)) + half * C::kRowsB;
+            w.b_tile = uniform((g * P.b_scale_rows + t.nt * C::kGroupsB) * P.scale_cols);
+            w.b_tile_step = P.scale_cols;
+            for (int k = 0; k < P.kt && ok; ++k) {
+                ok = load_stage(sh, st, half, it, w);
+                it += ok;
+                w.x += kStageK, w.a_tile += C::kSc, w.b_tile += C::kSc;
             }
         }
-        if (!ok) {
-            if (half == 0) settle<C::kStages>(sh.full, it);
-            else tc::pause(1000000);   // its copies count on the other block's barriers: time for them to land
-        }
+        if (!ok) settle_loads<C::kStages>(sh, half, it);
     } else if (warp == 1 && half == 0) {
         const int mine = unit < used ? uniform(static_cast<int>((used - unit + units - 1) / units)) : 0;
         int it = 0;
         bool ok = true;
-        for (int n = 0; n < mine && ok; ++n) {
-            const int a = n % C::kAcc;
-            if (n >= C::kAcc && !tc::bar_wait_warp(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) break;
-            tc::fence_after();
-            for (int k = 0; k < P.kt; ++k, ++it) {
-                const int s = it % C::kStages;
-                if (!tc::bar_wait_warp(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) {
-                    ok = false;
-                    break;
-                }
-                tc::fence_after();
-                if (tc::elect()) {
-                    // the last stage holds only what is left of k
-                    multiply_stage(st, s, tmem, tmem + a * BN, min(4, (P.k_bytes - k * kStageK) / 32), k == 0);
-                    tc::commit<kPair>(tc::smem_u32(&sh.empty[s]));
-                    if (k == P.kt - 1) tc::commit<kPair>(tc::smem_u32(&sh.acc_full[a]));
-                }
-                __syncwarp();
-            }
-        }
-        if (!ok || *dead) settle<C::kStages>(sh.empty, it);
+        for (int n = 0; n < mine && ok; ++n) ok = multiply_tile(sh, st, n, it, P.k_bytes);
+        if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, it);
     } else if (warp >= 4) {
         const int q = warp & 3, h = (warp - 4) >> 2;   // lanes 32 q .., column half h
         constexpr int kHalf = BN / 2;
         T *out = static_cast<T *>(P.out);
-        const int align = row_align(out, P.N);
+        const int align = row_align(out, P.N), r = half * kRowsT + 32 * q + lane;
         int g = 0, n = 0;
         for (int64_t i = unit; i < total; i += units) {
             const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
-            const int r = half * kRowsT + 32 * q + lane;
-            const int64_t c0 = static_cast<int64_t>(t.nt) * BN + h * kHalf;
+            const int64_t c0 = static_cast<int64_t>(t.nt) * BN + h * kHalf, cols = P.N - c0;
             T *o = out + (t.row + r) * P.N + c0;
-            const int64_t cols = P.N - c0;   // columns from c0 on
             if (g == P.E) {
                 if (r < t.rows) zeros(o, kHalf, cols, align);
-                continue;
+            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, g, o, cols, r < t.rows, align, false)) {
+                break;
             }
-            const int a = n % C::kAcc;
-            float ua = 1.0f, ub = 1.0f;
-            if (NV) {
-                ua = __fdiv_rn(1.0f, tensor_scale(P.amax_a[g]));
-                ub = __fdiv_rn(1.0f, tensor_scale(P.amax_b[g]));
-            }
-            if (!tc::bar_wait_warp(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, dead)) break;
-            ++n;
-            tc::fence_after();
-            drain<kHalf, NV>(tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16), ua, ub, o, cols, r < t.rows,
-                             align, false, [&] {
-                                 tc::fence_before();
-                                 __syncwarp();
-                                 if (lane == 0) {
-                                     const uint32_t bar = tc::smem_u32(&sh.acc_empty[a]);
-                                     if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
-                                     else tc::bar_arrive(bar);
-                                 }
-                             });
         }
     }
     close_block<kPair>(sh, warp, C::kCols);
@@ -467,141 +494,145 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
 //
 //   dw_e[n, k] = u_e sum_r A[r, n] B[r, k] over the rows r of expert e,
 // from columnwise copies: per expert [N, Mp_e] and [K, Mp_e], Mp_e the rows padded
-// to whole scale blocks, so that the sum runs along the contiguous axis again.
-// An expert's pitch is Mp_e codes: a multiple of 8 bytes only (NVFP4), which TMA
-// does not take, so three warps bring the stages in with 16- or 8-byte
-// asynchronous copies, zeros past the matrices.  Scales past Mp_e are padding that
-// nobody wrote: they are masked to zero, since a zero code times a NaN scale would
-// still be NaN.
+// to whole scale blocks, so that the sum runs along the contiguous axis again and
+// the tiles are those of the grouped product with N and K as the free sides.
+//
+// Every expert's matrices have an origin and a pitch of their own that only the
+// device knows, so a kernel before the products writes each expert's tensor maps.
+// TMA takes pitches of multiples of 16 bytes; an NVFP4 expert has Mp_e / 2, a
+// multiple of 8, so that kernel also copies the experts with an odd number of
+// 8-byte groups to rows 8 bytes longer.  (Bringing such rows in with loads instead
+// ran at 20 to 26 bytes a cycle and SM from L2, any width and number of warps,
+// against 65 to 76 by TMA: 577 us where the products of 65536 x 2048 x 2048 take
+// a fifth.)  Last, scales past Mp_e are padding that nobody wrote, and a zero code
+// times a NaN scale is NaN: where a product step of 64 rows is cut short, the
+// scale tiles of that last stage are copied with zeros there.
 
 struct WgradParams {
+    CUtensorMap tm_sa, tm_sb, tm_ta, tm_tb;   // scale tiles; the tail copies of the last stages'
     const uint8_t *a, *b, *sa, *sb;
     const int64_t *split;
     const float *amax_a, *amax_b;
     void *out;
+    CUtensorMap *maps;                 // [2][E]: A's and B's codes of each expert
+    uint8_t *tail_a, *tail_b;          // [E][row tiles][4] scale tiles
+    uint8_t *pack_a, *pack_b;          // copies of the experts with odd pitches
     int64_t M;
     int N, K, E;
-    int n_tiles, k_tiles;              // tiles along N (128) and K (BN)
+    int n_tiles, k_tiles;              // tiles along N and K
     int64_t a_bytes, b_bytes, sa_bytes, sb_bytes;
     int accumulate;
 };
 
-constexpr int kLoadWarps = 3;        // warps 0, 2 and 3; warp 1 multiplies, warps 4-11 drain
-constexpr int kLoaders = 32 * kLoadWarps;
-
-struct WgradShared : Shared {
+struct Pads {
     int64_t pad0[kMaxE + 1];    // padded rows before each expert
     int wide0[kMaxE + 1];       // scale tiles along the rows before each expert
+    int64_t rows[kMaxE];
+    int64_t scan[kMaxE / 32][3];
+    uint32_t bad;
+};
+struct WgradShared : Barriers {
+    Pads pads;
     int order[kMaxE];           // experts by descending size
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-// Writes to shared memory so far become visible to the tensor core's reads.
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
-
-// 128 rows of a matrix [n, pitch bytes] from row r0 on, as one loader thread sees
-// them.  A warp's copy takes 4 rows in chunks of 16 bytes, or 2 in chunks of 8
-// where the pitch is no multiple of 16; the warps take every kLoadWarps-th such
-// group.  Chunk c of row r lies at c ^ (r mod 8) of the swizzled stage.
-struct CodeLoad {
-    const uint8_t *p;   // the thread's chunk of its first row, at k = 0
-    int64_t step;       // bytes from a row of the thread to its next
-    int row, rows;      // its first row within the 128, and how many rows the matrix has from r0 on
-    int c;              // its chunk
-    bool wide;          // chunks of 16 bytes
-    __device__ CodeLoad(const uint8_t *m, int64_t pitch, int n, int r0, int warp, int lane) {
-        wide = pitch % 16 == 0;
-        c = wide ? lane & 7 : lane & 15;
-        row = wide ? 4 * warp + (lane >> 3) : 2 * warp + (lane >> 4);
-        rows = n - r0;
-        step = (wide ? 4 : 2) * kLoadWarps * pitch;
-        p = m + static_cast<int64_t>(r0 + row) * pitch + c * (wide ? 16 : 8);
-    }
-    // 128 bytes of k from k0 on (pitch: the matrix' bytes of k), zeros past the matrix.
-    __device__ __forceinline__ void operator()(uint32_t stage, int64_t k0, int64_t pitch) const {
-        const uint8_t *src = p + k0;
-        if (wide) {
-            const int left = k0 + 16 * c < pitch ? rows : 0;
-#pragma unroll
-            for (int j = 0; j < (32 + kLoadWarps - 1) / kLoadWarps; ++j) {
-                const int r = row + 4 * kLoadWarps * j;
-                if (r < kRowsT) cp_async16(stage + r * 128 + ((c ^ (r & 7)) << 4), r < left ? src : p, r < left ? 16 : 0);
-                src += step;
-            }
-        } else {
-            const int left = k0 + 8 * c < pitch ? rows : 0;
-#pragma unroll
-            for (int j = 0; j < (64 + kLoadWarps - 1) / kLoadWarps; ++j) {
-                const int r = row + 2 * kLoadWarps * j;
-                if (r < kRowsT)
-                    cp_async8(stage + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1), r < left ? src : p, r < left ? 8 : 0);
-                src += step;
-            }
-        }
-    }
-};
-
-// The scale tiles of a stage for 128-row groups g0 .. of a matrix: tiles
-// [c0, c0 + kSc) of each row of tiles, entries from `cols` on as zero.
-template <int kSc, int kGroups>
-__device__ __forceinline__ void load_scales(uint32_t dst, uint8_t *dst_p, const uint8_t *m, int groups, int g0, int wide,
-                                            int c0, int cols, int thread) {
-    constexpr int kChunks = kSc * (kScaleTile / 16);   // of a group: contiguous in memory and in the stage
-#pragma unroll
-    for (int i = thread; i < kGroups * kChunks; i += kLoaders) {
-        const int g = i / kChunks, j = (i % kChunks) >> 5;
-        const bool in = g0 + g < groups && c0 + j < wide;
-        const uint8_t *src = in ? m + (static_cast<int64_t>(g0 + g) * wide + c0) * kScaleTile + (i % kChunks) * 16 : m;
-        const int left = cols - 4 * (c0 + j);
-        if (!in || left >= 4) {
-            cp_async16(dst + i * 16, src, in ? 16 : 0);
-        } else {
-            const uint32_t keep = left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-            uint4 v = *reinterpret_cast<const uint4 *>(src);
-            v.x &= keep, v.y &= keep, v.z &= keep, v.w &= keep;
-            *reinterpret_cast<uint4 *>(dst_p + i * 16) = v;
-        }
-    }
-}
-
-// Padded rows and scale tiles before each expert, and the experts by descending size.  Every thread of the block.
-template <int kBlock> __device__ void scan_wgrad(const WgradParams &P, WgradShared &sh, bool nv) {
+// Padded rows and scale tiles before each expert.  Every thread of a block of at least 256.  A negative size, a sum
+// above M or more than the buffers hold sets bad.
+template <int kBlock, bool NV> __device__ void scan_pads(const WgradParams &P, Pads &d) {
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     int64_t m = t < P.E ? P.split[t] : 0;
     const bool neg = m < 0 || m > P.M;
     if (neg) m = 0;
-    if (t < P.E) sh.row0[t] = m;   // sizes, until sorted
+    if (t < P.E) d.rows[t] = m;
     int64_t rows = m, pad = (m + kBlock - 1) / kBlock * kBlock, wide = (m + 4 * kBlock - 1) / (4 * kBlock);
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, d), q = __shfl_up_sync(0xFFFFFFFFu, pad, d),
-                      u = __shfl_up_sync(0xFFFFFFFFu, wide, d);
-        if (lane >= d) rows += r, pad += q, wide += u;
+    for (int s = 1; s < 32; s <<= 1) {
+        const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, s), q = __shfl_up_sync(0xFFFFFFFFu, pad, s),
+                      u = __shfl_up_sync(0xFFFFFFFFu, wide, s);
+        if (lane >= s) rows += r, pad += q, wide += u;
     }
-    if (w < kThreads / 32 && lane == 31) sh.scan[w][0] = rows, sh.scan[w][1] = pad, sh.scan[w][2] = wide;
+    if (w < kMaxE / 32 && lane == 31) d.scan[w][0] = rows, d.scan[w][1] = pad, d.scan[w][2] = wide;
     const bool any_neg = __syncthreads_or(neg);
-    for (int k = 0; k < w && k < kThreads / 32; ++k) rows += sh.scan[k][0], pad += sh.scan[k][1], wide += sh.scan[k][2];
+    for (int k = 0; k < w && k < kMaxE / 32; ++k) rows += d.scan[k][0], pad += d.scan[k][1], wide += d.scan[k][2];
     if (t < P.E) {
-        sh.pad0[t + 1] = pad;
-        sh.wide0[t + 1] = static_cast<int>(wide);
-        int rank = 0;
-        for (int k = 0; k < P.E; ++k) rank += sh.row0[k] > m || (sh.row0[k] == m && k < t);
-        sh.order[rank] = t;
+        d.pad0[t + 1] = pad;
+        d.wide0[t + 1] = static_cast<int>(wide);
     }
-    if (t == 0) sh.pad0[0] = 0, sh.wide0[0] = 0;
+    if (t == 0) d.pad0[0] = 0, d.wide0[0] = 0;
     if (t == P.E - 1) {
-        const int64_t codes = nv ? pad / 2 : pad, tiles = wide * kScaleTile;
-        sh.bad = any_neg || rows > P.M || codes * P.N > P.a_bytes || codes * P.K > P.b_bytes ||
-                 tiles * ((P.N + 127) / 128) > P.sa_bytes || tiles * ((P.K + 127) / 128) > P.sb_bytes;
+        const int64_t codes = NV ? pad / 2 : pad, tiles = wide * kScaleTile;
+        d.bad = any_neg || rows > P.M || codes * P.N > P.a_bytes || codes * P.K > P.b_bytes ||
+                tiles * ((P.N + 127) / 128) > P.sa_bytes || tiles * ((P.K + 127) / 128) > P.sb_bytes;
     }
     __syncthreads();
+}
+
+// Where an expert's odd-pitch copy starts, in units of rows of the matrix: 8 bytes more than its codes.
+__device__ __forceinline__ int64_t pack_at(const Pads &d, int e) { return d.pad0[e] / 2 + 8 * static_cast<int64_t>(e); }
+
+constexpr int kPrepThreads = 256;
+
+template <bool NV>
+__global__ void __launch_bounds__(kPrepThreads) wgrad_prepare(const __grid_constant__ WgradParams P,
+                                                              const __grid_constant__ CUtensorMap plain) {
+    __shared__ Pads d;
+    __shared__ __align__(128) CUtensorMap map;
+    constexpr int kBlock = NV ? 16 : 32;
+    scan_pads<kBlock, NV>(P, d);
+    if (d.bad) return;   // the products report it
+    for (int i = blockIdx.x; i < 2 * P.E; i += gridDim.x) {
+        const int e = i < P.E ? i : i - P.E;
+        const int64_t mp = d.pad0[e + 1] - d.pad0[e], pitch = NV ? mp / 2 : mp, first = NV ? d.pad0[e] / 2 : d.pad0[e];
+        const int rows = i < P.E ? P.N : P.K;
+        if (threadIdx.x == 0 && mp > 0) {
+            const bool odd = pitch % 16 != 0;
+            const uint8_t *at = odd ? (i < P.E ? P.pack_a : P.pack_b) + pack_at(d, e) * rows
+                                    : (i < P.E ? P.a : P.b) + first * rows;
+            map = plain;
+            tc::edit_map(&map, at, static_cast<uint32_t>(pitch), static_cast<uint32_t>(rows), odd ? pitch + 8 : pitch);
+            P.maps[i] = map;
+        }
+        __syncthreads();
+    }
+    if (!NV) return;
+    const int warp = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kPrepThreads / 32);
+    const int lane = threadIdx.x & 31, both = P.N + P.K;
+    // rows of odd pitch: 8-byte halves (a row starts on 8 bytes), 16-byte stores
+    for (int64_t i = warp; i < static_cast<int64_t>(P.E) * both; i += warps) {
+        const int e = static_cast<int>(i / both), j = static_cast<int>(i - static_cast<int64_t>(e) * both);
+        const int64_t pitch = (d.pad0[e + 1] - d.pad0[e]) / 2;
+        if (pitch % 16 == 0) continue;
+        const bool is_a = j < P.N;
+        const int r = is_a ? j : j - P.N, rows = is_a ? P.N : P.K;
+        const uint8_t *src = (is_a ? P.a : P.b) + d.pad0[e] / 2 * rows + r * pitch;
+        uint8_t *dst = (is_a ? P.pack_a : P.pack_b) + pack_at(d, e) * rows + r * (pitch + 8);
+        for (int64_t c = 16 * lane; c < pitch; c += 512) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src + c));
+            const uint2 y = c + 8 < pitch ? __ldg(reinterpret_cast<const uint2 *>(src + c + 8)) : make_uint2(0, 0);
+            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(x.x, x.y, y.x, y.y);
+        }
+    }
+    // the last stages' scale tiles, zeros past the expert's scales
+    const int n128 = (P.N + 127) / 128, groups = n128 + (P.K + 127) / 128;
+    for (int64_t i = warp; i < static_cast<int64_t>(P.E) * groups * 4; i += warps) {
+        const int j = static_cast<int>(i & 3), x = static_cast<int>(i >> 2), e = x / groups, g = x - e * groups;
+        const int64_t mp = d.pad0[e + 1] - d.pad0[e];
+        const int cols = static_cast<int>(mp / 16);
+        if (cols % 4 == 0) continue;
+        const int wide = d.wide0[e + 1] - d.wide0[e], tile = (cols - 1) / 16 * 4 + j;
+        const bool is_a = g < n128;
+        const int row = is_a ? g : g - n128, tiles = is_a ? n128 : groups - n128;
+        uint8_t *dst = (is_a ? P.tail_a : P.tail_b) + ((static_cast<int64_t>(e) * tiles + row) * 4 + j) * kScaleTile + 16 * lane;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (tile < wide) {
+            v = *reinterpret_cast<const uint4 *>((is_a ? P.sa : P.sb) + (static_cast<int64_t>(d.wide0[e]) * tiles +
+                                                 static_cast<int64_t>(row) * wide + tile) * kScaleTile + 16 * lane);
+            const int left = cols - 4 * tile;
+            const uint32_t keep = left >= 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1u;
+            v.x &= keep, v.y &= keep, v.z &= keep, v.w &= keep;
+        }
+        *reinterpret_cast<uint4 *>(dst) = v;
+    }
 }
 
 // A tile of the weight gradients.  A unit's r-th tile goes back and forth over the
@@ -609,21 +640,23 @@ template <int kBlock> __device__ void scan_wgrad(const WgradParams &P, WgradShar
 // long and short sums even out.
 struct WTile {
     int e, nt, kt;
-    int64_t pad0, rows;   // padded rows before the expert, and its own
+    int64_t rows;   // padded rows of the expert
 };
-__device__ __forceinline__ int64_t wgrad_tile(int64_t r, int unit, int units) {
-    return r * units + ((r & 1) ? units - 1 - unit : unit);
-}
-__device__ __forceinline__ WTile wtile_at(const WgradParams &P, const WgradShared &sh, int64_t i) {
-    const int per = P.n_tiles * P.k_tiles;
-    WTile t;
-    const int x = static_cast<int>(i / per), j = static_cast<int>(i - static_cast<int64_t>(x) * per);
-    t.e = sh.order[x];
-    t.nt = j / P.k_tiles;
-    t.kt = j - t.nt * P.k_tiles;
-    t.pad0 = sh.pad0[t.e];
-    t.rows = sh.pad0[t.e + 1] - t.pad0;
-    return t;
+// The unit's next tile from round r on: false when there is none.
+__device__ __forceinline__ bool next_wtile(const WgradParams &P, const WgradShared &sh, int64_t &r, int unit, int units,
+                                           int64_t total, WTile &t) {
+    for (;; ++r) {
+        if (r * units >= total) return false;
+        const int64_t i = r * units + ((r & 1) ? units - 1 - unit : unit);
+        if (i >= total) continue;
+        ++r;
+        const int per = P.n_tiles * P.k_tiles, x = static_cast<int>(i / per), j = static_cast<int>(i - static_cast<int64_t>(x) * per);
+        t.e = sh.order[x];
+        t.nt = j / P.k_tiles;
+        t.kt = j - t.nt * P.k_tiles;
+        t.rows = sh.pads.pad0[t.e + 1] - sh.pads.pad0[t.e];
+        return true;
+    }
 }
 
 template <bool NV, int BN, bool kPair, typename T>
@@ -631,146 +664,86 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
     using C = Cfg<NV, BN, kPair>;
     extern __shared__ uint8_t dyn[];
     __shared__ WgradShared sh;
+    constexpr int kBlock = NV ? 16 : 32, kRows = kPair ? 2 * kRowsT : kRowsT;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    constexpr int kBlock = NV ? 16 : 32, kSc = C::kSc, kDepth = C::kStages - 2;
-    constexpr int kRows = kPair ? 2 * kRowsT : kRowsT;
-    scan_wgrad<kBlock>(P, sh, NV);
-    if (sh.bad) {
+    scan_pads<kBlock, NV>(P, sh.pads);
+    if (sh.pads.bad) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_status, ERR_SPLIT);
         return;
+    }
+    if (static_cast<int>(threadIdx.x) < P.E) {
+        const int64_t m = sh.pads.rows[threadIdx.x];
+        int rank = 0;
+        for (int k = 0; k < P.E; ++k) rank += sh.pads.rows[k] > m || (sh.pads.rows[k] == m && k < static_cast<int>(threadIdx.x));
+        sh.order[rank] = threadIdx.x;
     }
     const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x, units = kPair ? gridDim.x >> 1 : gridDim.x;
     const int half = kPair ? blockIdx.x & 1 : 0;
     const int64_t total = static_cast<int64_t>(P.E) * P.n_tiles * P.k_tiles;
     const Stages<NV, BN, kPair> st(dyn);
-    open_block<C::kStages, kPair>(sh, warp, (kPair ? 2 : 1) * kLoadWarps, C::kCols);
-    constexpr uint32_t tmem = 0;   // the block holds all columns
-    volatile uint32_t *dead = &sh.dead;
+    open_block<C::kStages, kPair>(sh, warp, 1, C::kCols);
+    WTile t;
+    int64_t r = 0;
 
-    if (warp == 1) {
-        if (half == 0) {
-            int it = 0, n = 0;
-            bool ok = true;
-            for (int64_t r = 0;; ++r) {
-                const int64_t i = wgrad_tile(r, unit, units);
-                if (i >= total) {
-                    if (r * units >= total) break;
-                    continue;
-                }
-                const WTile t = wtile_at(P, sh, i);
-                const int len = uniform(static_cast<int>(NV ? t.rows / 2 : t.rows));
-                if (len == 0) continue;
-                const int a = n % C::kAcc, kt = (len + kStageK - 1) / kStageK;
-                if (n >= C::kAcc && !tc::bar_wait_warp(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) break;
-                ++n;
-                tc::fence_after();
-                for (int k = 0; k < kt; ++k, ++it) {
-                    const int s = it % C::kStages;
-                    if (!tc::bar_wait_warp(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after();
-                    if (tc::elect()) {
-                        multiply_stage(st, s, tmem, tmem + a * BN, min(4, (len - k * kStageK + 31) / 32), k == 0);
-                        tc::commit<kPair>(tc::smem_u32(&sh.empty[s]));
-                        if (k == kt - 1) tc::commit<kPair>(tc::smem_u32(&sh.acc_full[a]));
-                    }
-                    __syncwarp();
-                }
-                if (!ok) break;
-            }
-            if (!ok || *dead) settle<C::kStages>(sh.empty, it);
-        }
-    } else if (warp < 4) {
-        const int loader = warp == 0 ? 0 : warp - 1, thread = 32 * loader + lane;
+    if (warp == 0) {
         const int n128 = (P.N + 127) / 128, k128 = (P.K + 127) / 128;
-        auto arrive = [&](int j) {   // stage j's copies of this warp have landed
-            fence_async();
-            __syncwarp();
-            if (lane == 0) {
-                const uint32_t bar = tc::smem_u32(&sh.full[j % C::kStages]);
-                if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
-                else tc::bar_arrive(bar);
-            }
-        };
-        int it = 0;
+        int it = 0, last = -1;
         bool ok = true;
-        for (int64_t r = 0; ok; ++r) {
-            const int64_t i = wgrad_tile(r, unit, units);
-            if (i >= total) {
-                if (r * units >= total) break;
-                continue;
+        while (ok && next_wtile(P, sh, r, unit, units, total, t)) {
+            const int e = uniform(t.e), nt = uniform(t.nt), kt = uniform(t.kt);
+            const int len = uniform(static_cast<int>(NV ? t.rows / 2 : t.rows)), cols = uniform(static_cast<int>(t.rows / kBlock));
+            const int wide0 = uniform(sh.pads.wide0[e]), wide = uniform(sh.pads.wide0[e + 1]) - wide0;
+            if (len == 0) continue;
+            StageAt w{P.maps + e, P.maps + P.E + e, &P.tm_sa, &P.tm_sb, 0};
+            if (e != last) {   // maps written by the kernel before
+                tc::acquire_map(w.a);
+                tc::acquire_map(w.b);
+                last = e;
             }
-            const WTile t = wtile_at(P, sh, i);
-            const int64_t pitch = NV ? t.rows / 2 : t.rows, first = NV ? t.pad0 / 2 : t.pad0;
-            const int wide = sh.wide0[t.e + 1] - sh.wide0[t.e], cols = static_cast<int>(t.rows / kBlock);
-            const uint8_t *sa = P.sa + static_cast<int64_t>(sh.wide0[t.e]) * n128 * kScaleTile;
-            const uint8_t *sb = P.sb + static_cast<int64_t>(sh.wide0[t.e]) * k128 * kScaleTile;
-            const CodeLoad load_a(P.a + first * P.N, pitch, P.N, t.nt * kRows + half * kRowsT, loader, lane);
-            const CodeLoad load_b(P.b + first * P.K, pitch, P.K, t.kt * BN + half * C::kRowsB, loader, lane);
-            for (int64_t k = 0; k < pitch; k += kStageK, ++it) {
-                const int s = it % C::kStages;
-                if (it >= C::kStages && !tc::bar_wait_warp(tc::smem_u32(&sh.empty[s]), (it / C::kStages - 1) & 1, dead)) {
-                    ok = false;
-                    break;
+            const int a_group = nt * (kRows / 128) + half, b_group = kt * C::kGroupsB;
+            w.a_row = nt * kRows + half * kRowsT;
+            w.b_row = kt * BN + half * C::kRowsB;
+            w.a_tile = wide0 * n128 + a_group * wide;
+            w.b_tile = wide0 * k128 + b_group * wide;
+            w.b_tile_step = wide;
+            const int stages = (len + kStageK - 1) / kStageK;
+            for (int k = 0; k < stages && ok; ++k) {
+                if (NV && k == stages - 1 && cols % 4 != 0) {
+                    w.sa = &P.tm_ta, w.sb = &P.tm_tb;
+                    w.a_tile = (e * n128 + a_group) * 4;
+                    w.b_tile = (e * k128 + b_group) * 4;
+                    w.b_tile_step = 4;
                 }
-                load_a(st.a(s), k, pitch);
-                load_b(st.b(s), k, pitch);
-                const int c0 = static_cast<int>(k / kStageK) * kSc;
-                uint8_t *p = dyn + (st.sa(s) - tc::smem_u32(dyn));
-                load_scales<kSc, 1>(st.sa(s), p, sa, n128, t.nt * (kRows / 128) + half, wide, c0, cols, thread);
-                load_scales<kSc, C::kGroupsB>(st.sb(s), p + C::kBytesSA, sb, k128, t.kt * C::kGroupsB, wide, c0, cols, thread);
-                cp_commit();
-                if (it >= kDepth) {   // the stage kDepth before this one has arrived
-                    cp_wait<kDepth>();
-                    arrive(it - kDepth);
-                }
+                ok = load_stage(sh, st, half, it, w);
+                it += ok;
+                w.x += kStageK, w.a_tile += C::kSc, w.b_tile += C::kSc;
             }
         }
-        cp_wait<0>();
-        if (ok)
-            for (int j = it < kDepth ? 0 : it - kDepth; j < it; ++j) arrive(j);
-    } else {
+        if (!ok) settle_loads<C::kStages>(sh, half, it);
+    } else if (warp == 1 && half == 0) {
+        int it = 0, n = 0;
+        bool ok = true;
+        while (ok && next_wtile(P, sh, r, unit, units, total, t)) {
+            const int len = uniform(static_cast<int>(NV ? t.rows / 2 : t.rows));
+            if (len > 0) ok = multiply_tile(sh, st, n++, it, len);
+        }
+        if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, it);
+    } else if (warp >= 4) {
         const int q = warp & 3, h = (warp - 4) >> 2;
         constexpr int kHalf = BN / 2;
         T *out = static_cast<T *>(P.out);
         const int align = row_align(out, P.K);
         const bool add = P.accumulate != 0;
         int n = 0;
-        for (int64_t r = 0;; ++r) {
-            const int64_t i = wgrad_tile(r, unit, units);
-            if (i >= total) {
-                if (r * units >= total) break;
-                continue;
-            }
-            const WTile t = wtile_at(P, sh, i);
+        while (next_wtile(P, sh, r, unit, units, total, t)) {
             const int row = t.nt * kRows + half * kRowsT + 32 * q + lane, c0 = t.kt * BN + h * kHalf;
             T *o = out + (static_cast<int64_t>(t.e) * P.N + row) * P.K + c0;
-            const int64_t left = static_cast<int64_t>(P.K) - c0;
+            const int64_t cols = static_cast<int64_t>(P.K) - c0;
             if (t.rows == 0) {   // no rows: a zero gradient
-                if (row < P.N && !add) zeros(o, kHalf, left, align);
-                continue;
+                if (row < P.N && !add) zeros(o, kHalf, cols, align);
+            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, t.e, o, cols, row < P.N, align, add)) {
+                break;
             }
-            const int a = n % C::kAcc;
-            float ua = 1.0f, ub = 1.0f;
-            if (NV) {
-                ua = __fdiv_rn(1.0f, tensor_scale(P.amax_a[t.e]));
-                ub = __fdiv_rn(1.0f, tensor_scale(P.amax_b[t.e]));
-            }
-            if (!tc::bar_wait_warp(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, dead)) break;
-            ++n;
-            tc::fence_after();
-            drain<kHalf, NV>(tmem + a * BN + h * kHalf + (static_cast<uint32_t>(32 * q) << 16), ua, ub, o, left, row < P.N,
-                             align, add, [&] {
-                                 tc::fence_before();
-                                 __syncwarp();
-                                 if (lane == 0) {
-                                     const uint32_t bar = tc::smem_u32(&sh.acc_empty[a]);
-                                     if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
-                                     else tc::bar_arrive(bar);
-                                 }
-                             });
         }
     }
     close_block<kPair>(sh, warp, C::kCols);
@@ -870,6 +843,26 @@ template <bool NV, int BN, bool kPair, typename T> gsa_status launch_wgrad(const
                                       static_cast<int64_t>(P.E) * P.n_tiles * P.k_tiles, s, pairs, once);
 }
 
+// Workspace of the weight gradient (byte offsets; the maps come first).
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 256 * 64, kMaxSide = int64_t(1) << 30;
+struct WgradSpace {
+    size_t tail_a = 0, tail_b = 0, pack_a = 0, pack_b = 0, bytes = 0;
+    WgradSpace(int64_t E, int64_t M, int64_t N, int64_t K, bool nv) {
+        auto take = [&](int64_t n) {
+            const size_t at = bytes;
+            bytes += (static_cast<size_t>(n) + 255) / 256 * 256;
+            return at;
+        };
+        take(2 * E * static_cast<int64_t>(sizeof(CUtensorMap)));
+        if (!nv) return;
+        tail_a = take(E * ((N + 127) / 128) * 4 * kScaleTile);
+        tail_b = take(E * ((K + 127) / 128) * 4 * kScaleTile);
+        const int64_t used = E < M ? E : M, cols = (M + 15 * used) / 2 + 8 * E;   // bytes of all padded rows, and 8 an expert
+        pack_a = take(cols * N);
+        pack_b = take(cols * K);
+    }
+};
+
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
@@ -938,25 +931,45 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     return st;
 }
 
+size_t gsa_grouped_gemm_wgrad_workspace_size(int64_t E, int64_t M, int64_t N, int64_t K, int32_t recipe_kind) {
+    if (E <= 0 || E > kMaxE || M < 0 || N <= 0 || K <= 0 || M >= kMaxRows || N >= kMaxSide || K >= kMaxSide ||
+        (recipe_kind != GSA_MXFP8 && recipe_kind != GSA_NVFP4))
+        return 0;
+    return WgradSpace(E, M, N, K, recipe_kind == GSA_NVFP4).bytes;
+}
+
 gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int64_t *split_sizes_dev, int64_t E,
-                                  int64_t M, int64_t N, int64_t K, int32_t recipe_kind, void *out, int32_t out_dtype,
-                                  int32_t accumulate, gsa_stream_t stream) {
+                                  int64_t M, int64_t N, int64_t K, int32_t recipe_kind, void *dw, int32_t out_dtype,
+                                  int32_t accumulate, void *workspace, size_t workspace_bytes, gsa_stream_t stream) {
     if (!a || !b || E <= 0 || M < 0 || N <= 0 || K <= 0) return GSA_ERR_INVALID_ARG;
     if (recipe_kind != GSA_MXFP8 && recipe_kind != GSA_NVFP4) return GSA_ERR_INVALID_ARG;
     if (out_dtype != GSA_BF16 && out_dtype != GSA_FP32) return GSA_ERR_INVALID_ARG;
     const bool nv = recipe_kind == GSA_NVFP4;
-    if (E > kMaxE || M >= (int64_t(1) << 31) - 256 * 64 || N >= (int64_t(1) << 30) || K >= (int64_t(1) << 30))
-        return GSA_ERR_UNSUPPORTED;
-    if (!a->data || !a->scale || !b->data || !b->scale || !split_sizes_dev || !out) return GSA_ERR_INVALID_ARG;
+    if (E > kMaxE || M >= kMaxRows || N >= kMaxSide || K >= kMaxSide) return GSA_ERR_UNSUPPORTED;
+    // TMA: an expert's NVFP4 codes start on 16 bytes (8 bytes of codes a block times the width)
+    if (nv && (N % 2 != 0 || K % 2 != 0)) return GSA_ERR_UNSUPPORTED;
+    if (!a->data || !a->scale || !b->data || !b->scale || !split_sizes_dev || !dw) return GSA_ERR_INVALID_ARG;
     if (nv && (!a->amax || !b->amax)) return GSA_ERR_INVALID_ARG;
     if (!aligned(a->data, 16) || !aligned(a->scale, 16) || !aligned(b->data, 16) || !aligned(b->scale, 16) ||
-        !aligned(out, 16) || !aligned(split_sizes_dev, 8) || !aligned(a->amax, 4) || !aligned(b->amax, 4))
+        !aligned(dw, 16) || !aligned(split_sizes_dev, 8) || !aligned(a->amax, 4) || !aligned(b->amax, 4) ||
+        !aligned(workspace, 256))
         return GSA_ERR_ALIGNMENT;
-    // an expert's codes start on 16 bytes: its padded rows (a multiple of the block) times the width
-    if ((nv ? N * 8 : N * 32) % 16 != 0 || (nv ? K * 8 : K * 32) % 16 != 0) return GSA_ERR_UNSUPPORTED;
+    const WgradSpace ws(E, M, N, K, nv);
+    if (!workspace || workspace_bytes < ws.bytes) return GSA_ERR_WORKSPACE;
 
+    const int64_t n128 = (N + 127) / 128, k128 = (K + 127) / 128;
+    const int64_t a_tiles = a->scale_bytes / kScaleTile, b_tiles = b->scale_bytes / kScaleTile;
+    if (a_tiles >= (int64_t(1) << 31) || b_tiles >= (int64_t(1) << 31)) return GSA_ERR_UNSUPPORTED;
+    if (a_tiles < 1 || b_tiles < 1) return GSA_ERR_INVALID_ARG;
+    uint8_t *w = static_cast<uint8_t *>(workspace);
     WgradParams P;
     std::memset(&P, 0, sizeof(P));
+    const int sc = nv ? 4 : 1;
+    CUtensorMap plain;   // the experts' maps but for origin, extents and pitch
+    if (!map_codes(&plain, w, 4096, 4096, 128) || !map_scales(&P.tm_sa, a->scale, a_tiles, sc) ||
+        !map_scales(&P.tm_sb, b->scale, b_tiles, sc) ||
+        (nv && (!map_scales(&P.tm_ta, w + ws.tail_a, E * n128 * 4, 4) || !map_scales(&P.tm_tb, w + ws.tail_b, E * k128 * 4, 4))))
+        return GSA_ERR_CUDA;
     P.a = static_cast<const uint8_t *>(a->data);
     P.b = static_cast<const uint8_t *>(b->data);
     P.sa = static_cast<const uint8_t *>(a->scale);
@@ -964,7 +977,12 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     P.split = split_sizes_dev;
     P.amax_a = a->amax;
     P.amax_b = b->amax;
-    P.out = out;
+    P.out = dw;
+    P.maps = reinterpret_cast<CUtensorMap *>(w);
+    P.tail_a = w + ws.tail_a;
+    P.tail_b = w + ws.tail_b;
+    P.pack_a = w + ws.pack_a;
+    P.pack_b = w + ws.pack_b;
     P.M = M;
     P.N = static_cast<int>(N);
     P.K = static_cast<int>(K);
@@ -980,6 +998,11 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     P.accumulate = accumulate != 0;
     if (static_cast<int64_t>(P.n_tiles) * P.k_tiles >= (int64_t(1) << 31)) return GSA_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int sms = sm_count();
+    if (!sms) return GSA_ERR_CUDA;
+    if (nv) wgrad_prepare<true><<<4 * sms, kPrepThreads, 0, s>>>(P, plain);
+    else wgrad_prepare<false><<<static_cast<unsigned>(2 * E < sms ? 2 * E : sms), kPrepThreads, 0, s>>>(P, plain);
+    if (cudaGetLastError() != cudaSuccess) return GSA_ERR_CUDA;
     gsa_status st;
     auto typed = [&](auto fmt, auto type) {
         return pair ? launch_wgrad<decltype(fmt)::value, 256, true, decltype(type)>(P, s)
@@ -987,7 +1010,7 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     };
     auto sized = [&](auto fmt) { return out_dtype == GSA_BF16 ? typed(fmt, __nv_bfloat16()) : typed(fmt, float()); };
     st = nv ? sized(std::true_type()) : sized(std::false_type());
-    if (st == GSA_OK) gsa::set_last_launches(1);
+    if (st == GSA_OK) gsa::set_last_launches(2);
     return st;
 }
 

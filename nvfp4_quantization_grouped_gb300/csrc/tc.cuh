@@ -114,6 +114,20 @@ __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap *tm
         : "memory");
 }
 
+// Origin, extents (bytes of a row, rows) and pitch of a tensor map of bytes in shared memory.
+__device__ __forceinline__ void edit_map(CUtensorMap *map, const void *p, uint32_t bytes, uint32_t rows, uint64_t pitch) {
+    const uint32_t m = smem_u32(map);
+    asm volatile("tensormap.replace.tile.global_address.shared::cta.b1024.b64 [%0], %1;" ::"r"(m), "l"(p) : "memory");
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 0, %1;" ::"r"(m), "r"(bytes) : "memory");
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(m), "r"(rows) : "memory");
+    asm volatile("tensormap.replace.tile.global_stride.shared::cta.b1024.b64 [%0], 0, %1;" ::"r"(m), "l"(pitch) : "memory");
+}
+
+// Before the first copy through a map that another kernel wrote to global memory.
+__device__ __forceinline__ void acquire_map(const CUtensorMap *map) {
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
+}
+
 // ----------------------------------------------------------------- cluster
 
 __device__ __forceinline__ uint32_t cluster_rank() {

@@ -29,7 +29,8 @@ EXPORTED = ["gsa_layout", "gsa_workspace_size", "grouped_scaled_act_fwd", "group
             "grouped_scaled_act_fwd_graph_safe", "grouped_scaled_act_bwd_graph_safe", "gsa_selftest_wait_timeout",
             "gsa_layout_ex", "gsa_layout_bound_ex", "gsa_moe_sort_workspace_size", "gsa_moe_sort", "gsa_moe_permute",
             "gsa_moe_permute_bwd", "gsa_moe_unpermute", "gsa_moe_unpermute_bwd", "gsa_grouped_gemm",
-            "gsa_grouped_gemm_wgrad", "gsa_grouped_gemm_status"]
+            "gsa_grouped_gemm_wgrad", "gsa_grouped_gemm_wgrad_workspace_size",
+            "gsa_grouped_gemm_status"]
 
 
 class GsaError(RuntimeError):
@@ -133,7 +134,10 @@ def load():
                                        ctypes.c_int32, _P, ctypes.c_int32, _P]
         L.gsa_grouped_gemm_wgrad.restype = ctypes.c_int
         L.gsa_grouped_gemm_wgrad.argtypes = [ctypes.POINTER(QIn), ctypes.POINTER(QIn), _P, _I64, _I64, _I64, _I64,
-                                             ctypes.c_int32, _P, ctypes.c_int32, ctypes.c_int32, _P]
+                                             ctypes.c_int32, _P, ctypes.c_int32, ctypes.c_int32, _P,
+                                             ctypes.c_size_t, _P]
+        L.gsa_grouped_gemm_wgrad_workspace_size.restype = ctypes.c_size_t
+        L.gsa_grouped_gemm_wgrad_workspace_size.argtypes = [_I64, _I64, _I64, _I64, ctypes.c_int32]
         L.gsa_grouped_gemm_status.restype = ctypes.c_int
         L.gsa_grouped_gemm_status.argtypes = [_P]
         L.gsa_version.restype = ctypes.c_int32
@@ -727,8 +731,12 @@ def grouped_gemm_wgrad(a: dict, b: dict, split, m: int, n: int, k: int, recipe_k
     qb, tb = _operand(b, "col", recipe_kind, experts, "grouped_gemm_wgrad: b", dev)
     on = _On(stream, dev, split, *ta, *tb)
     out = on.out(out, "grouped_gemm_wgrad: out", (experts, n, k), out_dtype, dev)
-    _check(load().gsa_grouped_gemm_wgrad(qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, out.data_ptr(),
-                                         code, int(bool(accumulate)), on.ptr), "gsa_grouped_gemm_wgrad")
+    L = load()
+    nbytes = L.gsa_grouped_gemm_wgrad_workspace_size(experts, m, n, k, recipe_kind)
+    ws = on.empty((max(256, nbytes),), torch.uint8, dev)
+    _check(L.gsa_grouped_gemm_wgrad(qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, out.data_ptr(), code,
+                                    int(bool(accumulate)), ws.data_ptr(), ws.numel(), on.ptr),
+           "gsa_grouped_gemm_wgrad")
     return out
 
 
