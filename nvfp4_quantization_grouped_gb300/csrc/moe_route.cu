@@ -39,113 +39,122 @@ __device__ __forceinline__ int bin_of(const void *idx, int idx_bytes, int64_t s,
     return e >= 0 && e < E ? static_cast<int>(e) : E;
 }
 
-// Slots [s0, s1) of one warp, 32 at a time in slot order, each counted into the
-// warp's own bins; lanes of the same bin find one another with match_any, so no
-// atomics are needed and the order is the slots' own.  kRank: the bins hold the
-// next free row of each expert and every slot's row is written.
-template <bool kRank>
-__device__ __forceinline__ void walk(const void *idx, int idx_bytes, int64_t s0, int64_t s1, int E, int *bins,
-                                     int32_t *row_of_slot) {
-    const int lane = threadIdx.x & 31;
-    for (int64_t s = s0; s < s1; s += 32) {
-        const bool in = s + lane < s1;
-        const int b = in ? bin_of(idx, idx_bytes, s + lane, E) : kMaxBins;
-        const uint32_t same = __match_any_sync(0xFFFFFFFFu, b);
-        const int before = __popc(same & ((1u << lane) - 1u));
-        const int base = in ? bins[b] : 0;
-        __syncwarp();
-        if (in && before == 0) bins[b] = base + __popc(same);
-        __syncwarp();
-        if (kRank && in) {
-            const int32_t row = base + before;
-            row_of_slot[s + lane] = b == E ? ~row : row;
-        }
-    }
-}
-
-// Block b counts slots [b * seg, (b + 1) * seg) into counts[b][bin].
+// Counts of segment blockIdx.x: counts[bin][blockIdx.x], rows of `pitch` entries.
 __global__ void __launch_bounds__(1024) sort_count(const void *idx, int idx_bytes, int64_t n, int E, int64_t seg,
-                                                   int *counts) {
-    __shared__ int bins[kSortWarps][kMaxBins];
-    const int w = threadIdx.x >> 5, nw = blockDim.x >> 5, nb = E + 1;
-    for (int i = threadIdx.x; i < nw * kMaxBins; i += blockDim.x) (&bins[0][0])[i] = 0;
+                                                   int pitch, int *counts) {
+    __shared__ int bins[kMaxBins];
+    for (int b = threadIdx.x; b <= E; b += blockDim.x) bins[b] = 0;
     __syncthreads();
-    const int64_t b0 = blockIdx.x * seg, b1 = min(n, b0 + seg);
-    const int64_t per = ((seg + nw - 1) / nw + 31) / 32 * 32;
-    walk<false>(idx, idx_bytes, b0 + w * per, min(b1, b0 + (w + 1) * per), E, bins[w], nullptr);
+    const int64_t s1 = min(n, (blockIdx.x + 1) * seg);
+    for (int64_t s = blockIdx.x * seg + threadIdx.x; s < s1; s += blockDim.x) atomicAdd(&bins[bin_of(idx, idx_bytes, s, E)], 1);
     __syncthreads();
-    for (int b = threadIdx.x; b < nb; b += blockDim.x) {
-        int c = 0;
-        for (int k = 0; k < nw; ++k) c += bins[k][b];
-        counts[static_cast<int64_t>(blockIdx.x) * nb + b] = c;
-    }
+    for (int b = threadIdx.x; b <= E; b += blockDim.x) counts[static_cast<int64_t>(b) * pitch + blockIdx.x] = bins[b];
 }
 
-// Ranks of the slots of one block.  counts: the blocks' counts (sort_count), or
-// nullptr when one block holds every slot and counts them itself.
-__global__ void __launch_bounds__(1024) sort_rank(const void *idx, int idx_bytes, int64_t n, int E, int64_t seg,
+// Rows of the slots of segment blockIdx.x.  counts: the segments' counts, or
+// nullptr when one block holds every slot (at most one chunk) and counts itself.
+// A warp takes 32 * kSteps consecutive slots of a chunk and ranks them among
+// themselves, 32 at a time in slot order: lanes of the same expert find one another
+// with match_any, so no atomics are needed and the order is the slots' own.
+template <int kSteps>
+__global__ void __launch_bounds__(1024) sort_rank(const void *idx, int idx_bytes, int64_t n, int E, int64_t seg, int pitch,
                                                   const int *counts, int32_t *row_of_slot, int64_t *split) {
-    __shared__ int bins[kSortWarps][kMaxBins];
-    __shared__ int before[kMaxBins];   // rows of this expert in earlier blocks
-    __shared__ int total[kMaxBins];    // rows of this expert, then the expert's first row
+    __shared__ int bins[kSortWarps][kMaxBins];   // a warp's slots of each expert, then the expert's next row for the warp
+    __shared__ int next[kMaxBins];               // next row of each expert for this block
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5, nb = E + 1;
-    for (int i = threadIdx.x; i < nw * kMaxBins; i += blockDim.x) (&bins[0][0])[i] = 0;
-    __syncthreads();
-    const int64_t b0 = blockIdx.x * seg, b1 = min(n, b0 + seg);
-    const int64_t per = ((seg + nw - 1) / nw + 31) / 32 * 32;
-    const int64_t w0 = b0 + w * per, w1 = min(b1, b0 + (w + 1) * per);
-    walk<false>(idx, idx_bytes, w0, w1, E, bins[w], nullptr);
-    __syncthreads();
-    for (int b = threadIdx.x; b < nb; b += blockDim.x) {
-        int mine = 0, first = 0, all = 0;
-        if (counts) {
-#pragma unroll 8
-            for (int k = 0; k < static_cast<int>(gridDim.x); ++k) {
-                const int c = counts[static_cast<int64_t>(k) * nb + b];
+    const int64_t s1 = min(n, (blockIdx.x + 1) * seg), chunk = static_cast<int64_t>(nw) * 32 * kSteps;
+    if (counts) {
+        // rows of each expert in all segments (into bins[0]) and in those before this one
+        for (int b = w; b < nb; b += nw) {
+            int all = 0, first = 0;
+            for (int k = lane; k < static_cast<int>(gridDim.x); k += 32) {
+                const int c = counts[static_cast<int64_t>(b) * pitch + k];
                 all += c;
-                if (k < static_cast<int>(blockIdx.x)) first += c;
+                first += k < static_cast<int>(blockIdx.x) ? c : 0;
             }
+            all = __reduce_add_sync(0xFFFFFFFFu, all);
+            first = __reduce_add_sync(0xFFFFFFFFu, first);
+            if (lane == 0) bins[0][b] = all, next[b] = first;
         }
-        for (int k = 0; k < nw; ++k) {   // warp prefixes within the block
-            const int c = bins[k][b];
-            bins[k][b] = mine;
-            mine += c;
-        }
-        before[b] = first;
-        total[b] = counts ? all : mine;
+        __syncthreads();
     }
-    __syncthreads();
-    if (w == 0) {   // exclusive scan over the bins; block 0 also writes the split
+    // expert b's first row, added to next[b]; the first block writes the split
+    auto first_rows = [&](const int *total) {
         int carry = 0;
         for (int b = lane; b < (nb + 31) / 32 * 32; b += 32) {
             const int c = b < nb ? total[b] : 0;
             int inc = c;
+#pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
                 if (lane >= d) inc += v;
             }
             if (b < nb) {
-                total[b] = carry + inc - c + before[b];
+                next[b] += carry + inc - c;
                 if (blockIdx.x == 0) split[b] = c;
             }
             carry += __shfl_sync(0xFFFFFFFFu, inc, 31);
         }
+    };
+    if (counts) {
+        if (w == 0) first_rows(bins[0]);
+        __syncthreads();
     }
-    __syncthreads();
-    for (int b = lane; b < nb; b += 32) bins[w][b] += total[b];
-    __syncwarp();
-    walk<true>(idx, idx_bytes, w0, w1, E, bins[w], row_of_slot);
+    for (int64_t c0 = blockIdx.x * seg; c0 == blockIdx.x * seg || c0 < s1; c0 += chunk) {
+        for (int b = lane; b < nb; b += 32) bins[w][b] = 0;
+        __syncwarp();
+        int bin[kSteps], rank[kSteps];
+        const int64_t w0 = c0 + static_cast<int64_t>(w) * 32 * kSteps + lane;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) bin[i] = w0 + 32 * i < s1 ? bin_of(idx, idx_bytes, w0 + 32 * i, E) : kMaxBins;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, bin[i]);
+            const int before = __popc(same & ((1u << lane) - 1u)), base = bin[i] < kMaxBins ? bins[w][bin[i]] : 0;
+            __syncwarp();
+            if (bin[i] < kMaxBins && before == 0) bins[w][bin[i]] = base + __popc(same);
+            __syncwarp();
+            rank[i] = base + before;
+        }
+        __syncthreads();
+        for (int b = threadIdx.x; b < nb; b += blockDim.x) {
+            int row = counts ? next[b] : 0;
+            for (int k = 0; k < nw; ++k) {
+                const int c = bins[k][b];
+                bins[k][b] = row;
+                row += c;
+            }
+            next[b] = row;
+        }
+        __syncthreads();
+        if (!counts) {   // the only chunk: its counts are the split
+            __shared__ int total[kMaxBins];
+            for (int b = threadIdx.x; b < nb; b += blockDim.x) total[b] = next[b], next[b] = 0;
+            __syncthreads();
+            if (w == 0) first_rows(total);
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            if (bin[i] < kMaxBins) {
+                const int32_t row = bins[w][bin[i]] + rank[i] + (counts ? 0 : next[bin[i]]);
+                row_of_slot[w0 + 32 * i] = bin[i] == E ? ~row : row;
+            }
+        }
+        __syncthreads();
+    }
 }
 
-// One block up to kOneBlockSlots slots, else blocks of `seg` slots and two launches.
+// One block up to kOneBlockSlots slots (a chunk of 32 warps x 8 steps), else segments
+// of 2048 slots (32 warps x 2 steps) and two launches; at most 512 segments, since
+// every block reads the counts of all.  One block against segments, sort alone:
 constexpr int64_t kOneBlockSlots = 8192;
-constexpr int kSegThreads = 256;
 
 int64_t sort_segment(int64_t n) {
     if (n <= kOneBlockSlots) return n;
-    const int64_t seg = (n + 255) / 256;   // at most 256 blocks: each reads every block's counts
-    return seg < 2048 ? 2048 : (seg + 31) / 32 * 32;
+    return ((n + 511) / 512 + 2047) / 2048 * 2048;
 }
+int sort_pitch(int64_t n) { return static_cast<int>((n + sort_segment(n) - 1) / sort_segment(n) + 31) / 32 * 32; }
 
 // ------------------------------------------------------- rows and vectors
 
@@ -208,10 +217,11 @@ __global__ void __launch_bounds__(256) permute_fwd(const uint8_t *x, const float
 }
 
 // out[t] = sum_j w_j rows[row(t, j)] (w = 1 without weights): unpermute, and the
-// gradient of permute (which also brings the probabilities' gradients back).
-// kGroup rows are loaded before the first is used.
-template <typename T, int V>
-__global__ void __launch_bounds__(256) combine(const uint8_t *ys, const float *weights, const int32_t *row_of_slot,
+// gradient of permute (which also brings the probabilities' gradients back).  A
+// thread loads kU columns of G rows before it uses the first: enough bytes in
+// flight for memory, whatever topk.
+template <typename T, int V, int G, int kU>
+__global__ void __launch_bounds__(256, 4) combine(const uint8_t *ys, const float *weights, const int32_t *row_of_slot,
                                                int tokens, int topk, int64_t nv, uint8_t *out, const float *dps,
                                                float *dprobs) {
     constexpr int N = V / sizeof(T);
@@ -225,36 +235,43 @@ __global__ void __launch_bounds__(256) combine(const uint8_t *ys, const float *w
             dprobs[static_cast<int64_t>(t) * topk + j] = r < 0 ? 0.0f : dps[r];
         }
     }
-    for (int64_t c = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; c < nv;
-         c += static_cast<int64_t>(gridDim.y) * blockDim.x) {
-        float acc[N];
+    const int64_t step = blockDim.x;
+    for (int64_t c = blockIdx.y * step * kU + threadIdx.x; c < nv; c += gridDim.y * step * kU) {
+        float acc[kU][N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-        for (int j0 = 0; j0 < topk; j0 += kGroup) {
-            Vec<T, V> v[kGroup];
-            float w[kGroup];
-            bool live[kGroup];
+        for (int u = 0; u < kU; ++u)
 #pragma unroll
-            for (int g = 0; g < kGroup; ++g) {
+            for (int i = 0; i < N; ++i) acc[u][i] = 0.0f;
+        for (int j0 = 0; j0 < topk; j0 += G) {
+            Vec<T, V> v[G][kU];
+            uint32_t live = 0;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
                 const int r = j0 + g < topk ? live_row(rows[j0 + g], n) : -1;
-                live[g] = r >= 0;
-                if (live[g]) {
-                    v[g].raw = load_once<V>(ys + (r * nv + c) * V);
-                    w[g] = weights ? weights[static_cast<int64_t>(t) * topk + j0 + g] : 1.0f;
-                }
+                if (r < 0) continue;
+                live |= 1u << g;
+                const uint8_t *p = ys + (r * nv + c) * V;
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    if (u == 0 || c + u * step < nv) v[g][u].raw = load_once<V>(p + u * step * V);
             }
 #pragma unroll
-            for (int g = 0; g < kGroup; ++g) {
-                if (live[g]) {
+            for (int g = 0; g < G; ++g)
+                if (live >> g & 1) {
+                    const float w = weights ? weights[static_cast<int64_t>(t) * topk + j0 + g] : 1.0f;
 #pragma unroll
-                    for (int i = 0; i < N; ++i) acc[i] = __fmaf_rn(w[g], as_f32(v[g].e[i]), acc[i]);
+                    for (int u = 0; u < kU; ++u)
+#pragma unroll
+                        for (int i = 0; i < N; ++i) acc[u][i] = __fmaf_rn(w, as_f32(v[g][u].e[i]), acc[u][i]);
                 }
-            }
         }
-        Vec<T, V> o;
 #pragma unroll
-        for (int i = 0; i < N; ++i) put(o.e[i], acc[i]);
-        *reinterpret_cast<typename Raw<V>::T *>(out + (t * nv + c) * V) = o.raw;
+        for (int u = 0; u < kU; ++u) {
+            Vec<T, V> o;
+#pragma unroll
+            for (int i = 0; i < N; ++i) put(o.e[i], acc[u][i]);
+            if (c + u * step < nv) *reinterpret_cast<typename Raw<V>::T *>(out + (t * nv + c + u * step) * V) = o.raw;
+        }
     }
 }
 
@@ -264,7 +281,7 @@ __global__ void __launch_bounds__(256) combine(const uint8_t *ys, const float *w
 // distances and over the token's warps in order: the sum's order depends on
 // wpt alone, which the launch takes from tokens and width.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) unpermute_bwd(const uint8_t *dout, const uint8_t *ys, const float *weights,
+__global__ void __launch_bounds__(256, 3) unpermute_bwd(const uint8_t *dout, const uint8_t *ys, const float *weights,
                                                      const int32_t *row_of_slot, int tokens, int topk, int64_t nv,
                                                      uint8_t *dys, float *dw) {
     constexpr int N = V / sizeof(T);
@@ -356,13 +373,13 @@ struct Shape {
     dim3 grid, block;
 };
 
-// Columns x tokens of a block of 256 threads; columns beyond one pass of a block
-// go to further blocks along grid.y.
-Shape row_shape(int64_t tokens, int64_t nv) {
+// Columns x tokens of a block of 256 threads, `unroll` columns a thread; columns
+// beyond one pass of a block go to further blocks along grid.y.
+Shape row_shape(int64_t tokens, int64_t nv, int unroll = 1) {
     int x = 1;
-    while (x < 256 && x < nv) x *= 2;
+    while (x < 256 && x * unroll < nv) x *= 2;
     const int y = 256 / x;
-    int64_t gy = (nv + x - 1) / x;
+    int64_t gy = (nv + static_cast<int64_t>(x) * unroll - 1) / (static_cast<int64_t>(x) * unroll);
     if (gy > 64) gy = 64;
     return {dim3(static_cast<unsigned>((tokens + y - 1) / y), static_cast<unsigned>(gy)), dim3(x, y)};
 }
@@ -404,11 +421,16 @@ gsa_status run_combine(const void *ys, const float *weights, const int32_t *row_
                        gsa_stream_t stream) {
     const int v = vector_bytes(hidden * elem_bytes(dtype));
     const int64_t nv = hidden * elem_bytes(dtype) / v;
-    const Shape s = row_shape(tokens, nv);
     with_type(dtype, v, [&](auto tag, auto width) {
-        combine<decltype(tag), decltype(width)::value><<<s.grid, s.block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-            static_cast<const uint8_t *>(ys), weights, row_of_slot, static_cast<int>(tokens), static_cast<int>(topk),
-            nv, static_cast<uint8_t *>(out), dps, dprobs);
+        auto go = [&](auto group, auto unroll) {
+            const Shape s = row_shape(tokens, nv, decltype(unroll)::value);
+            combine<decltype(tag), decltype(width)::value, decltype(group)::value, decltype(unroll)::value>
+                <<<s.grid, s.block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+                    static_cast<const uint8_t *>(ys), weights, row_of_slot, static_cast<int>(tokens),
+                    static_cast<int>(topk), nv, static_cast<uint8_t *>(out), dps, dprobs);
+        };
+        if (topk > 4) go(std::integral_constant<int, 8>(), std::integral_constant<int, decltype(width)::value == 16 ? 1 : 2>());
+        else go(std::integral_constant<int, 4>(), std::integral_constant<int, decltype(width)::value == 16 ? 2 : 4>());
     });
     return done(1);
 }
@@ -422,9 +444,7 @@ size_t gsa_moe_sort_workspace_size(int64_t tokens, int64_t topk, int64_t experts
         topk >= (int64_t(1) << 31) || tokens * topk >= (int64_t(1) << 31))
         return 0;
     const int64_t n = tokens * topk;
-    if (n <= kOneBlockSlots) return 0;
-    const int64_t seg = sort_segment(n);
-    return static_cast<size_t>((n + seg - 1) / seg * (experts + 1) * 4 + 15) / 16 * 16;
+    return n <= kOneBlockSlots ? 0 : static_cast<size_t>(sort_pitch(n)) * (experts + 1) * 4;
 }
 
 gsa_status gsa_moe_sort(const void *expert_idx, int32_t idx_bytes, int64_t tokens, int64_t topk, int64_t experts,
@@ -442,16 +462,17 @@ gsa_status gsa_moe_sort(const void *expert_idx, int32_t idx_bytes, int64_t token
     const int E = static_cast<int>(experts);
     const int64_t seg = sort_segment(n);
     if (n <= kOneBlockSlots) {
-        int threads = 32;
-        while (threads < 1024 && threads * 4 < n) threads *= 2;
-        sort_rank<<<1, threads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, nullptr, row_of_slot, split_sizes);
+        int threads = 128;   // also what the bins take
+        while (threads < 1024 && threads < n) threads *= 2;
+        if (n <= threads) sort_rank<1><<<1, threads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, 0, nullptr, row_of_slot, split_sizes);
+        else sort_rank<8><<<1, threads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, 0, nullptr, row_of_slot, split_sizes);
         return done(1);
     }
     if (!workspace || workspace_bytes < gsa_moe_sort_workspace_size(tokens, topk, experts)) return GSA_ERR_WORKSPACE;
     const unsigned blocks = static_cast<unsigned>((n + seg - 1) / seg);
-    sort_count<<<blocks, kSegThreads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, static_cast<int *>(workspace));
-    sort_rank<<<blocks, kSegThreads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, static_cast<const int *>(workspace),
-                                             row_of_slot, split_sizes);
+    int *counts = static_cast<int *>(workspace);
+    sort_count<<<blocks, 1024, 0, s>>>(expert_idx, idx_bytes, n, E, seg, sort_pitch(n), counts);
+    sort_rank<2><<<blocks, 1024, 0, s>>>(expert_idx, idx_bytes, n, E, seg, sort_pitch(n), counts, row_of_slot, split_sizes);
     return done(2);
 }
 

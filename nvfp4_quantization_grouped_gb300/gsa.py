@@ -499,147 +499,163 @@ def bwd_graph_safe(dy, x, probs, split_dev, act: str, recipe_kind: int, rht: boo
 
 
 # ------------------------------------------- tokens into expert order and back
+#
+# Small calls are bound by the host, so the checks below are written to be cheap:
+# no imports, no objects and no repeated lookups on the path of a good call.
 
 BF16, FP16, FP32 = 0, 1, 2
-_DTYPE_NAMES = {"torch.bfloat16": BF16, "torch.float16": FP16, "torch.float32": FP32}
+_torch = None
 _DTYPES: dict = {}
 
 
-def _dtype_code(t, what):
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        code = _DTYPE_NAMES.get(str(t.dtype))
-        if code is None:
-            raise GsaError(1, f"{what}: element type {t.dtype} (bfloat16, float16 or float32 expected)")
-        _DTYPES[t.dtype] = code
-    return code
+def _setup():
+    """The torch module, imported on the first call, and the element type codes."""
+    global _torch
+    import torch
+    _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+    load()
+    _torch = torch
+    return torch
 
 
-def _require(t, what, shape, dtype, device=None):
-    """A contiguous CUDA tensor of this shape and type (on `device`)."""
-    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous():
-        raise GsaError(1, f"{what}: contiguous CUDA {dtype} {list(shape)} expected, got {t.device} {t.dtype} "
-                          f"{list(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'}")
-    if device is not None and t.device != device:
-        raise GsaError(1, f"{what}: on {t.device}, expected {device}")
+def _refuse(t, what, shape, dtype):
+    raise GsaError(1, f"{what}: contiguous CUDA {dtype} {list(shape)} expected, got {t.device} {t.dtype} "
+                      f"{list(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'}")
 
 
-class _On:
-    """The stream of a call.  With `stream` given, new tensors are allocated for that stream and the inputs are
-    recorded on it, so that the caching allocator keeps both until the stream is done with them."""
+def _require(t, what, shape, dtype):
+    """A contiguous CUDA tensor of this shape and type."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _refuse(t, what, shape, dtype)
 
-    def __init__(self, stream, device, *inputs):
-        import torch
-        if stream is None:
-            self.ctx, self.ptr = None, torch.cuda.current_stream(device).cuda_stream
-        else:
-            self.ctx, self.ptr = torch.cuda.stream(stream), stream.cuda_stream
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(stream)
 
-    def empty(self, shape, dtype, device):
-        import torch
-        if self.ctx is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with self.ctx:
-            return torch.empty(shape, dtype=dtype, device=device)
+def _same_device(what, device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise GsaError(1, f"{what}: tensors on {t.device} and {device}")
 
-    def out(self, given, what, shape, dtype, device):
-        if given is None:
-            return self.empty(shape, dtype, device)
-        _require(given, what, shape, dtype, device)
+
+def _stream_of(stream, device, *inputs):
+    """Handle of `stream`, or of the device's current one.  Inputs of a call on an explicit stream are recorded on
+    it, so that the caching allocator keeps them until the stream is done with them."""
+    if stream is None:
+        return _torch.cuda.current_stream(device).cuda_stream
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _out(given, what, shape, dtype, device, stream):
+    """The caller's output tensor, or a new one that belongs to the call's stream."""
+    if given is not None:
+        _require(given, what, shape, dtype)
+        _same_device(what, device, given)
+        if stream is not None:
+            given.record_stream(stream)
         return given
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=device)
+    with _torch.cuda.stream(stream):
+        return _torch.empty(shape, dtype=dtype, device=device)
 
 
 def moe_sort(expert_idx, experts: int, out: tuple | None = None, stream=None):
     """Sort plan of expert_idx [tokens, topk] (int32 / int64; a value outside [0, experts) drops the slot):
     -> (row_of_slot [tokens, topk] int32, split_sizes [experts + 1] int64), both on the device."""
-    import torch
-    if expert_idx.dim() != 2 or expert_idx.dtype not in (torch.int32, torch.int64):
+    torch = _torch or _setup()
+    dt = expert_idx.dtype
+    if (dt is not torch.int64 and dt is not torch.int32) or expert_idx.dim() != 2:
         raise GsaError(1, "moe_sort: expert_idx must be int32 or int64 [tokens, topk]")
-    _require(expert_idx, "moe_sort: expert_idx", tuple(expert_idx.shape), expert_idx.dtype)
-    L, dev = load(), expert_idx.device
-    tokens, topk = expert_idx.shape
-    on = _On(stream, dev, expert_idx)
+    shape, dev = expert_idx.shape, expert_idx.device
+    _require(expert_idx, "moe_sort: expert_idx", shape, dt)
+    tokens, topk = shape
     row, split = out or (None, None)
-    row = on.out(row, "moe_sort: row_of_slot", (tokens, topk), torch.int32, dev)
-    split = on.out(split, "moe_sort: split_sizes", (max(0, experts) + 1,), torch.int64, dev)
-    nbytes = L.gsa_moe_sort_workspace_size(tokens, topk, experts)
-    ws = on.empty((nbytes,), torch.uint8, dev) if nbytes else None
-    _check(L.gsa_moe_sort(expert_idx.data_ptr(), expert_idx.element_size(), tokens, topk, experts, row.data_ptr(),
-                          split.data_ptr(), ws.data_ptr() if nbytes else None, nbytes, on.ptr), "gsa_moe_sort")
+    row = _out(row, "moe_sort: row_of_slot", shape, torch.int32, dev, stream)
+    split = _out(split, "moe_sort: split_sizes", (max(0, experts) + 1,), torch.int64, dev, stream)
+    nbytes = _lib.gsa_moe_sort_workspace_size(tokens, topk, experts)
+    ws = _out(None, "", (nbytes,), torch.uint8, dev, stream) if nbytes else None
+    st = _lib.gsa_moe_sort(expert_idx.data_ptr(), 8 if dt is torch.int64 else 4, tokens, topk, experts,
+                           row.data_ptr(), split.data_ptr(), ws.data_ptr() if nbytes else None, nbytes,
+                           _stream_of(stream, dev, expert_idx))
+    if st:
+        _check(st, "gsa_moe_sort")
     return row, split
 
 
-def _plan_shape(row_of_slot, what):
-    import torch
-    if row_of_slot.dim() != 2:
-        raise GsaError(1, f"{what}: row_of_slot must be [tokens, topk]")
-    _require(row_of_slot, f"{what}: row_of_slot", tuple(row_of_slot.shape), torch.int32)
-    return row_of_slot.shape
-
-
-def _rows(t, n, what):
-    """(hidden, dtype code) of a [n, hidden] row tensor."""
-    if t.dim() != 2:
-        raise GsaError(1, f"{what} must be [{n}, hidden]")
-    code = _dtype_code(t, what)
-    _require(t, what, (n, t.shape[1]), t.dtype)
-    return t.shape[1], code
+def _plan_and_rows(what, row_of_slot, rows, by_slot):
+    """(tokens, topk, hidden, dtype code, device) of a plan and a [tokens or tokens * topk, hidden] row tensor."""
+    torch = _torch or _setup()
+    if row_of_slot.dim() != 2 or rows.dim() != 2:
+        raise GsaError(1, f"{what}: row_of_slot [tokens, topk] and [rows, hidden] rows expected")
+    tokens, topk = row_of_slot.shape
+    _require(row_of_slot, what + ": row_of_slot", row_of_slot.shape, torch.int32)
+    hidden = rows.shape[1]
+    code = _DTYPES.get(rows.dtype)
+    if code is None:
+        raise GsaError(1, f"{what}: element type {rows.dtype} (bfloat16, float16 or float32 expected)")
+    _require(rows, what + ": rows", (tokens * topk if by_slot else tokens, hidden), rows.dtype)
+    dev = rows.device
+    if row_of_slot.device != dev:
+        _same_device(what, dev, row_of_slot)
+    return tokens, topk, hidden, code, dev
 
 
 def moe_permute(x, row_of_slot, probs=None, out: tuple | None = None, stream=None):
     """Token rows x [tokens, hidden] into expert order: xs [tokens * topk, hidden], and with probs
     [tokens, topk] (FP32) -> (xs, ps [tokens * topk])."""
-    import torch
-    tokens, topk = _plan_shape(row_of_slot, "moe_permute")
-    hidden, code = _rows(x, tokens, "moe_permute: x")
-    dev = x.device
-    on = _On(stream, dev, x, row_of_slot, probs)
+    tokens, topk, hidden, code, dev = _plan_and_rows("moe_permute", row_of_slot, x, False)
     xs, ps = (out if probs is not None else (out, None)) if out is not None else (None, None)
-    xs = on.out(xs, "moe_permute: xs", (tokens * topk, hidden), x.dtype, dev)
+    xs = _out(xs, "moe_permute: xs", (tokens * topk, hidden), x.dtype, dev, stream)
+    pp = po = None
     if probs is not None:
-        _require(probs, "moe_permute: probs", (tokens, topk), torch.float32, dev)
-        ps = on.out(ps, "moe_permute: ps", (tokens * topk,), torch.float32, dev)
-    _check(load().gsa_moe_permute(x.data_ptr(), None if probs is None else probs.data_ptr(), row_of_slot.data_ptr(),
-                                  tokens, topk, hidden, code, xs.data_ptr(), None if ps is None else ps.data_ptr(),
-                                  on.ptr), "gsa_moe_permute")
+        _require(probs, "moe_permute: probs", (tokens, topk), _torch.float32)
+        _same_device("moe_permute", dev, probs)
+        ps = _out(ps, "moe_permute: ps", (tokens * topk,), _torch.float32, dev, stream)
+        pp, po = probs.data_ptr(), ps.data_ptr()
+    st = _lib.gsa_moe_permute(x.data_ptr(), pp, row_of_slot.data_ptr(), tokens, topk, hidden, code, xs.data_ptr(), po,
+                              _stream_of(stream, dev, x, row_of_slot, probs))
+    if st:
+        _check(st, "gsa_moe_permute")
     return xs if probs is None else (xs, ps)
 
 
 def moe_permute_bwd(dxs, row_of_slot, dps=None, out: tuple | None = None, stream=None):
     """Gradient of moe_permute: dx [tokens, hidden], and with dps [tokens * topk] -> (dx, dprobs)."""
-    import torch
-    tokens, topk = _plan_shape(row_of_slot, "moe_permute_bwd")
-    hidden, code = _rows(dxs, tokens * topk, "moe_permute_bwd: dxs")
-    dev = dxs.device
-    on = _On(stream, dev, dxs, row_of_slot, dps)
+    tokens, topk, hidden, code, dev = _plan_and_rows("moe_permute_bwd", row_of_slot, dxs, True)
     dx, dprobs = (out if dps is not None else (out, None)) if out is not None else (None, None)
-    dx = on.out(dx, "moe_permute_bwd: dx", (tokens, hidden), dxs.dtype, dev)
+    dx = _out(dx, "moe_permute_bwd: dx", (tokens, hidden), dxs.dtype, dev, stream)
+    pp = po = None
     if dps is not None:
-        _require(dps, "moe_permute_bwd: dps", (tokens * topk,), torch.float32, dev)
-        dprobs = on.out(dprobs, "moe_permute_bwd: dprobs", (tokens, topk), torch.float32, dev)
-    _check(load().gsa_moe_permute_bwd(dxs.data_ptr(), None if dps is None else dps.data_ptr(), row_of_slot.data_ptr(),
-                                      tokens, topk, hidden, code, dx.data_ptr(),
-                                      None if dprobs is None else dprobs.data_ptr(), on.ptr), "gsa_moe_permute_bwd")
+        _require(dps, "moe_permute_bwd: dps", (tokens * topk,), _torch.float32)
+        _same_device("moe_permute_bwd", dev, dps)
+        dprobs = _out(dprobs, "moe_permute_bwd: dprobs", (tokens, topk), _torch.float32, dev, stream)
+        pp, po = dps.data_ptr(), dprobs.data_ptr()
+    st = _lib.gsa_moe_permute_bwd(dxs.data_ptr(), pp, row_of_slot.data_ptr(), tokens, topk, hidden, code,
+                                  dx.data_ptr(), po, _stream_of(stream, dev, dxs, row_of_slot, dps))
+    if st:
+        _check(st, "gsa_moe_permute_bwd")
     return dx if dps is None else (dx, dprobs)
+
+
+def _weights(what, weights, tokens, topk, dev):
+    if weights is None:
+        return None
+    _require(weights, what + ": weights", (tokens, topk), _torch.float32)
+    _same_device(what, dev, weights)
+    return weights.data_ptr()
 
 
 def moe_unpermute(ys, row_of_slot, weights=None, out=None, stream=None):
     """Expert rows ys [tokens * topk, hidden] back to tokens: out [tokens, hidden], the sum over a token's slots
     weighted by weights [tokens, topk] (FP32; None: 1)."""
-    import torch
-    tokens, topk = _plan_shape(row_of_slot, "moe_unpermute")
-    hidden, code = _rows(ys, tokens * topk, "moe_unpermute: ys")
-    dev = ys.device
-    on = _On(stream, dev, ys, row_of_slot, weights)
-    if weights is not None:
-        _require(weights, "moe_unpermute: weights", (tokens, topk), torch.float32, dev)
-    out = on.out(out, "moe_unpermute: out", (tokens, hidden), ys.dtype, dev)
-    _check(load().gsa_moe_unpermute(ys.data_ptr(), None if weights is None else weights.data_ptr(),
-                                    row_of_slot.data_ptr(), tokens, topk, hidden, code, out.data_ptr(), on.ptr),
-           "gsa_moe_unpermute")
+    tokens, topk, hidden, code, dev = _plan_and_rows("moe_unpermute", row_of_slot, ys, True)
+    wp = _weights("moe_unpermute", weights, tokens, topk, dev)
+    out = _out(out, "moe_unpermute: out", (tokens, hidden), ys.dtype, dev, stream)
+    st = _lib.gsa_moe_unpermute(ys.data_ptr(), wp, row_of_slot.data_ptr(), tokens, topk, hidden, code, out.data_ptr(),
+                                _stream_of(stream, dev, ys, row_of_slot, weights))
+    if st:
+        _check(st, "gsa_moe_unpermute")
     return out
 
 
@@ -647,23 +663,21 @@ def moe_unpermute_bwd(dout, ys, row_of_slot, weights=None, want_dys: bool = True
                       stream=None):
     """Gradient of moe_unpermute for dout [tokens, hidden]: (dys [tokens * topk, hidden], dweights [tokens, topk]
     FP32).  ys = None skips dweights, want_dys = False skips dys (None in its place)."""
-    import torch
-    tokens, topk = _plan_shape(row_of_slot, "moe_unpermute_bwd")
-    hidden, code = _rows(dout, tokens, "moe_unpermute_bwd: dout")
-    dev = dout.device
-    on = _On(stream, dev, dout, ys, row_of_slot, weights)
-    if weights is not None:
-        _require(weights, "moe_unpermute_bwd: weights", (tokens, topk), torch.float32, dev)
+    tokens, topk, hidden, code, dev = _plan_and_rows("moe_unpermute_bwd", row_of_slot, dout, False)
+    wp = _weights("moe_unpermute_bwd", weights, tokens, topk, dev)
     dys, dw = out if out is not None else (None, None)
     if want_dys:
-        dys = on.out(dys, "moe_unpermute_bwd: dys", (tokens * topk, hidden), dout.dtype, dev)
+        dys = _out(dys, "moe_unpermute_bwd: dys", (tokens * topk, hidden), dout.dtype, dev, stream)
     if ys is not None:
-        _require(ys, "moe_unpermute_bwd: ys", (tokens * topk, hidden), dout.dtype, dev)
-        dw = on.out(dw, "moe_unpermute_bwd: dweights", (tokens, topk), torch.float32, dev)
-    _check(load().gsa_moe_unpermute_bwd(dout.data_ptr(), None if ys is None else ys.data_ptr(),
-                                        None if weights is None else weights.data_ptr(), row_of_slot.data_ptr(),
-                                        tokens, topk, hidden, code, dys.data_ptr() if want_dys else None,
-                                        None if ys is None else dw.data_ptr(), on.ptr), "gsa_moe_unpermute_bwd")
+        _require(ys, "moe_unpermute_bwd: ys", (tokens * topk, hidden), dout.dtype)
+        _same_device("moe_unpermute_bwd", dev, ys)
+        dw = _out(dw, "moe_unpermute_bwd: dweights", (tokens, topk), _torch.float32, dev, stream)
+    st = _lib.gsa_moe_unpermute_bwd(dout.data_ptr(), None if ys is None else ys.data_ptr(), wp, row_of_slot.data_ptr(),
+                                    tokens, topk, hidden, code, dys.data_ptr() if want_dys else None,
+                                    None if ys is None else dw.data_ptr(),
+                                    _stream_of(stream, dev, dout, ys, row_of_slot, weights))
+    if st:
+        _check(st, "gsa_moe_unpermute_bwd")
     return dys if want_dys else None, dw if ys is not None else None
 
 
@@ -671,27 +685,31 @@ def moe_unpermute_bwd(dout, ys, row_of_slot, weights=None, want_dys: bool = True
 
 def _operand(q: dict, side: str, recipe_kind: int, experts: int, what: str, dev):
     """QIn of one copy of a quantized tensor (side 'row' or 'col'), and its tensors."""
-    import torch
-    t = [q.get(side + "_data"), q.get(side + "_scale"), q.get("amax_" + side) if recipe_kind == NVFP4 else None]
-    for name, v in zip((side + "_data", side + "_scale"), t):
-        if v is None:
-            raise GsaError(1, f"{what}: no {name} (a {side} copy with tiled scales is needed)")
-        _require(v, f"{what}: {name}", tuple(v.shape), torch.uint8, dev)
+    u8 = _torch.uint8
+    data, scale, amax = q.get(side + "_data"), q.get(side + "_scale"), None
+    if data is None or scale is None:
+        raise GsaError(1, f"{what}: no {side}_data or {side}_scale (a {side} copy with tiled scales is needed)")
+    for t in (data, scale):
+        if t.dtype is not u8 or not t.is_contiguous() or t.device != dev:
+            raise GsaError(1, f"{what}: contiguous uint8 {side} copy on {dev} expected")
+    pa = None
     if recipe_kind == NVFP4:
-        if t[2] is None:
-            raise GsaError(1, f"{what}: no amax_{side}")
-        _require(t[2], f"{what}: amax_{side}", (t[2].numel(),), torch.float32, dev)
-        if t[2].numel() < experts:
-            raise GsaError(1, f"{what}: amax_{side} has {t[2].numel()} entries for {experts} experts")
-    return QIn(t[0].data_ptr(), t[1].data_ptr(), t[2].data_ptr() if t[2] is not None else None, t[0].numel(),
-               t[1].numel()), t
+        amax = q.get("amax_" + side)
+        if amax is None or amax.dtype is not _torch.float32 or not amax.is_contiguous() or amax.device != dev or \
+                amax.numel() < experts:
+            raise GsaError(1, f"{what}: contiguous float32 amax_{side} of {experts} experts on {dev} expected")
+        pa = amax.data_ptr()
+    return QIn(data.data_ptr(), scale.data_ptr(), pa, data.numel(), scale.numel()), data, scale, amax
 
 
-def _out_code(out_dtype):
-    code = _DTYPE_NAMES.get(str(out_dtype))
-    if code not in (BF16, FP32):
-        raise GsaError(1, f"output type {out_dtype} (bfloat16 or float32 expected)")
-    return code
+def _product_args(what, split, out_dtype):
+    torch = _torch or _setup()
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise GsaError(1, f"{what}: output type {out_dtype} (bfloat16 or float32 expected)")
+    if split.dim() != 1:
+        raise GsaError(1, f"{what}: split must be [experts]")
+    _require(split, what + ": split", split.shape, torch.int64)
+    return split.device, split.shape[0], BF16 if out_dtype is torch.bfloat16 else FP32
 
 
 def grouped_gemm(a: dict, b: dict, split, m: int, n: int, k: int, recipe_kind: int, out_dtype=None,
@@ -701,17 +719,16 @@ def grouped_gemm(a: dict, b: dict, split, m: int, n: int, k: int, recipe_kind: i
     of [E * n, k] split into E times n rows, or with b_columnwise the columnwise copy of [E * k, n] split into E
     times k rows (the input gradient's product with weights [k, n]).  split: [E] int64 on the device, sum at most
     m (rows past it become zero).  out_dtype: torch.bfloat16 (default) or torch.float32."""
-    import torch
-    out_dtype = out_dtype or torch.bfloat16
-    code = _out_code(out_dtype)
-    _require(split, "grouped_gemm: split", (split.numel(),), torch.int64)
-    dev, experts = split.device, split.numel()
-    qa, ta = _operand(a, "row", recipe_kind, experts, "grouped_gemm: a", dev)
-    qb, tb = _operand(b, "col" if b_columnwise else "row", recipe_kind, experts, "grouped_gemm: b", dev)
-    on = _On(stream, dev, split, *ta, *tb)
-    out = on.out(out, "grouped_gemm: out", (m, n), out_dtype, dev)
-    _check(load().gsa_grouped_gemm(qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, out.data_ptr(), code,
-                                   on.ptr), "gsa_grouped_gemm")
+    torch = _torch or _setup()
+    out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
+    dev, experts, code = _product_args("grouped_gemm", split, out_dtype)
+    qa, *ta = _operand(a, "row", recipe_kind, experts, "grouped_gemm: a", dev)
+    qb, *tb = _operand(b, "col" if b_columnwise else "row", recipe_kind, experts, "grouped_gemm: b", dev)
+    out = _out(out, "grouped_gemm: out", (m, n), out_dtype, dev, stream)
+    st = _lib.gsa_grouped_gemm(qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, out.data_ptr(), code,
+                               _stream_of(stream, dev, split, *ta, *tb))
+    if st:
+        _check(st, "gsa_grouped_gemm")
     return out
 
 
@@ -720,23 +737,21 @@ def grouped_gemm_wgrad(a: dict, b: dict, split, m: int, n: int, k: int, recipe_k
     """dw [experts, n, k]: for each expert the product A^T B over its rows, from the columnwise copies (tiled scales)
     of the [m, n] and [m, k] tensors.  out_dtype: torch.float32 (default) or torch.bfloat16.  accumulate adds to
     `out`.  NVFP4 copies made with the RHT need the same sign mask on both sides."""
-    import torch
+    torch = _torch or _setup()
     out_dtype = out_dtype or (out.dtype if out is not None else torch.float32)
-    code = _out_code(out_dtype)
+    dev, experts, code = _product_args("grouped_gemm_wgrad", split, out_dtype)
     if accumulate and out is None:
         raise GsaError(1, "grouped_gemm_wgrad: accumulate needs out")
-    _require(split, "grouped_gemm_wgrad: split", (split.numel(),), torch.int64)
-    dev, experts = split.device, split.numel()
-    qa, ta = _operand(a, "col", recipe_kind, experts, "grouped_gemm_wgrad: a", dev)
-    qb, tb = _operand(b, "col", recipe_kind, experts, "grouped_gemm_wgrad: b", dev)
-    on = _On(stream, dev, split, *ta, *tb)
-    out = on.out(out, "grouped_gemm_wgrad: out", (experts, n, k), out_dtype, dev)
-    L = load()
-    nbytes = L.gsa_grouped_gemm_wgrad_workspace_size(experts, m, n, k, recipe_kind)
-    ws = on.empty((max(256, nbytes),), torch.uint8, dev)
-    _check(L.gsa_grouped_gemm_wgrad(qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, out.data_ptr(), code,
-                                    int(bool(accumulate)), ws.data_ptr(), ws.numel(), on.ptr),
-           "gsa_grouped_gemm_wgrad")
+    qa, *ta = _operand(a, "col", recipe_kind, experts, "grouped_gemm_wgrad: a", dev)
+    qb, *tb = _operand(b, "col", recipe_kind, experts, "grouped_gemm_wgrad: b", dev)
+    out = _out(out, "grouped_gemm_wgrad: out", (experts, n, k), out_dtype, dev, stream)
+    nbytes = _lib.gsa_grouped_gemm_wgrad_workspace_size(experts, m, n, k, recipe_kind)
+    ws = _out(None, "", (max(256, nbytes),), torch.uint8, dev, stream)
+    st = _lib.gsa_grouped_gemm_wgrad(qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, out.data_ptr(), code,
+                                     1 if accumulate else 0, ws.data_ptr(), nbytes,
+                                     _stream_of(stream, dev, split, *ta, *tb))
+    if st:
+        _check(st, "gsa_grouped_gemm_wgrad")
     return out
 
 
