@@ -34,6 +34,7 @@ constexpr int kStageK = 128;         // bytes of k per stage: one 128-byte swizz
 constexpr int kScaleTile = 512;      // bytes of one 128 x 4 scale tile
 constexpr int kThreads = 384;        // warp 0 loads, warp 1 multiplies, warps 4-11 drain
 constexpr int kEpiWarps = 8;
+constexpr int kOutBuf = 32 * 128, kOutBufs = 2;   // a draining warp's pieces of results: 32 rows x 128 bytes
 
 enum { ERR_SPLIT = 1, ERR_TIMEOUT = 2 };
 
@@ -41,7 +42,7 @@ enum { ERR_SPLIT = 1, ERR_TIMEOUT = 2 };
 __device__ uint32_t g_status;
 
 struct GemmParams {
-    CUtensorMap tm_a, tm_b, tm_sa, tm_sb;
+    CUtensorMap tm_a, tm_b, tm_sa, tm_sb, tm_out;
     const int64_t *split;
     const float *amax_a, *amax_b;
     void *out;
@@ -54,6 +55,7 @@ struct GemmParams {
     int b_scale_rows;      // scale tiles along N per expert
     int scale_cols;        // scale tiles along k
     int64_t a_scale_tiles; // row tiles that A's scale buffer holds
+    int tma_out;           // out's rows suit TMA
 };
 
 template <bool NV> struct Fmt;
@@ -74,10 +76,11 @@ template <bool NV, int BN, bool kPair> struct Cfg {
     static constexpr int kAcc = BN == 256 ? 1 : 2;       // accumulators in tensor memory
     static constexpr int kScCols = 4 * kSc * (1 + kGroupsB);   // scale columns of a stage
     static constexpr int kCols = 512;
-    static constexpr int kBySmem = (227 * 1024 - 8192 - 1024) / kStride, kByCols = (kCols - kAcc * BN) / kScCols;
+    static constexpr int kOut = kEpiWarps * kOutBufs * kOutBuf;   // results on their way out
+    static constexpr int kBySmem = (227 * 1024 - 7168 - 1024 - kOut) / kStride, kByCols = (kCols - kAcc * BN) / kScCols;
     static constexpr int kFit = kBySmem < kByCols ? kBySmem : kByCols;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
-    static constexpr int kSmem = kStages * kStride + 1024;
+    static constexpr int kSmem = kStages * kStride + kOut + 1024;
 };
 
 struct Barriers {
@@ -206,6 +209,7 @@ template <bool NV, int BN, bool kPair> struct Stages {
     __device__ uint32_t b(int s) const { return a(s) + C::kBytesA; }
     __device__ uint32_t sa(int s) const { return b(s) + C::kBytesB; }
     __device__ uint32_t sb(int s) const { return sa(s) + C::kBytesSA; }
+    __device__ uint32_t out(int warp) const { return a(C::kStages) + warp * kOutBufs * kOutBuf; }
 };
 
 // The products of one stage (one elected lane): scales to their columns of
@@ -305,19 +309,11 @@ __device__ __forceinline__ void finish_add(const __nv_bfloat16 *o, const uint32_
     }
 }
 
-// One accumulator to memory: this thread's lane and kHalf columns from tensor
-// memory, times ua and ub (kScale), to o[0 .. cols), or onto what is there (add).
-// on: the lane holds a row of the result.  The accumulator is handed back
-// (`release`) as soon as it is in registers: scaling, rounding and stores run while
-// the next tile is multiplied.
-template <int kHalf, bool kScale, typename T, typename F>
-__device__ __forceinline__ void drain(uint32_t src, float ua, float ub, T *o, int64_t cols, bool on, int align, bool add,
-                                      F &&release) {
+// Results of one lane, kHalf columns from `cols` on of row `o`, by row stores (rows that TMA does not suit, tiles cut
+// by an expert's last row, BF16 sums onto what is there).
+template <int kHalf, bool kScale, typename T>
+__device__ __forceinline__ void store_lane(const uint32_t *v, float ua, float ub, T *o, int64_t cols, int align, bool add) {
     constexpr int kPer = 32 / sizeof(T);
-    uint32_t v[kHalf];
-    tc::tmem_ld(src, v);
-    release();
-    if (!on) return;
 #pragma unroll
     for (int j = 0; j < kHalf; j += kPer) {
         if (j >= cols) break;
@@ -329,11 +325,65 @@ __device__ __forceinline__ void drain(uint32_t src, float ua, float ub, T *o, in
     }
 }
 
-template <typename T> __device__ __forceinline__ void zeros(T *o, int half, int64_t cols, int align) {
-    constexpr int kPer = 32 / sizeof(T);
-    const uint32_t zero[8] = {};
-    for (int c = 0; c < half && c < cols; c += kPer)
-        store_some(o + c, zero, cols - c < kPer ? static_cast<int>(cols - c) : kPer, align);
+// Results of a warp, 32 rows x kHalf columns at (x, y, z) of out's map, in pieces of
+// 32 rows x 128 bytes through shared memory: each lane writes its row's chunk c to c ^
+// (row mod 8), no two lanes of a quarter to the same banks, and TMA takes the piece
+// away (and clips it).  A row store by 32 lanes costs 32 passes of the pipe that also
+// feeds the tensor core: 4.5K (BF16) and 9.2K (FP32) cycles a tile of 128 x 256, against
+// 594 a stage for the operands.  count: pieces of this warp so far; two buffers.
+template <int kHalf, bool kScale, typename T>
+__device__ __forceinline__ void store_warp(const uint32_t *v, float ua, float ub, uint32_t buf, int &count, const CUtensorMap *tm,
+                                           int x, int y, int z, int64_t cols, int lane, bool add) {
+    constexpr int kPer = 32 / sizeof(T), kPiece = 128 / sizeof(T);
+#pragma unroll
+    for (int j = 0; j < kHalf; j += kPiece) {
+        if (j >= cols) break;
+        const uint32_t at = buf + (count & 1) * kOutBuf;
+        ++count;
+        if (lane == 0) tc::store_wait_read<kOutBufs - 1>();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t w[8];
+            finish<kScale>(v + j + c * kPer, ua, ub, w, T());
+            tc::st_shared(at + lane * 128 + (((2 * c) ^ (lane & 7)) << 4), w);
+            tc::st_shared(at + lane * 128 + (((2 * c + 1) ^ (lane & 7)) << 4), w + 4);
+        }
+        tc::fence_async();
+        __syncwarp();
+        if (lane == 0) {
+            if (add) tc::add_3d(tm, x + j, y, z, at);
+            else tc::store_3d(tm, x + j, y, z, at);
+            tc::store_commit();
+        }
+    }
+}
+
+// Where the results of one tile go: a lane's row (o, with `cols` columns from there on; on: it has one), and the
+// warp's 32 rows in out's map where TMA takes them.
+template <typename T> struct OutAt {
+    T *o;
+    int64_t cols;
+    const CUtensorMap *tm;
+    int x, y, z;
+    bool on, tma, add;
+    int align;
+};
+
+template <int kHalf, bool kScale, typename T>
+__device__ __forceinline__ void store_tile(const uint32_t *v, float ua, float ub, const OutAt<T> &w, uint32_t buf, int &count,
+                                           int lane) {
+    if (w.tma) store_warp<kHalf, kScale, T>(v, ua, ub, buf, count, w.tm, w.x, w.y, w.z, w.cols, lane, w.add);
+    else if (w.on) store_lane<kHalf, kScale, T>(v, ua, ub, w.o, w.cols, w.align, w.add);
+}
+
+// A tile without products.
+template <int kHalf, typename T>
+__device__ __forceinline__ void zero_tile(const OutAt<T> &w, uint32_t buf, int &count, int lane) {
+    uint32_t v[kHalf];
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) v[i] = 0;
+    store_tile<kHalf, false, T>(v, 1.0f, 1.0f, w, buf, count, lane);
 }
 
 // The products of one output tile, `len` bytes of k, by the (converged) issuing warp.  n: tiles so far of this unit;
@@ -395,10 +445,12 @@ template <int kStages> __device__ __forceinline__ void settle_loads(Barriers &sh
     else tc::pause(1000000);   // these copies count on the other block's barriers: time for them to land
 }
 
-// The finished accumulator of the unit's n-th tile to memory by one draining warp.  False: a wait ran out.
+// The finished accumulator of the unit's n-th tile to memory by one draining warp.
+// It is handed back as soon as it is in registers: scaling, rounding and stores run
+// while the next tile is multiplied.  False: a wait ran out.
 template <bool NV, int BN, bool kPair, typename T>
 __device__ __forceinline__ bool drain_tile(Barriers &sh, int n, int warp, int lane, const float *amax_a, const float *amax_b,
-                                           int g, T *o, int64_t cols, bool on, int align, bool add) {
+                                           int g, const OutAt<T> &w, uint32_t buf, int &count) {
     using C = Cfg<NV, BN, kPair>;
     const int a = n % C::kAcc, q = warp & 3, h = (warp - 4) >> 2;
     float ua = 1.0f, ub = 1.0f;
@@ -408,15 +460,16 @@ __device__ __forceinline__ bool drain_tile(Barriers &sh, int n, int warp, int la
     }
     if (!tc::bar_wait_warp(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, &sh.dead)) return false;
     tc::fence_after();
-    drain<BN / 2, NV>(a * BN + h * (BN / 2) + (static_cast<uint32_t>(32 * q) << 16), ua, ub, o, cols, on, align, add, [&] {
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) {
-            const uint32_t bar = tc::smem_u32(&sh.acc_empty[a]);
-            if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
-            else tc::bar_arrive(bar);
-        }
-    });
+    uint32_t v[BN / 2];
+    tc::tmem_ld(a * BN + h * (BN / 2) + (static_cast<uint32_t>(32 * q) << 16), v);
+    tc::fence_before();
+    __syncwarp();
+    if (lane == 0) {
+        const uint32_t bar = tc::smem_u32(&sh.acc_empty[a]);
+        if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
+        else tc::bar_arrive(bar);
+    }
+    store_tile<BN / 2, NV, T>(v, ua, ub, w, buf, count, lane);
     return true;
 }
 
@@ -473,19 +526,28 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
         const int q = warp & 3, h = (warp - 4) >> 2;   // lanes 32 q .., column half h
         constexpr int kHalf = BN / 2;
         T *out = static_cast<T *>(P.out);
-        const int align = row_align(out, P.N), r = half * kRowsT + 32 * q + lane;
-        int g = 0, n = 0;
+        const int r0 = half * kRowsT + 32 * q;   // the warp's first row of the tile
+        const uint32_t buf = st.out(warp - 4);
+        OutAt<T> w;
+        w.tm = &P.tm_out;
+        w.align = row_align(out, P.N);
+        w.add = false;
+        w.z = 0;
+        int g = 0, n = 0, count = 0;
         for (int64_t i = unit; i < total; i += units) {
             const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
-            const int64_t c0 = static_cast<int64_t>(t.nt) * BN + h * kHalf, cols = P.N - c0;
-            T *o = out + (t.row + r) * P.N + c0;
-            if (g == P.E) {
-                if (r < t.rows) zeros(o, kHalf, cols, align);
-            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, g, o, cols, r < t.rows, align, false)) {
-                break;
-            }
+            const int64_t c0 = static_cast<int64_t>(t.nt) * BN + h * kHalf;
+            w.o = out + (t.row + r0 + lane) * P.N + c0;
+            w.cols = P.N - c0;
+            w.on = r0 + lane < t.rows;
+            w.tma = P.tma_out && r0 + 32 <= t.rows;   // an expert's last rows are not the warp's to write past
+            w.x = static_cast<int>(c0);
+            w.y = static_cast<int>(t.row) + r0;
+            if (g == P.E) zero_tile<kHalf>(w, buf, count, lane);
+            else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, g, w, buf, count)) break;
         }
+        if (lane == 0) tc::store_wait_read<0>();
     }
     close_block<kPair>(sh, warp, C::kCols);
 }
@@ -510,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
 
 struct WgradParams {
     CUtensorMap tm_sa, tm_sb, tm_ta, tm_tb;   // scale tiles; the tail copies of the last stages'
+    CUtensorMap tm_out;
     const uint8_t *a, *b, *sa, *sb;
     const int64_t *split;
     const float *amax_a, *amax_b;
@@ -521,7 +584,7 @@ struct WgradParams {
     int N, K, E;
     int n_tiles, k_tiles;              // tiles along N and K
     int64_t a_bytes, b_bytes, sa_bytes, sb_bytes;
-    int accumulate;
+    int accumulate, tma_out;
 };
 
 struct Pads {
@@ -732,19 +795,30 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
         const int q = warp & 3, h = (warp - 4) >> 2;
         constexpr int kHalf = BN / 2;
         T *out = static_cast<T *>(P.out);
-        const int align = row_align(out, P.K);
-        const bool add = P.accumulate != 0;
-        int n = 0;
+        const uint32_t buf = st.out(warp - 4);
+        OutAt<T> w;
+        w.tm = &P.tm_out;
+        w.align = row_align(out, P.K);
+        w.add = P.accumulate != 0;
+        // onto what is there: in FP32 the memory adds, in BF16 that would round twice
+        const bool tma = P.tma_out && !(w.add && sizeof(T) == 2);
+        int n = 0, count = 0;
         while (next_wtile(P, sh, r, unit, units, total, t)) {
-            const int row = t.nt * kRows + half * kRowsT + 32 * q + lane, c0 = t.kt * BN + h * kHalf;
-            T *o = out + (static_cast<int64_t>(t.e) * P.N + row) * P.K + c0;
-            const int64_t cols = static_cast<int64_t>(P.K) - c0;
+            const int row = t.nt * kRows + half * kRowsT + 32 * q, c0 = t.kt * BN + h * kHalf;
+            w.o = out + (static_cast<int64_t>(t.e) * P.N + row + lane) * P.K + c0;
+            w.cols = static_cast<int64_t>(P.K) - c0;
+            w.on = row + lane < P.N;
+            w.tma = tma && row < P.N;   // the map ends with the expert's rows
+            w.x = c0;
+            w.y = row;
+            w.z = t.e;
             if (t.rows == 0) {   // no rows: a zero gradient
-                if (row < P.N && !add) zeros(o, kHalf, cols, align);
-            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, t.e, o, cols, row < P.N, align, add)) {
+                if (!w.add) zero_tile<kHalf>(w, buf, count, lane);
+            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, t.e, w, buf, count)) {
                 break;
             }
         }
+        if (lane == 0) tc::store_wait_read<0>();
     }
     close_block<kPair>(sh, warp, C::kCols);
 }
@@ -785,6 +859,21 @@ bool map_scales(CUtensorMap *tm, const void *p, int64_t tiles, int box) {
     cuuint32_t b[2] = {kScaleTile / 4, static_cast<cuuint32_t>(box)}, es[2] = {1, 1};
     return fn(tm, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void *>(p), dims, strides, b, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// out [planes, rows, cols]: pieces of 32 rows x 128 bytes.  tma: whether its rows suit TMA (16 bytes).
+bool map_out(CUtensorMap *tm, void *p, int64_t planes, int64_t rows, int64_t cols, int dtype, int *tma) {
+    const int es = dtype == GSA_BF16 ? 2 : 4;
+    *tma = cols * es % 16 == 0;
+    if (!*tma) return true;
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols * es), static_cast<cuuint64_t>(rows * cols * es)};
+    cuuint32_t b[3] = {static_cast<cuuint32_t>(128 / es), 32, 1}, e[3] = {1, 1, 1};
+    return fn(tm, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, b, e,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -902,7 +991,8 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     const bool pair = M >= 64 * E;
     const int sc = nv ? 4 : 1;
     if (!map_codes(&P.tm_a, a->data, M, k_bytes, kRowsT) || !map_codes(&P.tm_b, b->data, E * N, k_bytes, pair ? BN / 2 : BN) ||
-        !map_scales(&P.tm_sa, a->scale, a_rows * cols, sc) || !map_scales(&P.tm_sb, b->scale, E * n128 * cols, sc))
+        !map_scales(&P.tm_sa, a->scale, a_rows * cols, sc) || !map_scales(&P.tm_sb, b->scale, E * n128 * cols, sc) ||
+        !map_out(&P.tm_out, out, 1, M, N, out_dtype, &P.tma_out))
         return GSA_ERR_CUDA;
     P.split = split_sizes_dev;
     P.amax_a = a->amax;
@@ -967,7 +1057,7 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     const int sc = nv ? 4 : 1;
     CUtensorMap plain;   // the experts' maps but for origin, extents and pitch
     if (!map_codes(&plain, w, 4096, 4096, 128) || !map_scales(&P.tm_sa, a->scale, a_tiles, sc) ||
-        !map_scales(&P.tm_sb, b->scale, b_tiles, sc) ||
+        !map_scales(&P.tm_sb, b->scale, b_tiles, sc) || !map_out(&P.tm_out, dw, E, N, K, out_dtype, &P.tma_out) ||
         (nv && (!map_scales(&P.tm_ta, w + ws.tail_a, E * n128 * 4, 4) || !map_scales(&P.tm_tb, w + ws.tail_b, E * k128 * 4, 4))))
         return GSA_ERR_CUDA;
     P.a = static_cast<const uint8_t *>(a->data);

@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kMaxBins = 257;        // 256 experts and the dropped slots
 constexpr int kSortWarps = 32;
-constexpr int kGroup = 8;            // expert rows in flight per thread
+constexpr int kGradRows = 4, kGradBlocks = 4;   // unpermute_bwd: a token's slots at a time, blocks per SM
 
 // ------------------------------------------------------------------- sort
 
@@ -276,42 +276,45 @@ __global__ void __launch_bounds__(256, 4) combine(const uint8_t *ys, const float
 }
 
 // dys[row] = w dout[t] and dw = <dout[t], ys[row]> in one pass.  blockDim.y
-// groups of `wpt` warps take a token each; a thread keeps kGroup partial dot
-// products, summed over its columns in order, then over the lanes by halving
-// distances and over the token's warps in order: the sum's order depends on
-// wpt alone, which the launch takes from tokens and width.
+// groups of wpt warps take a token each and kGradRows of its slots at a time; a
+// thread keeps their partial dot products, summed over its columns in order, then
+// over the lanes by halving distances and over the token's warps in order: the
+// sum's order depends on wpt alone, which the launch takes from tokens and width.
+// Slots at a time / blocks per SM at 1, 2, 4 and 8 warps a token, 8192 tokens x 8 x
+// 2048 BF16, us: 8 / 2: 100.9, 96.6, 102.4, 119.2; 8 / 3 (spills): 115.1, 113.3, 113.6,
+// 125.3; 4 / 4: 98.8, 96.2, 93.8, 100.6; 4 / 5: 113.3, 100.9, 98.4, 102.9; 2 / 6: 127.4,
+// 102.3, 96.8, 103.4.  93.8 us is 6.1 TB/s of the bytes it has to move.
 template <typename T, int V>
-__global__ void __launch_bounds__(256, 3) unpermute_bwd(const uint8_t *dout, const uint8_t *ys, const float *weights,
-                                                     const int32_t *row_of_slot, int tokens, int topk, int64_t nv,
-                                                     uint8_t *dys, float *dw) {
-    constexpr int N = V / sizeof(T);
-    __shared__ float part[8][kGroup];
+__global__ void __launch_bounds__(256, kGradBlocks) unpermute_bwd(const uint8_t *dout, const uint8_t *ys,
+                                                                  const float *weights, const int32_t *row_of_slot,
+                                                                  int tokens, int topk, int64_t nv, uint8_t *dys,
+                                                                  float *dw) {
+    constexpr int N = V / sizeof(T), G = kGradRows;
+    __shared__ float part[8][G];
     const int t = blockIdx.x * blockDim.y + threadIdx.y;
     const int n = tokens * topk;
     const int lane = threadIdx.x & 31, wpt = blockDim.x >> 5, warp = threadIdx.y * wpt + (threadIdx.x >> 5);
     const bool on = t < tokens;
-    const int32_t *rows = row_of_slot + static_cast<int64_t>(on ? t : 0) * topk;
-    for (int j0 = 0; j0 < topk; j0 += kGroup) {
-        int32_t r[kGroup];
-        float w[kGroup], acc[kGroup];
+    const int64_t slot0 = static_cast<int64_t>(on ? t : 0) * topk;
+    for (int j0 = 0; j0 < topk; j0 += G) {
+        int32_t r[G];
+        float acc[G];
 #pragma unroll
-        for (int g = 0; g < kGroup; ++g) {
-            const bool has = on && j0 + g < topk;
-            r[g] = has ? rows[j0 + g] : n;   // n: nothing to do
-            w[g] = has && weights ? weights[static_cast<int64_t>(t) * topk + j0 + g] : 1.0f;
+        for (int g = 0; g < G; ++g) {
+            r[g] = on && j0 + g < topk ? row_of_slot[slot0 + j0 + g] : n;   // n: nothing to do
             acc[g] = 0.0f;
         }
         if (on) {
             for (int64_t c = threadIdx.x; c < nv; c += blockDim.x) {
-                Vec<T, V> d, y[kGroup];
+                Vec<T, V> d, y[G];
                 d.raw = *reinterpret_cast<const typename Raw<V>::T *>(dout + (t * nv + c) * V);
                 if (dw) {
 #pragma unroll
-                    for (int g = 0; g < kGroup; ++g)
+                    for (int g = 0; g < G; ++g)
                         if (live_row(r[g], n) >= 0) y[g].raw = load_once<V>(ys + (r[g] * nv + c) * V);
                 }
 #pragma unroll
-                for (int g = 0; g < kGroup; ++g) {
+                for (int g = 0; g < G; ++g) {
                     const bool live = live_row(r[g], n) >= 0;
                     const int at = r[g] < 0 ? ~r[g] : r[g];
                     if (dw && live) {
@@ -319,9 +322,10 @@ __global__ void __launch_bounds__(256, 3) unpermute_bwd(const uint8_t *dout, con
                         for (int i = 0; i < N; ++i) acc[g] = __fmaf_rn(as_f32(d.e[i]), as_f32(y[g].e[i]), acc[g]);
                     }
                     if (dys && at < n) {
+                        const float w = weights ? weights[slot0 + j0 + g] : 1.0f;
                         Vec<T, V> o;
 #pragma unroll
-                        for (int i = 0; i < N; ++i) put(o.e[i], live ? w[g] * as_f32(d.e[i]) : 0.0f);
+                        for (int i = 0; i < N; ++i) put(o.e[i], live ? w * as_f32(d.e[i]) : 0.0f);
                         *reinterpret_cast<typename Raw<V>::T *>(dys + (at * nv + c) * V) = o.raw;
                     }
                 }
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(256, 3) unpermute_bwd(const uint8_t *dout, con
         }
         if (dw) {
 #pragma unroll
-            for (int g = 0; g < kGroup; ++g) {
+            for (int g = 0; g < G; ++g) {
 #pragma unroll
                 for (int s = 16; s > 0; s >>= 1) acc[g] += __shfl_xor_sync(0xFFFFFFFFu, acc[g], s);
             }
@@ -337,21 +341,21 @@ __global__ void __launch_bounds__(256, 3) unpermute_bwd(const uint8_t *dout, con
                 __syncthreads();
                 if (lane == 0) {
 #pragma unroll
-                    for (int g = 0; g < kGroup; ++g) part[warp][g] = acc[g];
+                    for (int g = 0; g < G; ++g) part[warp][g] = acc[g];
                 }
                 __syncthreads();
             }
-            if (on && static_cast<int>(threadIdx.x) < kGroup && j0 + static_cast<int>(threadIdx.x) < topk) {
+            if (on && static_cast<int>(threadIdx.x) < G && j0 + static_cast<int>(threadIdx.x) < topk) {
                 const int g = threadIdx.x;
                 float s = 0.0f;
                 if (wpt > 1) {
                     for (int k = 0; k < wpt; ++k) s += part[threadIdx.y * wpt + k][g];
                 } else {
 #pragma unroll
-                    for (int k = 0; k < kGroup; ++k)
+                    for (int k = 0; k < G; ++k)
                         if (k == g) s = acc[k];
                 }
-                dw[static_cast<int64_t>(t) * topk + j0 + g] = s;
+                dw[slot0 + j0 + g] = s;
             }
         }
     }
@@ -538,9 +542,11 @@ gsa_status gsa_moe_unpermute_bwd(const void *dout, const void *ys, const float *
     if (tokens == 0) return done(0);
     const int v = vector_bytes(hidden * elem_bytes(dtype));
     const int64_t nv = hidden * elem_bytes(dtype) / v;
-    // warps per token: one while the tokens alone fill the machine
+    // warps per token: two vectors a thread and at most 4 (measured above), or one and
+    // at most 8 where the tokens are too few to fill the machine with 4
     int wpt = 1;
-    while (wpt < 8 && tokens * wpt < 152 * 32 && wpt * 32 < nv) wpt *= 2;
+    while (wpt < 4 && wpt * 128 <= nv) wpt *= 2;
+    while (wpt < 8 && tokens * wpt < 152 * 16 && wpt * 64 <= nv) wpt *= 2;
     const dim3 block(32 * wpt, 8 / wpt), grid(static_cast<unsigned>((tokens + block.y - 1) / block.y));
     with_type(dtype, v, [&](auto tag, auto width) {
         unpermute_bwd<decltype(tag), decltype(width)::value>

@@ -35,7 +35,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 1000000;\n"
+        " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, 1000000;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -91,6 +91,10 @@ __device__ __forceinline__ bool elect() {
     return p != 0;
 }
 
+__device__ __forceinline__ void st_shared(uint32_t at, const uint32_t *w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+
 // --------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *tm) {
@@ -113,6 +117,25 @@ __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap *tm
         "l"(tm), "r"(x), "r"(y), "r"(cluster_bar)
         : "memory");
 }
+
+// A 128-byte swizzled box from shared memory to a tensor (clipped to it), or added to what is there.
+__device__ __forceinline__ void store_3d(const CUtensorMap *tm, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tm), "r"(x), "r"(y),
+                 "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void add_3d(const CUtensorMap *tm, int x, int y, int z, uint32_t src) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tm),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// At most N of this thread's store groups still read shared memory.
+template <int N> __device__ __forceinline__ void store_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+// Writes to shared memory so far become visible to copies and products.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Origin, extents (bytes of a row, rows) and pitch of a tensor map of bytes in shared memory.
 __device__ __forceinline__ void edit_map(CUtensorMap *map, const void *p, uint32_t bytes, uint32_t rows, uint64_t pitch) {
@@ -147,8 +170,11 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// On a barrier of any block of the cluster.  Relaxed: it says that this warp has what it read from tensor memory (the
+// loads are complete, nothing is passed on).  A release at cluster scope would first wait for the warp's stores of the
+// tile before, 1.9K cycles in which the tensor core stands still.
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // ----------------------------------------------------------------- tcgen05
