@@ -34,7 +34,8 @@ constexpr int kStageK = 128;         // bytes of k per stage: one 128-byte swizz
 constexpr int kScaleTile = 512;      // bytes of one 128 x 4 scale tile
 constexpr int kThreads = 384;        // warp 0 loads, warp 1 multiplies, warps 4-11 drain
 constexpr int kEpiWarps = 8;
-constexpr int kOutBuf = 32 * 128, kOutBufs = 2;   // a draining warp's pieces of results: 32 rows x 128 bytes
+constexpr int kOutBuf = 32 * 128;    // a draining warp's piece of results: 32 rows x 128 bytes
+constexpr int kStatic = 4096;        // what the blocks' static shared memory stays below
 
 enum { ERR_SPLIT = 1, ERR_TIMEOUT = 2 };
 
@@ -76,8 +77,8 @@ template <bool NV, int BN, bool kPair> struct Cfg {
     static constexpr int kAcc = BN == 256 ? 1 : 2;       // accumulators in tensor memory
     static constexpr int kScCols = 4 * kSc * (1 + kGroupsB);   // scale columns of a stage
     static constexpr int kCols = 512;
-    static constexpr int kOut = kEpiWarps * kOutBufs * kOutBuf;   // results on their way out
-    static constexpr int kBySmem = (227 * 1024 - 7168 - 1024 - kOut) / kStride, kByCols = (kCols - kAcc * BN) / kScCols;
+    static constexpr int kOut = kEpiWarps * kOutBuf;   // results on their way out
+    static constexpr int kBySmem = (227 * 1024 - kStatic - 1024 - kOut) / kStride, kByCols = (kCols - kAcc * BN) / kScCols;
     static constexpr int kFit = kBySmem < kByCols ? kBySmem : kByCols;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
     static constexpr int kSmem = kStages * kStride + kOut + 1024;
@@ -89,7 +90,7 @@ struct Barriers {
 };
 
 struct GemmShared : Barriers {
-    int64_t row0[kMaxE + 2];    // first row of each group; group E: rows that no expert has
+    int row0[kMaxE + 2];        // first row of each group; group E: rows that no expert has
     int tile0[kMaxE + 2];       // first row tile of each group
     int scale0[kMaxE + 1];      // first 128-row scale tile of each expert
     int64_t scan[kThreads / 32][3];
@@ -117,17 +118,15 @@ template <int kRows> __device__ void scan_split(const GemmParams &P, GemmShared 
     const bool any_neg = __syncthreads_or(neg);
     for (int k = 0; k < w; ++k) rows += sh.scan[k][0], scales += sh.scan[k][1], tiles += sh.scan[k][2];
     if (t < P.E) {
-        sh.row0[t + 1] = rows;
+        sh.row0[t + 1] = static_cast<int>(rows);
         sh.scale0[t + 1] = static_cast<int>(scales);
         sh.tile0[t + 1] = static_cast<int>(tiles);
     }
     if (t == 0) sh.row0[0] = 0, sh.scale0[0] = 0, sh.tile0[0] = 0;
-    __syncthreads();
-    if (t == 0) {
-        const int64_t sum = sh.row0[P.E];
-        sh.bad = any_neg || sum > P.M || sh.scale0[P.E] > P.a_scale_tiles;
-        sh.row0[P.E + 1] = P.M;
-        sh.tile0[P.E + 1] = sh.tile0[P.E] + static_cast<int>((P.M - (sum > P.M ? P.M : sum) + kRows - 1) / kRows);
+    if (t == P.E - 1) {
+        sh.bad = any_neg || rows > P.M || scales > P.a_scale_tiles;
+        sh.row0[P.E + 1] = static_cast<int>(P.M);
+        sh.tile0[P.E + 1] = static_cast<int>(tiles + (P.M - (rows > P.M ? P.M : rows) + kRows - 1) / kRows);
     }
     __syncthreads();
 }
@@ -141,7 +140,7 @@ __device__ __forceinline__ float tensor_scale(float amax) {
 
 struct Tile {
     int g;          // group
-    int64_t row;    // first row
+    int row;        // first row
     int rows;       // rows of the tile that belong to the group
     int mt;         // row tile within the group
     int nt;         // column tile
@@ -155,9 +154,8 @@ template <int kRows> __device__ __forceinline__ Tile tile_at(const GemmParams &P
     t.g = g;
     t.nt = static_cast<int>(i - static_cast<int64_t>(q) * P.n_tiles);
     t.mt = q - sh.tile0[g];
-    t.row = sh.row0[g] + static_cast<int64_t>(t.mt) * kRows;
-    const int64_t left = sh.row0[g + 1] - t.row;
-    t.rows = left < kRows ? static_cast<int>(left) : kRows;
+    t.row = sh.row0[g] + t.mt * kRows;
+    t.rows = min(kRows, sh.row0[g + 1] - t.row);
     return t;
 }
 
@@ -209,7 +207,7 @@ template <bool NV, int BN, bool kPair> struct Stages {
     __device__ uint32_t b(int s) const { return a(s) + C::kBytesA; }
     __device__ uint32_t sa(int s) const { return b(s) + C::kBytesB; }
     __device__ uint32_t sb(int s) const { return sa(s) + C::kBytesSA; }
-    __device__ uint32_t out(int warp) const { return a(C::kStages) + warp * kOutBufs * kOutBuf; }
+    __device__ uint32_t out(int warp) const { return a(C::kStages) + warp * kOutBuf; }
 };
 
 // The products of one stage (one elected lane): scales to their columns of
@@ -330,30 +328,29 @@ __device__ __forceinline__ void store_lane(const uint32_t *v, float ua, float ub
 // (row mod 8), no two lanes of a quarter to the same banks, and TMA takes the piece
 // away (and clips it).  A row store by 32 lanes costs 32 passes of the pipe that also
 // feeds the tensor core: 4.5K (BF16) and 9.2K (FP32) cycles a tile of 128 x 256, against
-// 594 a stage for the operands.  count: pieces of this warp so far; two buffers.
+// 594 a stage for the operands.  One buffer a warp: a second one would cost a stage
+// of operands (125 us with one fewer, product of 65536 x 2048 x 2048 NVFP4).
 template <int kHalf, bool kScale, typename T>
-__device__ __forceinline__ void store_warp(const uint32_t *v, float ua, float ub, uint32_t buf, int &count, const CUtensorMap *tm,
+__device__ __forceinline__ void store_warp(const uint32_t *v, float ua, float ub, uint32_t buf, const CUtensorMap *tm,
                                            int x, int y, int z, int64_t cols, int lane, bool add) {
     constexpr int kPer = 32 / sizeof(T), kPiece = 128 / sizeof(T);
 #pragma unroll
     for (int j = 0; j < kHalf; j += kPiece) {
         if (j >= cols) break;
-        const uint32_t at = buf + (count & 1) * kOutBuf;
-        ++count;
-        if (lane == 0) tc::store_wait_read<kOutBufs - 1>();
+        if (lane == 0) tc::store_wait_read();
         __syncwarp();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             uint32_t w[8];
             finish<kScale>(v + j + c * kPer, ua, ub, w, T());
-            tc::st_shared(at + lane * 128 + (((2 * c) ^ (lane & 7)) << 4), w);
-            tc::st_shared(at + lane * 128 + (((2 * c + 1) ^ (lane & 7)) << 4), w + 4);
+            tc::st_shared(buf + lane * 128 + (((2 * c) ^ (lane & 7)) << 4), w);
+            tc::st_shared(buf + lane * 128 + (((2 * c + 1) ^ (lane & 7)) << 4), w + 4);
         }
         tc::fence_async();
         __syncwarp();
         if (lane == 0) {
-            if (add) tc::add_3d(tm, x + j, y, z, at);
-            else tc::store_3d(tm, x + j, y, z, at);
+            if (add) tc::add_3d(tm, x + j, y, z, buf);
+            else tc::store_3d(tm, x + j, y, z, buf);
             tc::store_commit();
         }
     }
@@ -371,19 +368,19 @@ template <typename T> struct OutAt {
 };
 
 template <int kHalf, bool kScale, typename T>
-__device__ __forceinline__ void store_tile(const uint32_t *v, float ua, float ub, const OutAt<T> &w, uint32_t buf, int &count,
+__device__ __forceinline__ void store_tile(const uint32_t *v, float ua, float ub, const OutAt<T> &w, uint32_t buf,
                                            int lane) {
-    if (w.tma) store_warp<kHalf, kScale, T>(v, ua, ub, buf, count, w.tm, w.x, w.y, w.z, w.cols, lane, w.add);
+    if (w.tma) store_warp<kHalf, kScale, T>(v, ua, ub, buf, w.tm, w.x, w.y, w.z, w.cols, lane, w.add);
     else if (w.on) store_lane<kHalf, kScale, T>(v, ua, ub, w.o, w.cols, w.align, w.add);
 }
 
 // A tile without products.
 template <int kHalf, typename T>
-__device__ __forceinline__ void zero_tile(const OutAt<T> &w, uint32_t buf, int &count, int lane) {
+__device__ __forceinline__ void zero_tile(const OutAt<T> &w, uint32_t buf, int lane) {
     uint32_t v[kHalf];
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) v[i] = 0;
-    store_tile<kHalf, false, T>(v, 1.0f, 1.0f, w, buf, count, lane);
+    store_tile<kHalf, false, T>(v, 1.0f, 1.0f, w, buf, lane);
 }
 
 // The products of one output tile, `len` bytes of k, by the (converged) issuing warp.  n: tiles so far of this unit;
@@ -450,7 +447,7 @@ template <int kStages> __device__ __forceinline__ void settle_loads(Barriers &sh
 // while the next tile is multiplied.  False: a wait ran out.
 template <bool NV, int BN, bool kPair, typename T>
 __device__ __forceinline__ bool drain_tile(Barriers &sh, int n, int warp, int lane, const float *amax_a, const float *amax_b,
-                                           int g, const OutAt<T> &w, uint32_t buf, int &count) {
+                                           int g, const OutAt<T> &w, uint32_t buf) {
     using C = Cfg<NV, BN, kPair>;
     const int a = n % C::kAcc, q = warp & 3, h = (warp - 4) >> 2;
     float ua = 1.0f, ub = 1.0f;
@@ -469,7 +466,7 @@ __device__ __forceinline__ bool drain_tile(Barriers &sh, int n, int warp, int la
         if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
         else tc::bar_arrive(bar);
     }
-    store_tile<BN / 2, NV, T>(v, ua, ub, w, buf, count, lane);
+    store_tile<BN / 2, NV, T>(v, ua, ub, w, buf, lane);
     return true;
 }
 
@@ -478,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
     using C = Cfg<NV, BN, kPair>;
     extern __shared__ uint8_t dyn[];
     __shared__ GemmShared sh;
+    static_assert(sizeof(GemmShared) <= kStatic, "shared memory");
     constexpr int kRows = kPair ? 2 * kRowsT : kRowsT;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     scan_split<kRows>(P, sh);
@@ -504,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
             const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
             StageAt w{&P.tm_a, &P.tm_b, &P.tm_sa, &P.tm_sb, 0};
-            w.a_row = uniform(static_cast<int>(t.row)) + half * kRowsT;
+            w.a_row = uniform(t.row) + half * kRowsT;
             w.a_tile = uniform((sh.scale0[g] + t.mt * (kRows / 128) + half) * P.scale_cols);
             w.b_row = uniform(static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN)) + half * C::kRowsB;
             w.b_tile = uniform((g * P.b_scale_rows + t.nt * C::kGroupsB) * P.scale_cols);
@@ -533,21 +531,21 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
         w.align = row_align(out, P.N);
         w.add = false;
         w.z = 0;
-        int g = 0, n = 0, count = 0;
+        int g = 0, n = 0;
         for (int64_t i = unit; i < total; i += units) {
             const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
             const int64_t c0 = static_cast<int64_t>(t.nt) * BN + h * kHalf;
-            w.o = out + (t.row + r0 + lane) * P.N + c0;
+            w.o = out + static_cast<int64_t>(t.row + r0 + lane) * P.N + c0;
             w.cols = P.N - c0;
             w.on = r0 + lane < t.rows;
             w.tma = P.tma_out && r0 + 32 <= t.rows;   // an expert's last rows are not the warp's to write past
             w.x = static_cast<int>(c0);
-            w.y = static_cast<int>(t.row) + r0;
-            if (g == P.E) zero_tile<kHalf>(w, buf, count, lane);
-            else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, g, w, buf, count)) break;
+            w.y = t.row + r0;
+            if (g == P.E) zero_tile<kHalf>(w, buf, lane);
+            else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, g, w, buf)) break;
         }
-        if (lane == 0) tc::store_wait_read<0>();
+        if (lane == 0) tc::store_wait_read();
     }
     close_block<kPair>(sh, warp, C::kCols);
 }
@@ -588,15 +586,15 @@ struct WgradParams {
 };
 
 struct Pads {
-    int64_t pad0[kMaxE + 1];    // padded rows before each expert
+    int pad0[kMaxE + 1];        // padded rows before each expert
     int wide0[kMaxE + 1];       // scale tiles along the rows before each expert
-    int64_t rows[kMaxE];
+    int rows[kMaxE];
     int64_t scan[kMaxE / 32][3];
     uint32_t bad;
 };
 struct WgradShared : Barriers {
     Pads pads;
-    int order[kMaxE];           // experts by descending size
+    uint16_t order[kMaxE];      // experts by descending size
 };
 
 // Padded rows and scale tiles before each expert.  Every thread of a block of at least 256.  A negative size, a sum
@@ -606,7 +604,7 @@ template <int kBlock, bool NV> __device__ void scan_pads(const WgradParams &P, P
     int64_t m = t < P.E ? P.split[t] : 0;
     const bool neg = m < 0 || m > P.M;
     if (neg) m = 0;
-    if (t < P.E) d.rows[t] = m;
+    if (t < P.E) d.rows[t] = static_cast<int>(m);
     int64_t rows = m, pad = (m + kBlock - 1) / kBlock * kBlock, wide = (m + 4 * kBlock - 1) / (4 * kBlock);
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
@@ -618,7 +616,7 @@ template <int kBlock, bool NV> __device__ void scan_pads(const WgradParams &P, P
     const bool any_neg = __syncthreads_or(neg);
     for (int k = 0; k < w && k < kMaxE / 32; ++k) rows += d.scan[k][0], pad += d.scan[k][1], wide += d.scan[k][2];
     if (t < P.E) {
-        d.pad0[t + 1] = pad;
+        d.pad0[t + 1] = static_cast<int>(pad);
         d.wide0[t + 1] = static_cast<int>(wide);
     }
     if (t == 0) d.pad0[0] = 0, d.wide0[0] = 0;
@@ -631,7 +629,7 @@ template <int kBlock, bool NV> __device__ void scan_pads(const WgradParams &P, P
 }
 
 // Where an expert's odd-pitch copy starts, in units of rows of the matrix: 8 bytes more than its codes.
-__device__ __forceinline__ int64_t pack_at(const Pads &d, int e) { return d.pad0[e] / 2 + 8 * static_cast<int64_t>(e); }
+__device__ __forceinline__ int64_t pack_at(const Pads &d, int e) { return d.pad0[e] / 2 + 8 * e; }
 
 constexpr int kPrepThreads = 256;
 
@@ -667,7 +665,7 @@ __global__ void __launch_bounds__(kPrepThreads) wgrad_prepare(const __grid_const
         if (pitch % 16 == 0) continue;
         const bool is_a = j < P.N;
         const int r = is_a ? j : j - P.N, rows = is_a ? P.N : P.K;
-        const uint8_t *src = (is_a ? P.a : P.b) + d.pad0[e] / 2 * rows + r * pitch;
+        const uint8_t *src = (is_a ? P.a : P.b) + static_cast<int64_t>(d.pad0[e] / 2) * rows + r * pitch;
         uint8_t *dst = (is_a ? P.pack_a : P.pack_b) + pack_at(d, e) * rows + r * (pitch + 8);
         for (int64_t c = 16 * lane; c < pitch; c += 512) {
             const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src + c));
@@ -727,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
     using C = Cfg<NV, BN, kPair>;
     extern __shared__ uint8_t dyn[];
     __shared__ WgradShared sh;
+    static_assert(sizeof(WgradShared) <= kStatic, "shared memory");
     constexpr int kBlock = NV ? 16 : 32, kRows = kPair ? 2 * kRowsT : kRowsT;
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     scan_pads<kBlock, NV>(P, sh.pads);
@@ -735,10 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
         return;
     }
     if (static_cast<int>(threadIdx.x) < P.E) {
-        const int64_t m = sh.pads.rows[threadIdx.x];
+        const int m = sh.pads.rows[threadIdx.x];
         int rank = 0;
         for (int k = 0; k < P.E; ++k) rank += sh.pads.rows[k] > m || (sh.pads.rows[k] == m && k < static_cast<int>(threadIdx.x));
-        sh.order[rank] = threadIdx.x;
+        sh.order[rank] = static_cast<uint16_t>(threadIdx.x);
     }
     const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x, units = kPair ? gridDim.x >> 1 : gridDim.x;
     const int half = kPair ? blockIdx.x & 1 : 0;
@@ -802,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
         w.add = P.accumulate != 0;
         // onto what is there: in FP32 the memory adds, in BF16 that would round twice
         const bool tma = P.tma_out && !(w.add && sizeof(T) == 2);
-        int n = 0, count = 0;
+        int n = 0;
         while (next_wtile(P, sh, r, unit, units, total, t)) {
             const int row = t.nt * kRows + half * kRowsT + 32 * q, c0 = t.kt * BN + h * kHalf;
             w.o = out + (static_cast<int64_t>(t.e) * P.N + row + lane) * P.K + c0;
@@ -813,12 +812,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
             w.y = row;
             w.z = t.e;
             if (t.rows == 0) {   // no rows: a zero gradient
-                if (!w.add) zero_tile<kHalf>(w, buf, count, lane);
-            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, t.e, w, buf, count)) {
+                if (!w.add) zero_tile<kHalf>(w, buf, lane);
+            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, t.e, w, buf)) {
                 break;
             }
         }
-        if (lane == 0) tc::store_wait_read<0>();
+        if (lane == 0) tc::store_wait_read();
     }
     close_block<kPair>(sh, warp, C::kCols);
 }
