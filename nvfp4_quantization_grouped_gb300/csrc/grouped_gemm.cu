@@ -214,23 +214,25 @@ template <bool NV, int BN, bool kPair> struct Stages {
 // tensor memory, then `steps` steps of 32 bytes of k.  The scale columns are the
 // stage's own, so the barrier that frees the stage frees them too.
 template <bool NV, int BN, bool kPair>
-__device__ __forceinline__ void multiply_stage(const Stages<NV, BN, kPair> &st, int s, uint32_t d, int steps, bool first) {
+__device__ __forceinline__ void multiply_stage(const Stages<NV, BN, kPair> &st, int s, uint32_t d, int steps, uint32_t add) {
     using C = Cfg<NV, BN, kPair>;
     constexpr uint32_t idesc = tc::idesc_block_scaled(NV, kPair ? 2 * kRowsT : kRowsT, BN);
     constexpr int kSc = C::kSc;
     const uint32_t sfa = C::kAcc * BN + s * C::kScCols, sfb = sfa + 4 * kSc;   // the block holds all columns: they start at 0
+    const uint32_t a = tc::desc_lo(st.a(0)) + s * (C::kStride / 16), b = a + C::kBytesA / 16, sa = b + C::kBytesB / 16,
+                   sb = sa + C::kBytesSA / 16;
 #pragma unroll
     for (int j = 0; j < kSc; ++j) {
-        tc::copy_scales<kPair>(sfa + 4 * j, tc::desc_scales(st.sa(s) + j * kScaleTile));
+        tc::copy_scales<kPair>(sfa + 4 * j, sa + j * (kScaleTile / 16));
 #pragma unroll
-        for (int b = 0; b < C::kGroupsB; ++b)
-            tc::copy_scales<kPair>(sfb + 4 * (j * C::kGroupsB + b), tc::desc_scales(st.sb(s) + (b * kSc + j) * kScaleTile));
+        for (int g = 0; g < C::kGroupsB; ++g)
+            tc::copy_scales<kPair>(sfb + 4 * (j * C::kGroupsB + g), sb + (g * kSc + j) * (kScaleTile / 16));
     }
-    for (int j = 0; j < steps; ++j) {
-        const uint64_t da = tc::desc_sw128(st.a(s) + 32 * j), db = tc::desc_sw128(st.b(s) + 32 * j);
-        const bool add = !first || j > 0;
-        if (NV) tc::mma_nvf4<kPair>(d, da, db, idesc, sfa + 4 * j, sfb + 4 * C::kGroupsB * j, add);
-        else tc::mma_mxf8<kPair>(d, da, db, idesc | tc::idesc_scale_id(j), sfa, sfb, add);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j > 0 && j >= steps) break;
+        if (NV) tc::mma_nvf4<kPair>(d, a + 2 * j, b + 2 * j, idesc, sfa + 4 * j, sfb + 4 * C::kGroupsB * j, j ? 1 : add);
+        else tc::mma_mxf8<kPair>(d, a + 2 * j, b + 2 * j, idesc | tc::idesc_scale_id(j), sfa, sfb, j ? 1 : add);
     }
 }
 
@@ -383,48 +385,63 @@ __device__ __forceinline__ void zero_tile(const OutAt<T> &w, uint32_t buf, int l
     store_tile<kHalf, false, T>(v, 1.0f, 1.0f, w, buf, lane);
 }
 
-// The products of one output tile, `len` bytes of k, by the (converged) issuing warp.  n: tiles so far of this unit;
-// it: stages so far.  False: a wait ran out.
-template <bool NV, int BN, bool kPair>
-__device__ __forceinline__ bool multiply_tile(Barriers &sh, const Stages<NV, BN, kPair> &st, int n, int &it, int len) {
+// A role's place in the ring of stages: the stage, the parity of the round, and how many were issued (for settle).
+template <int kStages> struct Ring {
+    int s = 0;
+    uint32_t round = 0;
+    int issued = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == kStages) s = 0, round ^= 1;
+    }
+};
+
+// The loops of the issuing warps do not leave when a wait runs out (then every further wait returns at once and nothing
+// more is issued): without such exits their counters are uniform, and so are the addresses and descriptors.
+
+// The products of one output tile, `len` bytes of k, by the (converged) issuing warp.  n: tiles so far of this unit.
+template <bool NV, int BN, bool kPair, typename R>
+__device__ __forceinline__ void multiply_tile(Barriers &sh, const Stages<NV, BN, kPair> &st, int n, R &ring, int len, bool &ok) {
     using C = Cfg<NV, BN, kPair>;
     volatile uint32_t *dead = &sh.dead;
     const int a = n % C::kAcc, kt = (len + kStageK - 1) / kStageK;
-    if (n >= C::kAcc && !tc::bar_wait_warp(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead)) return false;
+    ok = ok && (n < C::kAcc || tc::bar_wait(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead));
+    __syncwarp();
     tc::fence_after();
-    for (int k = 0; k < kt; ++k, ++it) {
-        const int s = it % C::kStages;
-        if (!tc::bar_wait_warp(tc::smem_u32(&sh.full[s]), (it / C::kStages) & 1, dead)) return false;
+    for (int k = 0; k < kt; ++k, ring.next()) {
+        ok = ok && tc::bar_wait(tc::smem_u32(&sh.full[ring.s]), ring.round, dead);
+        __syncwarp();
         tc::fence_after();
-        if (tc::elect()) {
+        if (tc::elect() && ok) {
             // the last stage holds only what is left of k
-            multiply_stage(st, s, a * BN, min(4, (len - k * kStageK + 31) / 32), k == 0);
-            tc::commit<kPair>(tc::smem_u32(&sh.empty[s]));
+            multiply_stage(st, ring.s, a * BN, (len - k * kStageK + 31) / 32, k > 0);
+            tc::commit<kPair>(tc::smem_u32(&sh.empty[ring.s]));
             if (k == kt - 1) tc::commit<kPair>(tc::smem_u32(&sh.acc_full[a]));
         }
         __syncwarp();
+        ring.issued += ok;
     }
-    return true;
 }
 
 // One stage's copies by the (converged) loading warp: 128 rows of A's codes, the
 // block's rows of B's, and the scale tiles, at (x, row) and (0, tile) of their
-// maps.  False: a wait ran out.
+// maps.
 struct StageAt {
     const CUtensorMap *a, *b, *sa, *sb;
     int x, a_row, b_row, a_tile, b_tile, b_tile_step;   // step: between the 128-row groups of B's scales
 };
-template <bool NV, int BN, bool kPair>
-__device__ __forceinline__ bool load_stage(Barriers &sh, const Stages<NV, BN, kPair> &st, int half, int it, const StageAt &w) {
+template <bool NV, int BN, bool kPair, typename R>
+__device__ __forceinline__ void load_stage(Barriers &sh, const Stages<NV, BN, kPair> &st, int half, R &ring, const StageAt &w,
+                                           bool &ok) {
     using C = Cfg<NV, BN, kPair>;
-    const int s = it % C::kStages;
-    if (it >= C::kStages && !tc::bar_wait_warp(tc::smem_u32(&sh.empty[s]), (it / C::kStages - 1) & 1, &sh.dead)) return false;
+    const int s = ring.s;
+    ok = ok && tc::bar_wait(tc::smem_u32(&sh.empty[s]), ring.round ^ 1, &sh.dead);   // the first round passes
+    __syncwarp();
     const uint32_t own = tc::smem_u32(&sh.full[s]), bar = kPair ? tc::map_to(own, 0) : own;
     auto load = [&](uint32_t dst, const CUtensorMap *tm, int x, int y) {
         if (kPair) tc::load_2d_pair(dst, tm, x, y, bar);
         else tc::load_2d(dst, tm, x, y, bar);
     };
-    if (tc::elect()) {
+    if (tc::elect() && ok) {
         if (half == 0) tc::bar_expect(own, kPair ? 2 * C::kStageBytes : C::kStageBytes);
         load(st.a(s), w.a, w.x, w.a_row);
         load(st.b(s), w.b, w.x, w.b_row);
@@ -433,7 +450,27 @@ __device__ __forceinline__ bool load_stage(Barriers &sh, const Stages<NV, BN, kP
         for (int b = 0; b < C::kGroupsB; ++b) load(st.sb(s) + b * C::kSc * kScaleTile, w.sb, 0, w.b_tile + b * w.b_tile_step);
     }
     __syncwarp();
-    return true;
+    ring.issued += ok;
+    ring.next();
+}
+
+// The same parts of a later tile's stage into L2: units that run side by side share
+// its rows and columns, so one of them asks memory for A, one for B, and all find them
+// there a tile later.
+template <bool NV, int BN, bool kPair> __device__ __forceinline__ void prefetch_stage(const StageAt &w, bool a, bool b) {
+    using C = Cfg<NV, BN, kPair>;
+    if ((a || b) && tc::elect()) {
+        if (a) {
+            tc::prefetch_2d(w.a, w.x, w.a_row);
+            tc::prefetch_2d(w.sa, 0, w.a_tile);
+        }
+        if (b) {
+            tc::prefetch_2d(w.b, w.x, w.b_row);
+#pragma unroll
+            for (int g = 0; g < C::kGroupsB; ++g) tc::prefetch_2d(w.sb, 0, w.b_tile + g * w.b_tile_step);
+        }
+    }
+    __syncwarp();
 }
 
 // After a wait of the loading warp ran out.
@@ -496,9 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
             tc::prefetch_map(&P.tm_a);
             tc::prefetch_map(&P.tm_b);
         }
-        int g = 0, it = 0;
-        bool ok = true;
-        for (int64_t i = unit; i < used && ok; i += units) {
+        Ring<C::kStages> ring;
+        int g = 0;
+        bool ok = true, first_row = false, first_col = false;   // of the tile: the first of its row tile, of its columns
+        auto at = [&](int64_t i) {
             const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
             StageAt w{&P.tm_a, &P.tm_b, &P.tm_sa, &P.tm_sb, 0};
@@ -507,19 +545,31 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
             w.b_row = uniform(static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN)) + half * C::kRowsB;
             w.b_tile = uniform((g * P.b_scale_rows + t.nt * C::kGroupsB) * P.scale_cols);
             w.b_tile_step = P.scale_cols;
-            for (int k = 0; k < P.kt && ok; ++k) {
-                ok = load_stage(sh, st, half, it, w);
-                it += ok;
+            first_row = uniform(t.nt) == 0;
+            first_col = uniform(t.mt) == 0;
+            return w;
+        };
+        StageAt w, next;
+        if (unit < used) next = at(unit);
+        for (int64_t i = unit; i < used; i += units) {
+            w = next;
+            const bool more = i + units < used;
+            if (more) next = at(i + units);
+            StageAt ahead = next;
+            for (int k = 0; k < P.kt; ++k) {
+                load_stage(sh, st, half, ring, w, ok);
+                if (more) prefetch_stage<NV, BN, kPair>(ahead, first_row, first_col);
                 w.x += kStageK, w.a_tile += C::kSc, w.b_tile += C::kSc;
+                ahead.x += kStageK, ahead.a_tile += C::kSc, ahead.b_tile += C::kSc;
             }
         }
-        if (!ok) settle_loads<C::kStages>(sh, half, it);
+        if (!ok) settle_loads<C::kStages>(sh, half, ring.issued);
     } else if (warp == 1 && half == 0) {
         const int mine = unit < used ? uniform(static_cast<int>((used - unit + units - 1) / units)) : 0;
-        int it = 0;
+        Ring<C::kStages> ring;
         bool ok = true;
-        for (int n = 0; n < mine && ok; ++n) ok = multiply_tile(sh, st, n, it, P.k_bytes);
-        if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, it);
+        for (int n = 0; n < mine; ++n) multiply_tile(sh, st, n, ring, P.k_bytes, ok);
+        if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, ring.issued);
     } else if (warp >= 4) {
         const int q = warp & 3, h = (warp - 4) >> 2;   // lanes 32 q .., column half h
         constexpr int kHalf = BN / 2;
@@ -749,9 +799,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
 
     if (warp == 0) {
         const int n128 = (P.N + 127) / 128, k128 = (P.K + 127) / 128;
-        int it = 0, last = -1;
+        Ring<C::kStages> ring;
+        int last = -1;
         bool ok = true;
-        while (ok && next_wtile(P, sh, r, unit, units, total, t)) {
+        while (next_wtile(P, sh, r, unit, units, total, t)) {
             const int e = uniform(t.e), nt = uniform(t.nt), kt = uniform(t.kt);
             const int len = uniform(static_cast<int>(NV ? t.rows / 2 : t.rows)), cols = uniform(static_cast<int>(t.rows / kBlock));
             const int wide0 = uniform(sh.pads.wide0[e]), wide = uniform(sh.pads.wide0[e + 1]) - wide0;
@@ -769,27 +820,27 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
             w.b_tile = wide0 * k128 + b_group * wide;
             w.b_tile_step = wide;
             const int stages = (len + kStageK - 1) / kStageK;
-            for (int k = 0; k < stages && ok; ++k) {
+            for (int k = 0; k < stages; ++k) {
                 if (NV && k == stages - 1 && cols % 4 != 0) {
                     w.sa = &P.tm_ta, w.sb = &P.tm_tb;
                     w.a_tile = (e * n128 + a_group) * 4;
                     w.b_tile = (e * k128 + b_group) * 4;
                     w.b_tile_step = 4;
                 }
-                ok = load_stage(sh, st, half, it, w);
-                it += ok;
+                load_stage(sh, st, half, ring, w, ok);
                 w.x += kStageK, w.a_tile += C::kSc, w.b_tile += C::kSc;
             }
         }
-        if (!ok) settle_loads<C::kStages>(sh, half, it);
+        if (!ok) settle_loads<C::kStages>(sh, half, ring.issued);
     } else if (warp == 1 && half == 0) {
-        int it = 0, n = 0;
+        Ring<C::kStages> ring;
+        int n = 0;
         bool ok = true;
-        while (ok && next_wtile(P, sh, r, unit, units, total, t)) {
+        while (next_wtile(P, sh, r, unit, units, total, t)) {
             const int len = uniform(static_cast<int>(NV ? t.rows / 2 : t.rows));
-            if (len > 0) ok = multiply_tile(sh, st, n++, it, len);
+            if (len > 0) multiply_tile(sh, st, n++, ring, len, ok);
         }
-        if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, it);
+        if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, ring.issued);
     } else if (warp >= 4) {
         const int q = warp & 3, h = (warp - 4) >> 2;
         constexpr int kHalf = BN / 2;

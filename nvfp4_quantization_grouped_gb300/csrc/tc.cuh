@@ -109,6 +109,11 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *tm, int
         : "memory");
 }
 
+// Brings what load_2d would copy into L2.
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *tm, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tm), "r"(x), "r"(y) : "memory");
+}
+
 // Into this block's shared memory; the bytes count on a barrier of the pair's first block.
 __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap *tm, int x, int y, uint32_t cluster_bar) {
     asm volatile(
@@ -209,54 +214,56 @@ template <bool kPair> __device__ __forceinline__ void commit(uint32_t bar) {
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Shared-memory matrix descriptor (tcgen05): rows of 128 bytes in the 128-byte
-// swizzle, 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
-    return (static_cast<uint64_t>(addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// 32 rows of 16 bytes without swizzle, 8-row groups 128 bytes apart: one 512-byte scale tile.
-__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
-    return (static_cast<uint64_t>(addr & 0x3FFFFu) >> 4) | (8ull << 16) | (8ull << 32) | (1ull << 46);
-}
+// Shared-memory matrix descriptors: the low word is the address in units of 16 bytes, which is all that changes
+// from step to step; the rest is constant.
+constexpr uint32_t kDescLo = 1u << 16;                             // (leading offset: unused)
+constexpr uint32_t kDescSw128 = 64u | (1u << 14) | (2u << 29);     // rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart
+constexpr uint32_t kDescScales = 8u | (1u << 14);                  // 32 rows of 16 bytes, 8-row groups 128 bytes apart: a 512-byte scale tile
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr >> 4) | kDescLo; }
 
 // One scale tile (128 rows x 4 scales) into 4 columns of tensor memory, repeated for the four lane quarters.
-template <bool kPair> __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-    if constexpr (kPair) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-    else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+template <bool kPair> __device__ __forceinline__ void copy_scales(uint32_t tmem, uint32_t lo) {
+    if constexpr (kPair)
+        asm volatile("{\n .reg .b64 a;\n mov.b64 a, {%1, %2};\n tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], a;\n}" ::"r"(tmem), "r"(lo),
+                     "n"(kDescScales)
+                     : "memory");
+    else
+        asm volatile("{\n .reg .b64 a;\n mov.b64 a, {%1, %2};\n tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], a;\n}" ::"r"(tmem), "r"(lo),
+                     "n"(kDescScales)
+                     : "memory");
 }
 
-// D += A B^T with block scales: E4M3 with one E8M0 scale per 32 (32 elements of K) ...
+// D += A B^T (add: else D =) with block scales: E4M3 with one E8M0 scale per 32 (32 elements of K) ...
 template <bool kPair>
-__device__ __forceinline__ void mma_mxf8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
+__device__ __forceinline__ void mma_mxf8(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t add) {
     if constexpr (kPair)
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(add))
+            "{\n .reg .b64 a, b;\n .reg .pred p;\n mov.b64 a, {%1, %7};\n mov.b64 b, {%2, %7};\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%4], [%5], p;\n}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add), "n"(kDescSw128)
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(add))
+            "{\n .reg .b64 a, b;\n .reg .pred p;\n mov.b64 a, {%1, %7};\n mov.b64 b, {%2, %7};\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, [%4], [%5], p;\n}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add), "n"(kDescSw128)
             : "memory");
 }
 
 // ... and E2M1 with one E4M3 scale per 16 (64 elements of K).
 template <bool kPair>
-__device__ __forceinline__ void mma_nvf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
+__device__ __forceinline__ void mma_nvf4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t add) {
     if constexpr (kPair)
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(add))
+            "{\n .reg .b64 a, b;\n .reg .pred p;\n mov.b64 a, {%1, %7};\n mov.b64 b, {%2, %7};\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %3, [%4], [%5], p;\n}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add), "n"(kDescSw128)
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(add))
+            "{\n .reg .b64 a, b;\n .reg .pred p;\n mov.b64 a, {%1, %7};\n mov.b64 b, {%2, %7};\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %3, [%4], [%5], p;\n}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(add), "n"(kDescSw128)
             : "memory");
 }
 
