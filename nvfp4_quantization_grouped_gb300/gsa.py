@@ -505,15 +505,19 @@ def bwd_graph_safe(dy, x, probs, split_dev, act: str, recipe_kind: int, rht: boo
 
 BF16, FP16, FP32 = 0, 1, 2
 _torch = None
+_raw_stream = None
 _DTYPES: dict = {}
 
 
 def _setup():
     """The torch module, imported on the first call, and the element type codes."""
-    global _torch
+    global _torch, _raw_stream
     import torch
     _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
     load()
+    # the current stream's handle without a Stream object (2 us), where this torch has the call
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
     _torch = torch
     return torch
 
@@ -539,7 +543,7 @@ def _stream_of(stream, device, *inputs):
     """Handle of `stream`, or of the device's current one.  Inputs of a call on an explicit stream are recorded on
     it, so that the caching allocator keeps them until the stream is done with them."""
     if stream is None:
-        return _torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(device.index)
     for t in inputs:
         if t is not None:
             t.record_stream(stream)
