@@ -43,7 +43,7 @@ enum { ERR_SPLIT = 1, ERR_TIMEOUT = 2 };
 __device__ uint32_t g_status;
 
 struct GemmParams {
-    CUtensorMap tm_a, tm_b, tm_sa, tm_sb, tm_out;
+    CUtensorMap tm_a, tm_b, tm_sa, tm_sb;
     const int64_t *split;
     const float *amax_a, *amax_b;
     void *out;
@@ -56,7 +56,6 @@ struct GemmParams {
     int b_scale_rows;      // scale tiles along N per expert
     int scale_cols;        // scale tiles along k
     int64_t a_scale_tiles; // row tiles that A's scale buffer holds
-    int tma_out;           // out's rows suit TMA
 };
 
 template <bool NV> struct Fmt;
@@ -159,45 +158,6 @@ template <int kRows> __device__ __forceinline__ Tile tile_at(const GemmParams &P
     return t;
 }
 
-// 32 bytes of results at o.  align: the bytes that o is aligned to (32, 16 or less); n: how many of the results
-// there are (at most 32 bytes of them).
-__device__ __forceinline__ void store_raw(uint8_t *o, const uint32_t *w, int align) {
-    if (align == 32)
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    else {
-        *reinterpret_cast<uint4 *>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4 *>(o + 16) = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-}
-
-__device__ __forceinline__ void store_some(__nv_bfloat16 *o, const uint32_t *w, int n, int align) {
-    if (n >= 16 && align >= 16) {
-        store_raw(reinterpret_cast<uint8_t *>(o), w, align);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (i < n) reinterpret_cast<uint16_t *>(o)[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
-}
-
-__device__ __forceinline__ void store_some(float *o, const uint32_t *w, int n, int align) {
-    if (n >= 8 && align >= 16) {
-        store_raw(reinterpret_cast<uint8_t *>(o), w, align);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) o[i] = __uint_as_float(w[i]);
-}
-
-// Largest of 32, 16 and 1 that every row start of out [.., n] is aligned to.
-template <typename T> __device__ __forceinline__ int row_align(const T *out, int64_t n) {
-    const uint64_t x = reinterpret_cast<uint64_t>(out) | static_cast<uint64_t>(n * static_cast<int64_t>(sizeof(T)));
-    return x % 32 == 0 ? 32 : x % 16 == 0 ? 16 : 1;
-}
-
 // Where a stage's parts lie in shared memory.
 template <bool NV, int BN, bool kPair> struct Stages {
     using C = Cfg<NV, BN, kPair>;
@@ -278,111 +238,103 @@ template <bool kPair> __device__ __forceinline__ void close_block(Barriers &sh, 
     if (threadIdx.x == 0 && sh.dead) atomicOr(&g_status, ERR_TIMEOUT);
 }
 
-// 32 bytes of results: accumulators times ua and ub (kScale), rounded to T.
-template <bool kScale> __device__ __forceinline__ void finish(const uint32_t *v, float ua, float ub, uint32_t (&w)[8], float) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = kScale ? __float_as_uint(__uint_as_float(v[i]) * ua * ub) : v[i];
-}
-template <bool kScale>
-__device__ __forceinline__ void finish(const uint32_t *v, float ua, float ub, uint32_t (&w)[8], __nv_bfloat16) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = __uint_as_float(v[2 * i]), y = __uint_as_float(v[2 * i + 1]);
-        const __nv_bfloat162 h = kScale ? __floats2bfloat162_rn(x * ua * ub, y * ua * ub) : __floats2bfloat162_rn(x, y);
-        memcpy(&w[i], &h, 4);
-    }
-}
-
-// The same onto the n values at o.
-__device__ __forceinline__ void finish_add(const float *o, const uint32_t *v, float ua, float ub, int n, uint32_t (&w)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint((i < n ? o[i] : 0.0f) + __uint_as_float(v[i]) * ua * ub);
-}
-__device__ __forceinline__ void finish_add(const __nv_bfloat16 *o, const uint32_t *v, float ua, float ub, int n,
-                                           uint32_t (&w)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = 2 * i < n ? __bfloat162float(o[2 * i]) : 0.0f, y = 2 * i + 1 < n ? __bfloat162float(o[2 * i + 1]) : 0.0f;
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x + __uint_as_float(v[2 * i]) * ua * ub,
-                                                       y + __uint_as_float(v[2 * i + 1]) * ua * ub);
-        memcpy(&w[i], &h, 4);
-    }
-}
-
-// Results of one lane, kHalf columns from `cols` on of row `o`, by row stores (rows that TMA does not suit, tiles cut
-// by an expert's last row, BF16 sums onto what is there).
-template <int kHalf, bool kScale, typename T>
-__device__ __forceinline__ void store_lane(const uint32_t *v, float ua, float ub, T *o, int64_t cols, int align, bool add) {
-    constexpr int kPer = 32 / sizeof(T);
-#pragma unroll
-    for (int j = 0; j < kHalf; j += kPer) {
-        if (j >= cols) break;
-        const int n = cols - j < kPer ? static_cast<int>(cols - j) : kPer;
-        uint32_t w[8];
-        if (add) finish_add(o + j, v + j, ua, ub, n, w);
-        else finish<kScale>(v + j, ua, ub, w, T());
-        store_some(o + j, w, n, align);
-    }
-}
-
-// Results of a warp, 32 rows x kHalf columns at (x, y, z) of out's map, in pieces of
-// 32 rows x 128 bytes through shared memory: each lane writes its row's chunk c to c ^
-// (row mod 8), no two lanes of a quarter to the same banks, and TMA takes the piece
-// away (and clips it).  A row store by 32 lanes costs 32 passes of the pipe that also
-// feeds the tensor core: 4.5K (BF16) and 9.2K (FP32) cycles a tile of 128 x 256, against
-// 594 a stage for the operands.  One buffer a warp: a second one would cost a stage
-// of operands (125 us with one fewer, product of 65536 x 2048 x 2048 NVFP4).
-template <int kHalf, bool kScale, typename T>
-__device__ __forceinline__ void store_warp(const uint32_t *v, float ua, float ub, uint32_t buf, const CUtensorMap *tm,
-                                           int x, int y, int z, int64_t cols, int lane, bool add) {
-    constexpr int kPer = 32 / sizeof(T), kPiece = 128 / sizeof(T);
-#pragma unroll
-    for (int j = 0; j < kHalf; j += kPiece) {
-        if (j >= cols) break;
-        if (lane == 0) tc::store_wait_read();
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t w[8];
-            finish<kScale>(v + j + c * kPer, ua, ub, w, T());
-            tc::st_shared(buf + lane * 128 + (((2 * c) ^ (lane & 7)) << 4), w);
-            tc::st_shared(buf + lane * 128 + (((2 * c + 1) ^ (lane & 7)) << 4), w + 4);
-        }
-        tc::fence_async();
-        __syncwarp();
-        if (lane == 0) {
-            if (add) tc::add_3d(tm, x + j, y, z, buf);
-            else tc::store_3d(tm, x + j, y, z, buf);
-            tc::store_commit();
-        }
-    }
-}
-
-// Where the results of one tile go: a lane's row (o, with `cols` columns from there on; on: it has one), and the
-// warp's 32 rows in out's map where TMA takes them.
+// Where the results of a warp go: its first row (o; 32 rows of `pitch` elements, `rows` of them its own), from the
+// tile's column on (`cols` of them are left).  add: onto what is there.  wide: rows start on 16 bytes.
 template <typename T> struct OutAt {
     T *o;
-    int64_t cols;
-    const CUtensorMap *tm;
-    int x, y, z;
-    bool on, tma, add;
-    int align;
+    int64_t pitch, cols;
+    int rows;
+    bool add, wide;
 };
 
+// 16 bytes of results: accumulators times ua and ub (kScale), rounded to T.
+template <bool kScale> __device__ __forceinline__ float scaled(uint32_t v, float ua, float ub) {
+    const float f = __uint_as_float(v);
+    return kScale ? f * ua * ub : f;
+}
+template <bool kScale> __device__ __forceinline__ void finish(const uint32_t *v, float ua, float ub, uint32_t (&w)[4], float) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(scaled<kScale>(v[i], ua, ub));
+}
+template <bool kScale>
+__device__ __forceinline__ void finish(const uint32_t *v, float ua, float ub, uint32_t (&w)[4], __nv_bfloat16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(scaled<kScale>(v[2 * i], ua, ub), scaled<kScale>(v[2 * i + 1], ua, ub));
+        memcpy(&w[i], &h, 4);
+    }
+}
+
+// Results of a warp, a row of kHalf columns in each lane, to memory by way of shared
+// memory: 32 rows x 128 bytes at a time, each lane writing its row's 16-byte chunk c to
+// c ^ (row mod 8) and reading back so that eight lanes hold 128 consecutive bytes of one
+// row: no bank conflicts either way, whole lines to memory.
+//   Rows straight from the lanes cost 32 passes of the load/store pipe an instruction,
+// 4.5K (BF16) and 9.2K (FP32) cycles for a tile of 128 x 256.  TMA stores take 129 cycles
+// for 4 KB and the operands' copies wait behind them in the same unit (a stage of 32 KB
+// 331 -> 1191 cycles).
 template <int kHalf, bool kScale, typename T>
-__device__ __forceinline__ void store_tile(const uint32_t *v, float ua, float ub, const OutAt<T> &w, uint32_t buf,
-                                           int lane) {
-    if (w.tma) store_warp<kHalf, kScale, T>(v, ua, ub, buf, w.tm, w.x, w.y, w.z, w.cols, lane, w.add);
-    else if (w.on) store_lane<kHalf, kScale, T>(v, ua, ub, w.o, w.cols, w.align, w.add);
+__device__ __forceinline__ void store_warp(const uint32_t *v, float ua, float ub, uint32_t buf, const OutAt<T> &w, int lane) {
+    constexpr int kPer = 16 / sizeof(T), kPiece = 8 * kPer;
+#pragma unroll
+    for (int j = 0; j < kHalf; j += kPiece) {
+        if (j >= w.cols) break;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint32_t x[4];
+            finish<kScale>(v + j + c * kPer, ua, ub, x, T());
+            tc::st_shared(buf + lane * 128 + ((c ^ (lane & 7)) << 4), x);
+        }
+        __syncwarp();
+        const int q = lane & 7, col = j + q * kPer;
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 4) {
+            const int r = r0 + (lane >> 3);
+            const uint4 x = tc::ld_shared(buf + r * 128 + ((q ^ (r & 7)) << 4));
+            if (r < w.rows && col < w.cols) *reinterpret_cast<uint4 *>(w.o + r * w.pitch + col) = x;
+        }
+        __syncwarp();
+    }
+}
+
+// The same for rows that do not start on 16 bytes and for results onto what is there (added in FP32, rounded once):
+// 32 rows x 32 columns at a time in FP32, a column a lane.
+template <int kHalf, bool kScale, typename T>
+__device__ __forceinline__ void store_warp_any(const uint32_t *v, float ua, float ub, uint32_t buf, const OutAt<T> &w, int lane) {
+#pragma unroll
+    for (int j = 0; j < kHalf; j += 32) {
+        if (j >= w.cols) break;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint32_t x[4];
+            finish<kScale>(v + j + c * 4, ua, ub, x, float());
+            tc::st_shared(buf + lane * 128 + ((c ^ (lane & 7)) << 4), x);
+        }
+        __syncwarp();
+        if (j + lane < w.cols) {
+            T *o = w.o + j + lane;
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+                if (r >= w.rows) break;
+                float f = tc::ld_shared1(buf + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3));
+                if (w.add) f += static_cast<float>(o[r * w.pitch]);
+                o[r * w.pitch] = static_cast<T>(f);
+            }
+        }
+        __syncwarp();
+    }
 }
 
 // A tile without products.
-template <int kHalf, typename T>
-__device__ __forceinline__ void zero_tile(const OutAt<T> &w, uint32_t buf, int lane) {
-    uint32_t v[kHalf];
-#pragma unroll
-    for (int i = 0; i < kHalf; ++i) v[i] = 0;
-    store_tile<kHalf, false, T>(v, 1.0f, 1.0f, w, buf, lane);
+template <int kHalf, typename T> __device__ __forceinline__ void zero_tile(const OutAt<T> &w, int lane) {
+    constexpr int kPer = 16 / sizeof(T);
+    for (int r = 0; r < 32 && r < w.rows; ++r) {
+        T *o = w.o + r * w.pitch;
+        if (w.wide)
+            for (int c = lane * kPer; c < kHalf && c < w.cols; c += 32 * kPer) *reinterpret_cast<uint4 *>(o + c) = make_uint4(0, 0, 0, 0);
+        else
+            for (int c = lane; c < kHalf && c < w.cols; c += 32) o[c] = static_cast<T>(0.0f);
+    }
 }
 
 // A role's place in the ring of stages: the stage, the parity of the round, and how many were issued (for settle).
@@ -481,16 +433,17 @@ template <int kStages> __device__ __forceinline__ void settle_loads(Barriers &sh
 
 // The finished accumulator of the unit's n-th tile to memory by one draining warp.
 // It is handed back as soon as it is in registers: scaling, rounding and stores run
-// while the next tile is multiplied.  False: a wait ran out.
-template <bool NV, int BN, bool kPair, typename T>
-__device__ __forceinline__ bool drain_tile(Barriers &sh, int n, int warp, int lane, const float *amax_a, const float *amax_b,
-                                           int g, const OutAt<T> &w, uint32_t buf) {
+// while the next tile is multiplied.  ahead(): what the next tile needs from memory,
+// asked for before the stores.  False: a wait ran out.
+template <bool NV, int BN, bool kPair, typename T, typename F>
+__device__ __forceinline__ bool drain_tile(Barriers &sh, int n, int warp, int lane, float amax_a, float amax_b, const OutAt<T> &w,
+                                           uint32_t buf, F &&ahead) {
     using C = Cfg<NV, BN, kPair>;
     const int a = n % C::kAcc, q = warp & 3, h = (warp - 4) >> 2;
     float ua = 1.0f, ub = 1.0f;
     if (NV) {
-        ua = __fdiv_rn(1.0f, tensor_scale(amax_a[g]));
-        ub = __fdiv_rn(1.0f, tensor_scale(amax_b[g]));
+        ua = __fdiv_rn(1.0f, tensor_scale(amax_a));
+        ub = __fdiv_rn(1.0f, tensor_scale(amax_b));
     }
     if (!tc::bar_wait_warp(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, &sh.dead)) return false;
     tc::fence_after();
@@ -503,7 +456,10 @@ __device__ __forceinline__ bool drain_tile(Barriers &sh, int n, int warp, int la
         if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
         else tc::bar_arrive(bar);
     }
-    store_tile<BN / 2, NV, T>(v, ua, ub, w, buf, lane);
+    const OutAt<T> here = w;
+    ahead();
+    if (here.wide && !here.add) store_warp<BN / 2, NV, T>(v, ua, ub, buf, here, lane);
+    else store_warp_any<BN / 2, NV, T>(v, ua, ub, buf, here, lane);
     return true;
 }
 
@@ -577,25 +533,30 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
         const int r0 = half * kRowsT + 32 * q;   // the warp's first row of the tile
         const uint32_t buf = st.out(warp - 4);
         OutAt<T> w;
-        w.tm = &P.tm_out;
-        w.align = row_align(out, P.N);
+        w.pitch = P.N;
+        w.wide = P.N * sizeof(T) % 16 == 0;
         w.add = false;
-        w.z = 0;
         int g = 0, n = 0;
-        for (int64_t i = unit; i < total; i += units) {
+        float amax_a = 0.0f, amax_b = 0.0f;
+        auto find = [&](int64_t i) {
+            if (i >= total) return;
             const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
             const int64_t c0 = static_cast<int64_t>(t.nt) * BN + h * kHalf;
-            w.o = out + static_cast<int64_t>(t.row + r0 + lane) * P.N + c0;
+            w.o = out + static_cast<int64_t>(t.row + r0) * P.N + c0;
             w.cols = P.N - c0;
-            w.on = r0 + lane < t.rows;
-            w.tma = P.tma_out && r0 + 32 <= t.rows;   // an expert's last rows are not the warp's to write past
-            w.x = static_cast<int>(c0);
-            w.y = t.row + r0;
-            if (g == P.E) zero_tile<kHalf>(w, buf, lane);
-            else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, g, w, buf)) break;
+            w.rows = t.rows - r0;
+            if (NV && g < P.E) amax_a = P.amax_a[g], amax_b = P.amax_b[g];
+        };
+        find(unit);
+        for (int64_t i = unit; i < total; i += units) {
+            if (g == P.E) {
+                zero_tile<kHalf>(w, lane);
+                find(i + units);
+            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, amax_a, amax_b, w, buf, [&] { find(i + units); })) {
+                break;
+            }
         }
-        if (lane == 0) tc::store_wait_read();
     }
     close_block<kPair>(sh, warp, C::kCols);
 }
@@ -620,7 +581,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
 
 struct WgradParams {
     CUtensorMap tm_sa, tm_sb, tm_ta, tm_tb;   // scale tiles; the tail copies of the last stages'
-    CUtensorMap tm_out;
     const uint8_t *a, *b, *sa, *sb;
     const int64_t *split;
     const float *amax_a, *amax_b;
@@ -632,7 +592,7 @@ struct WgradParams {
     int N, K, E;
     int n_tiles, k_tiles;              // tiles along N and K
     int64_t a_bytes, b_bytes, sa_bytes, sb_bytes;
-    int accumulate, tma_out;
+    int accumulate;
 };
 
 struct Pads {
@@ -707,20 +667,29 @@ __global__ void __launch_bounds__(kPrepThreads) wgrad_prepare(const __grid_const
     }
     if (!NV) return;
     const int warp = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kPrepThreads / 32);
-    const int lane = threadIdx.x & 31, both = P.N + P.K;
-    // rows of odd pitch: 8-byte halves (a row starts on 8 bytes), 16-byte stores
-    for (int64_t i = warp; i < static_cast<int64_t>(P.E) * both; i += warps) {
-        const int e = static_cast<int>(i / both), j = static_cast<int>(i - static_cast<int64_t>(e) * both);
+    const int lane = threadIdx.x & 31;
+    // rows of odd pitch, four at a time a warp: 8-byte halves (a row starts on 8 bytes), 16-byte stores
+    constexpr int kBatch = 4;
+    const int na = (P.N + kBatch - 1) / kBatch, batches = na + (P.K + kBatch - 1) / kBatch;
+    for (int64_t i = warp; i < static_cast<int64_t>(P.E) * batches; i += warps) {
+        const int e = static_cast<int>(i / batches), j = static_cast<int>(i - static_cast<int64_t>(e) * batches);
         const int64_t pitch = (d.pad0[e + 1] - d.pad0[e]) / 2;
         if (pitch % 16 == 0) continue;
-        const bool is_a = j < P.N;
-        const int r = is_a ? j : j - P.N, rows = is_a ? P.N : P.K;
+        const bool is_a = j < na;
+        const int r = (is_a ? j : j - na) * kBatch, rows = is_a ? P.N : P.K;
         const uint8_t *src = (is_a ? P.a : P.b) + static_cast<int64_t>(d.pad0[e] / 2) * rows + r * pitch;
         uint8_t *dst = (is_a ? P.pack_a : P.pack_b) + pack_at(d, e) * rows + r * (pitch + 8);
         for (int64_t c = 16 * lane; c < pitch; c += 512) {
-            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src + c));
-            const uint2 y = c + 8 < pitch ? __ldg(reinterpret_cast<const uint2 *>(src + c + 8)) : make_uint2(0, 0);
-            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(x.x, x.y, y.x, y.y);
+            uint2 x[kBatch], y[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const bool in = r + b < rows;
+                x[b] = in ? __ldcs(reinterpret_cast<const uint2 *>(src + b * pitch + c)) : make_uint2(0, 0);
+                y[b] = in && c + 8 < pitch ? __ldcs(reinterpret_cast<const uint2 *>(src + b * pitch + c + 8)) : make_uint2(0, 0);
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (r + b < rows) *reinterpret_cast<uint4 *>(dst + b * (pitch + 8) + c) = make_uint4(x[b].x, x[b].y, y[b].x, y[b].y);
         }
     }
     // the last stages' scale tiles, zeros past the expert's scales
@@ -751,17 +720,17 @@ __global__ void __launch_bounds__(kPrepThreads) wgrad_prepare(const __grid_const
 // long and short sums even out.
 struct WTile {
     int e, nt, kt;
-    int64_t rows;   // padded rows of the expert
+    int rows;   // padded rows of the expert
 };
 // The unit's next tile from round r on: false when there is none.
-__device__ __forceinline__ bool next_wtile(const WgradParams &P, const WgradShared &sh, int64_t &r, int unit, int units,
-                                           int64_t total, WTile &t) {
+__device__ __forceinline__ bool next_wtile(const WgradParams &P, const WgradShared &sh, uint32_t &r, uint32_t unit, uint32_t units,
+                                           uint32_t total, WTile &t) {
     for (;; ++r) {
         if (r * units >= total) return false;
-        const int64_t i = r * units + ((r & 1) ? units - 1 - unit : unit);
+        const uint32_t i = r * units + ((r & 1) ? units - 1 - unit : unit);
         if (i >= total) continue;
         ++r;
-        const int per = P.n_tiles * P.k_tiles, x = static_cast<int>(i / per), j = static_cast<int>(i - static_cast<int64_t>(x) * per);
+        const uint32_t per = P.n_tiles * P.k_tiles, x = i / per, j = i - x * per;
         t.e = sh.order[x];
         t.nt = j / P.k_tiles;
         t.kt = j - t.nt * P.k_tiles;
@@ -791,11 +760,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
     }
     const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x, units = kPair ? gridDim.x >> 1 : gridDim.x;
     const int half = kPair ? blockIdx.x & 1 : 0;
-    const int64_t total = static_cast<int64_t>(P.E) * P.n_tiles * P.k_tiles;
+    const uint32_t total = static_cast<uint32_t>(P.E) * P.n_tiles * P.k_tiles;
     const Stages<NV, BN, kPair> st(dyn);
     open_block<C::kStages, kPair>(sh, warp, 1, C::kCols);
     WTile t;
-    int64_t r = 0;
+    uint32_t r = 0;
 
     if (warp == 0) {
         const int n128 = (P.N + 127) / 128, k128 = (P.K + 127) / 128;
@@ -804,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
         bool ok = true;
         while (next_wtile(P, sh, r, unit, units, total, t)) {
             const int e = uniform(t.e), nt = uniform(t.nt), kt = uniform(t.kt);
-            const int len = uniform(static_cast<int>(NV ? t.rows / 2 : t.rows)), cols = uniform(static_cast<int>(t.rows / kBlock));
+            const int len = uniform(NV ? t.rows / 2 : t.rows), cols = uniform(t.rows / kBlock);
             const int wide0 = uniform(sh.pads.wide0[e]), wide = uniform(sh.pads.wide0[e + 1]) - wide0;
             if (len == 0) continue;
             StageAt w{P.maps + e, P.maps + P.E + e, &P.tm_sa, &P.tm_sb, 0};
@@ -837,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
         int n = 0;
         bool ok = true;
         while (next_wtile(P, sh, r, unit, units, total, t)) {
-            const int len = uniform(static_cast<int>(NV ? t.rows / 2 : t.rows));
+            const int len = uniform(NV ? t.rows / 2 : t.rows);
             if (len > 0) multiply_tile(sh, st, n++, ring, len, ok);
         }
         if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, ring.issued);
@@ -847,28 +816,30 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
         T *out = static_cast<T *>(P.out);
         const uint32_t buf = st.out(warp - 4);
         OutAt<T> w;
-        w.tm = &P.tm_out;
-        w.align = row_align(out, P.K);
+        w.pitch = P.K;
+        w.wide = P.K * sizeof(T) % 16 == 0;
         w.add = P.accumulate != 0;
-        // onto what is there: in FP32 the memory adds, in BF16 that would round twice
-        const bool tma = P.tma_out && !(w.add && sizeof(T) == 2);
         int n = 0;
-        while (next_wtile(P, sh, r, unit, units, total, t)) {
+        float amax_a = 0.0f, amax_b = 0.0f;
+        bool more = true;
+        auto find = [&] {
+            more = next_wtile(P, sh, r, unit, units, total, t);
+            if (!more) return;
             const int row = t.nt * kRows + half * kRowsT + 32 * q, c0 = t.kt * BN + h * kHalf;
-            w.o = out + (static_cast<int64_t>(t.e) * P.N + row + lane) * P.K + c0;
+            w.o = out + (static_cast<int64_t>(t.e) * P.N + row) * P.K + c0;
             w.cols = static_cast<int64_t>(P.K) - c0;
-            w.on = row + lane < P.N;
-            w.tma = tma && row < P.N;   // the map ends with the expert's rows
-            w.x = c0;
-            w.y = row;
-            w.z = t.e;
+            w.rows = P.N - row;
+            if (NV) amax_a = P.amax_a[t.e], amax_b = P.amax_b[t.e];
+        };
+        find();
+        while (more) {
             if (t.rows == 0) {   // no rows: a zero gradient
-                if (!w.add) zero_tile<kHalf>(w, buf, lane);
-            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, P.amax_a, P.amax_b, t.e, w, buf)) {
+                if (!w.add) zero_tile<kHalf>(w, lane);
+                find();
+            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, amax_a, amax_b, w, buf, find)) {
                 break;
             }
         }
-        if (lane == 0) tc::store_wait_read();
     }
     close_block<kPair>(sh, warp, C::kCols);
 }
@@ -909,21 +880,6 @@ bool map_scales(CUtensorMap *tm, const void *p, int64_t tiles, int box) {
     cuuint32_t b[2] = {kScaleTile / 4, static_cast<cuuint32_t>(box)}, es[2] = {1, 1};
     return fn(tm, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void *>(p), dims, strides, b, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// out [planes, rows, cols]: pieces of 32 rows x 128 bytes.  tma: whether its rows suit TMA (16 bytes).
-bool map_out(CUtensorMap *tm, void *p, int64_t planes, int64_t rows, int64_t cols, int dtype, int *tma) {
-    const int es = dtype == GSA_BF16 ? 2 : 4;
-    *tma = cols * es % 16 == 0;
-    if (!*tma) return true;
-    auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols * es), static_cast<cuuint64_t>(rows * cols * es)};
-    cuuint32_t b[3] = {static_cast<cuuint32_t>(128 / es), 32, 1}, e[3] = {1, 1, 1};
-    return fn(tm, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims, strides, b, e,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1041,8 +997,7 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     const bool pair = M >= 64 * E;
     const int sc = nv ? 4 : 1;
     if (!map_codes(&P.tm_a, a->data, M, k_bytes, kRowsT) || !map_codes(&P.tm_b, b->data, E * N, k_bytes, pair ? BN / 2 : BN) ||
-        !map_scales(&P.tm_sa, a->scale, a_rows * cols, sc) || !map_scales(&P.tm_sb, b->scale, E * n128 * cols, sc) ||
-        !map_out(&P.tm_out, out, 1, M, N, out_dtype, &P.tma_out))
+        !map_scales(&P.tm_sa, a->scale, a_rows * cols, sc) || !map_scales(&P.tm_sb, b->scale, E * n128 * cols, sc))
         return GSA_ERR_CUDA;
     P.split = split_sizes_dev;
     P.amax_a = a->amax;
@@ -1107,7 +1062,7 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     const int sc = nv ? 4 : 1;
     CUtensorMap plain;   // the experts' maps but for origin, extents and pitch
     if (!map_codes(&plain, w, 4096, 4096, 128) || !map_scales(&P.tm_sa, a->scale, a_tiles, sc) ||
-        !map_scales(&P.tm_sb, b->scale, b_tiles, sc) || !map_out(&P.tm_out, dw, E, N, K, out_dtype, &P.tma_out) ||
+        !map_scales(&P.tm_sb, b->scale, b_tiles, sc) ||
         (nv && (!map_scales(&P.tm_ta, w + ws.tail_a, E * n128 * 4, 4) || !map_scales(&P.tm_tb, w + ws.tail_b, E * k128 * 4, 4))))
         return GSA_ERR_CUDA;
     P.a = static_cast<const uint8_t *>(a->data);
@@ -1136,7 +1091,7 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     P.sa_bytes = a->scale_bytes;
     P.sb_bytes = b->scale_bytes;
     P.accumulate = accumulate != 0;
-    if (static_cast<int64_t>(P.n_tiles) * P.k_tiles >= (int64_t(1) << 31)) return GSA_ERR_UNSUPPORTED;
+    if (E * P.n_tiles * static_cast<int64_t>(P.k_tiles) >= (int64_t(1) << 31) - 4096) return GSA_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int sms = sm_count();
     if (!sms) return GSA_ERR_CUDA;

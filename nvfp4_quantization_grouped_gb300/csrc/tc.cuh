@@ -95,6 +95,17 @@ __device__ __forceinline__ void st_shared(uint32_t at, const uint32_t *w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_shared1(uint32_t at) {
+    float f;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(at) : "memory");
+    return f;
+}
+
 // --------------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *tm) {
@@ -122,23 +133,6 @@ __device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap *tm
         "l"(tm), "r"(x), "r"(y), "r"(cluster_bar)
         : "memory");
 }
-
-// A 128-byte swizzled box from shared memory to a tensor (clipped to it), or added to what is there.
-__device__ __forceinline__ void store_3d(const CUtensorMap *tm, int x, int y, int z, uint32_t src) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tm), "r"(x), "r"(y),
-                 "r"(z), "r"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void add_3d(const CUtensorMap *tm, int x, int y, int z, uint32_t src) {
-    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tm),
-                 "r"(x), "r"(y), "r"(z), "r"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// This thread's store groups no longer read shared memory.
-__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-// Writes to shared memory so far become visible to copies and products.
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Origin, extents (bytes of a row, rows) and pitch of a tensor map of bytes in shared memory.
 __device__ __forceinline__ void edit_map(CUtensorMap *map, const void *p, uint32_t bytes, uint32_t rows, uint64_t pitch) {
