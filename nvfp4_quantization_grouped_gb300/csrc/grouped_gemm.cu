@@ -34,6 +34,7 @@ constexpr int kStageK = 128;         // bytes of k per stage: one 128-byte swizz
 constexpr int kScaleTile = 512;      // bytes of one 128 x 4 scale tile
 constexpr int kThreads = 384;        // warp 0 loads, warp 1 multiplies, warps 4-11 drain
 constexpr int kEpiWarps = 8;
+constexpr int kBoxA = 32;            // rows of A that single blocks load at a time
 constexpr int kOutBuf = 32 * 128;    // a draining warp's piece of results: 32 rows x 128 bytes
 constexpr int kStatic = 4096;        // what the blocks' static shared memory stays below
 
@@ -380,6 +381,7 @@ __device__ __forceinline__ void multiply_tile(Barriers &sh, const Stages<NV, BN,
 struct StageAt {
     const CUtensorMap *a, *b, *sa, *sb;
     int x, a_row, b_row, a_tile, b_tile, b_tile_step;   // step: between the 128-row groups of B's scales
+    int a_boxes;                                        // single blocks: boxes of 32 rows of A that the tile has
 };
 template <bool NV, int BN, bool kPair, typename R>
 __device__ __forceinline__ void load_stage(Barriers &sh, const Stages<NV, BN, kPair> &st, int half, R &ring, const StageAt &w,
@@ -394,8 +396,13 @@ __device__ __forceinline__ void load_stage(Barriers &sh, const Stages<NV, BN, kP
         else tc::load_2d(dst, tm, x, y, bar);
     };
     if (tc::elect() && ok) {
-        if (half == 0) tc::bar_expect(own, kPair ? 2 * C::kStageBytes : C::kStageBytes);
-        load(st.a(s), w.a, w.x, w.a_row);
+        if (kPair) {
+            if (half == 0) tc::bar_expect(own, 2 * C::kStageBytes);
+            load(st.a(s), w.a, w.x, w.a_row);
+        } else {   // the rows of a short tile only: the others' products go nowhere
+            tc::bar_expect(own, C::kStageBytes - (kRowsT / kBoxA - w.a_boxes) * kBoxA * kStageK);
+            for (int b = 0; b < w.a_boxes; ++b) load(st.a(s) + b * kBoxA * kStageK, w.a, w.x, w.a_row + b * kBoxA);
+        }
         load(st.b(s), w.b, w.x, w.b_row);
         load(st.sa(s), w.sa, 0, w.a_tile);
 #pragma unroll
@@ -413,7 +420,7 @@ template <bool NV, int BN, bool kPair> __device__ __forceinline__ void prefetch_
     using C = Cfg<NV, BN, kPair>;
     if ((a || b) && tc::elect()) {
         if (a) {
-            tc::prefetch_2d(w.a, w.x, w.a_row);
+            for (int i = 0; i < (kPair ? 1 : w.a_boxes); ++i) tc::prefetch_2d(w.a, w.x, w.a_row + i * kBoxA);
             tc::prefetch_2d(w.sa, 0, w.a_tile);
         }
         if (b) {
@@ -495,8 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
         auto at = [&](int64_t i) {
             const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
-            StageAt w{&P.tm_a, &P.tm_b, &P.tm_sa, &P.tm_sb, 0};
+            StageAt w{&P.tm_a, &P.tm_b, &P.tm_sa, &P.tm_sb};
+            w.x = 0;
             w.a_row = uniform(t.row) + half * kRowsT;
+            w.a_boxes = uniform((t.rows + kBoxA - 1) / kBoxA);
             w.a_tile = uniform((sh.scale0[g] + t.mt * (kRows / 128) + half) * P.scale_cols);
             w.b_row = uniform(static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN)) + half * C::kRowsB;
             w.b_tile = uniform((g * P.b_scale_rows + t.nt * C::kGroupsB) * P.scale_cols);
@@ -645,7 +654,8 @@ constexpr int kPrepThreads = 256;
 
 template <bool NV>
 __global__ void __launch_bounds__(kPrepThreads) wgrad_prepare(const __grid_constant__ WgradParams P,
-                                                              const __grid_constant__ CUtensorMap plain) {
+                                                              const __grid_constant__ CUtensorMap plain_a,
+                                                              const __grid_constant__ CUtensorMap plain_b) {
     __shared__ Pads d;
     __shared__ __align__(128) CUtensorMap map;
     constexpr int kBlock = NV ? 16 : 32;
@@ -659,7 +669,7 @@ __global__ void __launch_bounds__(kPrepThreads) wgrad_prepare(const __grid_const
             const bool odd = pitch % 16 != 0;
             const uint8_t *at = odd ? (i < P.E ? P.pack_a : P.pack_b) + pack_at(d, e) * rows
                                     : (i < P.E ? P.a : P.b) + first * rows;
-            map = plain;
+            map = i < P.E ? plain_a : plain_b;
             tc::edit_map(&map, at, static_cast<uint32_t>(pitch), static_cast<uint32_t>(rows), odd ? pitch + 8 : pitch);
             P.maps[i] = map;
         }
@@ -776,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
             const int len = uniform(NV ? t.rows / 2 : t.rows), cols = uniform(t.rows / kBlock);
             const int wide0 = uniform(sh.pads.wide0[e]), wide = uniform(sh.pads.wide0[e + 1]) - wide0;
             if (len == 0) continue;
-            StageAt w{P.maps + e, P.maps + P.E + e, &P.tm_sa, &P.tm_sb, 0};
+            StageAt w{P.maps + e, P.maps + P.E + e, &P.tm_sa, &P.tm_sb};
+            w.x = 0;
             if (e != last) {   // maps written by the kernel before
                 tc::acquire_map(w.a);
                 tc::acquire_map(w.b);
@@ -784,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
             }
             const int a_group = nt * (kRows / 128) + half, b_group = kt * C::kGroupsB;
             w.a_row = nt * kRows + half * kRowsT;
+            w.a_boxes = (min(kRowsT, P.N - w.a_row) + kBoxA - 1) / kBoxA;
             w.b_row = kt * BN + half * C::kRowsB;
             w.a_tile = wide0 * n128 + a_group * wide;
             w.b_tile = wide0 * k128 + b_group * wide;
@@ -993,10 +1005,14 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
 
     GemmParams P;
     std::memset(&P, 0, sizeof(P));
-    const int BN = 256;
-    const bool pair = M >= 64 * E;
+    // Pairs (256 x 256) from 128 rows an expert on, single blocks (128 x 128) below, where tiles are mostly cut
+    // short and the weights are what there is to read.  Pairs / singles, us: 128 experts, 2048 x 4096, NVFP4: 64 rows an
+    // expert 124.8 / 118.5, 128 rows 135.4 / 140.6; MXFP8 322.9 / 305.9 and 334.6 / 332.3; 16 experts, 4096 x 4096, 128
+    // rows 42.7 / 42.2 and 86.0 / 85.8, 256 rows 51.3 / 51.8 and 100.4 / 96.0.
+    const bool pair = M >= 128 * E;
+    const int BN = pair ? 256 : 128;
     const int sc = nv ? 4 : 1;
-    if (!map_codes(&P.tm_a, a->data, M, k_bytes, kRowsT) || !map_codes(&P.tm_b, b->data, E * N, k_bytes, pair ? BN / 2 : BN) ||
+    if (!map_codes(&P.tm_a, a->data, M, k_bytes, pair ? kRowsT : kBoxA) || !map_codes(&P.tm_b, b->data, E * N, k_bytes, 128) ||
         !map_scales(&P.tm_sa, a->scale, a_rows * cols, sc) || !map_scales(&P.tm_sb, b->scale, E * n128 * cols, sc))
         return GSA_ERR_CUDA;
     P.split = split_sizes_dev;
@@ -1016,11 +1032,11 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     const int64_t tiles = (M + kRowsT - 1) / kRowsT + (E < M ? E : M);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     gsa_status st;
-    auto go = [&](auto fmt, auto two, auto type) {
-        return launch_gemm<decltype(fmt)::value, BN, decltype(two)::value, decltype(type)>(P, tiles, s);
+    auto typed = [&](auto fmt, auto type) {
+        return pair ? launch_gemm<decltype(fmt)::value, 256, true, decltype(type)>(P, tiles, s)
+                    : launch_gemm<decltype(fmt)::value, 128, false, decltype(type)>(P, tiles, s);
     };
-    auto typed = [&](auto fmt, auto two) { return out_dtype == GSA_BF16 ? go(fmt, two, __nv_bfloat16()) : go(fmt, two, float()); };
-    auto sized = [&](auto fmt) { return pair ? typed(fmt, std::true_type()) : typed(fmt, std::false_type()); };
+    auto sized = [&](auto fmt) { return out_dtype == GSA_BF16 ? typed(fmt, __nv_bfloat16()) : typed(fmt, float()); };
     st = nv ? sized(std::true_type()) : sized(std::false_type());
     if (st == GSA_OK) gsa::set_last_launches(1);
     return st;
@@ -1060,8 +1076,10 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     WgradParams P;
     std::memset(&P, 0, sizeof(P));
     const int sc = nv ? 4 : 1;
-    CUtensorMap plain;   // the experts' maps but for origin, extents and pitch
-    if (!map_codes(&plain, w, 4096, 4096, 128) || !map_scales(&P.tm_sa, a->scale, a_tiles, sc) ||
+    const bool pair = N > 128 && K > 128;
+    CUtensorMap plain_a, plain_b;   // the experts' maps but for origin, extents and pitch
+    if (!map_codes(&plain_a, w, 4096, 4096, pair ? kRowsT : kBoxA) || !map_codes(&plain_b, w, 4096, 4096, 128) ||
+        !map_scales(&P.tm_sa, a->scale, a_tiles, sc) ||
         !map_scales(&P.tm_sb, b->scale, b_tiles, sc) ||
         (nv && (!map_scales(&P.tm_ta, w + ws.tail_a, E * n128 * 4, 4) || !map_scales(&P.tm_tb, w + ws.tail_b, E * k128 * 4, 4))))
         return GSA_ERR_CUDA;
@@ -1082,7 +1100,6 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     P.N = static_cast<int>(N);
     P.K = static_cast<int>(K);
     P.E = static_cast<int>(E);
-    const bool pair = N > 128 && K > 128;
     const int tile = pair ? 256 : 128;
     P.n_tiles = static_cast<int>((N + tile - 1) / tile);
     P.k_tiles = static_cast<int>((K + tile - 1) / tile);
@@ -1095,8 +1112,8 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int sms = sm_count();
     if (!sms) return GSA_ERR_CUDA;
-    if (nv) wgrad_prepare<true><<<4 * sms, kPrepThreads, 0, s>>>(P, plain);
-    else wgrad_prepare<false><<<static_cast<unsigned>(2 * E < sms ? 2 * E : sms), kPrepThreads, 0, s>>>(P, plain);
+    if (nv) wgrad_prepare<true><<<4 * sms, kPrepThreads, 0, s>>>(P, plain_a, plain_b);
+    else wgrad_prepare<false><<<static_cast<unsigned>(2 * E < sms ? 2 * E : sms), kPrepThreads, 0, s>>>(P, plain_a, plain_b);
     if (cudaGetLastError() != cudaSuccess) return GSA_ERR_CUDA;
     gsa_status st;
     auto typed = [&](auto fmt, auto type) {

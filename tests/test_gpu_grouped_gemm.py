@@ -83,7 +83,9 @@ def rounded(v, dtype):
     return torch.from_numpy(v.astype(np.float32)).to(dtype).double().numpy()
 
 
-SPLITS = [[1], [5, 0, 130], [0, 0, 128, 1, 127, 129, 0], [300, 17, 0, 64], [2] * 40, [0, 0, 0]]
+# few rows an expert (single blocks), and many (pairs of blocks on 256 rows), with tiles cut short at every place
+SPLITS = [[1], [5, 0, 130], [0, 0, 128, 1, 127, 129, 0], [300, 17, 0, 64], [33, 97, 64, 1, 32], [2] * 40, [0, 0, 0],
+          [256], [700, 3, 0, 129], [0, 513, 255, 1, 1000, 31]]
 
 
 @pytest.mark.parametrize("recipe", [MX, NV])
