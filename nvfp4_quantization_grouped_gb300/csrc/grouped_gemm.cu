@@ -149,7 +149,11 @@ struct Tile {
 // Tile number i of kRows rows, searching from group g on (tile numbers only grow).
 template <int kRows> __device__ __forceinline__ Tile tile_at(const GemmParams &P, const GemmShared &sh, int64_t i, int g) {
     const int q = static_cast<int>(i / P.n_tiles);
-    while (q >= sh.tile0[g + 1]) ++g;
+    for (int end = P.E + 1; end - g > 1;) {   // the last group that starts at or before q: most may be empty
+        const int mid = (g + end) >> 1;
+        if (sh.tile0[mid] <= q) g = mid;
+        else end = mid;
+    }
     Tile t;
     t.g = g;
     t.nt = static_cast<int>(i - static_cast<int64_t>(q) * P.n_tiles);
@@ -413,21 +417,16 @@ __device__ __forceinline__ void load_stage(Barriers &sh, const Stages<NV, BN, kP
     ring.next();
 }
 
-// The same parts of a later tile's stage into L2: units that run side by side share
-// its rows and columns, so one of them asks memory for A, one for B, and all find them
-// there a tile later.
-template <bool NV, int BN, bool kPair> __device__ __forceinline__ void prefetch_stage(const StageAt &w, bool a, bool b) {
-    using C = Cfg<NV, BN, kPair>;
-    if ((a || b) && tc::elect()) {
-        if (a) {
-            for (int i = 0; i < (kPair ? 1 : w.a_boxes); ++i) tc::prefetch_2d(w.a, w.x, w.a_row + i * kBoxA);
-            tc::prefetch_2d(w.sa, 0, w.a_tile);
-        }
-        if (b) {
-            tc::prefetch_2d(w.b, w.x, w.b_row);
-#pragma unroll
-            for (int g = 0; g < C::kGroupsB; ++g) tc::prefetch_2d(w.sb, 0, w.b_tile + g * w.b_tile_step);
-        }
+// The rows' part of a later tile's stage into L2 (pairs): units that run side by side
+// share it, so one of them asks memory for it and all find it there a tile later (65536 x
+// 2048 x 2048 NVFP4 over 32 experts: 117.4 -> 112.7 us).  The columns' operand is left
+// alone: asking for it twice costs more than the wait wherever it is read only a few times
+// (128 rows an expert, 2048 x 4096 MXFP8: 226 us without, 327 with; single blocks at 16
+// rows an expert 171 and 302).
+__device__ __forceinline__ void prefetch_rows(const StageAt &w) {
+    if (tc::elect()) {
+        tc::prefetch_2d(w.a, w.x, w.a_row);
+        tc::prefetch_2d(w.sa, 0, w.a_tile);
     }
     __syncwarp();
 }
@@ -498,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
         }
         Ring<C::kStages> ring;
         int g = 0;
-        bool ok = true, first_row = false, first_col = false;   // of the tile: the first of its row tile, of its columns
+        bool ok = true, first = false;   // first: the next tile is its rows' first
         auto at = [&](int64_t i) {
             const Tile t = tile_at<kRows>(P, sh, i, g);
             g = t.g;
@@ -510,8 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
             w.b_row = uniform(static_cast<int>(g * P.N + static_cast<int64_t>(t.nt) * BN)) + half * C::kRowsB;
             w.b_tile = uniform((g * P.b_scale_rows + t.nt * C::kGroupsB) * P.scale_cols);
             w.b_tile_step = P.scale_cols;
-            first_row = uniform(t.nt) == 0;
-            first_col = uniform(t.mt) == 0;
+            first = uniform(t.nt) == 0;
             return w;
         };
         StageAt w, next;
@@ -523,9 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
             StageAt ahead = next;
             for (int k = 0; k < P.kt; ++k) {
                 load_stage(sh, st, half, ring, w, ok);
-                if (more) prefetch_stage<NV, BN, kPair>(ahead, first_row, first_col);
+                if (kPair && more && first) prefetch_rows(ahead);
                 w.x += kStageK, w.a_tile += C::kSc, w.b_tile += C::kSc;
-                ahead.x += kStageK, ahead.a_tile += C::kSc, ahead.b_tile += C::kSc;
+                ahead.x += kStageK, ahead.a_tile += C::kSc;
             }
         }
         if (!ok) settle_loads<C::kStages>(sh, half, ring.issued);
@@ -1006,9 +1004,9 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     GemmParams P;
     std::memset(&P, 0, sizeof(P));
     // Pairs (256 x 256) from 128 rows an expert on, single blocks (128 x 128) below, where tiles are mostly cut
-    // short and the weights are what there is to read.  Pairs / singles, us: 128 experts, 2048 x 4096, NVFP4: 64 rows an
-    // expert 124.8 / 118.5, 128 rows 135.4 / 140.6; MXFP8 322.9 / 305.9 and 334.6 / 332.3; 16 experts, 4096 x 4096, 128
-    // rows 42.7 / 42.2 and 86.0 / 85.8, 256 rows 51.3 / 51.8 and 100.4 / 96.0.
+    // short and the weights are what there is to read.  Pairs / singles, us, 128 experts, 2048 x 4096: 64 rows an
+    // expert 125 / 109 (NVFP4), 323 / 193 (MXFP8; both pairs' figures with B prefetched), 128 rows 125 / 132 and
+    // 226 / 230, 256 rows 159 / 185 and 293 / 320; 16 experts, 4096 x 4096, 256 rows 49.5 / 52.1 and 85.0 / 85.6.
     const bool pair = M >= 128 * E;
     const int BN = pair ? 256 : 128;
     const int sc = nv ? 4 : 1;
