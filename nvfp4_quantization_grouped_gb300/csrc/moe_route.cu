@@ -377,15 +377,18 @@ struct Shape {
     dim3 grid, block;
 };
 
-// Columns x tokens of a block of 256 threads, `unroll` columns a thread; columns
-// beyond one pass of a block go to further blocks along grid.y.
+// Columns x tokens of a block of at most 256 threads, `unroll` columns a thread;
+// columns beyond one pass of a block go to further blocks along grid.y, all as wide as
+// they need to be (1111 columns, unroll 4: 2 x 160 threads, not 256 and 22).
 Shape row_shape(int64_t tokens, int64_t nv, int unroll = 1) {
-    int x = 1;
-    while (x < 256 && x * unroll < nv) x *= 2;
-    const int y = 256 / x;
-    int64_t gy = (nv + static_cast<int64_t>(x) * unroll - 1) / (static_cast<int64_t>(x) * unroll);
+    const int64_t per = (nv + unroll - 1) / unroll;   // threads that the columns take
+    int64_t gy = (per + 255) / 256;
+    int64_t x = 1;
+    if (per < 32) while (x < per) x *= 2;
+    else x = ((per + gy - 1) / gy + 31) / 32 * 32;
+    const int y = static_cast<int>(256 / x);
     if (gy > 64) gy = 64;
-    return {dim3(static_cast<unsigned>((tokens + y - 1) / y), static_cast<unsigned>(gy)), dim3(x, y)};
+    return {dim3(static_cast<unsigned>((tokens + y - 1) / y), static_cast<unsigned>(gy)), dim3(static_cast<unsigned>(x), y)};
 }
 
 gsa_status check_shape(int64_t tokens, int64_t topk, int64_t hidden, int32_t dtype) {
