@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgsa.so")
 SOURCES = ["gsa_api.cu", "k_srelu.cu", "k_tanh_srelu.cu", "k_swiglu.cu", "k_clamped_swiglu.cu", "k_gelu.cu",
-           "k_sigmoid.cu", "k_identity.cu", "moe_route.cu", "grouped_gemm.cu"]
+           "k_sigmoid.cu", "k_identity.cu", "moe/route.cu", "moe/grouped_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC,-O2",
          "-I" + INCLUDE, "-I" + CSRC]
@@ -33,7 +33,8 @@ def nvcc() -> str:
 
 
 def _newest_input() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "gsa.h"), __file__]
+    files = [os.path.join(d, f) for d, _, names in os.walk(CSRC) for f in names] + [os.path.join(INCLUDE, "gsa.h"),
+                                                                                    __file__]
     return max(os.path.getmtime(f) for f in files)
 
 
@@ -44,7 +45,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     exe = nvcc()
 
     def compile_one(src):
-        obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+        obj = os.path.join(BUILD, os.path.splitext(src)[0].replace("/", "_") + ".o")
         cmd = [exe, *ARCH, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:

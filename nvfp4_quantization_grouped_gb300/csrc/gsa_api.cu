@@ -14,7 +14,6 @@
 
 #include "gsa.h"
 #include "gsa_kernel.cuh"
-#include "launches.h"
 
 namespace {
 
@@ -691,10 +690,6 @@ gsa_status setup_bwd(const Plan &pl, const void *dy_bf16, const void *x_bf16, co
 
 }  // namespace
 
-namespace gsa {
-void set_last_launches(int32_t n) { g_last_launches = n; }
-}  // namespace gsa
-
 extern "C" {
 
 gsa_status gsa_layout(int64_t E, const int64_t *split_sizes, int64_t width, int32_t recipe_kind,
@@ -908,7 +903,7 @@ const char *gsa_status_string(gsa_status s) {
     return "unknown status";
 }
 
-int32_t gsa_version(void) { return (1 << 16) | 2; }
+int32_t gsa_version(void) { return (1 << 16) | 1; }
 
 gsa_status gsa_fwd_noalloc(const void *x_bf16, const float *probs, const int64_t *split_sizes, int64_t E,
                            int64_t W_in, int32_t act_kind, const gsa_act_params *act_params,

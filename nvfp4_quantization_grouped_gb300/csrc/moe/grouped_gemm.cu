@@ -23,7 +23,6 @@
 #include <type_traits>
 
 #include "gsa.h"
-#include "launches.h"
 #include "tc.cuh"
 
 namespace {
@@ -984,10 +983,7 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     if (E > kMaxE || K % 64 != 0 || K > (int64_t(1) << 30) || M >= (int64_t(1) << 31) - 256 ||
         N >= (int64_t(1) << 31) / E - 256)
         return GSA_ERR_UNSUPPORTED;
-    if (M == 0) {
-        gsa::set_last_launches(0);
-        return GSA_OK;
-    }
+    if (M == 0) return GSA_OK;
     if (!a->data || !a->scale || !b->data || !b->scale || !split_sizes_dev || !out) return GSA_ERR_INVALID_ARG;
     if (nv && (!a->amax || !b->amax)) return GSA_ERR_INVALID_ARG;
     if (!aligned(a->data, 16) || !aligned(a->scale, 16) || !aligned(b->data, 16) || !aligned(b->scale, 16) ||
@@ -1036,7 +1032,6 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     };
     auto sized = [&](auto fmt) { return out_dtype == GSA_BF16 ? typed(fmt, __nv_bfloat16()) : typed(fmt, float()); };
     st = nv ? sized(std::true_type()) : sized(std::false_type());
-    if (st == GSA_OK) gsa::set_last_launches(1);
     return st;
 }
 
@@ -1120,7 +1115,6 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     };
     auto sized = [&](auto fmt) { return out_dtype == GSA_BF16 ? typed(fmt, __nv_bfloat16()) : typed(fmt, float()); };
     st = nv ? sized(std::true_type()) : sized(std::false_type());
-    if (st == GSA_OK) gsa::set_last_launches(2);
     return st;
 }
 

@@ -1,4 +1,4 @@
-// moe_route.cu -- tokens into expert order and back, for sm_103a: the sort plan
+// route.cu -- tokens into expert order and back, for sm_103a: the sort plan
 // of the routed expert indices, the gather of the token rows (permute), the
 // weighted way back (unpermute) and both gradients, with their C entry points.
 //
@@ -23,7 +23,6 @@
 #include <type_traits>
 
 #include "gsa.h"
-#include "launches.h"
 
 namespace {
 
@@ -400,11 +399,7 @@ gsa_status check_shape(int64_t tokens, int64_t topk, int64_t hidden, int32_t dty
     return GSA_OK;
 }
 
-gsa_status done(int launches) {
-    if (cudaGetLastError() != cudaSuccess) return GSA_ERR_CUDA;
-    gsa::set_last_launches(launches);
-    return GSA_OK;
-}
+gsa_status done() { return cudaGetLastError() == cudaSuccess ? GSA_OK : GSA_ERR_CUDA; }
 
 // Calls f<T, V>() for the element type and access width.
 template <typename T, typename F> void with_vector(int v, F &&f) {
@@ -439,7 +434,7 @@ gsa_status run_combine(const void *ys, const float *weights, const int32_t *row_
         if (topk > 4) go(std::integral_constant<int, 8>(), std::integral_constant<int, decltype(width)::value == 16 ? 1 : 2>());
         else go(std::integral_constant<int, 4>(), std::integral_constant<int, decltype(width)::value == 16 ? 2 : 4>());
     });
-    return done(1);
+    return done();
 }
 
 }  // namespace
@@ -473,14 +468,14 @@ gsa_status gsa_moe_sort(const void *expert_idx, int32_t idx_bytes, int64_t token
         while (threads < 1024 && threads < n) threads *= 2;
         if (n <= threads) sort_rank<1><<<1, threads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, 0, nullptr, row_of_slot, split_sizes);
         else sort_rank<8><<<1, threads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, 0, nullptr, row_of_slot, split_sizes);
-        return done(1);
+        return done();
     }
     if (!workspace || workspace_bytes < gsa_moe_sort_workspace_size(tokens, topk, experts)) return GSA_ERR_WORKSPACE;
     const unsigned blocks = static_cast<unsigned>((n + seg - 1) / seg);
     int *counts = static_cast<int *>(workspace);
     sort_count<<<blocks, 1024, 0, s>>>(expert_idx, idx_bytes, n, E, seg, sort_pitch(n), counts);
     sort_rank<2><<<blocks, 1024, 0, s>>>(expert_idx, idx_bytes, n, E, seg, sort_pitch(n), counts, row_of_slot, split_sizes);
-    return done(2);
+    return done();
 }
 
 gsa_status gsa_moe_permute(const void *x, const float *probs, const int32_t *row_of_slot, int64_t tokens, int64_t topk,
@@ -491,7 +486,7 @@ gsa_status gsa_moe_permute(const void *x, const float *probs, const int32_t *row
     if (tokens > 0 && (!x || !xs || !row_of_slot)) return GSA_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(xs, 16) || !aligned(row_of_slot, 4) || !aligned(probs, 4) || !aligned(ps, 4))
         return GSA_ERR_ALIGNMENT;
-    if (tokens == 0) return done(0);
+    if (tokens == 0) return GSA_OK;
     const int v = vector_bytes(hidden * elem_bytes(dtype));
     const int64_t nv = hidden * elem_bytes(dtype) / v;
     const Shape s = row_shape(tokens, nv);
@@ -506,7 +501,7 @@ gsa_status gsa_moe_permute(const void *x, const float *probs, const int32_t *row
     case 4: go(std::integral_constant<int, 4>()); break;
     default: go(std::integral_constant<int, 2>());
     }
-    return done(1);
+    return done();
 }
 
 gsa_status gsa_moe_permute_bwd(const void *dxs, const float *dps, const int32_t *row_of_slot, int64_t tokens,
@@ -518,7 +513,7 @@ gsa_status gsa_moe_permute_bwd(const void *dxs, const float *dps, const int32_t 
     if (tokens > 0 && (!dxs || !dx || !row_of_slot)) return GSA_ERR_INVALID_ARG;
     if (!aligned(dxs, 16) || !aligned(dx, 16) || !aligned(row_of_slot, 4) || !aligned(dps, 4) || !aligned(dprobs, 4))
         return GSA_ERR_ALIGNMENT;
-    if (tokens == 0) return done(0);
+    if (tokens == 0) return GSA_OK;
     return run_combine(dxs, nullptr, row_of_slot, tokens, topk, hidden, dtype, dx, dps, dprobs, stream);
 }
 
@@ -529,7 +524,7 @@ gsa_status gsa_moe_unpermute(const void *ys, const float *weights, const int32_t
     if (tokens > 0 && (!ys || !out || !row_of_slot)) return GSA_ERR_INVALID_ARG;
     if (!aligned(ys, 16) || !aligned(out, 16) || !aligned(row_of_slot, 4) || !aligned(weights, 4))
         return GSA_ERR_ALIGNMENT;
-    if (tokens == 0) return done(0);
+    if (tokens == 0) return GSA_OK;
     return run_combine(ys, weights, row_of_slot, tokens, topk, hidden, dtype, out, nullptr, nullptr, stream);
 }
 
@@ -542,7 +537,7 @@ gsa_status gsa_moe_unpermute_bwd(const void *dout, const void *ys, const float *
     if (!aligned(dout, 16) || !aligned(ys, 16) || !aligned(dys, 16) || !aligned(row_of_slot, 4) ||
         !aligned(weights, 4) || !aligned(dweights, 4))
         return GSA_ERR_ALIGNMENT;
-    if (tokens == 0) return done(0);
+    if (tokens == 0) return GSA_OK;
     const int v = vector_bytes(hidden * elem_bytes(dtype));
     const int64_t nv = hidden * elem_bytes(dtype) / v;
     // warps per token: two vectors a thread and at most 4 (measured above), or one and
@@ -557,7 +552,7 @@ gsa_status gsa_moe_unpermute_bwd(const void *dout, const void *ys, const float *
                 static_cast<const uint8_t *>(dout), static_cast<const uint8_t *>(ys), weights, row_of_slot,
                 static_cast<int>(tokens), static_cast<int>(topk), nv, static_cast<uint8_t *>(dys), dweights);
     });
-    return done(1);
+    return done();
 }
 
 }  // extern "C"
