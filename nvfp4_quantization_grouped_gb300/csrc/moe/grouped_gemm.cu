@@ -1063,17 +1063,21 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
 
     const int64_t n128 = (N + 127) / 128, k128 = (K + 127) / 128;
     const int64_t a_tiles = a->scale_bytes / kScaleTile, b_tiles = b->scale_bytes / kScaleTile;
-    if (a_tiles >= (int64_t(1) << 31) || b_tiles >= (int64_t(1) << 31)) return GSA_ERR_UNSUPPORTED;
-    if (a_tiles < 1 || b_tiles < 1) return GSA_ERR_INVALID_ARG;
+    if (a_tiles >= (int64_t(1) << 31) || b_tiles >= (int64_t(1) << 31) || E * n128 * 4 >= (int64_t(1) << 31) ||
+        E * k128 * 4 >= (int64_t(1) << 31))
+        return GSA_ERR_UNSUPPORTED;
+    const bool pair = N > 128 && K > 128;
+    const int64_t tile = pair ? 256 : 128, n_tiles = (N + tile - 1) / tile, k_tiles = (K + tile - 1) / tile;
+    if (E * n_tiles * k_tiles >= (int64_t(1) << 31) - 4096) return GSA_ERR_UNSUPPORTED;
     uint8_t *w = static_cast<uint8_t *>(workspace);
     WgradParams P;
     std::memset(&P, 0, sizeof(P));
     const int sc = nv ? 4 : 1;
-    const bool pair = N > 128 && K > 128;
     CUtensorMap plain_a, plain_b;   // the experts' maps but for origin, extents and pitch
     if (!map_codes(&plain_a, w, 4096, 4096, pair ? kRowsT : kBoxA) || !map_codes(&plain_b, w, 4096, 4096, 128) ||
-        !map_scales(&P.tm_sa, a->scale, a_tiles, sc) ||
-        !map_scales(&P.tm_sb, b->scale, b_tiles, sc) ||
+        // (without rows the scale buffers may be empty: nothing is loaded then)
+        !map_scales(&P.tm_sa, a_tiles ? a->scale : w, a_tiles ? a_tiles : 1, sc) ||
+        !map_scales(&P.tm_sb, b_tiles ? b->scale : w, b_tiles ? b_tiles : 1, sc) ||
         (nv && (!map_scales(&P.tm_ta, w + ws.tail_a, E * n128 * 4, 4) || !map_scales(&P.tm_tb, w + ws.tail_b, E * k128 * 4, 4))))
         return GSA_ERR_CUDA;
     P.a = static_cast<const uint8_t *>(a->data);
@@ -1093,15 +1097,13 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     P.N = static_cast<int>(N);
     P.K = static_cast<int>(K);
     P.E = static_cast<int>(E);
-    const int tile = pair ? 256 : 128;
-    P.n_tiles = static_cast<int>((N + tile - 1) / tile);
-    P.k_tiles = static_cast<int>((K + tile - 1) / tile);
+    P.n_tiles = static_cast<int>(n_tiles);
+    P.k_tiles = static_cast<int>(k_tiles);
     P.a_bytes = a->data_bytes;
     P.b_bytes = b->data_bytes;
     P.sa_bytes = a->scale_bytes;
     P.sb_bytes = b->scale_bytes;
     P.accumulate = accumulate != 0;
-    if (E * P.n_tiles * static_cast<int64_t>(P.k_tiles) >= (int64_t(1) << 31) - 4096) return GSA_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int sms = sm_count();
     if (!sms) return GSA_ERR_CUDA;

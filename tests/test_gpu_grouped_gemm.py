@@ -335,6 +335,19 @@ def test_wgrad_graph_and_determinism(recipe):
         assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("recipe", [MX, NV])
+def test_no_rows_at_all(recipe):
+    """Zero rows: an empty product, and zero weight gradients from empty copies."""
+    x, s = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), dev_split([0, 0])
+    q = gsa.fwd(x, None, [0, 0], "identity", recipe, scale_layout=gsa.SCALES_TILED)
+    w = Matrices(np.random.default_rng(1), [64, 64], 64, recipe).dev()
+    assert gsa.grouped_gemm(q, w, s, 0, 64, 64, recipe).shape == (0, 64)
+    dw = gsa.grouped_gemm_wgrad(q, q, s, 0, 64, 64, recipe, out=torch.full((2, 64, 64), 5.0, device="cuda"))
+    assert bool((dw == 0).all()) and gsa.grouped_gemm_status() == 0
+    gsa.grouped_gemm_wgrad(q, q, s, 0, 64, 64, recipe, out=dw.fill_(5.0), accumulate=True)
+    assert bool((dw == 5.0).all())
+
+
 def test_python_refusals():
     rng = np.random.default_rng(14)
     a, b, s = Matrices(rng, [4, 4], 64, NV).dev(), Matrices(rng, [64, 64], 64, NV).dev(), dev_split([4, 4])
