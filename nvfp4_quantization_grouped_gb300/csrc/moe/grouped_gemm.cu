@@ -8,11 +8,18 @@
 // scales and sums in FP32 (tcgen05.mma with block_scale); u_e and the rounding to
 // the output type are the epilogue.
 //
-// Persistent blocks walk the tiles of all experts (128 rows x BN columns, column
-// tiles of a row tile one after another so that its rows stay in L2).  Warp 0
-// loads stages of 128 bytes of k (A, B and their scale tiles, by TMA), warp 1
-// copies the scales to tensor memory and issues the products, and 8 warps drain
-// the accumulators.
+// Persistent blocks walk the tiles of all experts (column tiles of a row tile one
+// after another so that its rows stay in L2).  With many rows an expert, pairs of
+// blocks share tiles of 256 x 256 (a block then reads 32 KB of codes for 128 x 256 x 256
+// products instead of 48); with few, blocks take 128 x 128.  Warp 0 loads stages of 128
+// bytes of k (A, B and their scale tiles, by TMA), warp 1 copies the scales to tensor
+// memory and issues the products, and 8 warps drain the accumulators.
+//   What bounds it: an NVFP4 stage of a pair is 512 cycles of products and about 200 of
+// scale copies in the same queue, an MXFP8 one 512 and 50; a tile's end costs about 1000
+// more.  65536 x 2048 x 2048 NVFP4 over 32 experts: 112 us (4.9 PFLOP/s); 262144 x 4096 x
+// 2048 MXFP8 over 128 experts: 1500 us (2.9 PFLOP/s) at the clock that the power limit
+// leaves, 1355 us for a launch by itself; 512 rows over 128 experts, 2048 x 4096 NVFP4:
+// 74 us, the weights at 6.2 TB/s.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -580,8 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
 // multiple of 8, so that kernel also copies the experts with an odd number of
 // 8-byte groups to rows 8 bytes longer.  (Bringing such rows in with loads instead
 // ran at 20 to 26 bytes a cycle and SM from L2, any width and number of warps,
-// against 65 to 76 by TMA: 577 us where the products of 65536 x 2048 x 2048 take
-// a fifth.)  Last, scales past Mp_e are padding that nobody wrote, and a zero code
+// against 65 to 76 by TMA: 577 us for 65536 x 2048 x 2048 over 32 experts, against 193:
+// 24 for that kernel, 160 for the products, whose FP32 results of 128 KB a block and tile
+// one SM stores in 5900 cycles.)  Last, scales past Mp_e are padding that nobody wrote, and a zero code
 // times a NaN scale is NaN: where a product step of 64 rows is cut short, the
 // scale tiles of that last stage are copied with zeros there.
 

@@ -15,6 +15,8 @@
 // four kernels go by token: a token's own row is read (or written) once whatever
 // topk is, and only the expert side moves topk rows.  Sums run in FP32 in slot
 // order, so results do not depend on the launch shape (dw: see unpermute_bwd).
+//   32768 tokens x 8 x 2048 BF16, 128 experts: sort 10.5 us, permute 181 us (6.7 TB/s),
+// unpermute 180 us (6.7 TB/s); gradient of unpermute on a quarter of it 94 us (6.1 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -144,10 +146,11 @@ __global__ void __launch_bounds__(1024) sort_rank(const void *idx, int idx_bytes
     }
 }
 
-// One block up to kOneBlockSlots slots (a chunk of 32 warps x 8 steps), else segments
+// One block up to kOneBlockSlots slots (a chunk of 32 warps x 4 steps), else segments
 // of 2048 slots (32 warps x 2 steps) and two launches; at most 512 segments, since
-// every block reads the counts of all.  One block against segments, sort alone:
-constexpr int64_t kOneBlockSlots = 8192;
+// every block reads the counts of all.  One block / segments, 128 experts, us: 128 slots
+// 3.0 / 7.5, 1024 4.2 / 8.4, 4096 7.8 / 9.5, 8192 11.7 / 10.1 (262144: 10.5).
+constexpr int64_t kOneBlockSlots = 4096;
 
 int64_t sort_segment(int64_t n) {
     if (n <= kOneBlockSlots) return n;
@@ -180,6 +183,61 @@ template <typename T, int V> union Vec {
     T e[V / sizeof(T)];
     __device__ Vec() {}
 };
+
+// Rows that start anywhere, by 16-byte words all the same: a kernel goes by the words
+// of the row it writes, and reads the rows it reads at whatever offset that gives: two
+// words, the second of which the next lane has just asked for, shifted together.  What
+// lies before a row's first whole word and behind its last goes element by element.
+// Worth it where stores of 2 (or 4) bytes are the alternative; 8192 tokens x 8 x 2047 / 2046
+// / 2044 BF16 and 1111 FP32, by elements or pairs / by words, us: permute (with its sort)
+// 141 / 84, 94 / 84, 76 / 82, 102 / 95; gradient of unpermute 223 / 145, 148 / 144, 121 / 140,
+// 156 / 179; unpermute (one row written for 8 read) 95 / 95, 63 / 91, 47 / 80, 64 / 93.
+struct Edges {
+    int64_t words;      // whole words of the row
+    int head, count;    // elements before the first word; elements before it and behind the last
+    template <typename T> static __device__ __forceinline__ Edges of(const T *row, int64_t hidden) {
+        Edges x;
+        const int64_t head = static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T);
+        x.head = static_cast<int>(head < hidden ? head : hidden);
+        x.words = (hidden - x.head) * sizeof(T) / 16;
+        x.count = static_cast<int>(hidden - x.words * (16 / sizeof(T)));
+        return x;
+    }
+    // Column of the i-th edge element.
+    template <typename T> __device__ __forceinline__ int64_t column(int i) const {
+        return i < head ? i : words * static_cast<int64_t>(16 / sizeof(T)) + i;
+    }
+};
+
+// 16 bytes at p, a multiple of sizeof(T) (both words inside [.., end) but for the bytes that are not asked for).
+template <typename T> __device__ __forceinline__ uint4 load_any(const T *p, const T *end) {
+    const uint32_t s = reinterpret_cast<uintptr_t>(p) & 15;
+    const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - s);
+    const uint4 a = __ldg(q);
+    if (s == 0) return a;
+    Vec<T, 16> b;
+    b.raw = make_uint4(0, 0, 0, 0);
+    if (reinterpret_cast<uintptr_t>(q + 2) <= reinterpret_cast<uintptr_t>(end)) {
+        b.raw = __ldg(q + 1);
+    } else {   // the tensor ends inside the second word
+        const T *r = reinterpret_cast<const T *>(q + 1);
+#pragma unroll
+        for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i)
+            if (i < static_cast<int>(s / sizeof(T))) b.e[i] = r[i];
+    }
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.raw.x, b.raw.y, b.raw.z, b.raw.w};
+    if (s & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (s & 4) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    const uint32_t bits = 8 * (s & 3);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits), __funnelshift_r(w[2], w[3], bits),
+                      __funnelshift_r(w[3], w[4], bits));
+}
 
 // Row index of a plan entry, -1 where the slot is dropped (or out of range).
 __device__ __forceinline__ int live_row(int32_t r, int n) {
@@ -274,6 +332,38 @@ __global__ void __launch_bounds__(256, 4) combine(const uint8_t *ys, const float
     }
 }
 
+// G partial dot products of a token's warps summed and written: over the lanes by halving distances, over the warps in
+// order.  Every thread of the block; left: slots that the token still has.
+template <int G>
+__device__ __forceinline__ void finish_dots(float (&part)[8][G], float (&acc)[G], bool on, int wpt, int warp, int lane, int left,
+                                            float *dw) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) acc[g] += __shfl_xor_sync(0xFFFFFFFFu, acc[g], s);
+    }
+    if (wpt > 1) {
+        __syncthreads();
+        if (lane == 0) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) part[warp][g] = acc[g];
+        }
+        __syncthreads();
+    }
+    const int mine = threadIdx.x;
+    if (on && mine < G && mine < left) {
+        float s = 0.0f;
+        if (wpt > 1) {
+            for (int k = 0; k < wpt; ++k) s += part[threadIdx.y * wpt + k][mine];
+        } else {
+#pragma unroll
+            for (int k = 0; k < G; ++k)
+                if (k == mine) s = acc[k];
+        }
+        dw[mine] = s;
+    }
+}
+
 // dys[row] = w dout[t] and dw = <dout[t], ys[row]> in one pass.  blockDim.y
 // groups of wpt warps take a token each and kGradRows of its slots at a time; a
 // thread keeps their partial dot products, summed over its columns in order, then
@@ -330,33 +420,97 @@ __global__ void __launch_bounds__(256, kGradBlocks) unpermute_bwd(const uint8_t 
                 }
             }
         }
-        if (dw) {
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-#pragma unroll
-                for (int s = 16; s > 0; s >>= 1) acc[g] += __shfl_xor_sync(0xFFFFFFFFu, acc[g], s);
+        if (dw) finish_dots<G>(part, acc, on, wpt, warp, lane, topk - j0, dw + slot0 + j0);
+    }
+}
+
+// ------------------------------------------------ rows that start anywhere
+
+template <typename T>
+__global__ void __launch_bounds__(256) any_permute_fwd(const T *x, const float *probs, const int32_t *row_of_slot, int tokens,
+                                                       int topk, int64_t hidden, T *xs, float *ps) {
+    const int t = blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= tokens) return;
+    const int n = tokens * topk;
+    const int32_t *rows = row_of_slot + static_cast<int64_t>(t) * topk;
+    if (ps && blockIdx.y == 0) {
+        for (int j = threadIdx.x; j < topk; j += blockDim.x) {
+            const int32_t r = rows[j];
+            const int at = r < 0 ? ~r : r;
+            if (at < n) ps[at] = r < 0 ? 0.0f : probs[static_cast<int64_t>(t) * topk + j];
+        }
+    }
+    const T *src = x + t * hidden, *end = x + tokens * hidden;
+#pragma unroll 2
+    for (int j = 0; j < topk; ++j) {
+        const int32_t r = rows[j];
+        const int at = r < 0 ? ~r : r;
+        if (at >= n) continue;
+        T *dst = xs + at * hidden;
+        const Edges e = Edges::of(dst, hidden);
+        for (int64_t c = blockIdx.y * static_cast<int64_t>(blockDim.x) + threadIdx.x; c < e.words;
+             c += static_cast<int64_t>(gridDim.y) * blockDim.x) {
+            const int64_t col = e.head + c * static_cast<int64_t>(16 / sizeof(T));
+            *reinterpret_cast<uint4 *>(dst + col) = r < 0 ? make_uint4(0, 0, 0, 0) : load_any(src + col, end);
+        }
+        if (blockIdx.y == 0)
+            for (int i = threadIdx.x; i < e.count; i += blockDim.x) {
+                const int64_t col = e.column<T>(i);
+                T v;
+                put(v, 0.0f);
+                dst[col] = r < 0 ? v : src[col];
             }
-            if (wpt > 1) {
-                __syncthreads();
-                if (lane == 0) {
+    }
+}
+
+// dys and ys rows lie alike, dout at an offset; a slot at a time.  (The order of a dot product's terms goes by the
+// words of its row.)
+template <typename T>
+__global__ void __launch_bounds__(256) any_unpermute_bwd(const T *dout, const T *ys, const float *weights,
+                                                         const int32_t *row_of_slot, int tokens, int topk, int64_t hidden,
+                                                         T *dys, float *dw) {
+    constexpr int N = 16 / sizeof(T), G = 2;
+    __shared__ float part[8][G];
+    const int t = blockIdx.x * blockDim.y + threadIdx.y;
+    const int n = tokens * topk;
+    const int lane = threadIdx.x & 31, wpt = blockDim.x >> 5, warp = threadIdx.y * wpt + (threadIdx.x >> 5);
+    const bool on = t < tokens;
+    const int64_t slot0 = static_cast<int64_t>(on ? t : 0) * topk;
+    const T *src = dout + (on ? t : 0) * hidden, *end = dout + tokens * hidden;
+    for (int j0 = 0; j0 < topk; j0 += G) {
+        float acc[G];
 #pragma unroll
-                    for (int g = 0; g < G; ++g) part[warp][g] = acc[g];
+        for (int g = 0; g < G; ++g) {
+            acc[g] = 0.0f;
+            const int32_t r = on && j0 + g < topk ? row_of_slot[slot0 + j0 + g] : n;
+            const int at = r < 0 ? ~r : r;
+            const bool live = live_row(r, n) >= 0;
+            if (at >= n || (!live && !dys)) continue;
+            const float w = live && weights ? weights[slot0 + j0 + g] : 1.0f;
+            const Edges e = Edges::of((dys ? dys : ys) + at * hidden, hidden);   // both tensors start on 16 bytes
+            for (int64_t c = threadIdx.x; c < e.words; c += blockDim.x) {
+                const int64_t col = e.head + c * N;
+                Vec<T, 16> d, y, o;
+                if (dw && live) y.raw = load_once<16>(ys + at * hidden + col);
+                if (live) d.raw = load_any(src + col, end);
+                if (dw && live) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[g] = __fmaf_rn(as_f32(d.e[i]), as_f32(y.e[i]), acc[g]);
                 }
-                __syncthreads();
+                if (dys) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) put(o.e[i], live ? w * as_f32(d.e[i]) : 0.0f);
+                    *reinterpret_cast<uint4 *>(dys + at * hidden + col) = o.raw;
+                }
             }
-            if (on && static_cast<int>(threadIdx.x) < G && j0 + static_cast<int>(threadIdx.x) < topk) {
-                const int g = threadIdx.x;
-                float s = 0.0f;
-                if (wpt > 1) {
-                    for (int k = 0; k < wpt; ++k) s += part[threadIdx.y * wpt + k][g];
-                } else {
-#pragma unroll
-                    for (int k = 0; k < G; ++k)
-                        if (k == g) s = acc[k];
-                }
-                dw[slot0 + j0 + g] = s;
+            for (int i = threadIdx.x; i < e.count; i += blockDim.x) {
+                const int64_t col = e.column<T>(i);
+                const float d = live ? as_f32(src[col]) : 0.0f;
+                if (dw && live) acc[g] = __fmaf_rn(d, as_f32(ys[at * hidden + col]), acc[g]);
+                if (dys) put(dys[at * hidden + col], live ? w * d : 0.0f);
             }
         }
+        if (dw) finish_dots<G>(part, acc, on, wpt, warp, lane, topk - j0, dw + slot0 + j0);
     }
 }
 
@@ -412,10 +566,13 @@ template <typename T, typename F> void with_vector(int v, F &&f) {
     }
 }
 
+template <typename F> void with_type(int dtype, F &&f) {
+    if (dtype == GSA_BF16) f(__nv_bfloat16());
+    else if (dtype == GSA_FP16) f(__half());
+    else f(float());
+}
 template <typename F> void with_type(int dtype, int v, F &&f) {
-    if (dtype == GSA_BF16) with_vector<__nv_bfloat16>(v, f);
-    else if (dtype == GSA_FP16) with_vector<__half>(v, f);
-    else with_vector<float>(v, f);
+    with_type(dtype, [&](auto tag) { with_vector<decltype(tag)>(v, f); });
 }
 
 gsa_status run_combine(const void *ys, const float *weights, const int32_t *row_of_slot, int64_t tokens, int64_t topk,
@@ -467,7 +624,7 @@ gsa_status gsa_moe_sort(const void *expert_idx, int32_t idx_bytes, int64_t token
         int threads = 128;   // also what the bins take
         while (threads < 1024 && threads < n) threads *= 2;
         if (n <= threads) sort_rank<1><<<1, threads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, 0, nullptr, row_of_slot, split_sizes);
-        else sort_rank<8><<<1, threads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, 0, nullptr, row_of_slot, split_sizes);
+        else sort_rank<4><<<1, threads, 0, s>>>(expert_idx, idx_bytes, n, E, seg, 0, nullptr, row_of_slot, split_sizes);
         return done();
     }
     if (!workspace || workspace_bytes < gsa_moe_sort_workspace_size(tokens, topk, experts)) return GSA_ERR_WORKSPACE;
@@ -488,19 +645,20 @@ gsa_status gsa_moe_permute(const void *x, const float *probs, const int32_t *row
         return GSA_ERR_ALIGNMENT;
     if (tokens == 0) return GSA_OK;
     const int v = vector_bytes(hidden * elem_bytes(dtype));
-    const int64_t nv = hidden * elem_bytes(dtype) / v;
-    const Shape s = row_shape(tokens, nv);
-    auto go = [&](auto width) {
-        permute_fwd<decltype(width)::value><<<s.grid, s.block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-            static_cast<const uint8_t *>(x), probs, row_of_slot, static_cast<int>(tokens), static_cast<int>(topk), nv,
-            static_cast<uint8_t *>(xs), ps);
-    };
-    switch (v) {
-    case 16: go(std::integral_constant<int, 16>()); break;
-    case 8: go(std::integral_constant<int, 8>()); break;
-    case 4: go(std::integral_constant<int, 4>()); break;
-    default: go(std::integral_constant<int, 2>());
-    }
+    const int64_t bytes = hidden * elem_bytes(dtype), nv = v >= 8 ? bytes / v : (bytes + 15) / 16;
+    const Shape g = row_shape(tokens, nv);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int nt = static_cast<int>(tokens), nk = static_cast<int>(topk);
+    const uint8_t *from = static_cast<const uint8_t *>(x);
+    uint8_t *to = static_cast<uint8_t *>(xs);
+    if (v == 16) permute_fwd<16><<<g.grid, g.block, 0, s>>>(from, probs, row_of_slot, nt, nk, nv, to, ps);
+    else if (v == 8) permute_fwd<8><<<g.grid, g.block, 0, s>>>(from, probs, row_of_slot, nt, nk, nv, to, ps);
+    else
+        with_type(dtype, [&](auto tag) {
+            using T = decltype(tag);
+            any_permute_fwd<T><<<g.grid, g.block, 0, s>>>(static_cast<const T *>(x), probs, row_of_slot, nt, nk, hidden,
+                                                          static_cast<T *>(xs), ps);
+        });
     return done();
 }
 
@@ -539,19 +697,28 @@ gsa_status gsa_moe_unpermute_bwd(const void *dout, const void *ys, const float *
         return GSA_ERR_ALIGNMENT;
     if (tokens == 0) return GSA_OK;
     const int v = vector_bytes(hidden * elem_bytes(dtype));
-    const int64_t nv = hidden * elem_bytes(dtype) / v;
+    const int64_t bytes = hidden * elem_bytes(dtype), nv = v == 2 ? (bytes + 15) / 16 : bytes / v;   // v 2: by words
     // warps per token: two vectors a thread and at most 4 (measured above), or one and
     // at most 8 where the tokens are too few to fill the machine with 4
     int wpt = 1;
     while (wpt < 4 && wpt * 128 <= nv) wpt *= 2;
     while (wpt < 8 && tokens * wpt < 152 * 16 && wpt * 64 <= nv) wpt *= 2;
     const dim3 block(32 * wpt, 8 / wpt), grid(static_cast<unsigned>((tokens + block.y - 1) / block.y));
-    with_type(dtype, v, [&](auto tag, auto width) {
-        unpermute_bwd<decltype(tag), decltype(width)::value>
-            <<<grid, block, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-                static_cast<const uint8_t *>(dout), static_cast<const uint8_t *>(ys), weights, row_of_slot,
-                static_cast<int>(tokens), static_cast<int>(topk), nv, static_cast<uint8_t *>(dys), dweights);
-    });
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int nt = static_cast<int>(tokens), nk = static_cast<int>(topk);
+    if (v == 2)
+        with_type(dtype, [&](auto tag) {
+            using T = decltype(tag);
+            any_unpermute_bwd<T><<<grid, block, 0, s>>>(static_cast<const T *>(dout), static_cast<const T *>(ys), weights,
+                                                        row_of_slot, nt, nk, hidden, static_cast<T *>(dys), dweights);
+        });
+    else
+        with_type(dtype, v, [&](auto tag, auto width) {
+            if constexpr (decltype(width)::value > 2)
+                unpermute_bwd<decltype(tag), decltype(width)::value><<<grid, block, 0, s>>>(
+                    static_cast<const uint8_t *>(dout), static_cast<const uint8_t *>(ys), weights, row_of_slot, nt, nk, nv,
+                    static_cast<uint8_t *>(dys), dweights);
+        });
     return done();
 }
 
