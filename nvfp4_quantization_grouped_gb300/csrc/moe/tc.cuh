@@ -148,6 +148,14 @@ __device__ __forceinline__ void acquire_map(const CUtensorMap *map) {
     asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
 }
 
+// -------------------------------------------------------- dependent launch
+
+// A kernel launched as a programmatic dependent may start while the kernel before it in the stream ends: this waits until
+// that one is done and its results are visible (at once where the launch was an ordinary one).  The other lets the next
+// such kernel start.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ----------------------------------------------------------------- cluster
 
 __device__ __forceinline__ uint32_t cluster_rank() {
