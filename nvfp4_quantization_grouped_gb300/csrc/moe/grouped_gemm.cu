@@ -5,8 +5,8 @@
 // A and B_e given as codes with one scale per 32 (E8M0) or 16 (E4M3) elements of
 // k, and for NVFP4 u_e = 1 / (S_A,e S_B,e) from the experts' amax (S = 2688 / amax,
 // what the quantizer multiplied by).  The tensor core multiplies codes and block
-// scales and sums in FP32 (tcgen05.mma with block_scale); u_e and the rounding to
-// the output type are the epilogue.
+// scales and sums in FP32 (tcgen05.mma with block_scale; long sums in pieces, see
+// kPiece); u_e and the rounding to the output type are the epilogue.
 //
 // Persistent blocks walk the tiles of all experts (column tiles of a row tile one
 // after another so that its rows stay in L2).  With many rows an expert, pairs of
@@ -16,7 +16,7 @@
 // memory and issues the products, and 8 warps drain the accumulators.
 //   What bounds it: an NVFP4 stage of a pair is 512 cycles of products and about 200 of
 // scale copies in the same queue, an MXFP8 one 512 and 50; a tile's end costs about 1000
-// more.  65536 x 2048 x 2048 NVFP4 over 32 experts: 109 us (5.0 PFLOP/s); 262144 x 4096 x
+// more.  65536 x 2048 x 2048 NVFP4 over 32 experts: 110 us (5.0 PFLOP/s); 262144 x 4096 x
 // 2048 MXFP8 over 128 experts: 1500 us (2.9 PFLOP/s) at the clock that the power limit
 // leaves, 1355 us for a launch by itself; 512 rows over 128 experts, 2048 x 4096 NVFP4:
 // 74 us, the weights at 6.2 TB/s.  Launched as a programmatic dependent, a block sets up
@@ -40,7 +40,7 @@ constexpr int kRowsT = 128;          // rows of a tile: the lanes of tensor memo
 constexpr int kStageK = 128;         // bytes of k per stage: one 128-byte swizzled row
 constexpr int kScaleTile = 512;      // bytes of one 128 x 4 scale tile
 constexpr int kThreads = 384;        // warp 0 loads, warp 1 multiplies, warps 4-11 drain
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 8, kDrain = 4;   // the draining warps, the first of them
 constexpr int kBoxA = 32;            // rows of A that single blocks load at a time
 constexpr int kOutBuf = 32 * 128;    // a draining warp's piece of results: 32 rows x 128 bytes
 constexpr int kStatic = 4096;        // what the blocks' static shared memory stays below
@@ -362,27 +362,40 @@ template <int kStages> struct Ring {
 // The loops of the issuing warps do not leave when a wait runs out (then every further wait returns at once and nothing
 // more is issued): without such exits their counters are uniform, and so are the addresses and descriptors.
 
-// The products of one output tile, `len` bytes of k, by the (converged) issuing warp.  n: tiles so far of this unit.
-template <bool NV, int BN, bool kPair, typename R>
-__device__ __forceinline__ void multiply_tile(Barriers &sh, const Stages<NV, BN, kPair> &st, int n, R &ring, int len, bool &ok) {
+// The tensor core cuts off what its FP32 sum does not hold at every step of 32 bytes of
+// k, toward zero: an error of 1 to 2e-8 of the sum a step that grows with the length
+// (MXFP8, one expert of 4096 / 65536 rows: 1e-6 / 2.5e-5 of the weight gradient, sums of one
+// sign twice that).  So a sum longer than this many stages is taken in pieces, which the
+// draining warps add in FP32, rounding to nearest: 5e-7 at any length.  A piece costs a
+// tile's end: MXFP8 weight gradients of 8192 rows an expert 72.8 -> 79.2 us, NVFP4 63.6 ->
+// 65.9, products of 4096 MXFP8 columns 97.5 -> 101.  BF16 results, whose own rounding is
+// 2e-3, have longer pieces (2e-5).
+template <typename T> constexpr int kPiece = sizeof(T) == 4 ? 16 : 256;
+
+// The products of one output tile, `len` bytes of k, by the (converged) issuing warp.  n: pieces so far of this unit.
+template <typename T, bool NV, int BN, bool kPair, typename R>
+__device__ __forceinline__ void multiply_tile(Barriers &sh, const Stages<NV, BN, kPair> &st, int &n, R &ring, int len, bool &ok) {
     using C = Cfg<NV, BN, kPair>;
     volatile uint32_t *dead = &sh.dead;
-    const int a = n % C::kAcc, kt = (len + kStageK - 1) / kStageK;
-    ok = ok && (n < C::kAcc || tc::bar_wait(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead));
-    __syncwarp();
-    tc::fence_after();
-    for (int k = 0; k < kt; ++k, ring.next()) {
-        ok = ok && tc::bar_wait(tc::smem_u32(&sh.full[ring.s]), ring.round, dead);
+    const int kt = (len + kStageK - 1) / kStageK;
+    for (int k0 = 0; k0 < kt; k0 += kPiece<T>, ++n) {
+        const int a = n % C::kAcc, k1 = min(kt, k0 + kPiece<T>);
+        ok = ok && (n < C::kAcc || tc::bar_wait(tc::smem_u32(&sh.acc_empty[a]), (n / C::kAcc - 1) & 1, dead));
         __syncwarp();
         tc::fence_after();
-        if (tc::elect() && ok) {
-            // the last stage holds only what is left of k
-            multiply_stage(st, ring.s, a * BN, (len - k * kStageK + 31) / 32, k > 0);
-            tc::commit<kPair>(tc::smem_u32(&sh.empty[ring.s]));
-            if (k == kt - 1) tc::commit<kPair>(tc::smem_u32(&sh.acc_full[a]));
+        for (int k = k0; k < k1; ++k, ring.next()) {
+            ok = ok && tc::bar_wait(tc::smem_u32(&sh.full[ring.s]), ring.round, dead);
+            __syncwarp();
+            tc::fence_after();
+            if (tc::elect() && ok) {
+                // the last stage holds only what is left of k
+                multiply_stage(st, ring.s, a * BN, (len - k * kStageK + 31) / 32, k > k0);
+                tc::commit<kPair>(tc::smem_u32(&sh.empty[ring.s]));
+                if (k == k1 - 1) tc::commit<kPair>(tc::smem_u32(&sh.acc_full[a]));
+            }
+            __syncwarp();
+            ring.issued += ok;
         }
-        __syncwarp();
-        ring.issued += ok;
     }
 }
 
@@ -444,30 +457,50 @@ template <int kStages> __device__ __forceinline__ void settle_loads(Barriers &sh
     else tc::pause(1000000);   // these copies count on the other block's barriers: time for them to land
 }
 
-// The finished accumulator of the unit's n-th tile to memory by one draining warp.
-// It is handed back as soon as it is in registers: scaling, rounding and stores run
-// while the next tile is multiplied.  ahead(): what the next tile needs from memory,
+// A finished tile of `kt` stages to memory by one draining warp; n: pieces so far of this
+// unit.  An accumulator is handed back as soon as it is in registers: scaling, rounding
+// and stores run while the next tile is multiplied.  ahead(): what the next tile needs from memory,
 // asked for before the stores.  False: a wait ran out.
 template <bool NV, int BN, bool kPair, typename T, typename F>
-__device__ __forceinline__ bool drain_tile(Barriers &sh, int n, int warp, int lane, float amax_a, float amax_b, const OutAt<T> &w,
+__device__ __forceinline__ bool drain_tile(Barriers &sh, int &n, int kt, int warp, int lane, float amax_a, float amax_b, const OutAt<T> &w,
                                            uint32_t buf, F &&ahead) {
     using C = Cfg<NV, BN, kPair>;
-    const int a = n % C::kAcc, q = warp & 3, h = (warp - 4) >> 2;
+    const int q = warp & 3, h = (warp - kDrain) >> 2;
     float ua = 1.0f, ub = 1.0f;
     if (NV) {
         ua = __fdiv_rn(1.0f, tensor_scale(amax_a));
         ub = __fdiv_rn(1.0f, tensor_scale(amax_b));
     }
-    if (!tc::bar_wait_warp(tc::smem_u32(&sh.acc_full[a]), (n / C::kAcc) & 1, &sh.dead)) return false;
-    tc::fence_after();
+    const uint32_t at = h * (BN / 2) + (static_cast<uint32_t>(32 * q) << 16);
+    auto wait = [&] {
+        const bool ok = tc::bar_wait_warp(tc::smem_u32(&sh.acc_full[n % C::kAcc]), (n / C::kAcc) & 1, &sh.dead);
+        tc::fence_after();
+        return ok;
+    };
+    auto hand_back = [&] {
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            const uint32_t bar = tc::smem_u32(&sh.acc_empty[n % C::kAcc]);
+            if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
+            else tc::bar_arrive(bar);
+        }
+        ++n;
+    };
+    if (!wait()) return false;
     uint32_t v[BN / 2];
-    tc::tmem_ld(a * BN + h * (BN / 2) + (static_cast<uint32_t>(32 * q) << 16), v);
-    tc::fence_before();
-    __syncwarp();
-    if (lane == 0) {
-        const uint32_t bar = tc::smem_u32(&sh.acc_empty[a]);
-        if (kPair) tc::bar_arrive_cluster(tc::map_to(bar, 0));
-        else tc::bar_arrive(bar);
+    tc::tmem_ld(at + (n % C::kAcc) * BN, v);
+    hand_back();
+    for (int k = kPiece<T>; k < kt; k += kPiece<T>) {
+        if (!wait()) return false;
+#pragma unroll
+        for (int j = 0; j < BN / 2; j += 8) {   // (16 at a time spills)
+            uint32_t x[8];
+            tc::tmem_ld(at + (n % C::kAcc) * BN + j, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[j + i] = __float_as_uint(__uint_as_float(v[j + i]) + __uint_as_float(x[i]));
+        }
+        hand_back();
     }
     const OutAt<T> here = w;
     ahead();
@@ -535,15 +568,16 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
     } else if (warp == 1 && half == 0) {
         const int mine = unit < used ? uniform(static_cast<int>((used - unit + units - 1) / units)) : 0;
         Ring<C::kStages> ring;
+        int n = 0;
         bool ok = true;
-        for (int n = 0; n < mine; ++n) multiply_tile(sh, st, n, ring, P.k_bytes, ok);
+        for (int i = 0; i < mine; ++i) multiply_tile<T>(sh, st, n, ring, P.k_bytes, ok);
         if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, ring.issued);
-    } else if (warp >= 4) {
-        const int q = warp & 3, h = (warp - 4) >> 2;   // lanes 32 q .., column half h
+    } else if (warp >= kDrain) {
+        const int q = warp & 3, h = (warp - kDrain) >> 2;   // lanes 32 q .., column half h
         constexpr int kHalf = BN / 2;
         T *out = static_cast<T *>(P.out);
         const int r0 = half * kRowsT + 32 * q;   // the warp's first row of the tile
-        const uint32_t buf = st.out(warp - 4);
+        const uint32_t buf = st.out(warp - kDrain);
         OutAt<T> w;
         w.pitch = P.N;
         w.wide = P.N * sizeof(T) % 16 == 0;
@@ -565,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
             if (g == P.E) {
                 zero_tile<kHalf>(w, lane);
                 find(i + units);
-            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, amax_a, amax_b, w, buf, [&] { find(i + units); })) {
+            } else if (!drain_tile<NV, BN, kPair>(sh, n, P.kt, warp, lane, amax_a, amax_b, w, buf, [&] { find(i + units); })) {
                 break;
             }
         }
@@ -824,14 +858,14 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
         bool ok = true;
         while (next_wtile(P, sh, r, unit, units, total, t)) {
             const int len = uniform(NV ? t.rows / 2 : t.rows);
-            if (len > 0) multiply_tile(sh, st, n++, ring, len, ok);
+            if (len > 0) multiply_tile<T>(sh, st, n, ring, len, ok);
         }
         if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, ring.issued);
-    } else if (warp >= 4) {
-        const int q = warp & 3, h = (warp - 4) >> 2;
+    } else if (warp >= kDrain) {
+        const int q = warp & 3, h = (warp - kDrain) >> 2;
         constexpr int kHalf = BN / 2;
         T *out = static_cast<T *>(P.out);
-        const uint32_t buf = st.out(warp - 4);
+        const uint32_t buf = st.out(warp - kDrain);
         OutAt<T> w;
         w.pitch = P.K;
         w.wide = P.K * sizeof(T) % 16 == 0;
@@ -853,8 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
             if (t.rows == 0) {   // no rows: a zero gradient
                 if (!w.add) zero_tile<kHalf>(w, lane);
                 find();
-            } else if (!drain_tile<NV, BN, kPair>(sh, n++, warp, lane, amax_a, amax_b, w, buf, find)) {
-                break;
+            } else {
+                const int stages = ((NV ? t.rows / 2 : t.rows) + kStageK - 1) / kStageK;
+                if (!drain_tile<NV, BN, kPair>(sh, n, stages, warp, lane, amax_a, amax_b, w, buf, find)) break;
             }
         }
     }

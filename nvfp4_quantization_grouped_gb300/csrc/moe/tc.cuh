@@ -269,8 +269,17 @@ __device__ __forceinline__ void mma_nvf4(uint32_t d, uint32_t a, uint32_t b, uin
             : "memory");
 }
 
-// The next 64 or 128 columns of this warp's 32 lanes, thread i holding lane i's.  The load and its wait are
+// The next 8, 64 or 128 columns of this warp's 32 lanes, thread i holding lane i's.  The load and its wait are
 // one statement: nothing can use the registers before they are written.
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(addr)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[64]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
