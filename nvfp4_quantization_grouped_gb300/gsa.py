@@ -506,18 +506,20 @@ def bwd_graph_safe(dy, x, probs, split_dev, act: str, recipe_kind: int, rht: boo
 BF16, FP16, FP32 = 0, 1, 2
 _torch = None
 _raw_stream = None
+_current_device = None
 _DTYPES: dict = {}
 
 
 def _setup():
     """The torch module, imported on the first call, and the element type codes."""
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     import torch
     _DTYPES.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
     load()
     # the current stream's handle without a Stream object (2 us), where this torch has the call
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
     return torch
 
@@ -541,9 +543,14 @@ def _same_device(what, device, *tensors):
 
 def _stream_of(stream, device, *inputs):
     """Handle of `stream`, or of the device's current one.  Inputs of a call on an explicit stream are recorded on
-    it, so that the caching allocator keeps them until the stream is done with them."""
+    it, so that the caching allocator keeps them until the stream is done with them.  The library launches on the
+    current device (whose null stream a handle of 0 is), so tensors or a stream of another one are refused."""
+    if device.index != _current_device():
+        raise GsaError(1, f"tensors on {device}, but the current device is cuda:{_current_device()}")
     if stream is None:
         return _raw_stream(device.index)
+    if stream.device != device:
+        raise GsaError(1, f"tensors on {device}, stream of {stream.device}")
     for t in inputs:
         if t is not None:
             t.record_stream(stream)
