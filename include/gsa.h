@@ -431,10 +431,12 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
                                   int64_t M, int64_t N, int64_t K, int32_t recipe_kind, void *dw, int32_t out_dtype,
                                   int32_t accumulate, void *workspace, size_t workspace_bytes, gsa_stream_t stream);
 
-/* Synchronizes `stream`; then what grouped products on the current device have
- * reported since the last query, which it clears: GSA_OK, GSA_ERR_INVALID_ARG
- * (a device split), GSA_ERR_DEVICE_TIMEOUT (a bounded wait ran out).  Errors:
- * CUDA. */
+/* Takes one report out of the current device's word and synchronizes `stream`:
+ * GSA_ERR_DEVICE_TIMEOUT (a bounded wait ran out), GSA_ERR_INVALID_ARG (a device
+ * split) or GSA_OK when there is none left.  The word is one a device: it collects
+ * what products report on any stream, each kind once until it is taken, so a
+ * program that runs them on several streams joins them first.  Queries may run
+ * on several threads; none loses a report.  Errors: CUDA. */
 gsa_status gsa_grouped_gemm_status(gsa_stream_t stream);
 
 /* Failure-detection self-test.  Enqueues a one-thread kernel that runs one of

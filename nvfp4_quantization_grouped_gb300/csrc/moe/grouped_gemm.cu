@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "gsa.h"
+#include "moe/status.cuh"
 #include "tc.cuh"
 
 namespace {
@@ -45,10 +46,17 @@ constexpr int kBoxA = 32;            // rows of A that single blocks load at a t
 constexpr int kOutBuf = 32 * 128;    // a draining warp's piece of results: 32 rows x 128 bytes
 constexpr int kStatic = 4096;        // what the blocks' static shared memory stays below
 
-enum { ERR_SPLIT = 1, ERR_TIMEOUT = 2 };
+using gemm_status::ERR_SPLIT;
+using gemm_status::ERR_TIMEOUT;
 
-// What went wrong in grouped products on this device since the last query.
-__device__ uint32_t g_status;
+// What went wrong in grouped products on this device and was not yet asked for, and what the query under way took.
+__device__ uint32_t g_status, g_taken;
+
+// The kernel of a query: reports only ever set bits and queries run one at a time, so a bit seen is the bit cleared.
+__global__ void take_status() {
+    g_taken = gemm_status::next_report(atomicOr(&g_status, 0u));
+    atomicAnd(&g_status, ~g_taken);
+}
 
 struct GemmParams {
     CUtensorMap tm_a, tm_b, tm_sa, tm_sb;
@@ -1167,12 +1175,19 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
 }
 
 gsa_status gsa_grouped_gemm_status(gsa_stream_t stream) {
-    if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return GSA_ERR_CUDA;
-    uint32_t err = 0, zero = 0;
-    if (cudaMemcpyFromSymbol(&err, g_status, 4) != cudaSuccess) return GSA_ERR_CUDA;
-    if (err && cudaMemcpyToSymbol(g_status, &zero, 4) != cudaSuccess) return GSA_ERR_CUDA;
-    if (err & ERR_SPLIT) return GSA_ERR_INVALID_ARG;
-    return err ? GSA_ERR_DEVICE_TIMEOUT : GSA_OK;
+    static std::mutex one;   // g_taken is one query's at a time
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    std::lock_guard<std::mutex> lock(one);
+    uint32_t report = 0;
+    take_status<<<1, 1, 0, s>>>();
+    const bool ok = cudaGetLastError() == cudaSuccess &&
+                    cudaMemcpyFromSymbolAsync(&report, g_taken, sizeof(report), 0, cudaMemcpyDeviceToHost, s) == cudaSuccess &&
+                    cudaStreamSynchronize(s) == cudaSuccess;
+    if (!ok) {
+        cudaGetLastError();
+        return GSA_ERR_CUDA;
+    }
+    return gemm_status::status_of(report);
 }
 
 }  // extern "C"

@@ -767,5 +767,6 @@ def grouped_gemm_wgrad(a: dict, b: dict, split, m: int, n: int, k: int, recipe_k
 
 
 def grouped_gemm_status(stream=None) -> int:
-    """What the grouped products on this device have reported since the last query (synchronizes the stream)."""
+    """Takes one report of the grouped products on the current device (synchronizes the stream): 6 (a bounded wait ran
+    out), 1 (a bad device split: that call wrote nothing, an output it allocated holds anything) or 0."""
     return load().gsa_grouped_gemm_status(_stream_ptr(stream))
