@@ -436,7 +436,8 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
  * split) or GSA_OK when there is none left.  The word is one a device: it collects
  * what products report on any stream, each kind once until it is taken, so a
  * program that runs them on several streams joins them first.  Queries may run
- * on several threads; none loses a report.  Errors: CUDA. */
+ * on several threads; none loses a report.  Errors: CUDA (also on a stream that
+ * is being captured, whose capture goes on). */
 gsa_status gsa_grouped_gemm_status(gsa_stream_t stream);
 
 /* Failure-detection self-test.  Enqueues a one-thread kernel that runs one of

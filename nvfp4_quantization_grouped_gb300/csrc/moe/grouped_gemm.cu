@@ -1177,12 +1177,21 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
 gsa_status gsa_grouped_gemm_status(gsa_stream_t stream) {
     static std::mutex one;   // g_taken is one query's at a time
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &capturing) != cudaSuccess || capturing != cudaStreamCaptureStatusNone) {
+        cudaGetLastError();
+        return GSA_ERR_CUDA;
+    }
     std::lock_guard<std::mutex> lock(one);
+    // nothing here touches a capture that another thread may have under way
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GSA_ERR_CUDA;
     uint32_t report = 0;
     take_status<<<1, 1, 0, s>>>();
     const bool ok = cudaGetLastError() == cudaSuccess &&
                     cudaMemcpyFromSymbolAsync(&report, g_taken, sizeof(report), 0, cudaMemcpyDeviceToHost, s) == cudaSuccess &&
                     cudaStreamSynchronize(s) == cudaSuccess;
+    cudaThreadExchangeStreamCaptureMode(&mode);
     if (!ok) {
         cudaGetLastError();
         return GSA_ERR_CUDA;
