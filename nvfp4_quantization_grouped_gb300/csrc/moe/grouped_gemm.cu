@@ -1126,8 +1126,11 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     WgradParams P;
     std::memset(&P, 0, sizeof(P));
     const int sc = nv ? 4 : 1;
-    CUtensorMap plain_a, plain_b;   // the experts' maps but for origin, extents and pitch
-    if (!map_codes(&plain_a, w, 4096, 4096, pair ? kRowsT : kBoxA) || !map_codes(&plain_b, w, 4096, 4096, 128) ||
+    // The experts' maps but for origin, extents and pitch.  Encoded for the smallest matrix: from a large one something
+    // stays in the map that editing does not change, and copies then touch memory up to 128 KB behind an expert's origin,
+    // past the operand's end (encoded 4096 x 4096, 128 x 4096 or 65536 x 128: seen; 128 x 128 and below: none).
+    CUtensorMap plain_a, plain_b;
+    if (!map_codes(&plain_a, w, 1, 16, pair ? kRowsT : kBoxA) || !map_codes(&plain_b, w, 1, 16, 128) ||
         // (without rows the scale buffers may be empty: nothing is loaded then)
         !map_scales(&P.tm_sa, a_tiles ? a->scale : w, a_tiles ? a_tiles : 1, sc) ||
         !map_scales(&P.tm_sb, b_tiles ? b->scale : w, b_tiles ? b_tiles : 1, sc) ||
