@@ -712,13 +712,16 @@ __global__ void __launch_bounds__(kPrepThreads) wgrad_prepare(const __grid_const
         const int e = i < P.E ? i : i - P.E;
         const int64_t mp = d.pad0[e + 1] - d.pad0[e], pitch = NV ? mp / 2 : mp, first = NV ? d.pad0[e] / 2 : d.pad0[e];
         const int rows = i < P.E ? P.N : P.K;
-        if (threadIdx.x == 0 && mp > 0) {
-            const bool odd = pitch % 16 != 0;
-            const uint8_t *at = odd ? (i < P.E ? P.pack_a : P.pack_b) + pack_at(d, e) * rows
-                                    : (i < P.E ? P.a : P.b) + first * rows;
-            map = i < P.E ? plain_a : plain_b;
-            tc::edit_map(&map, at, static_cast<uint32_t>(pitch), static_cast<uint32_t>(rows), odd ? pitch + 8 : pitch);
-            P.maps[i] = map;
+        if (threadIdx.x < 32 && mp > 0) {
+            if (threadIdx.x == 0) {
+                const bool odd = pitch % 16 != 0;
+                const uint8_t *at = odd ? (i < P.E ? P.pack_a : P.pack_b) + pack_at(d, e) * rows
+                                        : (i < P.E ? P.a : P.b) + first * rows;
+                map = i < P.E ? plain_a : plain_b;
+                tc::edit_map(&map, at, static_cast<uint32_t>(pitch), static_cast<uint32_t>(rows), odd ? pitch + 8 : pitch);
+            }
+            __syncwarp();
+            tc::publish_map(P.maps + i, &map);
         }
         __syncthreads();
     }

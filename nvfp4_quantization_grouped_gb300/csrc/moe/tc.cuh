@@ -143,6 +143,14 @@ __device__ __forceinline__ void edit_map(CUtensorMap *map, const void *p, uint32
     asm volatile("tensormap.replace.tile.global_stride.shared::cta.b1024.b64 [%0], 0, %1;" ::"r"(m), "l"(pitch) : "memory");
 }
 
+// Whole warp: a finished map from shared to global memory, released to the proxy through which copies read maps (which
+// plain stores and the end of a kernel do not order).
+__device__ __forceinline__ void publish_map(CUtensorMap *to, const CUtensorMap *map) {
+    asm volatile("tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(to),
+                 "r"(smem_u32(map))
+                 : "memory");
+}
+
 // Before the first copy through a map that another kernel wrote to global memory.
 __device__ __forceinline__ void acquire_map(const CUtensorMap *map) {
     asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
