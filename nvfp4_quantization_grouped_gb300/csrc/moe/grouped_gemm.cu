@@ -216,8 +216,8 @@ __device__ __forceinline__ void multiply_stage(const Stages<NV, BN, kPair> &st, 
     }
 }
 
-// After a wait that ran out: waits (bounded) for the last stages' barriers, so
-// that no copy or product is in flight when the block leaves.
+// Waits (bounded) for the last stages' barriers, so that no copy, product or arrival
+// is in flight when the block leaves.
 template <int kStages> __device__ __forceinline__ void settle(uint64_t *bars, int it) {
     uint32_t none = 0;
     for (int j = it < kStages ? 0 : it - kStages; j < it; ++j)
@@ -459,9 +459,12 @@ __device__ __forceinline__ void prefetch_rows(const StageAt &w) {
     __syncwarp();
 }
 
-// After a wait of the loading warp ran out.
-template <int kStages> __device__ __forceinline__ void settle_loads(Barriers &sh, int half, int it) {
-    if (half == 0) settle<kStages>(sh.full, it);
+// The loading warp's end: the block stays until the products' arrivals on its last stages' barriers are in (they go to
+// both blocks of a pair; a later one would change the shared memory of whatever block comes next).  After a wait that ran
+// out: until its copies are.
+template <int kStages> __device__ __forceinline__ void end_loads(Barriers &sh, int half, int it, bool ok) {
+    if (ok) settle<kStages>(sh.empty, it);
+    else if (half == 0) settle<kStages>(sh.full, it);
     else tc::pause(1000000);   // these copies count on the other block's barriers: time for them to land
 }
 
@@ -572,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
                 ahead.x += kStageK, ahead.a_tile += C::kSc;
             }
         }
-        if (!ok) settle_loads<C::kStages>(sh, half, ring.issued);
+        end_loads<C::kStages>(sh, half, ring.issued, ok);
     } else if (warp == 1 && half == 0) {
         const int mine = unit < used ? uniform(static_cast<int>((used - unit + units - 1) / units)) : 0;
         Ring<C::kStages> ring;
@@ -862,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
                 w.x += kStageK, w.a_tile += C::kSc, w.b_tile += C::kSc;
             }
         }
-        if (!ok) settle_loads<C::kStages>(sh, half, ring.issued);
+        end_loads<C::kStages>(sh, half, ring.issued, ok);
     } else if (warp == 1 && half == 0) {
         Ring<C::kStages> ring;
         int n = 0;
