@@ -288,6 +288,14 @@ def _stream_ptr(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _record_layout(out: dict, scale_layout: int, keys=("row_scale", "col_scale")) -> None:
+    """Notes on the scale buffers the layout they are written in: the products take tiled scales only, and the byte
+    counts of both layouts are often the same."""
+    for k in keys:
+        if k in out:
+            out[k].scale_layout = scale_layout
+
+
 def alloc_qtensor(split_sizes, width: int, recipe_kind: int, rowwise: bool, columnwise: bool, device,
                   amax_experts: int | None = None, scale_layout: int = SCALES_COMPACT) -> dict:
     """Allocate the quantized copies of a [M, width] grouped tensor (uint8).
@@ -309,6 +317,7 @@ def alloc_qtensor(split_sizes, width: int, recipe_kind: int, rowwise: bool, colu
         if columnwise:
             out["amax_col"] = torch.empty(E, dtype=torch.float32, device=device)
     out["_info"] = info
+    _record_layout(out, scale_layout)
     return out
 
 
@@ -360,6 +369,7 @@ def fwd(x, probs, split_sizes, act: str, recipe_kind: int, rht: bool = False, rh
     st = grouped_scaled_act_fwd(_ptr(x), _ptr(probs), split_sizes, w_in, a, params, rec, qout_of(out),
                                 _ptr(out.get("y")), ctypes.c_void_p(ws.ptr), ws.nbytes, _stream_ptr(stream))
     _check(st, "grouped_scaled_act_fwd")
+    _record_layout(out, scale_layout)
     return out
 
 
@@ -397,6 +407,7 @@ def bwd(dy, x, probs, split_sizes, act: str, recipe_kind: int, rht: bool = False
                                 _ptr(out.get("dx")), dxq, _ptr(out.get("dprobs")), yq,
                                 ctypes.c_void_p(ws.ptr), ws.nbytes, _stream_ptr(stream))
     _check(st, "grouped_scaled_act_bwd")
+    _record_layout(out, scale_layout, (("row_scale", "col_scale") if dxq else ()) + (("y_col_scale",) if yq else ()))
     return out
 
 
@@ -421,6 +432,7 @@ def alloc_qtensor_bound(E: int, M: int, width: int, recipe_kind: int, rowwise: b
         if columnwise:
             out["amax_col"] = torch.empty(E, dtype=torch.float32, device=device)
     out["_info"] = info
+    _record_layout(out, scale_layout)
     return out
 
 
@@ -459,6 +471,7 @@ def fwd_graph_safe(x, probs, split_dev, act: str, recipe_kind: int, rht: bool = 
                                            qout_of(out), _ptr(out.get("y")), _ptr(out.get("pad")),
                                            ctypes.c_void_p(ws.ptr), ws.nbytes, _stream_ptr(stream))
     _check(st, "grouped_scaled_act_fwd_graph_safe")
+    _record_layout(out, scale_layout)
     return out
 
 
@@ -495,6 +508,7 @@ def bwd_graph_safe(dy, x, probs, split_dev, act: str, recipe_kind: int, rht: boo
                                            _ptr(out.get("pad")), ctypes.c_void_p(ws.ptr), ws.nbytes,
                                            _stream_ptr(stream))
     _check(st, "grouped_scaled_act_bwd_graph_safe")
+    _record_layout(out, scale_layout, (("row_scale", "col_scale") if dxq else ()) + (("y_col_scale",) if yq else ()))
     return out
 
 
@@ -700,6 +714,8 @@ def _operand(q: dict, side: str, recipe_kind: int, experts: int, what: str, dev)
     data, scale, amax = q.get(side + "_data"), q.get(side + "_scale"), None
     if data is None or scale is None:
         raise GsaError(1, f"{what}: no {side}_data or {side}_scale (a {side} copy with tiled scales is needed)")
+    if getattr(scale, "scale_layout", SCALES_TILED) != SCALES_TILED:
+        raise GsaError(1, f"{what}: compact scales (a copy written with scale_layout=SCALES_TILED is needed)")
     for t in (data, scale):
         if t.dtype is not u8 or not t.is_contiguous() or t.device != dev:
             raise GsaError(1, f"{what}: contiguous uint8 {side} copy on {dev} expected")
@@ -726,10 +742,11 @@ def _product_args(what, split, out_dtype):
 def grouped_gemm(a: dict, b: dict, split, m: int, n: int, k: int, recipe_kind: int, out_dtype=None,
                  b_columnwise: bool = False, out=None, stream=None):
     """out [m, n] = A B_e^T over the rows of each expert, on the quantized copies that fwd / bwd write with
-    scale_layout=SCALES_TILED.  a: the rowwise copy of the [m, k] rows.  b: the experts' weights, the rowwise copy
-    of [E * n, k] split into E times n rows, or with b_columnwise the columnwise copy of [E * k, n] split into E
-    times k rows (the input gradient's product with weights [k, n]).  split: [E] int64 on the device, sum at most
-    m (rows past it become zero).  out_dtype: torch.bfloat16 (default) or torch.float32."""
+    scale_layout=SCALES_TILED (their compact scales are refused, buffers of the caller's own are taken as tiled).
+    a: the rowwise copy of the [m, k] rows.  b: the experts' weights, the rowwise copy of [E * n, k] split into E
+    times n rows, or with b_columnwise the columnwise copy of [E * k, n] split into E times k rows (the input
+    gradient's product with weights [k, n]).  split: [E] int64 on the device, sum at most m (rows past it become
+    zero).  out_dtype: torch.bfloat16 (default) or torch.float32."""
     torch = _torch or _setup()
     out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
     dev, experts, code = _product_args("grouped_gemm", split, out_dtype)
