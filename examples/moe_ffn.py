@@ -43,7 +43,8 @@ class MoeFfn:
         """x [tokens, H] BF16, expert_idx [tokens, topk] (outside [0, E): dropped), probs [tokens, topk] FP32
         -> out [tokens, H] and what the backward needs."""
         r, e = self.recipe, self.experts
-        row, split = gsa.moe_sort(expert_idx, e)             # split [E + 1]: the dropped rows are the last group
+        row, split = gsa.moe_sort(expert_idx, e)
+        split = gsa.moe_groups(split)                        # the dropped rows are the last group (or the last expert's)
         xs, ps = gsa.moe_permute(x, row, probs)
         m, used = xs.shape[0], split[:e]
         qx = self._quantize(xs, split)

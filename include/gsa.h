@@ -330,9 +330,11 @@ gsa_status grouped_scaled_act_bwd_graph_safe(const void *dy_bf16, const void *x_
  *     one expert in slot order (a stable sort).  Dropped slots follow the last
  *     expert's rows; their entry is ~row (negative).
  *   split_sizes [experts + 1] int64, device: rows per expert, then the dropped
- *     rows.  The whole array is a split of n rows over experts + 1 groups for
- *     the graph-safe calls; its first `experts` entries are the split of the
- *     grouped products.
+ *     rows.  Up to 255 experts the whole array is a split of n rows over
+ *     experts + 1 groups for the graph-safe calls, and its first `experts`
+ *     entries are the split of the grouped products.  With 256 experts, add the
+ *     last entry to the one before it and pass 256 groups to both: the dropped
+ *     rows are zeros behind the last expert's own and change no result.
  * Rows have `hidden` elements of one element type (GSA_BF16, GSA_FP16,
  * GSA_FP32), any hidden >= 1; probs, weights and their gradients are FP32.
  * Sums run in FP32 in slot order and are rounded once.  Nothing synchronizes or

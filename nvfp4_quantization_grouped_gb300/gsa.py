@@ -608,6 +608,21 @@ def moe_sort(expert_idx, experts: int, out: tuple | None = None, stream=None):
     return row, split
 
 
+MAX_GROUPS = 256
+
+
+def moe_groups(split_sizes):
+    """The groups of the sorted rows, from moe_sort's split_sizes [experts + 1]: that split itself, the dropped rows its
+    last group.  With 256 experts, one group more than the graph-safe calls take: [256], the dropped rows counted to the
+    last expert (rows of zeros behind its own, which change no result).  The first `experts` entries are the split of
+    the products."""
+    if split_sizes.shape[0] <= MAX_GROUPS:
+        return split_sizes
+    groups = split_sizes[:-1].clone()
+    groups[-1:] += split_sizes[-1:]
+    return groups
+
+
 def _plan_and_rows(what, row_of_slot, rows, by_slot):
     """(tokens, topk, hidden, dtype code, device) of a plan and a [tokens or tokens * topk, hidden] row tensor."""
     torch = _torch or _setup()
