@@ -481,6 +481,9 @@ __device__ __forceinline__ bool drain_tile(Barriers &sh, int &n, int kt, int war
     if (NV) {
         ua = __fdiv_rn(1.0f, tensor_scale(amax_a));
         ub = __fdiv_rn(1.0f, tensor_scale(amax_b));
+        // A sum (2^-20 to 2^53 units) times ua, then ub: their product may leave FP32's range where the result does not.
+        // So may the first step, but only with ua far out and ub leading back, and then the product is in range.
+        if ((ua > 0x1p64f && ub < 1.0f) || (ua < 0x1p-64f && ub > 4.0f)) ua *= ub, ub = 1.0f;
     }
     const uint32_t at = h * (BN / 2) + (static_cast<uint32_t>(32 * q) << 16);
     auto wait = [&] {
