@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cstring>
 #include <mutex>
 #include <type_traits>
@@ -915,16 +916,21 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_wgrad(const __grid_consta
 
 // -------------------------------------------------------------------- host
 
+// A CUDA call failed: the next call must not take its error, which the runtime keeps, for one of its own.
+gsa_status cuda_error() {
+    cudaGetLastError();
+    return GSA_ERR_CUDA;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+    PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_relaxed);
+    if (fn) return fn;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+        known.store(fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p), std::memory_order_relaxed);
     return fn;
 }
 
@@ -952,25 +958,35 @@ bool map_scales(CUtensorMap *tm, const void *p, int64_t tiles, int box) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Number of SMs of the current device (0: a CUDA error), asked once per device.
+// What is asked once per device: only answers are kept, a failed query is made again.
+struct PerDevice {
+    std::mutex mu;
+    int n[64] = {};
+    template <typename F> int get(F &&ask) {   // 0: a CUDA error
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!n[dev]) {
+            int v = 0;
+            if (ask(dev, v) == cudaSuccess && v > 0) n[dev] = v;
+        }
+        return n[dev];
+    }
+};
+
+// Number of SMs of the current device (0: a CUDA error).
 int sm_count() {
-    static std::mutex mu;
-    static int n[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!n[dev] && cudaDeviceGetAttribute(&n[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n[dev];
+    static PerDevice known;
+    return known.get([](int dev, int &v) { return cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev); });
 }
 
 // A persistent launch of at most `want` blocks (kPair: pairs of blocks), as many as run at once.
 template <bool kPair, typename P>
-gsa_status launch(void (*kernel)(P), const P &params, int threads, size_t smem, int64_t want, cudaStream_t s, int &pairs,
-                  std::once_flag &once) {
+gsa_status launch(void (*kernel)(P), const P &params, int threads, size_t smem, int64_t want, cudaStream_t s, PerDevice &pairs) {
     const int sms = sm_count();
-    if (!sms) return GSA_ERR_CUDA;
+    if (!sms) return cuda_error();
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-        return GSA_ERR_CUDA;
+        return cuda_error();
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
@@ -983,30 +999,30 @@ gsa_status launch(void (*kernel)(P), const P &params, int threads, size_t smem, 
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    if (kPair)   // the machine's clusters may not fill every SM
-        std::call_once(once, [&] {
+    int64_t units = sms;
+    if (kPair) {   // the machine's clusters may not fill every SM
+        units = pairs.get([&](int, int &v) {
             cfg.gridDim = dim3(2 * (sms / 2));
-            if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess) pairs = 0;
+            return cudaOccupancyMaxActiveClusters(&v, kernel, &cfg);
         });
-    if (kPair && pairs <= 0) return GSA_ERR_CUDA;
-    const int64_t units = kPair ? pairs : sms, n = want < units ? want : units;
+        if (!units) return cuda_error();
+    }
+    const int64_t n = want < units ? want : units;
     cfg.gridDim = dim3(static_cast<unsigned>(kPair ? 2 * n : n));
-    return cudaLaunchKernelEx(&cfg, kernel, params) == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, params) == cudaSuccess ? GSA_OK : cuda_error();
 }
 
 template <bool NV, int BN, bool kPair, typename T>
 gsa_status launch_gemm(const GemmParams &P, int64_t tiles, cudaStream_t s) {
-    static std::once_flag once;
-    static int pairs = 0;
+    static PerDevice pairs;
     return launch<kPair, GemmParams>(grouped_gemm<NV, BN, kPair, T>, P, kThreads, Cfg<NV, BN, kPair>::kSmem, tiles * P.n_tiles,
-                                     s, pairs, once);
+                                     s, pairs);
 }
 
 template <bool NV, int BN, bool kPair, typename T> gsa_status launch_wgrad(const WgradParams &P, cudaStream_t s) {
-    static std::once_flag once;
-    static int pairs = 0;
+    static PerDevice pairs;
     return launch<kPair, WgradParams>(grouped_wgrad<NV, BN, kPair, T>, P, kThreads, Cfg<NV, BN, kPair>::kSmem,
-                                      static_cast<int64_t>(P.E) * P.n_tiles * P.k_tiles, s, pairs, once);
+                                      static_cast<int64_t>(P.E) * P.n_tiles * P.k_tiles, s, pairs);
 }
 
 // Workspace of the weight gradient (byte offsets; the maps come first).
@@ -1070,7 +1086,7 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     const int sc = nv ? 4 : 1;
     if (!map_codes(&P.tm_a, a->data, M, k_bytes, pair ? kRowsT : kBoxA) || !map_codes(&P.tm_b, b->data, E * N, k_bytes, 128) ||
         !map_scales(&P.tm_sa, a->scale, a_rows * cols, sc) || !map_scales(&P.tm_sb, b->scale, E * n128 * cols, sc))
-        return GSA_ERR_CUDA;
+        return cuda_error();
     P.split = split_sizes_dev;
     P.amax_a = a->amax;
     P.amax_b = b->amax;
@@ -1144,7 +1160,7 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
         !map_scales(&P.tm_sa, a_tiles ? a->scale : w, a_tiles ? a_tiles : 1, sc) ||
         !map_scales(&P.tm_sb, b_tiles ? b->scale : w, b_tiles ? b_tiles : 1, sc) ||
         (nv && (!map_scales(&P.tm_ta, w + ws.tail_a, E * n128 * 4, 4) || !map_scales(&P.tm_tb, w + ws.tail_b, E * k128 * 4, 4))))
-        return GSA_ERR_CUDA;
+        return cuda_error();
     P.a = static_cast<const uint8_t *>(a->data);
     P.b = static_cast<const uint8_t *>(b->data);
     P.sa = static_cast<const uint8_t *>(a->scale);
@@ -1171,7 +1187,7 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     P.accumulate = accumulate != 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int sms = sm_count();
-    if (!sms) return GSA_ERR_CUDA;
+    if (!sms) return cuda_error();
     // An ordinary launch: as a programmatic dependent too, a pass of 65536 rows, 32 experts took 208 us instead of 191.
     if (nv) wgrad_prepare<true><<<4 * sms, kPrepThreads, 0, s>>>(P, plain_a, plain_b);
     else wgrad_prepare<false><<<static_cast<unsigned>(2 * E < sms ? 2 * E : sms), kPrepThreads, 0, s>>>(P, plain_a, plain_b);
@@ -1190,24 +1206,18 @@ gsa_status gsa_grouped_gemm_status(gsa_stream_t stream) {
     static std::mutex one;   // g_taken is one query's at a time
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &capturing) != cudaSuccess || capturing != cudaStreamCaptureStatusNone) {
-        cudaGetLastError();
-        return GSA_ERR_CUDA;
-    }
+    if (cudaStreamIsCapturing(s, &capturing) != cudaSuccess || capturing != cudaStreamCaptureStatusNone) return cuda_error();
     std::lock_guard<std::mutex> lock(one);
     // nothing here touches a capture that another thread may have under way
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GSA_ERR_CUDA;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return cuda_error();
     uint32_t report = 0;
     take_status<<<1, 1, 0, s>>>();
     const bool ok = cudaGetLastError() == cudaSuccess &&
                     cudaMemcpyFromSymbolAsync(&report, g_taken, sizeof(report), 0, cudaMemcpyDeviceToHost, s) == cudaSuccess &&
                     cudaStreamSynchronize(s) == cudaSuccess;
     cudaThreadExchangeStreamCaptureMode(&mode);
-    if (!ok) {
-        cudaGetLastError();
-        return GSA_ERR_CUDA;
-    }
+    if (!ok) return cuda_error();
     return gemm_status::status_of(report);
 }
 
