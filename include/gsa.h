@@ -338,9 +338,9 @@ gsa_status grouped_scaled_act_bwd_graph_safe(const void *dy_bf16, const void *x_
  * Rows have `hidden` elements of one element type (GSA_BF16, GSA_FP16,
  * GSA_FP32), any hidden >= 1; probs, weights and their gradients are FP32.
  * Sums run in FP32 in slot order and are rounded once.  Nothing synchronizes or
- * allocates: every call can be captured in a CUDA graph.  Tensors of rows,
- * expert_idx and row_of_slot (as an output) start on 16 bytes.  With tokens = 0
- * pointers may be NULL.  A plan entry outside [-n, n) is skipped.
+ * allocates: every call can be captured in a CUDA graph.  Tensors of rows and
+ * row_of_slot (as an output) start on 16 bytes, all others on their element's
+ * size.  With tokens = 0 pointers may be NULL.  A plan entry outside [-n, n) is skipped.
  * Errors: INVALID_ARG, UNSUPPORTED (experts > 256, n or hidden >= 2^31),
  * ALIGNMENT, WORKSPACE (the sort), CUDA. */
 typedef enum { GSA_BF16 = 0, GSA_FP16 = 1, GSA_FP32 = 2 } gsa_dtype;

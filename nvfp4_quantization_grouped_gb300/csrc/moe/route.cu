@@ -615,7 +615,7 @@ gsa_status gsa_moe_sort(const void *expert_idx, int32_t idx_bytes, int64_t token
         return GSA_ERR_UNSUPPORTED;
     const int64_t n = tokens * topk;
     if (!split_sizes || (n > 0 && (!expert_idx || !row_of_slot))) return GSA_ERR_INVALID_ARG;
-    if (!aligned(expert_idx, 16) || !aligned(row_of_slot, 16) || !aligned(split_sizes, 8) || !aligned(workspace, 16))
+    if (!aligned(expert_idx, idx_bytes) || !aligned(row_of_slot, 16) || !aligned(split_sizes, 8) || !aligned(workspace, 16))
         return GSA_ERR_ALIGNMENT;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int E = static_cast<int>(experts);
