@@ -466,7 +466,8 @@ int32_t gsa_last_launch_count(void);
 
 const char *gsa_status_string(gsa_status status);
 
-/* ABI version: (major << 16) | minor. */
+/* ABI version: (major << 16) | minor.  Minor 2 added the gsa_moe_* and
+ * gsa_grouped_gemm* calls. */
 int32_t gsa_version(void);
 
 #ifdef __cplusplus
