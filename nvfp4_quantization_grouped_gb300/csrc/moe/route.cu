@@ -31,6 +31,7 @@ namespace {
 constexpr int kMaxBins = 257;        // 256 experts and the dropped slots
 constexpr int kSortWarps = 32;
 constexpr int kGradRows = 4, kGradBlocks = 4;   // unpermute_bwd: a token's slots at a time, blocks per SM
+constexpr int kFewWarps = 16 * 152;   // unpermute_bwd: 16 warps an SM (a constant: sizes alone decide the order of sums)
 
 // ------------------------------------------------------------------- sort
 
@@ -702,7 +703,7 @@ gsa_status gsa_moe_unpermute_bwd(const void *dout, const void *ys, const float *
     // at most 8 where the tokens are too few to fill the machine with 4
     int wpt = 1;
     while (wpt < 4 && wpt * 128 <= nv) wpt *= 2;
-    while (wpt < 8 && tokens * wpt < 152 * 16 && wpt * 64 <= nv) wpt *= 2;
+    while (wpt < 8 && tokens * wpt < kFewWarps && wpt * 64 <= nv) wpt *= 2;
     const dim3 block(32 * wpt, 8 / wpt), grid(static_cast<unsigned>((tokens + block.y - 1) / block.y));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int nt = static_cast<int>(tokens), nk = static_cast<int>(topk);
