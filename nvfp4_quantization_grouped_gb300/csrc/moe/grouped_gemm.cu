@@ -16,11 +16,12 @@
 // memory and issues the products, and 8 warps drain the accumulators.
 //   What bounds it: an NVFP4 stage of a pair is 512 cycles of products and about 200 of
 // scale copies in the same queue, an MXFP8 one 512 and 50; a tile's end costs about 1000
-// more.  65536 x 2048 x 2048 NVFP4 over 32 experts: 110 us (5.0 PFLOP/s); 262144 x 4096 x
-// 2048 MXFP8 over 128 experts: 1500 us (2.9 PFLOP/s) at the clock that the power limit
-// leaves, 1355 us for a launch by itself; 512 rows over 128 experts, 2048 x 4096 NVFP4:
-// 74 us, the weights at 6.2 TB/s.  Launched as a programmatic dependent, a block sets up
-// while the kernel before it ends: 32 rows over 128 experts 20.3 -> 18.0 us.
+// more.  65536 x 2048 x 2048 NVFP4 over 32 experts: 112 to 122 us on different machines (4.5
+// to 4.9 PFLOP/s); 262144 x 4096 x 2048 MXFP8 over 128 experts: 1500 to 1560 us (2.9 PFLOP/s)
+// at the clock that the power limit leaves, 1345 us for a launch by itself; 512 rows over 128
+// experts, 2048 x 4096 NVFP4: 70 to 74 us, the weights at 6.2 TB/s.  Launched as a
+// programmatic dependent, a block sets up while the kernel before it ends: 32 rows over 128
+// experts 20.3 -> 18.0 us on one machine (17 to 21 over all).
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_gemm(const __grid_constan
 // multiple of 8, so that kernel also copies the experts with an odd number of
 // 8-byte groups to rows 8 bytes longer.  (Bringing such rows in with loads instead
 // ran at 20 to 26 bytes a cycle and SM from L2, any width and number of warps,
-// against 65 to 76 by TMA: 577 us for 65536 x 2048 x 2048 over 32 experts, against 193:
+// against 65 to 76 by TMA: 577 us for 65536 x 2048 x 2048 over 32 experts, against 184 to 199:
 // 24 for that kernel, 160 for the products, whose FP32 results of 128 KB a block and tile
 // one SM stores in 5900 cycles.)  Last, scales past Mp_e are padding that nobody wrote, and a zero code
 // times a NaN scale is NaN: where a product step of 64 rows is cut short, the
@@ -1081,6 +1082,8 @@ gsa_status gsa_grouped_gemm(const gsa_qin *a, const gsa_qin *b, const int64_t *s
     // short and the weights are what there is to read.  Pairs / singles, us, 128 experts, 2048 x 4096: 64 rows an
     // expert 125 / 109 (NVFP4), 323 / 193 (MXFP8; both pairs' figures with B prefetched), 128 rows 125 / 132 and
     // 226 / 230, 256 rows 159 / 185 and 293 / 320; 16 experts, 4096 x 4096, 256 rows 49.5 / 52.1 and 85.0 / 85.6.
+    // All of these have tiles for every unit; the rule does not look at how many there are, and few tiles (few experts,
+    // small N) leave units without one in either shape.
     const bool pair = M >= 128 * E;
     const int BN = pair ? 256 : 128;
     const int sc = nv ? 4 : 1;
@@ -1144,6 +1147,7 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
     if (a_tiles >= (int64_t(1) << 31) || b_tiles >= (int64_t(1) << 31) || E * n128 * 4 >= (int64_t(1) << 31) ||
         E * k128 * 4 >= (int64_t(1) << 31))
         return GSA_ERR_UNSUPPORTED;
+    // Pairs wherever a side has more than one tile of 128 (not measured against single blocks where tiles are few).
     const bool pair = N > 128 && K > 128;
     const int64_t tile = pair ? 256 : 128, n_tiles = (N + tile - 1) / tile, k_tiles = (K + tile - 1) / tile;
     if (E * n_tiles * k_tiles >= (int64_t(1) << 31) - 4096) return GSA_ERR_UNSUPPORTED;

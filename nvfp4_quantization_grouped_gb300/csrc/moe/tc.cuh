@@ -184,7 +184,8 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // On a barrier of any block of the cluster.  Relaxed: it says that this warp has what it read from tensor memory (the
-// loads are complete, nothing is passed on).  A release at cluster scope would first wait for the warp's stores of the
+// loads are complete, nothing is passed on in memory); with the tcgen05 fences on both sides this is the order that the
+// ISA gives tcgen05 operations of different threads.  A release at cluster scope would first wait for the warp's stores of the
 // tile before, 1.9K cycles in which the tensor core stands still.
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
