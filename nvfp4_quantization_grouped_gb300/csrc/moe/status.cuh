@@ -21,4 +21,7 @@ inline gsa_status status_of(uint32_t report) {
     return report == ERR_SPLIT ? GSA_ERR_INVALID_ARG : GSA_OK;
 }
 
+// The current device's word, for the kernels of other translation units (nullptr: a CUDA error).
+uint32_t *word();
+
 }  // namespace gemm_status
