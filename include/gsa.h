@@ -433,6 +433,75 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
                                   int64_t M, int64_t N, int64_t K, int32_t recipe_kind, void *dw, int32_t out_dtype,
                                   int32_t accumulate, void *workspace, size_t workspace_bytes, gsa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The gated first projection in one product, and its gradient.
+ *
+ * For the rows r of expert e, with B_e [2 N, K] the expert's weights, N gate rows
+ * and then N linear rows:
+ *   g[r, n] = sum_k A[r, k] B_e[n, k],  u[r, n] = sum_k A[r, k] B_e[N + n, k]
+ *   y[r, n] = p_r act(g, u)
+ * with act GSA_ACT_SWIGLU or GSA_ACT_CLAMPED_SWIGLU (act_params as for the
+ * activation step, may be NULL for SwiGLU) and p = probs ([M] FP32, NULL: 1).  g and u
+ * stay in FP32 and are not written; y is rounded once.  (The activation step reads
+ * BF16 pre-activations: results differ by their rounding.)  A NaN g or u gives NaN.
+ *   a    rowwise copy of the [M, K] rows grouped by split_sizes_dev, as for
+ *        gsa_grouped_gemm, with the same rules for the split; rows of y past its sum
+ *        are zero.
+ *   b    rowwise copy of [E * 2 N, K].  b_groups = 1: quantized in E groups of 2 N
+ *        rows (what gsa_grouped_gemm takes; N % 128 = 0, so that the linear rows'
+ *        scales start on a tile).  b_groups = 2: in 2 E groups of N rows, any N.
+ *        Scales hold 2 E ceil(N / 128) row tiles either way, amax E * b_groups values.
+ *   y    [M, N] row-major, out_dtype GSA_BF16 or GSA_FP32.
+ * Errors: as gsa_grouped_gemm, and UNSUPPORTED (b_groups 1 with N % 128). */
+gsa_status gsa_grouped_glu(const gsa_qin *a, const gsa_qin *b, const int64_t *split_sizes_dev, int64_t E, int64_t M,
+                           int64_t N, int64_t K, int32_t recipe_kind, int32_t act_kind,
+                           const gsa_act_params *act_params, const float *probs, int32_t b_groups, void *y,
+                           int32_t out_dtype, gsa_stream_t stream);
+
+/* Workspace bytes of gsa_grouped_glu_bwd for dprobs (256-byte aligned; any content).
+ * 0 on invalid arguments and without rows. */
+size_t gsa_grouped_glu_bwd_workspace_size(int64_t M, int64_t N);
+
+/* Gradient of gsa_grouped_glu for dy [M, N] BF16, with g and u multiplied again:
+ *   dx [M, 2 N] = dy p d act / d(g, u)   (gate half, linear half; GSA_BF16 or GSA_FP32),
+ *   dprobs [M] FP32 = sum_n dy act(g, u).
+ * A clamped side has derivative 0 beyond its limit and 1 at it.  Rows past the split's
+ * sum are zero in both.  Either output may be NULL; the workspace is needed for
+ * dprobs alone.  The rows' and the weights' gradients are the grouped products of
+ * quantized dx.  One launch, or two with dprobs.  Errors: as gsa_grouped_glu, and
+ * WORKSPACE. */
+gsa_status gsa_grouped_glu_bwd(const void *dy_bf16, const gsa_qin *a, const gsa_qin *b, const int64_t *split_sizes_dev,
+                               int64_t E, int64_t M, int64_t N, int64_t K, int32_t recipe_kind, int32_t act_kind,
+                               const gsa_act_params *act_params, const float *probs, int32_t b_groups, void *dx_opt,
+                               int32_t out_dtype, float *dprobs_opt, void *workspace, size_t workspace_bytes,
+                               gsa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Products of a few unquantized rows (decoding).
+ *
+ *   out[r, n] = sum_k x[r, k] B_e[n, k],   rows r of expert e
+ * with x [M, K] of x_dtype (GSA_BF16, GSA_FP16, GSA_FP32) and b, split_sizes_dev as for
+ * gsa_grouped_gemm (rows past the split's sum are zero; a bad split writes nothing and
+ * is reported by gsa_grouped_gemm_status).  With E = 1 split_sizes_dev may be NULL: all
+ * rows.  Right for any number of rows, made for up to about 16 an expert: the weights
+ * are read once for 8.  out_dtype: any of the three, rounded once from FP32 sums.
+ * K is a multiple of 64.  A row's x is multiplied in FP16, scaled by a power of two so
+ * that its largest value fits (FP32 rows as the sum of two such): values are exact
+ * (BF16, FP16) or within 2^-22 (FP32) of themselves down to 2^-29 of the row's
+ * largest, and within 2^-40 of that largest below.
+ * Errors: INVALID_ARG, UNSUPPORTED (E > 256, K % 64, K > 65536, sizes past 2^31),
+ * ALIGNMENT, CUDA. */
+gsa_status gsa_grouped_gemv(const void *x, int32_t x_dtype, const gsa_qin *b, const int64_t *split_sizes_dev, int64_t E,
+                            int64_t M, int64_t N, int64_t K, int32_t recipe_kind, void *out, int32_t out_dtype,
+                            gsa_stream_t stream);
+
+/* gsa_grouped_glu for such rows: y[r, n] = p_r act(sum_k x[r, k] B_e[n, k],
+ * sum_k x[r, k] B_e[N + n, k]), b and b_groups as there, the rest as gsa_grouped_gemv. */
+gsa_status gsa_grouped_glu_gemv(const void *x, int32_t x_dtype, const gsa_qin *b, const int64_t *split_sizes_dev,
+                                int64_t E, int64_t M, int64_t N, int64_t K, int32_t recipe_kind, int32_t act_kind,
+                                const gsa_act_params *act_params, const float *probs, int32_t b_groups, void *y,
+                                int32_t out_dtype, gsa_stream_t stream);
+
 /* Takes one report out of the current device's word and synchronizes `stream`:
  * GSA_ERR_DEVICE_TIMEOUT (a bounded wait ran out), GSA_ERR_INVALID_ARG (a device
  * split) or GSA_OK when there is none left.  The word is one a device: it collects
@@ -467,7 +536,8 @@ int32_t gsa_last_launch_count(void);
 const char *gsa_status_string(gsa_status status);
 
 /* ABI version: (major << 16) | minor.  Minor 2 added the gsa_moe_* and
- * gsa_grouped_gemm* calls. */
+ * gsa_grouped_gemm* calls, minor 3 gsa_grouped_glu*, gsa_grouped_gemv and
+ * gsa_grouped_glu_gemv. */
 int32_t gsa_version(void);
 
 #ifdef __cplusplus

@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgsa.so")
 SOURCES = ["gsa_api.cu", "k_srelu.cu", "k_tanh_srelu.cu", "k_swiglu.cu", "k_clamped_swiglu.cu", "k_gelu.cu",
-           "k_sigmoid.cu", "k_identity.cu", "moe/route.cu", "moe/grouped_gemm.cu"]
+           "k_sigmoid.cu", "k_identity.cu", "moe/route.cu", "moe/grouped_gemm.cu", "moe/grouped_glu.cu", "moe/grouped_gemv.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC,-O2",
          "-I" + INCLUDE, "-I" + CSRC]

@@ -903,7 +903,7 @@ const char *gsa_status_string(gsa_status s) {
     return "unknown status";
 }
 
-int32_t gsa_version(void) { return (1 << 16) | 2; }
+int32_t gsa_version(void) { return (1 << 16) | 3; }
 
 gsa_status gsa_fwd_noalloc(const void *x_bf16, const float *probs, const int64_t *split_sizes, int64_t E,
                            int64_t W_in, int32_t act_kind, const gsa_act_params *act_params,

@@ -30,7 +30,8 @@ EXPORTED = ["gsa_layout", "gsa_workspace_size", "grouped_scaled_act_fwd", "group
             "gsa_layout_ex", "gsa_layout_bound_ex", "gsa_moe_sort_workspace_size", "gsa_moe_sort", "gsa_moe_permute",
             "gsa_moe_permute_bwd", "gsa_moe_unpermute", "gsa_moe_unpermute_bwd", "gsa_grouped_gemm",
             "gsa_grouped_gemm_wgrad", "gsa_grouped_gemm_wgrad_workspace_size",
-            "gsa_grouped_gemm_status"]
+            "gsa_grouped_gemm_status", "gsa_grouped_glu", "gsa_grouped_glu_bwd", "gsa_grouped_glu_bwd_workspace_size",
+            "gsa_grouped_gemv", "gsa_grouped_glu_gemv"]
 
 
 class GsaError(RuntimeError):
@@ -140,6 +141,17 @@ def load():
         L.gsa_grouped_gemm_wgrad_workspace_size.argtypes = [_I64, _I64, _I64, _I64, ctypes.c_int32]
         L.gsa_grouped_gemm_status.restype = ctypes.c_int
         L.gsa_grouped_gemm_status.argtypes = [_P]
+        i32, q = ctypes.c_int32, ctypes.POINTER(QIn)
+        shape = [_P, _I64, _I64, _I64, _I64, i32]                     # split, E, M, N, K, recipe
+        gated = [i32, ctypes.POINTER(ActParams), _P, i32]             # activation, its parameters, probs, b_groups
+        for name, args in (("gsa_grouped_glu", [q, q, *shape, *gated, _P, i32, _P]),
+                           ("gsa_grouped_glu_bwd", [_P, q, q, *shape, *gated, _P, i32, _P, _P, ctypes.c_size_t, _P]),
+                           ("gsa_grouped_gemv", [_P, i32, q, *shape, _P, i32, _P]),
+                           ("gsa_grouped_glu_gemv", [_P, i32, q, *shape, *gated, _P, i32, _P])):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = args
+        L.gsa_grouped_glu_bwd_workspace_size.restype = ctypes.c_size_t
+        L.gsa_grouped_glu_bwd_workspace_size.argtypes = [_I64, _I64]
         L.gsa_version.restype = ctypes.c_int32
         L.gsa_version.argtypes = []
         _lib = L
@@ -795,6 +807,118 @@ def grouped_gemm_wgrad(a: dict, b: dict, split, m: int, n: int, k: int, recipe_k
                                      _stream_of(stream, dev, split, *ta, *tb))
     if st:
         _check(st, "gsa_grouped_gemm_wgrad")
+    return out
+
+
+def _gated(what, act, params, probs, m, b_groups, dev):
+    """(activation code, its parameters or None, pointer of probs [m]) of a gated projection."""
+    kind = ACT.get(act) if isinstance(act, str) else int(act)
+    if kind not in GLU_ACTS:
+        raise GsaError(1, f"{what}: activation {act} (swiglu or clamped_swiglu expected)")
+    if b_groups != 1 and b_groups != 2:
+        raise GsaError(1, f"{what}: b_groups {b_groups} (1 or 2 expected)")
+    if probs is None:
+        return kind, params or act_params(kind), None
+    _require(probs, what + ": probs", (m,), _torch.float32)
+    _same_device(what, dev, probs)
+    return kind, params or act_params(kind), probs.data_ptr()
+
+
+def grouped_glu(a: dict, b: dict, split, m: int, n: int, k: int, recipe_kind: int, act="swiglu", probs=None,
+                params: ActParams | None = None, b_groups: int = 1, out_dtype=None, out=None, stream=None):
+    """The gated first projection in one product: y [m, n] = probs * act(A Bg_e^T, A Bl_e^T) over the rows of each expert,
+    act "swiglu" or "clamped_swiglu", probs [m] FP32 (None: 1).  a, split as for grouped_gemm.  b: the rowwise copy of the
+    experts' weights [E * 2 n, k], n gate rows and then n linear rows an expert, quantized in E groups of 2 n rows
+    (b_groups 1, n a multiple of 128) or 2 E groups of n rows (b_groups 2).  out_dtype: torch.bfloat16 (default) or
+    torch.float32.  The pre-activations stay in FP32 and are not written: grouped_glu_bwd multiplies again."""
+    torch = _torch or _setup()
+    out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
+    dev, experts, code = _product_args("grouped_glu", split, out_dtype)
+    kind, prm, pp = _gated("grouped_glu", act, params, probs, m, b_groups, dev)
+    qa, *ta = _operand(a, "row", recipe_kind, experts, "grouped_glu: a", dev)
+    qb, *tb = _operand(b, "row", recipe_kind, experts * b_groups, "grouped_glu: b", dev)
+    out = _out(out, "grouped_glu: out", (m, n), out_dtype, dev, stream)
+    st = _lib.gsa_grouped_glu(qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, kind, prm, pp, b_groups,
+                              out.data_ptr(), code, _stream_of(stream, dev, split, probs, *ta, *tb))
+    if st:
+        _check(st, "gsa_grouped_glu")
+    return out
+
+
+def grouped_glu_bwd(dy, a: dict, b: dict, split, m: int, n: int, k: int, recipe_kind: int, act="swiglu", probs=None,
+                    params: ActParams | None = None, b_groups: int = 1, want_dx: bool = True, want_dprobs: bool = True,
+                    out_dtype=None, out: tuple | None = None, stream=None):
+    """Gradient of grouped_glu for dy [m, n] BF16: (dx [m, 2 n], the pre-activations' gradient, dprobs [m] FP32), None in
+    the place of what is not wanted.  The other arguments are the forward's; the rows' and the weights' gradients are
+    grouped_gemm and grouped_gemm_wgrad of quantized dx."""
+    torch = _torch or _setup()
+    dx, dprobs = out if out is not None else (None, None)
+    out_dtype = out_dtype or (dx.dtype if dx is not None else torch.bfloat16)
+    dev, experts, code = _product_args("grouped_glu_bwd", split, out_dtype)
+    kind, prm, pp = _gated("grouped_glu_bwd", act, params, probs, m, b_groups, dev)
+    _require(dy, "grouped_glu_bwd: dy", (m, n), torch.bfloat16)
+    _same_device("grouped_glu_bwd", dev, dy)
+    qa, *ta = _operand(a, "row", recipe_kind, experts, "grouped_glu_bwd: a", dev)
+    qb, *tb = _operand(b, "row", recipe_kind, experts * b_groups, "grouped_glu_bwd: b", dev)
+    dx = _out(dx, "grouped_glu_bwd: dx", (m, 2 * n), out_dtype, dev, stream) if want_dx else None
+    ws, nbytes = None, 0
+    if want_dprobs:
+        dprobs = _out(dprobs, "grouped_glu_bwd: dprobs", (m,), torch.float32, dev, stream)
+        nbytes = _lib.gsa_grouped_glu_bwd_workspace_size(m, n)
+        ws = _out(None, "", (max(256, nbytes),), torch.uint8, dev, stream)
+    st = _lib.gsa_grouped_glu_bwd(dy.data_ptr(), qa, qb, split.data_ptr(), experts, m, n, k, recipe_kind, kind, prm, pp, b_groups,
+                                  dx.data_ptr() if want_dx else None, code, dprobs.data_ptr() if want_dprobs else None,
+                                  ws.data_ptr() if want_dprobs else None, nbytes,
+                                  _stream_of(stream, dev, dy, split, probs, *ta, *tb))
+    if st:
+        _check(st, "gsa_grouped_glu_bwd")
+    return dx, dprobs if want_dprobs else None
+
+
+def _few_rows(what, x, b, split, b_groups, recipe_kind, n, out_dtype, out, stream):
+    """(QIn of b, its tensors, split's pointer, experts, out) of a product of unquantized rows."""
+    torch = _torch or _setup()
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise GsaError(1, f"{what}: x must be bfloat16, float16 or float32 [rows, k], got {x.dtype} {list(x.shape)}")
+    _require(x, what + ": x", x.shape, x.dtype)
+    dev, sp, experts = x.device, None, 1
+    if split is not None:
+        if split.dim() != 1:
+            raise GsaError(1, f"{what}: split must be [experts]")
+        _require(split, what + ": split", split.shape, torch.int64)
+        _same_device(what, dev, split)
+        sp, experts = split.data_ptr(), split.shape[0]
+    qb, *tb = _operand(b, "row", recipe_kind, experts * b_groups, what + ": b", dev)
+    out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
+    if out_dtype not in _DTYPES:
+        raise GsaError(1, f"{what}: output type {out_dtype} (bfloat16, float16 or float32 expected)")
+    out = _out(out, what + ": out", (x.shape[0], n), out_dtype, dev, stream)
+    return qb, tb, sp, experts, out, _DTYPES[out_dtype]
+
+
+def grouped_gemv(x, b: dict, split, n: int, recipe_kind: int, out_dtype=None, out=None, stream=None):
+    """out [rows, n] = x B_e^T over the rows of each expert, for a few unquantized rows an expert (decoding): x [rows, k]
+    bfloat16, float16 or float32; b, split as for grouped_gemm (split None: one matrix takes all rows).  out_dtype: any
+    of the three (default: x's)."""
+    qb, tb, sp, experts, out, code = _few_rows("grouped_gemv", x, b, split, 1, recipe_kind, n, out_dtype, out, stream)
+    st = _lib.gsa_grouped_gemv(x.data_ptr(), _DTYPES[x.dtype], qb, sp, experts, x.shape[0], n, x.shape[1], recipe_kind,
+                               out.data_ptr(), code, _stream_of(stream, x.device, x, split, *tb))
+    if st:
+        _check(st, "gsa_grouped_gemv")
+    return out
+
+
+def grouped_glu_gemv(x, b: dict, split, n: int, recipe_kind: int, act="swiglu", probs=None, params: ActParams | None = None,
+                     b_groups: int = 1, out_dtype=None, out=None, stream=None):
+    """grouped_glu for a few unquantized rows an expert: y [rows, n] = probs * act(x Bg_e^T, x Bl_e^T), x as for
+    grouped_gemv, the rest as for grouped_glu."""
+    _torch or _setup()
+    kind, prm, pp = _gated("grouped_glu_gemv", act, params, probs, x.shape[0], b_groups, x.device)
+    qb, tb, sp, experts, out, code = _few_rows("grouped_glu_gemv", x, b, split, b_groups, recipe_kind, n, out_dtype, out, stream)
+    st = _lib.gsa_grouped_glu_gemv(x.data_ptr(), _DTYPES[x.dtype], qb, sp, experts, x.shape[0], n, x.shape[1], recipe_kind, kind, prm,
+                                   pp, b_groups, out.data_ptr(), code, _stream_of(stream, x.device, x, split, probs, *tb))
+    if st:
+        _check(st, "gsa_grouped_glu_gemv")
     return out
 
 
