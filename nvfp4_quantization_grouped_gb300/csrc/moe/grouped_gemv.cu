@@ -98,6 +98,11 @@ template <bool NV> __device__ __forceinline__ float weight(const GemvParams &P, 
     return (code & 8 ? -v : v) * e4m3(s);
 }
 
+__device__ __forceinline__ float gated(const glu::Act &A, float g, float u) {
+    const float2 a = make_float2(g, g), b = make_float2(u, u);
+    return A.clamped ? glu::value<true>(A, a, b).x : glu::value<false>(A, a, b).x;
+}
+
 constexpr int kRowsAtOnce = 8;
 
 template <bool NV, bool kGlu> __global__ void __launch_bounds__(kThreads) gemv(const __grid_constant__ GemvParams P) {
@@ -135,7 +140,7 @@ template <bool NV, bool kGlu> __global__ void __launch_bounds__(kThreads) gemv(c
                     if (NV) v[s] *= unit_of(P.amax[e * P.b_groups + (s ? P.b_groups - 1 : 0)]);
                 }
                 const float p = P.probs ? P.probs[r0 + r] : 1.0f;
-                if (lane == 0) put(P.out, P.out_type, (r0 + r) * P.N + n, kGlu ? p * glu::value(P.act, v[0], v[1]) : v[0]);
+                if (lane == 0) put(P.out, P.out_type, (r0 + r) * P.N + n, kGlu ? p * gated(P.act, v[0], v[1]) : v[0]);
             }
         }
     }

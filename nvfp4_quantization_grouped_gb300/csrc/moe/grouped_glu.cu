@@ -63,11 +63,16 @@ __device__ __forceinline__ void wait_dy() {
     __syncwarp();
 }
 
+template <bool NV> __device__ __forceinline__ float2 pair_of(const uint32_t *v, float ua, float ub) {
+    const float2 f = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    return NV ? glu::mul2(glu::mul2(f, ua), ub) : f;
+}
+
 // What a draining warp knows of its tile.
 struct Here {
     int64_t row, cols;   // the lane's row of the tensors; columns left from the warp's first on
     float p;
-    float ag, au, bg, bu;   // amax
+    float ug, vg, uu, vu;   // NVFP4: what a gate sum (ug, then vg) and a linear sum are multiplied by
     int nt, rows;           // column tile; the warp's rows
 };
 
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
         w.wide = P.N * sizeof(T) % 16 == 0;
         w.add = false;
         Here c;
-        int g = 0, n = 0;
+        int g = 0, n = 0, last = -1;
         auto find = [&](int64_t i) {
             if (i >= total) return;
             const Tile t = tile_at<kRows>(P, sh, i, g);
@@ -169,10 +174,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
             w.rows = c.rows;
             if (kBwd) d.o = P.dy + row * P.N + c0, d.cols = c.cols, d.rows = c.rows;
             c.p = P.probs && lane < c.rows && g < P.E ? P.probs[c.row] : 1.0f;
-            if (NV && g < P.E) {
-                c.ag = c.au = P.amax_a[g];
-                c.bg = P.amax_b[g * P.b_groups];
-                c.bu = P.amax_b[g * P.b_groups + P.b_groups - 1];
+            if (NV && g < P.E && g != last) {
+                const float a = P.amax_a[g];
+                units_of(a, P.amax_b[g * P.b_groups], c.ug, c.vg);
+                c.uu = c.ug, c.vu = c.vg;
+                if (P.b_groups == 2) units_of(a, P.amax_b[2 * g + 1], c.uu, c.vu);
+                last = g;
             }
         };
         auto partial = [&](const Here &at, float dp) {
@@ -198,36 +205,41 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
                 find(i + units);
                 continue;
             }
-            float ug = 1.0f, vg = 1.0f, uu = 1.0f, vu = 1.0f;
-            if (NV) units_of(c.ag, c.bg, ug, vg), units_of(c.au, c.bu, uu, vu);
             uint32_t v[kSide];   // 64 columns of g, and of u
             if (!take_tile<kBN, C::kAcc, kPair, kLen, 2>(sh, n, P.kt, q, lane, h * kCols64, kSide + h * kCols64, v)) break;
+            const Here at = c;
+            OutAt<T> here = w;
             if (kBwd) {
                 wait_dy();
-                float dp = 0.0f;
-                if (c.cols < kCols64) {   // past the last column: whatever the next rows and the scales' padding give, NaN too
-                    const int left = static_cast<int>(c.cols);
+                if (at.cols < kCols64) {   // past the last column: whatever the next rows and the scales' padding give, NaN too
+                    const int left = static_cast<int>(at.cols);
 #pragma unroll
                     for (int j = 0; j < kCols64; ++j)
                         if (j >= left) v[j] = v[kCols64 + j] = 0;
                 }
+                float2 dp = make_float2(0.0f, 0.0f);
+                auto all = [&](auto clamp) {
 #pragma unroll
-                for (int j = 0; j < kCols64; j += 8) {
-                    const uint4 x = tc::ld_shared(buf + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4));
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                    for (int j = 0; j < kCols64; j += 8) {
+                        const uint4 x = tc::ld_shared(buf + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4));
+                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float dy = __uint_as_float(k & 1 ? xs[k >> 1] & 0xFFFF0000u : xs[k >> 1] << 16);
-                        float dg, du;
-                        const float y = glu::gradient(P.act, scaled<NV>(v[j + k], ug, vg), scaled<NV>(v[kCols64 + j + k], uu, vu), dy * c.p, dg, du);
-                        dp = __fmaf_rn(dy, y, dp);
-                        v[j + k] = __float_as_uint(dg);
-                        v[kCols64 + j + k] = __float_as_uint(du);
+                        for (int k = 0; k < 8; k += 2) {
+                            const float2 dy = make_float2(__uint_as_float(xs[k >> 1] << 16), __uint_as_float(xs[k >> 1] & 0xFFFF0000u));
+                            uint32_t *vg = v + j + k, *vu = v + kCols64 + j + k;
+                            float2 dg, du;
+                            const float2 y = glu::gradient<decltype(clamp)::value>(P.act, pair_of<NV>(vg, at.ug, at.vg), pair_of<NV>(vu, at.uu, at.vu),
+                                                                                   glu::mul2(dy, at.p), dg, du);
+                            dp = glu::fma2(dy, y, dp);
+                            vg[0] = __float_as_uint(dg.x), vg[1] = __float_as_uint(dg.y);
+                            vu[0] = __float_as_uint(du.x), vu[1] = __float_as_uint(du.y);
+                        }
                     }
-                }
+                };
+                if (P.act.clamped) all(std::true_type());
+                else all(std::false_type());
                 __syncwarp();
-                partial(c, dp);
-                OutAt<T> here = w;
+                partial(at, dp.x + dp.y);
                 find(i + units);
                 if (P.out) {
                     store(v, here);
@@ -236,10 +248,16 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
                 }
                 if (i + units < used) load_dy(buf, d, P.dy, lane);
             } else {
+                auto all = [&](auto clamp) {
 #pragma unroll
-                for (int j = 0; j < kCols64; ++j)
-                    v[j] = __float_as_uint(c.p * glu::value(P.act, scaled<NV>(v[j], ug, vg), scaled<NV>(v[kCols64 + j], uu, vu)));
-                const OutAt<T> here = w;
+                    for (int j = 0; j < kCols64; j += 2) {
+                        const float2 y = glu::mul2(glu::value<decltype(clamp)::value>(P.act, pair_of<NV>(v + j, at.ug, at.vg),
+                                                                                      pair_of<NV>(v + kCols64 + j, at.uu, at.vu)), at.p);
+                        v[j] = __float_as_uint(y.x), v[j + 1] = __float_as_uint(y.y);
+                    }
+                };
+                if (P.act.clamped) all(std::true_type());
+                else all(std::false_type());
                 find(i + units);
                 store(v, here);
             }
