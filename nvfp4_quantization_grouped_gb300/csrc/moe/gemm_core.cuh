@@ -55,7 +55,8 @@ template <> struct Fmt<true> { static constexpr int kScaleTiles = 4; };
 // A block's tile is 128 rows (its lanes of tensor memory) x BN columns.  kPair: two
 // blocks of a cluster share a tile of 256 rows; each brings its own rows and half
 // of the columns' operand, and the pair's products read both halves.
-template <bool NV, int BN, bool kPair> struct Cfg {
+// kBufs: buffers of 32 rows x 128 bytes a draining warp has.
+template <bool NV, int BN, bool kPair, int kBufs = 1> struct Cfg {
     static constexpr int kSc = Fmt<NV>::kScaleTiles;
     static constexpr int kRowsB = kPair ? BN / 2 : BN;
     static constexpr int kBytesA = kRowsT * kStageK, kBytesB = kRowsB * kStageK;
@@ -66,7 +67,7 @@ template <bool NV, int BN, bool kPair> struct Cfg {
     static constexpr int kAcc = BN == 256 ? 1 : 2;       // accumulators in tensor memory
     static constexpr int kScCols = 4 * kSc * (1 + kGroupsB);   // scale columns of a stage
     static constexpr int kCols = 512;
-    static constexpr int kOut = kEpiWarps * kOutBuf;   // results on their way out
+    static constexpr int kOut = kEpiWarps * kBufs * kOutBuf;   // results on their way out
     static constexpr int kBySmem = (227 * 1024 - kStatic - 1024 - kOut) / kStride, kByCols = (kCols - kAcc * BN) / kScCols;
     static constexpr int kFit = kBySmem < kByCols ? kBySmem : kByCols;
     static constexpr int kStages = kFit < 8 ? kFit : 8;

@@ -68,17 +68,38 @@ template <bool NV> __device__ __forceinline__ float2 pair_of(const uint32_t *v, 
     return NV ? glu::mul2(glu::mul2(f, ua), ub) : f;
 }
 
-// What a draining warp knows of its tile.
-struct Here {
-    int64_t row, cols;   // the lane's row of the tensors; columns left from the warp's first on
-    float p;
-    float ug, vg, uu, vu;   // NVFP4: what a gate sum (ug, then vg) and a linear sum are multiplied by
-    int nt, rows;           // column tile; the warp's rows
+// The tiles of a unit, without divisions: q counts row tiles over all groups (n_tiles column tiles each, one after another).
+struct Walk {
+    int q, nt, g, dq, dn;
+    __device__ __forceinline__ Walk(const GluParams &P, int unit, int units)
+        : q(unit / P.n_tiles), nt(unit % P.n_tiles), g(0), dq(units / P.n_tiles), dn(units % P.n_tiles) {}
+    __device__ __forceinline__ void next(const GluParams &P) {
+        q += dq, nt += dn;
+        if (nt >= P.n_tiles) nt -= P.n_tiles, ++q;
+    }
+    // The group that q is in: this one or a later one.
+    template <int kRows> __device__ __forceinline__ Tile tile(const GluParams &P, const GemmShared &sh) {
+        if (sh.tile0[g + 1] <= q) {
+            ++g;
+            for (int end = P.E + 1; end - g > 1;) {   // the last group that starts at or before q: most may be empty
+                const int mid = (g + end) >> 1;
+                if (sh.tile0[mid] <= q) g = mid;
+                else end = mid;
+            }
+        }
+        Tile t;
+        t.g = g, t.nt = nt;
+        t.mt = q - sh.tile0[g];
+        t.row = sh.row0[g] + t.mt * kRows;
+        t.rows = min(kRows, sh.row0[g + 1] - t.row);
+        return t;
+    }
 };
 
 template <bool NV, bool kPair, bool kBwd, typename T>
 __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant__ GluParams P) {
-    using C = Cfg<NV, kBN, kPair>;
+    constexpr int kBufs = kBwd ? 2 : 1;   // the gradient: dy of this tile, whose place dx takes, and of the next
+    using C = Cfg<NV, kBN, kPair, kBufs>;
     // Sums of the gradient in short pieces: dp is an FP32 result, and adds up what the tensor core cuts off of both sides.
     constexpr int kLen = kBwd ? kPiece<float> : kPiece<T>;
     extern __shared__ uint8_t dyn[];
@@ -97,8 +118,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
         if (sh.bad) atomicOr(P.status, ERR_SPLIT);
         if (kBwd && P.part) *P.bad = sh.bad;
     }
-    const int64_t total = sh.bad ? 0 : static_cast<int64_t>(sh.tile0[P.E + 1]) * P.n_tiles;
-    const int64_t used = sh.bad ? 0 : static_cast<int64_t>(sh.tile0[P.E]) * P.n_tiles;   // the rest is zeros
+    const int total = sh.bad ? 0 : sh.tile0[P.E + 1], used = sh.bad ? 0 : sh.tile0[P.E];   // row tiles; the rest is zeros
+    Walk walk(P, unit, units);
 
     if (warp == 0) {
         if (tc::elect()) {
@@ -106,11 +127,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
             tc::prefetch_map(&P.tm_b);
         }
         Ring<C::kStages> ring;
-        int g = 0;
         bool ok = true, first = false;
-        auto at = [&](int64_t i) {
-            const Tile t = tile_at<kRows>(P, sh, i, g);
-            g = t.g;
+        auto at = [&] {
+            const Tile t = walk.tile<kRows>(P, sh);
+            const int g = uniform(t.g);
             StageAt w{&P.tm_a, &P.tm_b, &P.tm_sa, &P.tm_sb};
             w.x = 0;
             w.a_row = uniform(t.row) + half * kRowsT;
@@ -124,11 +144,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
             return w;
         };
         StageAt w, next;
-        if (unit < used) next = at(unit);
-        for (int64_t i = unit; i < used; i += units) {
+        if (walk.q < used) next = at();
+        while (uniform(walk.q) < used) {
             w = next;
-            const bool more = i + units < used;
-            if (more) next = at(i + units);
+            walk.next(P);
+            const bool more = uniform(walk.q) < used;
+            if (more) next = at();
             StageAt ahead = next;
             for (int k = 0; k < P.kt; ++k) {
                 load_stage(sh, st, half, ring, w, ok);
@@ -139,83 +160,80 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
         }
         end_loads<C::kStages>(sh, half, ring.issued, ok);
     } else if (warp == 1 && half == 0) {
-        const int mine = unit < used ? uniform(static_cast<int>((used - unit + units - 1) / units)) : 0;
         Ring<C::kStages> ring;
         int n = 0;
         bool ok = true;
-        for (int i = 0; i < mine; ++i) multiply_tile<kLen>(sh, st, n, ring, P.k_bytes, ok);
+        for (; uniform(walk.q) < used; walk.next(P)) multiply_tile<kLen>(sh, st, n, ring, P.k_bytes, ok);
         if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, ring.issued);
     } else if (warp >= kDrain) {
         const int q = warp & 3, h = (warp - kDrain) >> 2;   // lanes 32 q .., 64 columns of both sides from 64 h
-        const int64_t pitch = kBwd ? 2 * P.N : P.N;
-        T *out = static_cast<T *>(P.out);
-        const int r0 = half * kRowsT + 32 * q;
-        const uint32_t buf = st.out(warp - kDrain);
-        OutAt<const __nv_bfloat16> d;
-        d.pitch = P.N;
-        d.wide = P.N % 8 == 0;
-        OutAt<T> w;
-        w.pitch = pitch;
-        w.wide = P.N * sizeof(T) % 16 == 0;
-        w.add = false;
-        Here c;
-        int g = 0, n = 0, last = -1;
-        auto find = [&](int64_t i) {
-            if (i >= total) return;
-            const Tile t = tile_at<kRows>(P, sh, i, g);
-            g = t.g;
-            const int64_t c0 = static_cast<int64_t>(t.nt) * kSide + h * kCols64, row = t.row + r0;
-            c.nt = t.nt;
-            c.row = row + lane;
-            c.cols = P.N - c0;
-            c.rows = t.rows - r0;
-            w.o = out + row * pitch + c0;
-            w.cols = c.cols;
-            w.rows = c.rows;
-            if (kBwd) d.o = P.dy + row * P.N + c0, d.cols = c.cols, d.rows = c.rows;
-            c.p = P.probs && lane < c.rows && g < P.E ? P.probs[c.row] : 1.0f;
-            if (NV && g < P.E && g != last) {
-                const float a = P.amax_a[g];
-                units_of(a, P.amax_b[g * P.b_groups], c.ug, c.vg);
-                c.uu = c.ug, c.vu = c.vg;
-                if (P.b_groups == 2) units_of(a, P.amax_b[2 * g + 1], c.uu, c.vu);
-                last = g;
-            }
+        const int r0 = half * kRowsT + 32 * q, c0 = h * kCols64;
+        const uint32_t buf0 = st.a(C::kStages) + (warp - kDrain) * kBufs * kOutBuf;
+        uint32_t buf = buf0;
+        int n = 0, last = -1;
+        float ug = 1.0f, vg = 1.0f, uu = 1.0f, vu = 1.0f;   // NVFP4: what a gate sum (ug, then vg) and a linear sum are multiplied by
+        auto out_at = [&](int row, int nt, int rows, int cols) {
+            OutAt<T> w;
+            w.pitch = kBwd ? 2 * P.N : P.N;
+            w.o = static_cast<T *>(P.out) + row * w.pitch + nt * kSide + c0;
+            w.cols = cols, w.rows = rows;
+            w.wide = P.N * sizeof(T) % 16 == 0;
+            w.add = false;
+            return w;
         };
-        auto partial = [&](const Here &at, float dp) {
-            if (kBwd && P.part && lane < at.rows) P.part[(2 * static_cast<int64_t>(at.nt) + h) * P.M + at.row] = dp;
+        auto get_dy = [&](uint32_t to) {   // of the tile that the walk has come to
+            if (walk.q >= used) return;
+            const Tile t = walk.tile<kRows>(P, sh);
+            OutAt<const __nv_bfloat16> d;
+            d.o = P.dy + (t.row + r0) * P.N + t.nt * kSide + c0;
+            d.pitch = P.N;
+            d.cols = P.N - t.nt * kSide - c0, d.rows = t.rows - r0;
+            d.wide = P.N % 8 == 0;
+            load_dy(to, d, P.dy, lane);
         };
         auto store = [&](const uint32_t *v, const OutAt<T> &at) {
             if (at.wide) store_warp<kCols64, false, T>(v, 1.0f, 1.0f, buf, at, lane);
             else store_warp_any<kCols64, false, T>(v, 1.0f, 1.0f, buf, at, lane);
         };
-        find(unit);
-        if (kBwd && unit < used) load_dy(buf, d, P.dy, lane);
-        for (int64_t i = unit; i < total; i += units) {
-            if (g == P.E) {
+        if (kBwd) get_dy(buf);
+        while (walk.q < total) {
+            const Tile t = walk.tile<kRows>(P, sh);
+            const int row = t.row + r0, rows = t.rows - r0, nt = t.nt, cols = static_cast<int>(P.N) - nt * kSide - c0;   // the warp's part
+            auto partial = [&](float dp) {
+                if (kBwd && P.part && lane < rows) P.part[(2 * nt + h) * P.M + row + lane] = dp;
+            };
+            walk.next(P);
+            if (t.g == P.E) {
                 if (P.out) {
+                    OutAt<T> w = out_at(row, nt, rows, cols);
                     zero_tile<kCols64>(w, lane);
                     if (kBwd) {
-                        OutAt<T> up = w;
-                        up.o += P.N;
-                        zero_tile<kCols64>(up, lane);
+                        w.o += P.N;
+                        zero_tile<kCols64>(w, lane);
                     }
                 }
-                partial(c, 0.0f);
-                find(i + units);
+                partial(0.0f);
                 continue;
             }
-            uint32_t v[kSide];   // 64 columns of g, and of u
-            if (!take_tile<kBN, C::kAcc, kPair, kLen, 2>(sh, n, P.kt, q, lane, h * kCols64, kSide + h * kCols64, v)) break;
-            const Here at = c;
-            OutAt<T> here = w;
+            const float p = P.probs && lane < rows ? P.probs[row + lane] : 1.0f;
+            if (NV && t.g != last) {
+                const float a = P.amax_a[t.g];
+                units_of(a, P.amax_b[t.g * P.b_groups], ug, vg);
+                uu = ug, vu = vg;
+                if (P.b_groups == 2) units_of(a, P.amax_b[2 * t.g + 1], uu, vu);
+                last = t.g;
+            }
             if (kBwd) {
                 wait_dy();
-                if (at.cols < kCols64) {   // past the last column: whatever the next rows and the scales' padding give, NaN too
-                    const int left = static_cast<int>(at.cols);
+                get_dy(2 * buf0 + kOutBuf - buf);   // a tile ahead, into the other buffer
+            }
+            uint32_t v[kSide];   // 64 columns of g, and of u
+            if (!take_tile<kBN, C::kAcc, kPair, kLen, 2>(sh, n, P.kt, q, lane, c0, kSide + c0, v)) break;
+            if (kBwd) {
+                if (cols < kCols64) {   // past the last column: whatever the next rows and the scales' padding give, NaN too
 #pragma unroll
                     for (int j = 0; j < kCols64; ++j)
-                        if (j >= left) v[j] = v[kCols64 + j] = 0;
+                        if (j >= cols) v[j] = v[kCols64 + j] = 0;
                 }
                 float2 dp = make_float2(0.0f, 0.0f);
                 auto all = [&](auto clamp) {
@@ -226,40 +244,38 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
 #pragma unroll
                         for (int k = 0; k < 8; k += 2) {
                             const float2 dy = make_float2(__uint_as_float(xs[k >> 1] << 16), __uint_as_float(xs[k >> 1] & 0xFFFF0000u));
-                            uint32_t *vg = v + j + k, *vu = v + kCols64 + j + k;
+                            uint32_t *g = v + j + k, *u = v + kCols64 + j + k;
                             float2 dg, du;
-                            const float2 y = glu::gradient<decltype(clamp)::value>(P.act, pair_of<NV>(vg, at.ug, at.vg), pair_of<NV>(vu, at.uu, at.vu),
-                                                                                   glu::mul2(dy, at.p), dg, du);
+                            const float2 y = glu::gradient<decltype(clamp)::value>(P.act, pair_of<NV>(g, ug, vg), pair_of<NV>(u, uu, vu),
+                                                                                   glu::mul2(dy, p), dg, du);
                             dp = glu::fma2(dy, y, dp);
-                            vg[0] = __float_as_uint(dg.x), vg[1] = __float_as_uint(dg.y);
-                            vu[0] = __float_as_uint(du.x), vu[1] = __float_as_uint(du.y);
+                            g[0] = __float_as_uint(dg.x), g[1] = __float_as_uint(dg.y);
+                            u[0] = __float_as_uint(du.x), u[1] = __float_as_uint(du.y);
                         }
                     }
                 };
                 if (P.act.clamped) all(std::true_type());
                 else all(std::false_type());
                 __syncwarp();
-                partial(at, dp.x + dp.y);
-                find(i + units);
+                partial(dp.x + dp.y);
                 if (P.out) {
-                    store(v, here);
-                    here.o += P.N;
-                    store(v + kCols64, here);
+                    OutAt<T> w = out_at(row, nt, rows, cols);
+                    store(v, w);
+                    w.o += P.N;
+                    store(v + kCols64, w);
                 }
-                if (i + units < used) load_dy(buf, d, P.dy, lane);
+                buf = 2 * buf0 + kOutBuf - buf;
             } else {
                 auto all = [&](auto clamp) {
 #pragma unroll
                     for (int j = 0; j < kCols64; j += 2) {
-                        const float2 y = glu::mul2(glu::value<decltype(clamp)::value>(P.act, pair_of<NV>(v + j, at.ug, at.vg),
-                                                                                      pair_of<NV>(v + kCols64 + j, at.uu, at.vu)), at.p);
+                        const float2 y = glu::mul2(glu::value<decltype(clamp)::value>(P.act, pair_of<NV>(v + j, ug, vg), pair_of<NV>(v + kCols64 + j, uu, vu)), p);
                         v[j] = __float_as_uint(y.x), v[j + 1] = __float_as_uint(y.y);
                     }
                 };
                 if (P.act.clamped) all(std::true_type());
                 else all(std::false_type());
-                find(i + units);
-                store(v, here);
+                store(v, out_at(row, nt, rows, cols));
             }
         }
         if (kBwd) wait_dy();   // after a wait that ran out: the copies under way
@@ -278,7 +294,7 @@ __global__ void __launch_bounds__(256) sum_partials(const float *part, const uin
 
 template <bool NV, bool kPair, bool kBwd, typename T> gsa_status launch_glu(const GluParams &P, int64_t tiles, cudaStream_t s) {
     static PerDevice pairs;
-    return launch<kPair, GluParams>(grouped_glu<NV, kPair, kBwd, T>, P, kThreads, Cfg<NV, kBN, kPair>::kSmem, tiles * P.n_tiles, s, pairs);
+    return launch<kPair, GluParams>(grouped_glu<NV, kPair, kBwd, T>, P, kThreads, Cfg<NV, kBN, kPair, kBwd ? 2 : 1>::kSmem, tiles * P.n_tiles, s, pairs);
 }
 
 // Checks the arguments that both directions take, fills P and says whether pairs take the tiles.
