@@ -24,6 +24,7 @@ constexpr int kRowsT = 128;          // rows of a tile: the lanes of tensor memo
 constexpr int kStageK = 128;         // bytes of k per stage: one 128-byte swizzled row
 constexpr int kScaleTile = 512;      // bytes of one 128 x 4 scale tile
 constexpr int kThreads = 384;        // warp 0 loads, warp 1 multiplies, warps 4-11 drain
+constexpr int kMaxThreads = 640;     // of the kernels that share the split's scan
 constexpr int kEpiWarps = 8, kDrain = 4;   // the draining warps, the first of them
 constexpr int kBoxA = 32;            // rows of A that single blocks load at a time
 constexpr int kOutBuf = 32 * 128;    // a draining warp's piece of results: 32 rows x 128 bytes
@@ -55,8 +56,8 @@ template <> struct Fmt<true> { static constexpr int kScaleTiles = 4; };
 // A block's tile is 128 rows (its lanes of tensor memory) x BN columns.  kPair: two
 // blocks of a cluster share a tile of 256 rows; each brings its own rows and half
 // of the columns' operand, and the pair's products read both halves.
-// kBufs: buffers of 32 rows x 128 bytes a draining warp has.
-template <bool NV, int BN, bool kPair, int kBufs = 1> struct Cfg {
+// kOut: bytes of the draining warps' buffers.
+template <bool NV, int BN, bool kPair, int kOut = kEpiWarps * kOutBuf> struct Cfg {
     static constexpr int kSc = Fmt<NV>::kScaleTiles;
     static constexpr int kRowsB = kPair ? BN / 2 : BN;
     static constexpr int kBytesA = kRowsT * kStageK, kBytesB = kRowsB * kStageK;
@@ -67,7 +68,6 @@ template <bool NV, int BN, bool kPair, int kBufs = 1> struct Cfg {
     static constexpr int kAcc = BN == 256 ? 1 : 2;       // accumulators in tensor memory
     static constexpr int kScCols = 4 * kSc * (1 + kGroupsB);   // scale columns of a stage
     static constexpr int kCols = 512;
-    static constexpr int kOut = kEpiWarps * kBufs * kOutBuf;   // results on their way out
     static constexpr int kBySmem = (227 * 1024 - kStatic - 1024 - kOut) / kStride, kByCols = (kCols - kAcc * BN) / kScCols;
     static constexpr int kFit = kBySmem < kByCols ? kBySmem : kByCols;
     static constexpr int kStages = kFit < 8 ? kFit : 8;
@@ -83,7 +83,7 @@ struct GemmShared : Barriers {
     int row0[kMaxE + 2];        // first row of each group; group E: rows that no expert has
     int tile0[kMaxE + 2];       // first row tile of each group
     int scale0[kMaxE + 1];      // first 128-row scale tile of each expert
-    int64_t scan[kThreads / 32][3];
+    int64_t scan[kMaxThreads / 32][3];
     uint32_t bad;
 };
 
@@ -200,7 +200,7 @@ template <int kStages> __device__ __forceinline__ void settle(uint64_t *bars, in
 }
 
 // Barriers, tensor memory, and the block's (the pair's) start and end.
-template <int kStages, bool kPair>
+template <int kStages, bool kPair, int kWarps = kEpiWarps>
 __device__ __forceinline__ void open_block(Barriers &sh, int warp, uint32_t full_count, uint32_t cols) {
     if (threadIdx.x == 0) {
         sh.dead = 0;
@@ -210,7 +210,7 @@ __device__ __forceinline__ void open_block(Barriers &sh, int warp, uint32_t full
         }
         for (int a = 0; a < 2; ++a) {
             tc::bar_init(tc::smem_u32(&sh.acc_full[a]), 1);
-            tc::bar_init(tc::smem_u32(&sh.acc_empty[a]), kPair ? 2 * kEpiWarps : kEpiWarps);
+            tc::bar_init(tc::smem_u32(&sh.acc_empty[a]), kPair ? 2 * kWarps : kWarps);
         }
         tc::bar_init_fence();
     }
@@ -456,13 +456,13 @@ __device__ __forceinline__ void units_of(float amax_a, float amax_b, float &ua, 
     if ((ua > 0x1p64f && ub < 1.0f) || (ua < 0x1p-64f && ub > 4.0f)) ua *= ub, ub = 1.0f;
 }
 
-// The accumulators of a finished tile of `kt` stages, in pieces of kLen, into the registers of one draining warp: BN / 2
+// The accumulators of a finished tile of `kt` stages, in pieces of kLen, into the registers of one draining warp: kN
 // columns, one run of them at c0 or (kRuns 2) half of them at c0 and half at c1; n: pieces so far of this unit.  An
 // accumulator is handed back as soon as it is in registers: scaling, rounding and stores run while the next tile is
 // multiplied.  False: a wait ran out.
-template <int BN, int kAcc, bool kPair, int kLen, int kRuns>
-__device__ __forceinline__ bool take_tile(Barriers &sh, int &n, int kt, int q, int lane, uint32_t c0, uint32_t c1, uint32_t (&v)[BN / 2]) {
-    constexpr int kRun = BN / 2 / kRuns;
+template <int BN, int kAcc, bool kPair, int kLen, int kRuns, int kN>
+__device__ __forceinline__ bool take_tile(Barriers &sh, int &n, int kt, int q, int lane, uint32_t c0, uint32_t c1, uint32_t (&v)[kN]) {
+    constexpr int kRun = kN / kRuns;
     const uint32_t row = static_cast<uint32_t>(32 * q) << 16;
     auto wait = [&] {
         const bool ok = tc::bar_wait_warp(tc::smem_u32(&sh.acc_full[n % kAcc]), (n / kAcc) & 1, &sh.dead);
@@ -494,7 +494,7 @@ __device__ __forceinline__ bool take_tile(Barriers &sh, int &n, int kt, int q, i
         if (!wait()) return false;
         const uint32_t at = row + (n % kAcc) * BN;
 #pragma unroll
-        for (int j = 0; j < BN / 2; j += 8) {   // (16 at a time spills)
+        for (int j = 0; j < kN; j += 8) {   // (16 at a time spills)
             uint32_t x[8];
             tc::tmem_ld(at + (j < kRun ? c0 + j : c1 + j - kRun), x);
 #pragma unroll

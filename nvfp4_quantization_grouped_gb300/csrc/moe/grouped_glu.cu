@@ -16,13 +16,20 @@
 
 namespace {
 
-constexpr int kBN = 256, kSide = kBN / 2, kCols64 = 64;   // columns of a tile, of one side, of a warp
+constexpr int kBN = 256, kSide = kBN / 2, kCols = 32;   // columns of a tile; of one side; of one side that a warp drains
+// Sixteen warps drain (8 in the grouped product): two of them a scheduler cannot hide the latencies of the activation, with
+// the registers that 64 accumulators a side leave them (gradient, 65536 x 2048 x 2048 NVFP4: @@ -> @@ us).
+constexpr int kWarps = 16, kGluThreads = 32 * (kDrain + kWarps);
+constexpr int kBuf = 32 * 64;   // a warp's piece of dy or results: 32 rows x 64 bytes
+static_assert(kGluThreads <= kMaxThreads, "threads");
+
+constexpr int kParts = kSide / kCols;   // of a row's sum of dp, a tile
 
 struct GluParams : GemmParams {   // N: columns of one side; out: y, or dx
     glu::Act act;
     const float *probs;
     const __nv_bfloat16 *dy;
-    float *part;          // [2 n_tiles][M] partial sums of dp
+    float *part;          // [kParts n_tiles][M] partial sums of dp
     uint32_t *status;     // the device's word for reports
     uint32_t *bad;        // this call's: a bad split (with part)
     int up_tiles;         // scale tiles from a gate row's to its linear row's, in rows of tiles
@@ -33,40 +40,95 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// A warp's 32 x 64 piece of dy into its buffer: row r's 16-byte chunk c at c ^ (r mod 8), zeros where there is none.
+// Row r's 16-byte chunk c of a warp's buffer: eight lanes that hold one chunk of eight rows, or both of two rows' four, meet
+// no bank twice.
+__device__ __forceinline__ uint32_t chunk(uint32_t buf, int r, int c) { return buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
+
+// A warp's 32 x 32 piece of dy into its buffer, zeros where there is none.
 __device__ __forceinline__ void load_dy(uint32_t buf, const OutAt<const __nv_bfloat16> &w, const __nv_bfloat16 *any, int lane) {
     if (w.wide) {
-        const int c = lane & 7;
+        const int c = lane & 3;
 #pragma unroll
-        for (int r0 = 0; r0 < 32; r0 += 4) {
-            const int r = r0 + (lane >> 3);
+        for (int r0 = 0; r0 < 32; r0 += 8) {
+            const int r = r0 + (lane >> 2);
             const bool in = r < w.rows && 8 * c < w.cols;
-            copy_async(buf + r * 128 + ((c ^ (r & 7)) << 4), in ? w.o + r * w.pitch + 8 * c : any, in ? 16 : 0);
+            copy_async(chunk(buf, r, c), in ? w.o + r * w.pitch + 8 * c : any, in ? 16 : 0);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    } else {   // a column a lane, twice
-#pragma unroll
-        for (int j = 0; j < kCols64; j += 32) {
-            const int col = j + lane;
+    } else {   // a column a lane
 #pragma unroll 8
-            for (int r = 0; r < 32; ++r) {
-                uint16_t x = 0;
-                if (r < w.rows && col < w.cols) x = __ldcs(reinterpret_cast<const uint16_t *>(w.o + r * w.pitch + col));
-                asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + r * 128 + (((col >> 3) ^ (r & 7)) << 4) + 2 * (col & 7)), "h"(x) : "memory");
-            }
+        for (int r = 0; r < 32; ++r) {
+            uint16_t x = 0;
+            if (r < w.rows && lane < w.cols) x = __ldcs(reinterpret_cast<const uint16_t *>(w.o + r * w.pitch + lane));
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(chunk(buf, r, lane >> 3) + 2 * (lane & 7)), "h"(x) : "memory");
         }
     }
 }
 
-__device__ __forceinline__ void wait_dy() {
+// A warp's 32 x 32 results, a row a lane, to memory by way of its buffer: pieces of 64 bytes a row, four lanes a row.
+template <typename T> __device__ __forceinline__ void store_rows(const uint32_t *v, uint32_t buf, const OutAt<T> &w, int lane) {
+    if (w.wide) {
+        constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4 * kPer) {
+            if (j >= w.cols) break;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t x[4];
+                finish<false>(v + j + c * kPer, 1.0f, 1.0f, x, T());
+                tc::st_shared(chunk(buf, lane, c), x);
+            }
+            __syncwarp();
+            const int c = lane & 3, col = j + c * kPer;
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+                const int r = r0 + (lane >> 2);
+                const uint4 x = tc::ld_shared(chunk(buf, r, c));
+                if (r < w.rows && col < w.cols) *reinterpret_cast<uint4 *>(w.o + r * w.pitch + col) = x;
+            }
+            __syncwarp();
+        }
+    } else {   // rows that do not start on 16 bytes: 16 columns at a time in FP32, a column a lane, two rows at once
+#pragma unroll
+        for (int j = 0; j < kCols; j += 16) {
+            if (j >= w.cols) break;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t x[4];
+                finish<false>(v + j + 4 * c, 1.0f, 1.0f, x, float());
+                tc::st_shared(chunk(buf, lane, c), x);
+            }
+            __syncwarp();
+            const int c = lane & 15;
+            if (j + c < w.cols) {
+#pragma unroll 8
+                for (int r = lane >> 4; r < 32; r += 2)
+                    if (r < w.rows) w.o[r * w.pitch + j + c] = static_cast<T>(tc::ld_shared1(chunk(buf, r, c >> 2) + 4 * (c & 3)));
+            }
+            __syncwarp();
+        }
+    }
+}
+
+__device__ __forceinline__ void wait_copies() {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
 }
 
-template <bool NV> __device__ __forceinline__ float2 pair_of(const uint32_t *v, float ua, float ub) {
+// A pair of sums times what their units leave (NVFP4).
+template <bool NV> __device__ __forceinline__ float2 pair_of(const uint32_t *v, float u) {
     const float2 f = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
-    return NV ? glu::mul2(glu::mul2(f, ua), ub) : f;
+    return NV ? glu::mul2(f, u) : f;
 }
+
+// 1 / (S_A S_B).  Past FP32's end (every sum but 0 is then past it too) it stays finite: 0 times it is 0.
+__device__ __forceinline__ float unit_of(float amax_a, float amax_b) {
+    const float u = __fdiv_rn(1.0f, tensor_scale(amax_a)) * __fdiv_rn(1.0f, tensor_scale(amax_b));
+    return u > 3.402823466e38f ? 3.402823466e38f : u;
+}
+
+// The same value of all lanes as one that the compiler knows to be the same: it then lives in a uniform register, of which
+// the draining warps have plenty, while their accumulators leave them few others.
+__device__ __forceinline__ int known_uniform(int v) { return __reduce_min_sync(0xFFFFFFFFu, v); }
 
 // The tiles of a unit, without divisions: q counts row tiles over all groups (n_tiles column tiles each, one after another).
 struct Walk {
@@ -77,40 +139,45 @@ struct Walk {
         q += dq, nt += dn;
         if (nt >= P.n_tiles) nt -= P.n_tiles, ++q;
     }
-    // The group that q is in: this one or a later one.
+    // Its tile, by a whole warp; the group that q is in is this one or a later one.
     template <int kRows> __device__ __forceinline__ Tile tile(const GluParams &P, const GemmShared &sh) {
-        if (sh.tile0[g + 1] <= q) {
+        if (known_uniform(sh.tile0[g + 1]) <= q) {
             ++g;
             for (int end = P.E + 1; end - g > 1;) {   // the last group that starts at or before q: most may be empty
                 const int mid = (g + end) >> 1;
-                if (sh.tile0[mid] <= q) g = mid;
+                if (known_uniform(sh.tile0[mid]) <= q) g = mid;
                 else end = mid;
             }
         }
         Tile t;
         t.g = g, t.nt = nt;
-        t.mt = q - sh.tile0[g];
-        t.row = sh.row0[g] + t.mt * kRows;
-        t.rows = min(kRows, sh.row0[g + 1] - t.row);
+        t.mt = q - known_uniform(sh.tile0[g]);
+        t.row = known_uniform(sh.row0[g]) + t.mt * kRows;
+        t.rows = min(kRows, known_uniform(sh.row0[g + 1]) - t.row);
         return t;
     }
 };
 
-template <bool NV, bool kPair, bool kBwd, typename T>
-__global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant__ GluParams P) {
-    constexpr int kBufs = kBwd ? 2 : 1;   // the gradient: dy of this tile, whose place dx takes, and of the next
-    using C = Cfg<NV, kBN, kPair, kBufs>;
+// What a draining warp has in shared memory: a buffer for results, or (gradient) two for dy of this tile, whose place dx
+// takes, and of the next; probs of the rows of both.
+constexpr int kProbs = 32 * 4;
+template <bool kBwd> constexpr int kOwn = (kBwd ? 2 : 1) * kBuf + 2 * kProbs;
+template <bool NV, bool kPair, bool kBwd> using GluCfg = Cfg<NV, kBN, kPair, kWarps * kOwn<kBwd>>;
+
+template <bool NV, bool kPair, bool kBwd, bool kClamp, typename T>
+__global__ void __launch_bounds__(kGluThreads, 1) grouped_glu(const __grid_constant__ GluParams P) {
+    using C = GluCfg<NV, kPair, kBwd>;
     // Sums of the gradient in short pieces: dp is an FP32 result, and adds up what the tensor core cuts off of both sides.
     constexpr int kLen = kBwd ? kPiece<float> : kPiece<T>;
     extern __shared__ uint8_t dyn[];
     __shared__ GemmShared sh;
     static_assert(sizeof(GemmShared) <= kStatic, "shared memory");
     constexpr int kRows = kPair ? 2 * kRowsT : kRowsT;
-    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int warp = known_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x, units = kPair ? gridDim.x >> 1 : gridDim.x;
     const int half = kPair ? blockIdx.x & 1 : 0;
     const Stages<NV, kBN, kPair> st(dyn);
-    open_block<C::kStages, kPair>(sh, warp, 1, C::kCols);
+    open_block<C::kStages, kPair, kWarps>(sh, warp, 1, C::kCols);
     tc::allow_next();
     tc::wait_for_previous();
     scan_split<kRows>(P, sh);
@@ -118,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
         if (sh.bad) atomicOr(P.status, ERR_SPLIT);
         if (kBwd && P.part) *P.bad = sh.bad;
     }
-    const int total = sh.bad ? 0 : sh.tile0[P.E + 1], used = sh.bad ? 0 : sh.tile0[P.E];   // row tiles; the rest is zeros
+    const int total = known_uniform(sh.bad ? 0 : sh.tile0[P.E + 1]), used = known_uniform(sh.bad ? 0 : sh.tile0[P.E]);   // row tiles; the rest is zeros
     Walk walk(P, unit, units);
 
     if (warp == 0) {
@@ -127,33 +194,31 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
             tc::prefetch_map(&P.tm_b);
         }
         Ring<C::kStages> ring;
-        bool ok = true, first = false;
-        auto at = [&] {
-            const Tile t = walk.tile<kRows>(P, sh);
-            const int g = uniform(t.g);
-            StageAt w{&P.tm_a, &P.tm_b, &P.tm_sa, &P.tm_sb};
-            w.x = 0;
-            w.a_row = uniform(t.row) + half * kRowsT;
-            w.a_boxes = uniform((t.rows + kBoxA - 1) / kBoxA);
-            w.a_tile = uniform((sh.scale0[g] + t.mt * (kRows / 128) + half) * P.scale_cols);
-            w.b_row = uniform(static_cast<int>((2 * g + half) * P.N) + t.nt * kSide);   // the pair's second block has the linear side
+        bool ok = true;
+        while (walk.q < used) {
+            Tile t = walk.tile<kRows>(P, sh);
+            StageAt w{&P.tm_a, &P.tm_b, &P.tm_sa, &P.tm_sb}, ahead = w;
+            auto rows_at = [&](StageAt &s) {   // what the column tiles of a row tile share
+                s.x = 0;
+                s.a_row = t.row + half * kRowsT;
+                s.a_tile = (known_uniform(sh.scale0[t.g]) + t.mt * (kRows / 128) + half) * P.scale_cols;
+            };
+            rows_at(w);
+            w.a_boxes = (t.rows + kBoxA - 1) / kBoxA;
+            w.b_row = static_cast<int>((2 * t.g + half) * P.N) + t.nt * kSide;   // the pair's second block has the linear side
             w.b_row_step = static_cast<int>(P.N);
-            w.b_tile = uniform((g * P.b_scale_rows + t.nt) * P.scale_cols);
+            w.b_tile = (t.g * P.b_scale_rows + t.nt) * P.scale_cols;
             w.b_tile_step = P.up_tiles * P.scale_cols;
-            first = uniform(t.nt) == 0;
-            return w;
-        };
-        StageAt w, next;
-        if (walk.q < used) next = at();
-        while (uniform(walk.q) < used) {
-            w = next;
             walk.next(P);
-            const bool more = uniform(walk.q) < used;
-            if (more) next = at();
-            StageAt ahead = next;
+            bool first = false;   // the next tile is its rows' first
+            if (kPair && walk.q < used && walk.nt == 0) {
+                first = true;
+                t = walk.tile<kRows>(P, sh);
+                rows_at(ahead);
+            }
             for (int k = 0; k < P.kt; ++k) {
                 load_stage(sh, st, half, ring, w, ok);
-                if (kPair && more && first) prefetch_rows(ahead);
+                if (first) prefetch_rows(ahead);
                 w.x += kStageK, w.a_tile += C::kSc, w.b_tile += C::kSc;
                 ahead.x += kStageK, ahead.a_tile += C::kSc;
             }
@@ -163,15 +228,16 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
         Ring<C::kStages> ring;
         int n = 0;
         bool ok = true;
-        for (; uniform(walk.q) < used; walk.next(P)) multiply_tile<kLen>(sh, st, n, ring, P.k_bytes, ok);
+        for (; walk.q < used; walk.next(P)) multiply_tile<kLen>(sh, st, n, ring, P.k_bytes, ok);
         if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, ring.issued);
     } else if (warp >= kDrain) {
-        const int q = warp & 3, h = (warp - kDrain) >> 2;   // lanes 32 q .., 64 columns of both sides from 64 h
-        const int r0 = half * kRowsT + 32 * q, c0 = h * kCols64;
-        const uint32_t buf0 = st.a(C::kStages) + (warp - kDrain) * kBufs * kOutBuf;
-        uint32_t buf = buf0;
+        const int q = warp & 3, h = (warp - kDrain) >> 2;   // lanes 32 q .., 32 columns of both sides from 32 h
+        const int r0 = half * kRowsT + 32 * q, c0 = h * kCols;
+        const uint32_t own = st.a(C::kStages) + (warp - kDrain) * kOwn<kBwd>;
+        uint32_t turn = 0;   // 0 or 1: which dy buffer and probs are this tile's
+        auto buf = [&](uint32_t i) { return own + 2 * kProbs + (kBwd ? i * kBuf : 0); };
         int n = 0, last = -1;
-        float ug = 1.0f, vg = 1.0f, uu = 1.0f, vu = 1.0f;   // NVFP4: what a gate sum (ug, then vg) and a linear sum are multiplied by
+        float ug = 1.0f, uu = 1.0f;   // NVFP4: the units of a gate sum and of a linear sum
         auto out_at = [&](int row, int nt, int rows, int cols) {
             OutAt<T> w;
             w.pitch = kBwd ? 2 * P.N : P.N;
@@ -181,104 +247,94 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_glu(const __grid_constant
             w.add = false;
             return w;
         };
-        auto get_dy = [&](uint32_t to) {   // of the tile that the walk has come to
+        auto ask = [&](uint32_t i) {   // what the tile that the walk has come to needs from memory
             if (walk.q >= used) return;
             const Tile t = walk.tile<kRows>(P, sh);
-            OutAt<const __nv_bfloat16> d;
-            d.o = P.dy + (t.row + r0) * P.N + t.nt * kSide + c0;
-            d.pitch = P.N;
-            d.cols = P.N - t.nt * kSide - c0, d.rows = t.rows - r0;
-            d.wide = P.N % 8 == 0;
-            load_dy(to, d, P.dy, lane);
+            const int row = t.row + r0, rows = t.rows - r0;
+            if (P.probs && lane < rows)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(own + i * kProbs + 4 * lane), "l"(P.probs + row + lane) : "memory");
+            if (kBwd) {
+                OutAt<const __nv_bfloat16> d;
+                d.o = P.dy + row * P.N + t.nt * kSide + c0;
+                d.pitch = P.N;
+                d.cols = P.N - t.nt * kSide - c0, d.rows = rows;
+                d.wide = P.N % 8 == 0;
+                load_dy(buf(i), d, P.dy, lane);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        auto store = [&](const uint32_t *v, const OutAt<T> &at) {
-            if (at.wide) store_warp<kCols64, false, T>(v, 1.0f, 1.0f, buf, at, lane);
-            else store_warp_any<kCols64, false, T>(v, 1.0f, 1.0f, buf, at, lane);
-        };
-        if (kBwd) get_dy(buf);
+        ask(0);
         while (walk.q < total) {
             const Tile t = walk.tile<kRows>(P, sh);
             const int row = t.row + r0, rows = t.rows - r0, nt = t.nt, cols = static_cast<int>(P.N) - nt * kSide - c0;   // the warp's part
             auto partial = [&](float dp) {
-                if (kBwd && P.part && lane < rows) P.part[(2 * nt + h) * P.M + row + lane] = dp;
+                if (kBwd && P.part && lane < rows) P.part[(kParts * nt + h) * P.M + row + lane] = dp;
             };
             walk.next(P);
             if (t.g == P.E) {
                 if (P.out) {
                     OutAt<T> w = out_at(row, nt, rows, cols);
-                    zero_tile<kCols64>(w, lane);
+                    zero_tile<kCols>(w, lane);
                     if (kBwd) {
                         w.o += P.N;
-                        zero_tile<kCols64>(w, lane);
+                        zero_tile<kCols>(w, lane);
                     }
                 }
                 partial(0.0f);
                 continue;
             }
-            const float p = P.probs && lane < rows ? P.probs[row + lane] : 1.0f;
             if (NV && t.g != last) {
                 const float a = P.amax_a[t.g];
-                units_of(a, P.amax_b[t.g * P.b_groups], ug, vg);
-                uu = ug, vu = vg;
-                if (P.b_groups == 2) units_of(a, P.amax_b[2 * t.g + 1], uu, vu);
+                ug = uu = unit_of(a, P.amax_b[t.g * P.b_groups]);
+                if (P.b_groups == 2) uu = unit_of(a, P.amax_b[2 * t.g + 1]);
                 last = t.g;
             }
-            if (kBwd) {
-                wait_dy();
-                get_dy(2 * buf0 + kOutBuf - buf);   // a tile ahead, into the other buffer
-            }
-            uint32_t v[kSide];   // 64 columns of g, and of u
+            wait_copies();
+            ask(turn ^ 1);
+            uint32_t v[2 * kCols];   // columns of g, and of u
             if (!take_tile<kBN, C::kAcc, kPair, kLen, 2>(sh, n, P.kt, q, lane, c0, kSide + c0, v)) break;
+            const float p = P.probs ? tc::ld_shared1(own + turn * kProbs + 4 * lane) : 1.0f;
             if (kBwd) {
-                if (cols < kCols64) {   // past the last column: whatever the next rows and the scales' padding give, NaN too
+                if (cols < kCols) {   // past the last column: whatever the next rows and the scales' padding give, NaN too
 #pragma unroll
-                    for (int j = 0; j < kCols64; ++j)
-                        if (j >= cols) v[j] = v[kCols64 + j] = 0;
+                    for (int j = 0; j < kCols; ++j)
+                        if (j >= cols) v[j] = v[kCols + j] = 0;
                 }
                 float2 dp = make_float2(0.0f, 0.0f);
-                auto all = [&](auto clamp) {
 #pragma unroll
-                    for (int j = 0; j < kCols64; j += 8) {
-                        const uint4 x = tc::ld_shared(buf + lane * 128 + (((j >> 3) ^ (lane & 7)) << 4));
-                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                for (int j = 0; j < kCols; j += 8) {
+                    const uint4 x = tc::ld_shared(chunk(buf(turn), lane, j >> 3));
+                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                        for (int k = 0; k < 8; k += 2) {
-                            const float2 dy = make_float2(__uint_as_float(xs[k >> 1] << 16), __uint_as_float(xs[k >> 1] & 0xFFFF0000u));
-                            uint32_t *g = v + j + k, *u = v + kCols64 + j + k;
-                            float2 dg, du;
-                            const float2 y = glu::gradient<decltype(clamp)::value>(P.act, pair_of<NV>(g, ug, vg), pair_of<NV>(u, uu, vu),
-                                                                                   glu::mul2(dy, p), dg, du);
-                            dp = glu::fma2(dy, y, dp);
-                            g[0] = __float_as_uint(dg.x), g[1] = __float_as_uint(dg.y);
-                            u[0] = __float_as_uint(du.x), u[1] = __float_as_uint(du.y);
-                        }
+                    for (int k = 0; k < 8; k += 2) {
+                        const float2 dy = make_float2(__uint_as_float(xs[k >> 1] << 16), __uint_as_float(xs[k >> 1] & 0xFFFF0000u));
+                        uint32_t *g = v + j + k, *u = v + kCols + j + k;
+                        float2 dg, du;
+                        const float2 y = glu::gradient<kClamp>(P.act, pair_of<NV>(g, ug), pair_of<NV>(u, uu), glu::mul2(dy, p), dg, du);
+                        dp = glu::fma2(dy, y, dp);
+                        g[0] = __float_as_uint(dg.x), g[1] = __float_as_uint(dg.y);
+                        u[0] = __float_as_uint(du.x), u[1] = __float_as_uint(du.y);
                     }
-                };
-                if (P.act.clamped) all(std::true_type());
-                else all(std::false_type());
+                }
                 __syncwarp();
                 partial(dp.x + dp.y);
                 if (P.out) {
                     OutAt<T> w = out_at(row, nt, rows, cols);
-                    store(v, w);
+                    store_rows(v, buf(turn), w, lane);
                     w.o += P.N;
-                    store(v + kCols64, w);
+                    store_rows(v + kCols, buf(turn), w, lane);
                 }
-                buf = 2 * buf0 + kOutBuf - buf;
             } else {
-                auto all = [&](auto clamp) {
 #pragma unroll
-                    for (int j = 0; j < kCols64; j += 2) {
-                        const float2 y = glu::mul2(glu::value<decltype(clamp)::value>(P.act, pair_of<NV>(v + j, ug, vg), pair_of<NV>(v + kCols64 + j, uu, vu)), p);
-                        v[j] = __float_as_uint(y.x), v[j + 1] = __float_as_uint(y.y);
-                    }
-                };
-                if (P.act.clamped) all(std::true_type());
-                else all(std::false_type());
-                store(v, out_at(row, nt, rows, cols));
+                for (int j = 0; j < kCols; j += 2) {
+                    const float2 y = glu::mul2(glu::value<kClamp>(P.act, pair_of<NV>(v + j, ug), pair_of<NV>(v + kCols + j, uu)), p);
+                    v[j] = __float_as_uint(y.x), v[j + 1] = __float_as_uint(y.y);
+                }
+                store_rows(v, buf(0), out_at(row, nt, rows, cols), lane);
             }
+            turn ^= 1;
         }
-        if (kBwd) wait_dy();   // after a wait that ran out: the copies under way
+        wait_copies();   // after a wait that ran out: those under way
     }
     close_block<kPair>(sh, warp, C::kCols, P.status);
 }
@@ -292,9 +348,19 @@ __global__ void __launch_bounds__(256) sum_partials(const float *part, const uin
     dprobs[r] = s;
 }
 
-template <bool NV, bool kPair, bool kBwd, typename T> gsa_status launch_glu(const GluParams &P, int64_t tiles, cudaStream_t s) {
-    static PerDevice pairs;
-    return launch<kPair, GluParams>(grouped_glu<NV, kPair, kBwd, T>, P, kThreads, Cfg<NV, kBN, kPair, kBwd ? 2 : 1>::kSmem, tiles * P.n_tiles, s, pairs);
+template <bool kBwd> gsa_status launch_glu(const GluParams &P, bool nv, bool pair, int32_t out_dtype, int64_t tiles, cudaStream_t s) {
+    auto go = [&](auto fmt, auto pairs, auto clamp, auto type) {
+        constexpr bool NV = decltype(fmt)::value, kPair = decltype(pairs)::value;
+        static PerDevice clusters;
+        return launch<kPair, GluParams>(grouped_glu<NV, kPair, kBwd, decltype(clamp)::value, decltype(type)>, P, kGluThreads,
+                                        GluCfg<NV, kPair, kBwd>::kSmem, tiles * P.n_tiles, s, clusters);
+    };
+    auto typed = [&](auto fmt, auto pairs, auto clamp) {
+        return out_dtype == GSA_BF16 ? go(fmt, pairs, clamp, __nv_bfloat16()) : go(fmt, pairs, clamp, float());
+    };
+    auto clamped = [&](auto fmt, auto pairs) { return P.act.clamped ? typed(fmt, pairs, std::true_type()) : typed(fmt, pairs, std::false_type()); };
+    auto paired = [&](auto fmt) { return pair ? clamped(fmt, std::true_type()) : clamped(fmt, std::false_type()); };
+    return nv ? paired(std::true_type()) : paired(std::false_type());
 }
 
 // Checks the arguments that both directions take, fills P and says whether pairs take the tiles.
@@ -368,17 +434,12 @@ gsa_status gsa_grouped_glu(const gsa_qin *a, const gsa_qin *b, const int64_t *sp
     if (st != GSA_OK || M == 0) return st;
     P.out = y;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    auto typed = [&](auto fmt, auto type) {
-        return pair ? launch_glu<decltype(fmt)::value, true, false, decltype(type)>(P, tiles, s)
-                    : launch_glu<decltype(fmt)::value, false, false, decltype(type)>(P, tiles, s);
-    };
-    auto sized = [&](auto fmt) { return out_dtype == GSA_BF16 ? typed(fmt, __nv_bfloat16()) : typed(fmt, float()); };
-    return recipe_kind == GSA_NVFP4 ? sized(std::true_type()) : sized(std::false_type());
+    return launch_glu<false>(P, recipe_kind == GSA_NVFP4, pair, out_dtype, tiles, s);
 }
 
 size_t gsa_grouped_glu_bwd_workspace_size(int64_t M, int64_t N) {
     if (M <= 0 || N <= 0 || M >= (int64_t(1) << 31) || N >= (int64_t(1) << 30)) return 0;
-    return kHead + (static_cast<size_t>((N + 127) / 128) * 2 * M * 4 + 255) / 256 * 256;
+    return kHead + (static_cast<size_t>((N + kSide - 1) / kSide) * kParts * M * 4 + 255) / 256 * 256;
 }
 
 gsa_status gsa_grouped_glu_bwd(const void *dy_bf16, const gsa_qin *a, const gsa_qin *b, const int64_t *split_sizes_dev, int64_t E, int64_t M,
@@ -400,14 +461,9 @@ gsa_status gsa_grouped_glu_bwd(const void *dy_bf16, const gsa_qin *a, const gsa_
     P.dy = static_cast<const __nv_bfloat16 *>(dy_bf16);
     P.out = dx_opt;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    auto typed = [&](auto fmt, auto type) {
-        return pair ? launch_glu<decltype(fmt)::value, true, true, decltype(type)>(P, tiles, s)
-                    : launch_glu<decltype(fmt)::value, false, true, decltype(type)>(P, tiles, s);
-    };
-    auto sized = [&](auto fmt) { return out_dtype == GSA_BF16 ? typed(fmt, __nv_bfloat16()) : typed(fmt, float()); };
-    st = recipe_kind == GSA_NVFP4 ? sized(std::true_type()) : sized(std::false_type());
+    st = launch_glu<true>(P, recipe_kind == GSA_NVFP4, pair, out_dtype, tiles, s);
     if (st != GSA_OK || !dprobs_opt) return st;
-    sum_partials<<<static_cast<unsigned>((M + 255) / 256), 256, 0, s>>>(P.part, P.bad, 2 * P.n_tiles, M, dprobs_opt);
+    sum_partials<<<static_cast<unsigned>((M + 255) / 256), 256, 0, s>>>(P.part, P.bad, kParts * P.n_tiles, M, dprobs_opt);
     return cudaGetLastError() == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
 }
 
