@@ -64,29 +64,37 @@ __device__ __forceinline__ void load_dy(uint32_t buf, const OutAt<const __nv_bfl
     }
 }
 
-// A warp's 32 x 32 results, a row a lane, to memory by way of its buffer: pieces of 64 bytes a row, four lanes a row.
+// 32 bytes of results to memory in one instruction, or 16.
+template <int kBytes> __device__ __forceinline__ void store_chunk(void *p, const uint32_t *x) {
+    if constexpr (kBytes == 32)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]),
+                     "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    else
+        *static_cast<uint4 *>(p) = make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// A lane's row of 32 results, straight from its registers.
+template <int kBytes, typename T> __device__ __forceinline__ void store_lane(const uint32_t *v, const OutAt<T> &w, int lane) {
+    constexpr int kPer = kBytes / sizeof(T);
+    if (lane >= w.rows) return;
+    T *o = w.o + lane * w.pitch;
+#pragma unroll
+    for (int j = 0; j < kCols; j += kPer) {
+        uint32_t x[kBytes / 4];
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i) finish<false>(v + j + i * (kPer / (kBytes / 16)), 1.0f, 1.0f, reinterpret_cast<uint32_t(&)[4]>(x[4 * i]), T());
+        if (j < w.cols) store_chunk<kBytes>(o + j, x);
+    }
+}
+
+// A warp's 32 x 32 results, a row a lane, to memory.  Whole sectors from the lanes' registers wherever rows start on them:
+// shared memory is what the products and their copies live on (117 of its 128 bytes a cycle, NVFP4), and passing results
+// through it slows them (@@).  Else by way of the warp's buffer.
 template <typename T> __device__ __forceinline__ void store_rows(const uint32_t *v, uint32_t buf, const OutAt<T> &w, int lane) {
     if (w.wide) {
-        constexpr int kPer = 16 / sizeof(T);
-#pragma unroll
-        for (int j = 0; j < kCols; j += 4 * kPer) {
-            if (j >= w.cols) break;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t x[4];
-                finish<false>(v + j + c * kPer, 1.0f, 1.0f, x, T());
-                tc::st_shared(chunk(buf, lane, c), x);
-            }
-            __syncwarp();
-            const int c = lane & 3, col = j + c * kPer;
-#pragma unroll
-            for (int r0 = 0; r0 < 32; r0 += 8) {
-                const int r = r0 + (lane >> 2);
-                const uint4 x = tc::ld_shared(chunk(buf, r, c));
-                if (r < w.rows && col < w.cols) *reinterpret_cast<uint4 *>(w.o + r * w.pitch + col) = x;
-            }
-            __syncwarp();
-        }
+        if ((w.pitch | w.cols) * sizeof(T) % 32 == 0 && reinterpret_cast<uintptr_t>(w.o) % 32 == 0) store_lane<32>(v, w, lane);
+        else store_lane<16>(v, w, lane);
     } else {   // rows that do not start on 16 bytes: 16 columns at a time in FP32, a column a lane, two rows at once
 #pragma unroll
         for (int j = 0; j < kCols; j += 16) {
