@@ -3,21 +3,41 @@
 //
 //   out[r, n] = u_e sum_k x[r, k] B_e[n, k],   rows r of expert e
 //   y[r, n] = p_r act(u_g sum_k x[r, k] B_e[n, k], u_l sum_k x[r, k] B_e[N + n, k])
+//
+// What there is to do is to read the weights once: 0.56 (NVFP4) or 1.03 bytes each, so at the
+// memory's rate an SM decodes 20 to 45 of them a cycle, and a multiply-add for each row of x and
+// weight would not keep up.  So the weights go to the tensor core (mma.sync, 16 weight rows x 8
+// rows of x x 16 k), as FP16: an NVFP4 code times its block scale has 6 bits and lies between
+// 2^-10 and 2688, exact; an MXFP8 code is exact, and its block's scale, any power of two, is
+// applied to the block's sums in FP32.  x is brought to FP16 too: scaled by a power of two to
+// [2^14, 2^15), FP32 rows as the sum of two.
+//   A block holds the rows of x of one expert in shared memory (up to 16, a pass) and walks
+// a run of tiles of 16 weight rows, its 16 warps sharing out the steps of 128 k of each; their
+// sums meet in shared memory.  Loads run kDepth steps ahead, over the ends of tiles, passes and
+// experts.  How a sum is split goes by K alone: a row's result has the same bits whatever rows it
+// comes with.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <cstring>
+#include <mutex>
 #include <type_traits>
 
 #include "glu_act.cuh"
 #include "gsa.h"
 #include "moe/status.cuh"
+#include "tc.cuh"
 
 namespace {
 
-constexpr int kMaxE = 256, kThreads = 256, kScaleTile = 512;
+constexpr int kMaxE = 256, kWarps = 16, kThreads = 32 * kWarps, kScaleTile = 512;
+constexpr int kStep = 128;                  // k of a step
+constexpr int kStepX = kStep * 2;           // bytes of a step of a row of x in shared memory
+constexpr int kMaxRows = 16;                // rows of x a pass
+constexpr int kSpace = 150 * 1024;          // bytes of x a block holds, at most
+constexpr int64_t kMaxK = 32768;
 
 struct GemvParams {
     const void *x;
@@ -31,31 +51,39 @@ struct GemvParams {
     int E, x_type, out_type;
     int scale_cols, scale_rows, up_tiles;   // scale tiles along k; of an expert along its rows; from a gate row to its linear row
     int b_groups;
+    int steps, wk;          // steps of k; warps that share them out (a power of two)
+    int tiles;              // tiles of 16 * (kWarps / wk) weight rows an expert
+    int rows16;             // tiles of 16 weight rows an expert
+    int pass_rows, pitch;   // rows of x a pass; bytes of a row in shared memory
     glu::Act act;
 };
 
 struct Shared {
-    int row0[kMaxE + 2];
-    int64_t scan[kThreads / 32];
+    int row0[kMaxE + 1];     // first row of each expert
+    int pass0[kMaxE + 1];    // first pass of each expert
+    int64_t scan[kWarps][2];
     uint32_t bad;
+    uint32_t largest[kMaxRows];   // bits of a row's largest finite value
+    float unscale[kMaxRows];      // 2^-s of a row
 };
 
+// Rows and passes before each expert; every thread.
 __device__ void scan_rows(const GemvParams &P, Shared &sh) {
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     int64_t m = t < P.E ? (P.split ? P.split[t] : P.M) : 0;
     const bool neg = m < 0 || m > P.M;
     if (neg) m = 0;
-    int64_t rows = m;
+    int64_t rows = m, passes = (m + P.pass_rows - 1) / P.pass_rows;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, d);
-        if (lane >= d) rows += r;
+        const int64_t r = __shfl_up_sync(0xFFFFFFFFu, rows, d), q = __shfl_up_sync(0xFFFFFFFFu, passes, d);
+        if (lane >= d) rows += r, passes += q;
     }
-    if (lane == 31) sh.scan[w] = rows;
+    if (lane == 31) sh.scan[w][0] = rows, sh.scan[w][1] = passes;
     const bool any_neg = __syncthreads_or(neg);
-    for (int k = 0; k < w; ++k) rows += sh.scan[k];
-    if (t < P.E) sh.row0[t + 1] = static_cast<int>(rows < P.M ? rows : P.M);
-    if (t == 0) sh.row0[0] = 0;
+    for (int k = 0; k < w; ++k) rows += sh.scan[k][0], passes += sh.scan[k][1];
+    if (t < P.E) sh.row0[t + 1] = static_cast<int>(rows), sh.pass0[t + 1] = static_cast<int>(passes);
+    if (t == 0) sh.row0[0] = 0, sh.pass0[0] = 0;
     if (t == P.E - 1) sh.bad = any_neg || rows > P.M;
     __syncthreads();
 }
@@ -66,86 +94,388 @@ __device__ __forceinline__ float unit_of(float amax) {
     return __fdiv_rn(1.0f, s <= 3.402823466e38f ? s : 3.402823466e38f);
 }
 
-__device__ __forceinline__ float element(const void *p, int type, int64_t i) {
-    if (type == GSA_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-    if (type == GSA_FP16) return __half2float(static_cast<const __half *>(p)[i]);
-    return static_cast<const float *>(p)[i];
-}
-
 __device__ __forceinline__ void put(void *p, int type, int64_t i, float v) {
     if (type == GSA_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
     else if (type == GSA_FP16) static_cast<__half *>(p)[i] = __float2half_rn(v);
     else static_cast<float *>(p)[i] = v;
 }
 
-__device__ __forceinline__ float e4m3(uint8_t c) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-    return __half2float(__half(h));
+// -------------------------------------------------------------- rows of x
+
+// Eight consecutive values (i a multiple of 8) in FP32.
+__device__ __forceinline__ void load8(const void *x, int type, int64_t i, float (&v)[8]) {
+    if (type == GSA_FP32) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i));
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i + 4));
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        return;
+    }
+    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (type == GSA_BF16) {
+            v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        } else {
+            __half2 h;
+            memcpy(&h, &w[j], 4);
+            const float2 f = __half22float2(h);
+            v[2 * j] = f.x, v[2 * j + 1] = f.y;
+        }
+    }
 }
 
-__device__ __forceinline__ float e8m0(uint8_t c) {
-    return __uint_as_float(c == 255 ? 0x7FFFFFFFu : c == 0 ? 0x00400000u : static_cast<uint32_t>(c) << 23);
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    uint32_t u;
+    memcpy(&u, &h, 4);
+    return u;
 }
 
-// Weight (row of all, row of its scale tile, k), without the unit.
-template <bool NV> __device__ __forceinline__ float weight(const GemvParams &P, int64_t row, int64_t tile_row, int lr, int64_t k) {
-    constexpr int B = NV ? 16 : 32;
-    const int64_t c = k / B;
-    const uint8_t s = P.scales[(tile_row * P.scale_cols + c / 4) * kScaleTile + 16 * (lr % 32) + 4 * (lr / 32) + c % 4];
-    if (!NV) return e4m3(P.codes[row * P.K + k]) * e8m0(s);
-    const int code = P.codes[row * (P.K / 2) + k / 2] >> (k & 1 ? 4 : 0) & 15, m = code & 7;
-    const float v = m < 2 ? 0.5f * m : __uint_as_float((126u + (m >> 1)) << 23 | (m & 1u) << 22);
-    return (code & 8 ? -v : v) * e4m3(s);
+// Where the eight values from k on (a multiple of 8) lie in a row: in order (MXFP8: a lane's eight codes of a block of 32
+// meet them in one 16-byte load), or with the 16-byte words of a step transposed, 4 x 4 (NVFP4: a lane has 32 codes in a
+// row, and the four lanes of a weight row meet the words jj of theirs at once).
+template <bool NV> __device__ __forceinline__ int place(int k) {
+    const int step = k / kStep, c = k % kStep / 8;
+    return step * kStepX + 16 * (NV ? (c & 3) * 4 + (c >> 2) : c);
 }
+
+// Rows r0 .. r0 + rows of x to shared memory (kPieces 2: the FP16 halves of FP32 values, `rows` rows apart); every thread.
+template <bool NV, int kPieces> __device__ void stage_rows(const GemvParams &P, Shared &sh, uint8_t *xs, int r0, int rows) {
+    int threads = kThreads;   // a row: whole warps
+    for (int r = 1; r < rows; r *= 2) threads /= 2;
+    const int row = threadIdx.x / threads, t = threadIdx.x % threads, words = P.steps * (kStep / 8);
+    const int64_t at = (r0 + static_cast<int64_t>(row)) * P.K;
+    if (threadIdx.x < kMaxRows) sh.largest[threadIdx.x] = 0;
+    __syncthreads();   // also: nobody reads the rows before any more
+    if (P.x_type != GSA_FP16) {
+        uint32_t most = 0;
+        if (row < rows)
+            for (int c = t; c < words; c += threads) {
+                if (8 * c >= P.K) break;
+                float v[8];
+                load8(P.x, P.x_type, at + 8 * c, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+                    if (a < 0x7F800000u && a > most) most = a;
+                }
+            }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+        if (row < rows && threadIdx.x % 32 == 0) atomicMax(&sh.largest[row], most);
+        __syncthreads();
+    }
+    if (row < rows) {
+        float scale = 1.0f;
+        if (P.x_type != GSA_FP16) {
+            const uint32_t most = sh.largest[row];
+            int s = 14 - (static_cast<int>(most >> 23) - 127);   // (subnormal: 141, cut off below)
+            if (most == 0) s = 0;
+            if (s > 126) s = 126;
+            scale = __uint_as_float(static_cast<uint32_t>(127 + s) << 23);
+            if (t == 0) sh.unscale[row] = __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
+        } else if (t == 0) {
+            sh.unscale[row] = 1.0f;
+        }
+        for (int c = t; c < words; c += threads) {
+            float v[8] = {};
+            if (8 * c < P.K) load8(P.x, P.x_type, at + 8 * c, v);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = v[2 * j] * scale, b = v[2 * j + 1] * scale;
+                hi[j] = half2_bits(a, b);
+                if (kPieces == 2) {
+                    const float ha = __half2float(__float2half_rn(a)), hb = __half2float(__float2half_rn(b));
+                    // an infinite value's rest would be NaN
+                    lo[j] = half2_bits(fabsf(a) <= 65504.0f ? a - ha : 0.0f, fabsf(b) <= 65504.0f ? b - hb : 0.0f);
+                }
+            }
+            uint8_t *to = xs + row * P.pitch + place<NV>(8 * c);
+            *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (kPieces == 2) *reinterpret_cast<uint4 *>(to + P.pass_rows * P.pitch) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- weights
+
+// A lane's part of a step: weight rows a (its low row of the tile) and b = a + 64.
+template <bool NV> struct Item;
+template <> struct Item<true> {    // 32 codes and 2 scales of each row
+    uint4 a, b;
+    uint32_t sa, sb;
+};
+template <> struct Item<false> {   // 8 codes of each of 4 blocks, and their scales
+    uint2 a[4], b[4];
+    uint32_t sa, sb;
+};
+
+template <typename T> __device__ __forceinline__ T load_stream(const void *p) { return __ldcs(static_cast<const T *>(p)); }
+
+// The tile row i of 16 holds rows 4 (i mod 8) .. + 3 of each quarter of scale tile i / 8: their scales are 64 bytes in a row.
+template <bool NV>
+__device__ __forceinline__ void load_item(const GemvParams &P, Item<NV> &it, int e, int side, int sides, int i, int step, int lane, bool on) {
+    const int g = lane >> 2, t = lane & 3;
+    const int inside = 4 * (i & 7) + (g & 3), row = 128 * (i >> 3) + inside + 32 * (g >> 2);
+    const int64_t pitch = NV ? P.K / 2 : P.K;
+    const uint8_t *c = P.codes + (static_cast<int64_t>(e * sides + side) * P.N + row) * pitch;
+    const uint8_t *s = P.scales +
+                       (static_cast<int64_t>(e * P.scale_rows + side * P.up_tiles + (i >> 3)) * P.scale_cols + (NV ? 2 * step + (t >> 1) : step)) * kScaleTile +
+                       16 * inside + 4 * (g >> 2);
+    const bool in_a = on && row < P.N, in_b = on && row + 64 < P.N;
+    if constexpr (NV) {
+        const bool k = step * kStep + 32 * t < P.K;
+        c += step * (kStep / 2) + 16 * t;
+        s += 2 * (t & 1);
+        it.a = it.b = make_uint4(0, 0, 0, 0);
+        it.sa = it.sb = 0;
+        if (in_a && k) it.a = load_stream<uint4>(c), it.sa = load_stream<uint16_t>(s);
+        if (in_b && k) it.b = load_stream<uint4>(c + 64 * pitch), it.sb = load_stream<uint16_t>(s + 8);
+    } else {
+        c += step * kStep + 8 * t;
+        it.sa = it.sb = 0;
+        if (in_a) it.sa = load_stream<uint32_t>(s);
+        if (in_b) it.sb = load_stream<uint32_t>(s + 8);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const bool k = step * kStep + 32 * b < P.K;
+            it.a[b] = it.b[b] = make_uint2(0, 0);
+            if (in_a && k) it.a[b] = load_stream<uint2>(c + 32 * b);
+            if (in_b && k) it.b[b] = load_stream<uint2>(c + 32 * b + 64 * pitch);
+        }
+    }
+}
+
+// Two E2M1 codes (a byte) and two E4M3 codes (16 bits) as FP16.
+__device__ __forceinline__ uint32_t e2m1x2(uint32_t byte) {
+    uint32_t h;
+    asm("{\n .reg .b8 c;\n cvt.u8.u32 c, %1;\n cvt.rn.f16x2.e2m1x2 %0, c;\n}" : "=r"(h) : "r"(byte));
+    return h;
+}
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t pair) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(pair)));
+    return h;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 2^(c - 127); 255: NaN.
+__device__ __forceinline__ float e8m0(uint32_t c) { return __uint_as_float(c == 255 ? 0x7FFFFFFFu : c == 0 ? 0x00400000u : c << 23); }
+
+// The products of one step with `groups` groups of 8 rows of x (xs: the lane's place in the step, by group 8 rows apart;
+// left: k from the step's first on, MXFP8: a word of scales holds padding behind the last block, maybe NaN).  The
+// sums of a step start from zero and are added in FP32: the tensor core cuts off what it adds to (about 2^-24 of it a step of
+// 16), which would grow with the length.
+template <bool NV, int kG, int kPieces>
+__device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4], const uint8_t *const (&xs)[kG], int groups, int piece_bytes, int left) {
+    if constexpr (NV) {
+        const uint32_t sa = e4m3x2(it.sa), sb = e4m3x2(it.sb);
+        const uint32_t wa[4] = {it.a.x, it.a.y, it.a.z, it.a.w}, wb[4] = {it.b.x, it.b.y, it.b.z, it.b.w};
+        uint32_t A[8][4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t fa = __byte_perm(sa, 0, j < 4 ? 0x1010 : 0x3232), fb = __byte_perm(sb, 0, j < 4 ? 0x1010 : 0x3232);
+            const uint32_t ca = wa[j >> 1] >> (j & 1 ? 16 : 0), cb = wb[j >> 1] >> (j & 1 ? 16 : 0);
+            A[j][0] = mul_half2(e2m1x2(ca), fa);
+            A[j][1] = mul_half2(e2m1x2(cb), fb);
+            A[j][2] = mul_half2(e2m1x2(ca >> 8), fa);
+            A[j][3] = mul_half2(e2m1x2(cb >> 8), fb);
+        }
+#pragma unroll
+        for (int q = 0; q < kG; ++q) {
+            if (q >= groups) break;
+            float d[4] = {};
+#pragma unroll
+            for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) {
+                    const uint4 b = *reinterpret_cast<const uint4 *>(xs[q] + p * piece_bytes + 64 * jj);
+                    mma(d, A[2 * jj], b.x, b.y);
+                    mma(d, A[2 * jj + 1], b.z, b.w);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[q][i] += d[i];
+        }
+    } else {
+        const uint32_t keep = left > 64 ? 0xFFFFFFFFu : 0xFFFFu, sa = it.sa & keep, sb = it.sb & keep;   // K is a multiple of 64
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const float fa = e8m0(sa >> (8 * b) & 255), fb = e8m0(sb >> (8 * b) & 255);
+            const uint32_t A0[4] = {e4m3x2(it.a[b].x), e4m3x2(it.b[b].x), e4m3x2(it.a[b].x >> 16), e4m3x2(it.b[b].x >> 16)};
+            const uint32_t A1[4] = {e4m3x2(it.a[b].y), e4m3x2(it.b[b].y), e4m3x2(it.a[b].y >> 16), e4m3x2(it.b[b].y >> 16)};
+#pragma unroll
+            for (int q = 0; q < kG; ++q) {
+                if (q >= groups) break;
+                float d[4] = {};
+#pragma unroll
+                for (int p = 0; p < kPieces; ++p) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(xs[q] + p * piece_bytes + 64 * b);
+                    mma(d, A0, x.x, x.y);
+                    mma(d, A1, x.z, x.w);
+                }
+                acc[q][0] = __fmaf_rn(fa, d[0], acc[q][0]);
+                acc[q][1] = __fmaf_rn(fa, d[1], acc[q][1]);
+                acc[q][2] = __fmaf_rn(fb, d[2], acc[q][2]);
+                acc[q][3] = __fmaf_rn(fb, d[3], acc[q][3]);
+            }
+        }
+    }
+}
+
+// A place in a block's run of tiles.
+struct Cursor {
+    int e, pass, tile;
+    __device__ __forceinline__ void next(const GemvParams &P, const Shared &sh) {
+        if (++tile < P.tiles) return;
+        tile = 0;
+        if (++pass < sh.pass0[e + 1]) return;
+        while (sh.pass0[e + 1] <= pass) ++e;   // (only asked for where there is a next tile)
+    }
+};
 
 __device__ __forceinline__ float gated(const glu::Act &A, float g, float u) {
     const float2 a = make_float2(g, g), b = make_float2(u, u);
     return A.clamped ? glu::value<true>(A, a, b).x : glu::value<false>(A, a, b).x;
 }
 
-constexpr int kRowsAtOnce = 8;
+// A sum times the weights' unit and the row's 2^-s: in the order that leaves FP32's range last.
+__device__ __forceinline__ float scaled(float v, float unit, float unscale) {
+    if ((unit > 0x1p64f && unscale < 1.0f) || (unit < 0x1p-64f && unscale > 4.0f)) return v * (unit * unscale);
+    return v * unit * unscale;
+}
 
-template <bool NV, bool kGlu> __global__ void __launch_bounds__(kThreads) gemv(const __grid_constant__ GemvParams P) {
+template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_bounds__(kThreads, 1) gemv(const __grid_constant__ GemvParams P) {
+    constexpr int kSides = kGlu ? 2 : 1;
+    constexpr int kDepth = NV ? 4 : 2;
+    extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ Shared sh;
+    using Sums = float[kSides * kG * 128];
+    Sums *sums[2] = {reinterpret_cast<Sums *>(dyn), reinterpret_cast<Sums *>(dyn) + kWarps};
+    uint8_t *xs = dyn + 2 * kWarps * sizeof(Sums);
+    tc::allow_next();
+    tc::wait_for_previous();
     scan_rows(P, sh);
     if (sh.bad) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(P.status, gemm_status::ERR_SPLIT);
         return;
     }
-    const int lane = threadIdx.x & 31;
-    const int64_t warp = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5, warps = gridDim.x * static_cast<int64_t>(kThreads / 32);
-    const int64_t sides = kGlu ? 2 : 1;
-    for (int64_t i = warp; i < P.E * P.N; i += warps) {
-        const int e = static_cast<int>(i / P.N);
-        const int64_t n = i - e * P.N;
-        for (int r0 = sh.row0[e]; r0 < sh.row0[e + 1]; r0 += kRowsAtOnce) {
-            const int rows = min(kRowsAtOnce, sh.row0[e + 1] - r0);
-            float acc[2][kRowsAtOnce] = {};
-            for (int64_t k = lane; k < P.K; k += 32) {
-                float w[2];
-                for (int s = 0; s < sides; ++s)
-                    w[s] = weight<NV>(P, (e * sides + s) * P.N + n, static_cast<int64_t>(e) * P.scale_rows + s * P.up_tiles + n / 128, n % 128, k);
-#pragma unroll
-                for (int r = 0; r < kRowsAtOnce; ++r) {
-                    if (r >= rows) break;
-                    const float x = element(P.x, P.x_type, (r0 + r) * P.K + k);
-                    for (int s = 0; s < sides; ++s) acc[s][r] = __fmaf_rn(x, w[s], acc[s][r]);
-                }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wk = warp & (P.wk - 1), wn = warp / P.wk, wns = kWarps / P.wk;
+    const int64_t all = static_cast<int64_t>(sh.pass0[P.E]) * P.tiles;
+    const int64_t first = all * blockIdx.x / gridDim.x, left = all * (blockIdx.x + 1) / gridDim.x - first;
+    if (left > 0) {
+        Cursor ahead;   // of the loads
+        ahead.pass = static_cast<int>(first / P.tiles);
+        ahead.tile = static_cast<int>(first - static_cast<int64_t>(ahead.pass) * P.tiles);
+        ahead.e = 0;
+        while (sh.pass0[ahead.e + 1] <= ahead.pass) ++ahead.e;
+        Cursor at = ahead;
+        const int rounds = (P.steps + P.wk - 1) / P.wk, per = rounds * kSides;   // a warp's items a tile
+        const int64_t items = left * per;
+        int64_t asked = 0;
+        int ahead_item = 0;
+        auto ask = [&](Item<NV> &it) {
+            if (asked >= items) return;
+            const int side = kGlu ? ahead_item & 1 : 0, step = (kGlu ? ahead_item >> 1 : ahead_item) * P.wk + wk, i = ahead.tile * wns + wn;
+            load_item<NV>(P, it, ahead.e, side, kSides, i, step, lane, step < P.steps && i < P.rows16);
+            ++asked;
+            if (++ahead_item == per) {
+                ahead_item = 0;
+                if (asked < items) ahead.next(P, sh);
             }
-            for (int r = 0; r < rows; ++r) {
-                float v[2];
-                for (int s = 0; s < sides; ++s) {
-                    v[s] = acc[s][r];
-                    for (int d = 16; d > 0; d >>= 1) v[s] += __shfl_xor_sync(0xFFFFFFFFu, v[s], d);
-                    if (NV) v[s] *= unit_of(P.amax[e * P.b_groups + (s ? P.b_groups - 1 : 0)]);
+        };
+        Item<NV> ring[kDepth];
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) ask(ring[d]);
+
+        float acc[kSides][kG][4] = {};
+        const uint8_t *place_of[kG];
+        const int piece_bytes = P.pass_rows * P.pitch;
+        int staged = -1, rows = 0, groups = 0, r0 = 0, item = 0, buffer = 0;
+        auto stage = [&] {
+            staged = at.pass;
+            const int p = at.pass - sh.pass0[at.e];
+            r0 = sh.row0[at.e] + p * P.pass_rows;
+            rows = min(P.pass_rows, sh.row0[at.e + 1] - r0);
+            groups = (rows + 7) / 8;
+            stage_rows<NV, kPieces>(P, sh, xs, r0, rows);
+#pragma unroll
+            for (int q = 0; q < kG; ++q)   // lanes past the last row read it again: their columns are not stored
+                place_of[q] = xs + min(8 * q + (lane >> 2), rows - 1) * P.pitch + 16 * (lane & 3);
+        };
+        // The tile's sums over the warps, and its results.
+        auto finish = [&] {
+            float *mine = sums[buffer][warp];
+#pragma unroll
+            for (int s = 0; s < kSides; ++s)
+#pragma unroll
+                for (int q = 0; q < kG; ++q) {
+                    if (q >= groups) break;
+                    float2 *to = reinterpret_cast<float2 *>(mine + (s * kG + q) * 128);
+                    to[lane] = make_float2(acc[s][q][0], acc[s][q][1]);
+                    to[32 + lane] = make_float2(acc[s][q][2], acc[s][q][3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) acc[s][q][k] = 0.0f;
                 }
-                const float p = P.probs ? P.probs[r0 + r] : 1.0f;
-                if (lane == 0) put(P.out, P.out_type, (r0 + r) * P.N + n, kGlu ? p * gated(P.act, v[0], v[1]) : v[0]);
+            __syncthreads();
+            for (int o = threadIdx.x; o < wns * groups * 128; o += kThreads) {
+                const int j = o & 7, a = (o >> 3) & 15, q = (o >> 7) % groups, b = (o >> 7) / groups;   // row of x, weight row, group, warp row
+                const int i = at.tile * wns + b, r = 8 * q + j;
+                const int n = 128 * (i >> 3) + 4 * (i & 7) + (a & 3) + 32 * (a >> 2);
+                if (r >= rows || i >= P.rows16 || n >= P.N) continue;
+                float v[kSides];
+#pragma unroll
+                for (int s = 0; s < kSides; ++s) {
+                    v[s] = 0.0f;
+                    for (int k = 0; k < P.wk; ++k) v[s] += sums[buffer][b * P.wk + k][(s * kG + q) * 128 + a * 8 + j];
+                    const float unit = NV ? unit_of(P.amax[at.e * P.b_groups + (s ? P.b_groups - 1 : 0)]) : 1.0f;
+                    v[s] = scaled(v[s], unit, sh.unscale[r]);
+                }
+                float y = v[0];
+                if constexpr (kGlu) y = (P.probs ? P.probs[r0 + r] : 1.0f) * gated(P.act, v[0], v[1]);
+                put(P.out, P.out_type, (r0 + static_cast<int64_t>(r)) * P.N + n, y);
+            }
+            buffer ^= 1;
+        };
+        for (int64_t done = 0; done < items;) {
+#pragma unroll
+            for (int d = 0; d < kDepth; ++d) {
+                if (done >= items) break;
+                if (item == 0 && staged != at.pass) stage();
+                const int side = kGlu ? item & 1 : 0, step = (kGlu ? item >> 1 : item) * P.wk + wk;
+                if (step < P.steps) {
+                    const int left_k = static_cast<int>(P.K) - step * kStep;
+                    const uint8_t *from[kG];
+#pragma unroll
+                    for (int q = 0; q < kG; ++q) from[q] = place_of[q] + step * kStepX;
+                    if (kGlu && side) multiply<NV, kG, kPieces>(ring[d], acc[kSides - 1], from, groups, piece_bytes, left_k);
+                    else multiply<NV, kG, kPieces>(ring[d], acc[0], from, groups, piece_bytes, left_k);
+                }
+                ask(ring[d]);
+                ++done;
+                if (++item == per) {
+                    item = 0;
+                    finish();
+                    if (done < items) at.next(P, sh);
+                }
             }
         }
     }
-    const int64_t first = sh.row0[P.E] * P.N;   // rows that no expert has
-    for (int64_t i = first + blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; i < P.M * P.N; i += gridDim.x * static_cast<int64_t>(kThreads))
+    // rows that no expert has
+    const int64_t tail = sh.row0[P.E] * P.N;
+    for (int64_t i = tail + blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; i < P.M * P.N; i += gridDim.x * static_cast<int64_t>(kThreads))
         put(P.out, P.out_type, i, 0.0f);
 }
 
@@ -158,6 +488,38 @@ gsa_status cuda_error() {
 
 bool known_type(int32_t t) { return t == GSA_BF16 || t == GSA_FP16 || t == GSA_FP32; }
 
+int sm_count() {
+    static std::mutex mu;
+    static int known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!known[dev]) {
+        int v = 0;
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) known[dev] = v;
+    }
+    return known[dev];
+}
+
+template <bool NV, bool kGlu, int kG, int kPieces> gsa_status launch_gemv(const GemvParams &P, cudaStream_t s) {
+    const int sms = sm_count();
+    if (!sms) return cuda_error();
+    const int smem = P.pass_rows * P.pitch * kPieces + 2 * kWarps * (kGlu ? 2 : 1) * kG * 128 * static_cast<int>(sizeof(float));
+    auto kernel = gemv<NV, kGlu, kG, kPieces>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return cuda_error();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see tc::wait_for_previous
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess ? GSA_OK : cuda_error();
+}
+
 gsa_status run_gemv(GemvParams &P, bool glu, const void *x, int32_t x_dtype, const gsa_qin *b, const int64_t *split, int64_t E, int64_t M, int64_t N,
                     int64_t K, int32_t recipe_kind, int32_t b_groups, void *out, int32_t out_dtype, gsa_stream_t stream) {
     if (!b || E <= 0 || M < 0 || N <= 0 || K <= 0) return GSA_ERR_INVALID_ARG;
@@ -165,7 +527,7 @@ gsa_status run_gemv(GemvParams &P, bool glu, const void *x, int32_t x_dtype, con
     if (!known_type(x_dtype) || !known_type(out_dtype) || (b_groups != 1 && b_groups != 2)) return GSA_ERR_INVALID_ARG;
     const bool nv = recipe_kind == GSA_NVFP4;
     const int64_t sides = glu ? 2 : 1;
-    if (E > kMaxE || K % 64 != 0 || K > 65536 || M >= (int64_t(1) << 31) - 256 || N >= (int64_t(1) << 30) / E - 256) return GSA_ERR_UNSUPPORTED;
+    if (E > kMaxE || K % 64 != 0 || K > kMaxK || M >= (int64_t(1) << 31) - 256 || N >= (int64_t(1) << 30) / E - 256) return GSA_ERR_UNSUPPORTED;
     if (glu && b_groups == 1 && N % 128 != 0) return GSA_ERR_UNSUPPORTED;
     if (M == 0) return GSA_OK;
     if (!x || !b->data || !b->scale || !out || (!split && E != 1) || (nv && !b->amax)) return GSA_ERR_INVALID_ARG;
@@ -189,13 +551,30 @@ gsa_status run_gemv(GemvParams &P, bool glu, const void *x, int32_t x_dtype, con
     P.b_groups = b_groups;
     P.status = gemm_status::word();
     if (!P.status) return cuda_error();
+    P.steps = static_cast<int>((K + kStep - 1) / kStep);
+    P.wk = 1;
+    while (P.wk < kWarps && P.wk < P.steps) P.wk *= 2;
+    const int64_t rest = N % 128;
+    P.rows16 = static_cast<int>(8 * (N / 128) + (rest >= 32 ? 8 : (rest + 3) / 4));
+    const int wns = kWarps / P.wk;
+    P.tiles = (P.rows16 + wns - 1) / wns;
+    P.pitch = P.steps * kStepX + 64;   // rows on alternating halves of the banks
+    const int pieces = x_dtype == GSA_FP32 ? 2 : 1;
+    int64_t rows = kSpace / (P.pitch * pieces);
+    if (rows > kMaxRows) rows = kMaxRows;
+    if (rows > 8) rows = rows / 8 * 8;
+    P.pass_rows = static_cast<int>(rows < M ? rows : M);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const unsigned grid = 152 * 4;
-    if (nv && glu) gemv<true, true><<<grid, kThreads, 0, s>>>(P);
-    else if (nv) gemv<true, false><<<grid, kThreads, 0, s>>>(P);
-    else if (glu) gemv<false, true><<<grid, kThreads, 0, s>>>(P);
-    else gemv<false, false><<<grid, kThreads, 0, s>>>(P);
-    return cudaGetLastError() == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
+    auto go = [&](auto fmt, auto gated, auto groups) {
+        constexpr bool NV = decltype(fmt)::value, kGlu = decltype(gated)::value;
+        constexpr int kG = decltype(groups)::value;
+        return pieces == 2 ? launch_gemv<NV, kGlu, kG, 2>(P, s) : launch_gemv<NV, kGlu, kG, 1>(P, s);
+    };
+    auto grouped = [&](auto fmt, auto gated) {
+        return P.pass_rows <= 8 ? go(fmt, gated, std::integral_constant<int, 1>()) : go(fmt, gated, std::integral_constant<int, kMaxRows / 8>());
+    };
+    auto sided = [&](auto fmt) { return glu ? grouped(fmt, std::true_type()) : grouped(fmt, std::false_type()); };
+    return nv ? sided(std::true_type()) : sided(std::false_type());
 }
 
 }  // namespace

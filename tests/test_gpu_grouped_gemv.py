@@ -3,7 +3,8 @@
 Rows of small integers give sums that are exact in FP32 in any order: FP32 results must be equal, others equal to their one
 rounding.  Rows of any values: a result is off by at most (K / 16 + 16) units of 2^-23 of the sum of magnitudes (a unit a
 step of 16 products and for each of the last sums), and by what FP32 rows lose in two FP16 halves: 2^-22 of each term, and
-2^-40 of the row's largest value times the weights'."""
+2^-39 of the row's largest value (half a step of FP16 below 2^-14, with the largest brought to 2^14 at least) times the
+weights'."""
 import numpy as np
 import pytest
 import torch
@@ -34,7 +35,7 @@ def mass_bound(x, w, k):
     """Of x w^T before the last rounding (x [m, k], w [n, k] in FP64)."""
     ax, aw = np.abs(x), np.abs(w)
     largest = ax.max(1, initial=0.0)[:, None] * aw.max(1, initial=0.0)[None, :]
-    return ((k / 16 + 16) * 2.0 ** -23 + 2.0 ** -22) * (ax @ aw.T) + k * 2.0 ** -40 * largest
+    return ((k / 16 + 16) * 2.0 ** -23 + 2.0 ** -22) * (ax @ aw.T) + k * 2.0 ** -39 * largest
 
 
 # from here on rounding to the nearest gives infinity: half a step above the type's largest value
