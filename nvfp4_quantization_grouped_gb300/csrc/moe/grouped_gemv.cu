@@ -58,6 +58,9 @@ struct GemvParams {
     glu::Act act;
 };
 
+// A warp's sums of `n` groups of 128.  Two floats more, so that four slabs further on lie eight banks on.
+__host__ __device__ constexpr int slab(int n) { return 128 * n + 2; }
+
 struct Shared {
     int row0[kMaxE + 1];     // first row of each expert
     int pass0[kMaxE + 1];    // first pass of each expert
@@ -65,6 +68,8 @@ struct Shared {
     uint32_t bad;
     uint32_t largest[kMaxRows];   // bits of a row's largest finite value
     float unscale[kMaxRows];      // 2^-s of a row
+    float probs[kMaxRows];
+    float unit[2];                // of the weights: plain or gate, linear
 };
 
 // Rows and passes before each expert; every thread.
@@ -141,13 +146,14 @@ template <bool NV> __device__ __forceinline__ int place(int k) {
 }
 
 // Rows r0 .. r0 + rows of x to shared memory (kPieces 2: the FP16 halves of FP32 values, `rows` rows apart); every thread.
-template <bool NV, int kPieces> __device__ void stage_rows(const GemvParams &P, Shared &sh, uint8_t *xs, int r0, int rows) {
+template <bool NV, int kPieces> __device__ void stage_rows(const GemvParams &P, Shared &sh, uint8_t *xs, int r0, int rows, float unit, int sides) {
     int threads = kThreads;   // a row: whole warps
     for (int r = 1; r < rows; r *= 2) threads /= 2;
     const int row = threadIdx.x / threads, t = threadIdx.x % threads, words = P.steps * (kStep / 8);
     const int64_t at = (r0 + static_cast<int64_t>(row)) * P.K;
     if (threadIdx.x < kMaxRows) sh.largest[threadIdx.x] = 0;
     __syncthreads();   // also: nobody reads the rows before any more
+    if (threadIdx.x < sides) sh.unit[threadIdx.x] = unit;
     if (P.x_type != GSA_FP16) {
         uint32_t most = 0;
         if (row < rows)
@@ -178,6 +184,7 @@ template <bool NV, int kPieces> __device__ void stage_rows(const GemvParams &P, 
         } else if (t == 0) {
             sh.unscale[row] = 1.0f;
         }
+        if (t == 0) sh.probs[row] = P.probs ? P.probs[r0 + row] : 1.0f;
         for (int c = t; c < words; c += threads) {
             float v[8] = {};
             if (8 * c < P.K) load8(P.x, P.x_type, at + 8 * c, v);
@@ -362,9 +369,9 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
     constexpr int kDepth = NV ? 4 : 2;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ Shared sh;
-    using Sums = float[kSides * kG * 128];
-    Sums *sums[2] = {reinterpret_cast<Sums *>(dyn), reinterpret_cast<Sums *>(dyn) + kWarps};
-    uint8_t *xs = dyn + 2 * kWarps * sizeof(Sums);
+    float *const sums = reinterpret_cast<float *>(dyn);   // [2][warp][kSlab]
+    constexpr int kSlab = slab(kSides * kG);
+    uint8_t *xs = dyn + 2 * kWarps * kSlab * sizeof(float);
     tc::allow_next();
     tc::wait_for_previous();
     scan_rows(P, sh);
@@ -403,21 +410,24 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         float acc[kSides][kG][4] = {};
         const uint8_t *place_of[kG];
         const int piece_bytes = P.pass_rows * P.pitch;
+        const int parts = min(4, P.wk), parts_log = parts >> 1, each = P.wk / parts;
         int staged = -1, rows = 0, groups = 0, r0 = 0, item = 0, buffer = 0;
         auto stage = [&] {
             staged = at.pass;
+            float unit = 1.0f;
             const int p = at.pass - sh.pass0[at.e];
             r0 = sh.row0[at.e] + p * P.pass_rows;
             rows = min(P.pass_rows, sh.row0[at.e + 1] - r0);
             groups = (rows + 7) / 8;
-            stage_rows<NV, kPieces>(P, sh, xs, r0, rows);
+            if (NV && threadIdx.x < kSides) unit = unit_of(P.amax[at.e * P.b_groups + (threadIdx.x ? P.b_groups - 1 : 0)]);
+            stage_rows<NV, kPieces>(P, sh, xs, r0, rows, unit, kSides);
 #pragma unroll
             for (int q = 0; q < kG; ++q)   // lanes past the last row read it again: their columns are not stored
                 place_of[q] = xs + min(8 * q + (lane >> 2), rows - 1) * P.pitch + 16 * (lane & 3);
         };
         // The tile's sums over the warps, and its results.
         auto finish = [&] {
-            float *mine = sums[buffer][warp];
+            float *mine = sums + (buffer * kWarps + warp) * kSlab;
 #pragma unroll
             for (int s = 0; s < kSides; ++s)
 #pragma unroll
@@ -430,21 +440,32 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
                     for (int k = 0; k < 4; ++k) acc[s][q][k] = 0.0f;
                 }
             __syncthreads();
-            for (int o = threadIdx.x; o < wns * groups * 128; o += kThreads) {
-                const int j = o & 7, a = (o >> 3) & 15, q = (o >> 7) % groups, b = (o >> 7) / groups;   // row of x, weight row, group, warp row
-                const int i = at.tile * wns + b, r = 8 * q + j;
-                const int n = 128 * (i >> 3) + 4 * (i & 7) + (a & 3) + 32 * (a >> 2);
-                if (r >= rows || i >= P.rows16 || n >= P.N) continue;
+            // up to four lanes a result, up to four warps' sums each: first one after the other, then across the lanes
+            const int part = threadIdx.x & (parts - 1);
+            for (int base = 0; base < wns * groups * 128 * parts; base += kThreads) {
+                const int o = (base + static_cast<int>(threadIdx.x)) >> parts_log;
+                const int j = o & 7, a = (o >> 3) & 15, q = (o >> 7) & (groups - 1), b = (o >> 7) >> (groups - 1);   // row of x, weight row, group, warp row
+                const float *from = sums + (buffer * kWarps + min(b, wns - 1) * P.wk + part * each) * kSlab + q * 128 + a * 8 + j;
                 float v[kSides];
 #pragma unroll
                 for (int s = 0; s < kSides; ++s) {
                     v[s] = 0.0f;
-                    for (int k = 0; k < P.wk; ++k) v[s] += sums[buffer][b * P.wk + k][(s * kG + q) * 128 + a * 8 + j];
-                    const float unit = NV ? unit_of(P.amax[at.e * P.b_groups + (s ? P.b_groups - 1 : 0)]) : 1.0f;
-                    v[s] = scaled(v[s], unit, sh.unscale[r]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < each) v[s] += from[s * kG * 128 + k * kSlab];
                 }
-                float y = v[0];
-                if constexpr (kGlu) y = (P.probs ? P.probs[r0 + r] : 1.0f) * gated(P.act, v[0], v[1]);
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1)
+                    if (d < parts) {
+#pragma unroll
+                        for (int s = 0; s < kSides; ++s) v[s] += __shfl_xor_sync(0xFFFFFFFFu, v[s], d);
+                    }
+                const int i = at.tile * wns + b, r = 8 * q + j;
+                const int n = 128 * (i >> 3) + 4 * (i & 7) + (a & 3) + 32 * (a >> 2);
+                if (part != 0 || b >= wns || r >= rows || i >= P.rows16 || n >= P.N) continue;
+                const float unscale = sh.unscale[r];
+                float y = scaled(v[0], sh.unit[0], unscale);
+                if constexpr (kGlu) y = sh.probs[r] * gated(P.act, y, scaled(v[kSides - 1], sh.unit[1], unscale));
                 put(P.out, P.out_type, (r0 + static_cast<int64_t>(r)) * P.N + n, y);
             }
             buffer ^= 1;
@@ -504,7 +525,7 @@ int sm_count() {
 template <bool NV, bool kGlu, int kG, int kPieces> gsa_status launch_gemv(const GemvParams &P, cudaStream_t s) {
     const int sms = sm_count();
     if (!sms) return cuda_error();
-    const int smem = P.pass_rows * P.pitch * kPieces + 2 * kWarps * (kGlu ? 2 : 1) * kG * 128 * static_cast<int>(sizeof(float));
+    const int smem = P.pass_rows * P.pitch * kPieces + 2 * kWarps * slab((kGlu ? 2 : 1) * kG) * static_cast<int>(sizeof(float));
     auto kernel = gemv<NV, kGlu, kG, kPieces>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return cuda_error();
     cudaLaunchConfig_t cfg = {};
