@@ -222,50 +222,64 @@ template <> struct Item<false> {   // 8 codes of each of 4 blocks, and their sca
 
 template <typename T> __device__ __forceinline__ T load_stream(const void *p) { return __ldcs(static_cast<const T *>(p)); }
 
-// The tile row i of 16 holds rows 4 (i mod 8) .. + 3 of each quarter of scale tile i / 8: their scales are 64 bytes in a row.
-template <bool NV>
-__device__ __forceinline__ void load_item(const GemvParams &P, Item<NV> &it, int e, int side, int sides, int i, int step, int lane, bool on) {
-    const int g = lane >> 2, t = lane & 3;
-    const int inside = 4 * (i & 7) + (g & 3), row = 128 * (i >> 3) + inside + 32 * (g >> 2);
-    const int64_t pitch = NV ? P.K / 2 : P.K;
-    const uint8_t *c = P.codes + (static_cast<int64_t>(e * sides + side) * P.N + row) * pitch;
-    const uint8_t *s = P.scales +
-                       (static_cast<int64_t>(e * P.scale_rows + side * P.up_tiles + (i >> 3)) * P.scale_cols + (NV ? 2 * step + (t >> 1) : step)) * kScaleTile +
-                       16 * inside + 4 * (g >> 2);
-    const bool in_a = on && row < P.N, in_b = on && row + 64 < P.N;
-    if constexpr (NV) {
-        const bool k = step * kStep + 32 * t < P.K;
-        c += step * (kStep / 2) + 16 * t;
-        s += 2 * (t & 1);
-        it.a = it.b = make_uint4(0, 0, 0, 0);
-        it.sa = it.sb = 0;
-        if (in_a && k) it.a = load_stream<uint4>(c), it.sa = load_stream<uint16_t>(s);
-        if (in_b && k) it.b = load_stream<uint4>(c + 64 * pitch), it.sb = load_stream<uint16_t>(s + 8);
-    } else {
-        c += step * kStep + 8 * t;
-        it.sa = it.sb = 0;
-        if (in_a) it.sa = load_stream<uint32_t>(s);
-        if (in_b) it.sb = load_stream<uint32_t>(s + 8);
+// Where a lane reads one side of a tile.  The tile i of 16 weight rows holds rows 4 (i mod 8) .. + 3 of each quarter of scale
+// tile i / 8, whose scales are 64 bytes in a row.  Nothing is predicated: rows past the last read the last (their results are
+// not stored), and what lies past the end of k reads the step's first half again (x is zero there).
+struct Aim {
+    const uint8_t *a, *b, *s;
+    template <bool NV> __device__ __forceinline__ void at(const GemvParams &P, int e, int side, int sides, int i, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+        const int inside = 4 * (i & 7) + (g & 3), row = 128 * (i >> 3) + inside + 32 * (g >> 2), last = static_cast<int>(P.N) - 1;
+        const int64_t pitch = NV ? P.K / 2 : P.K, first = static_cast<int64_t>(e * sides + side) * P.N;
+        a = P.codes + (first + min(row, last)) * pitch;
+        b = P.codes + (first + min(row + 64, last)) * pitch;
+        s = P.scales + static_cast<int64_t>(e * P.scale_rows + side * P.up_tiles + (i >> 3)) * P.scale_cols * kScaleTile + 16 * inside + 4 * (g >> 2) +
+            (NV ? 2 * (t & 1) : 0);
+    }
+    template <bool NV> __device__ __forceinline__ void load(const GemvParams &P, Item<NV> &it, int step, int lane) const {
+        const int t = lane & 3, K = static_cast<int>(P.K);
+        if constexpr (NV) {
+            const uint32_t c = min(step * (kStep / 2) + 16 * t, K / 2 - 32 + 16 * (t & 1));
+            const uint32_t q = min(2 * step + (t >> 1), K / 64 - 1) * kScaleTile;
+            it.a = load_stream<uint4>(a + c);
+            it.b = load_stream<uint4>(b + c);
+            it.sa = load_stream<uint16_t>(s + q);
+            it.sb = load_stream<uint16_t>(s + q + 8);
+        } else {
+            step = min(step, P.steps - 1);
+            const uint32_t c = step * kStep + 8 * t, half = c + 64 < K ? 64 : 0, q = step * kScaleTile;
+            it.sa = load_stream<uint32_t>(s + q);
+            it.sb = load_stream<uint32_t>(s + q + 8);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const bool k = step * kStep + 32 * b < P.K;
-            it.a[b] = it.b[b] = make_uint2(0, 0);
-            if (in_a && k) it.a[b] = load_stream<uint2>(c + 32 * b);
-            if (in_b && k) it.b[b] = load_stream<uint2>(c + 32 * b + 64 * pitch);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t from = c + 32 * (j & 1) + (j & 2 ? half : 0);
+                it.a[j] = load_stream<uint2>(a + from);
+                it.b[j] = load_stream<uint2>(b + from);
+            }
         }
     }
-}
+};
 
-// Two E2M1 codes (a byte) and two E4M3 codes (16 bits) as FP16.
-__device__ __forceinline__ uint32_t e2m1x2(uint32_t byte) {
-    uint32_t h;
-    asm("{\n .reg .b8 c;\n cvt.u8.u32 c, %1;\n cvt.rn.f16x2.e2m1x2 %0, c;\n}" : "=r"(h) : "r"(byte));
-    return h;
+// Eight E2M1 codes, four E4M3 codes as FP16, and two E8M0 scales as FP32 (255: NaN).
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+__device__ __forceinline__ void e4m3x4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
 }
 __device__ __forceinline__ uint32_t e4m3x2(uint32_t pair) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(pair)));
     return h;
+}
+__device__ __forceinline__ void e8m0x4(uint32_t w, float (&f)[4]) {
+    uint32_t lo, hi;
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.bf16x2.ue8m0x2 %0, a;\n cvt.rn.bf16x2.ue8m0x2 %1, b;\n}" : "=r"(lo), "=r"(hi) : "r"(w));
+    f[0] = __uint_as_float(lo << 16), f[1] = __uint_as_float(lo & 0xFFFF0000u);
+    f[2] = __uint_as_float(hi << 16), f[3] = __uint_as_float(hi & 0xFFFF0000u);
 }
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -279,9 +293,6 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// 2^(c - 127); 255: NaN.
-__device__ __forceinline__ float e8m0(uint32_t c) { return __uint_as_float(c == 255 ? 0x7FFFFFFFu : c == 0 ? 0x00400000u : c << 23); }
-
 // The products of one step with `groups` groups of 8 rows of x (xs: the lane's place in the step, by group 8 rows apart;
 // left: k from the step's first on, MXFP8: a word of scales holds padding behind the last block, maybe NaN).  The
 // sums of a step start from zero and are added in FP32: the tensor core cuts off what it adds to (about 2^-24 of it a step of
@@ -293,13 +304,16 @@ __device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4]
         const uint32_t wa[4] = {it.a.x, it.a.y, it.a.z, it.a.w}, wb[4] = {it.b.x, it.b.y, it.b.z, it.b.w};
         uint32_t A[8][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t fa = __byte_perm(sa, 0, j < 4 ? 0x1010 : 0x3232), fb = __byte_perm(sb, 0, j < 4 ? 0x1010 : 0x3232);
-            const uint32_t ca = wa[j >> 1] >> (j & 1 ? 16 : 0), cb = wb[j >> 1] >> (j & 1 ? 16 : 0);
-            A[j][0] = mul_half2(e2m1x2(ca), fa);
-            A[j][1] = mul_half2(e2m1x2(cb), fb);
-            A[j][2] = mul_half2(e2m1x2(ca >> 8), fa);
-            A[j][3] = mul_half2(e2m1x2(cb >> 8), fb);
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t fa = __byte_perm(sa, 0, w < 2 ? 0x1010 : 0x3232), fb = __byte_perm(sb, 0, w < 2 ? 0x1010 : 0x3232);
+            uint32_t a[4], b[4];
+            e2m1x8(wa[w], a);
+            e2m1x8(wb[w], b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                A[2 * w + (i >> 1)][2 * (i & 1)] = mul_half2(a[i], fa);
+                A[2 * w + (i >> 1)][2 * (i & 1) + 1] = mul_half2(b[i], fb);
+            }
         }
 #pragma unroll
         for (int q = 0; q < kG; ++q) {
@@ -317,12 +331,17 @@ __device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4]
             for (int i = 0; i < 4; ++i) acc[q][i] += d[i];
         }
     } else {
-        const uint32_t keep = left > 64 ? 0xFFFFFFFFu : 0xFFFFu, sa = it.sa & keep, sb = it.sb & keep;   // K is a multiple of 64
+        const uint32_t keep = left > 64 ? 0xFFFFFFFFu : 0xFFFFu;   // K is a multiple of 64
+        float fa[4], fb[4];
+        e8m0x4(it.sa & keep, fa);
+        e8m0x4(it.sb & keep, fb);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const float fa = e8m0(sa >> (8 * b) & 255), fb = e8m0(sb >> (8 * b) & 255);
-            const uint32_t A0[4] = {e4m3x2(it.a[b].x), e4m3x2(it.b[b].x), e4m3x2(it.a[b].x >> 16), e4m3x2(it.b[b].x >> 16)};
-            const uint32_t A1[4] = {e4m3x2(it.a[b].y), e4m3x2(it.b[b].y), e4m3x2(it.a[b].y >> 16), e4m3x2(it.b[b].y >> 16)};
+            uint32_t A0[4], A1[4];
+            e4m3x4(it.a[b].x, A0[0], A0[2]);
+            e4m3x4(it.b[b].x, A0[1], A0[3]);
+            e4m3x4(it.a[b].y, A1[0], A1[2]);
+            e4m3x4(it.b[b].y, A1[1], A1[3]);
 #pragma unroll
             for (int q = 0; q < kG; ++q) {
                 if (q >= groups) break;
@@ -333,10 +352,10 @@ __device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4]
                     mma(d, A0, x.x, x.y);
                     mma(d, A1, x.z, x.w);
                 }
-                acc[q][0] = __fmaf_rn(fa, d[0], acc[q][0]);
-                acc[q][1] = __fmaf_rn(fa, d[1], acc[q][1]);
-                acc[q][2] = __fmaf_rn(fb, d[2], acc[q][2]);
-                acc[q][3] = __fmaf_rn(fb, d[3], acc[q][3]);
+                acc[q][0] = __fmaf_rn(fa[b], d[0], acc[q][0]);
+                acc[q][1] = __fmaf_rn(fa[b], d[1], acc[q][1]);
+                acc[q][2] = __fmaf_rn(fb[b], d[2], acc[q][2]);
+                acc[q][3] = __fmaf_rn(fb[b], d[3], acc[q][3]);
             }
         }
     }
@@ -389,29 +408,35 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         ahead.e = 0;
         while (sh.pass0[ahead.e + 1] <= ahead.pass) ++ahead.e;
         Cursor at = ahead;
-        const int rounds = (P.steps + P.wk - 1) / P.wk, per = rounds * kSides;   // a warp's items a tile
-        const int64_t items = left * per;
-        int64_t asked = 0;
-        int ahead_item = 0;
+        const int rounds = (P.steps + P.wk - 1) / P.wk;   // a warp's steps of a side of a tile
+        int64_t to_ask = left, to_do = left;              // tiles
+        Aim aim;
+        int ask_side = 0, ask_round = 0;
+        auto take_aim = [&] { aim.at<NV>(P, ahead.e, ask_side, kSides, min(ahead.tile * wns + wn, P.rows16 - 1), lane); };
         auto ask = [&](Item<NV> &it) {
-            if (asked >= items) return;
-            const int side = kGlu ? ahead_item & 1 : 0, step = (kGlu ? ahead_item >> 1 : ahead_item) * P.wk + wk, i = ahead.tile * wns + wn;
-            load_item<NV>(P, it, ahead.e, side, kSides, i, step, lane, step < P.steps && i < P.rows16);
-            ++asked;
-            if (++ahead_item == per) {
-                ahead_item = 0;
-                if (asked < items) ahead.next(P, sh);
+            if (to_ask == 0) return;
+            aim.load<NV>(P, it, ask_round * P.wk + wk, lane);
+            if (++ask_round < rounds) return;
+            ask_round = 0;
+            if (kGlu && ask_side == 0) {
+                ask_side = 1;
+            } else {
+                ask_side = 0;
+                if (--to_ask == 0) return;
+                ahead.next(P, sh);
             }
+            take_aim();
         };
+        take_aim();
         Item<NV> ring[kDepth];
 #pragma unroll
         for (int d = 0; d < kDepth; ++d) ask(ring[d]);
 
-        float acc[kSides][kG][4] = {};
+        float acc[kG][4] = {};
         const uint8_t *place_of[kG];
         const int piece_bytes = P.pass_rows * P.pitch;
         const int parts = min(4, P.wk), parts_log = parts >> 1, each = P.wk / parts;
-        int staged = -1, rows = 0, groups = 0, r0 = 0, item = 0, buffer = 0;
+        int staged = -1, rows = 0, groups = 0, r0 = 0, side = 0, round = 0, buffer = 0;
         auto stage = [&] {
             staged = at.pass;
             float unit = 1.0f;
@@ -425,20 +450,21 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
             for (int q = 0; q < kG; ++q)   // lanes past the last row read it again: their columns are not stored
                 place_of[q] = xs + min(8 * q + (lane >> 2), rows - 1) * P.pitch + 16 * (lane & 3);
         };
+        // A warp's sums of a side of the tile to shared memory.
+        auto hand_in = [&] {
+            float *mine = sums + (buffer * kWarps + warp) * kSlab + side * kG * 128;
+#pragma unroll
+            for (int q = 0; q < kG; ++q) {
+                if (q >= groups) break;
+                float2 *to = reinterpret_cast<float2 *>(mine + q * 128);
+                to[lane] = make_float2(acc[q][0], acc[q][1]);
+                to[32 + lane] = make_float2(acc[q][2], acc[q][3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[q][k] = 0.0f;
+            }
+        };
         // The tile's sums over the warps, and its results.
         auto finish = [&] {
-            float *mine = sums + (buffer * kWarps + warp) * kSlab;
-#pragma unroll
-            for (int s = 0; s < kSides; ++s)
-#pragma unroll
-                for (int q = 0; q < kG; ++q) {
-                    if (q >= groups) break;
-                    float2 *to = reinterpret_cast<float2 *>(mine + (s * kG + q) * 128);
-                    to[lane] = make_float2(acc[s][q][0], acc[s][q][1]);
-                    to[32 + lane] = make_float2(acc[s][q][2], acc[s][q][3]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[s][q][k] = 0.0f;
-                }
             __syncthreads();
             // up to four lanes a result, up to four warps' sums each: first one after the other, then across the lanes
             const int part = threadIdx.x & (parts - 1);
@@ -470,27 +496,29 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
             }
             buffer ^= 1;
         };
-        for (int64_t done = 0; done < items;) {
+        while (to_do > 0) {
 #pragma unroll
             for (int d = 0; d < kDepth; ++d) {
-                if (done >= items) break;
-                if (item == 0 && staged != at.pass) stage();
-                const int side = kGlu ? item & 1 : 0, step = (kGlu ? item >> 1 : item) * P.wk + wk;
+                if (to_do == 0) break;
+                if (staged != at.pass) stage();
+                const int step = round * P.wk + wk;
                 if (step < P.steps) {
-                    const int left_k = static_cast<int>(P.K) - step * kStep;
                     const uint8_t *from[kG];
 #pragma unroll
                     for (int q = 0; q < kG; ++q) from[q] = place_of[q] + step * kStepX;
-                    if (kGlu && side) multiply<NV, kG, kPieces>(ring[d], acc[kSides - 1], from, groups, piece_bytes, left_k);
-                    else multiply<NV, kG, kPieces>(ring[d], acc[0], from, groups, piece_bytes, left_k);
+                    multiply<NV, kG, kPieces>(ring[d], acc, from, groups, piece_bytes, static_cast<int>(P.K) - step * kStep);
                 }
                 ask(ring[d]);
-                ++done;
-                if (++item == per) {
-                    item = 0;
-                    finish();
-                    if (done < items) at.next(P, sh);
+                if (++round < rounds) continue;
+                round = 0;
+                hand_in();
+                if (kGlu && side == 0) {
+                    side = 1;
+                    continue;
                 }
+                side = 0;
+                finish();
+                if (--to_do > 0) at.next(P, sh);
             }
         }
     }
@@ -577,6 +605,9 @@ gsa_status run_gemv(GemvParams &P, bool glu, const void *x, int32_t x_dtype, con
     while (P.wk < kWarps && P.wk < P.steps) P.wk *= 2;
     const int64_t rest = N % 128;
     P.rows16 = static_cast<int>(8 * (N / 128) + (rest >= 32 ? 8 : (rest + 3) / 4));
+    // As few warps to a sum as leave six tiles a block (of as many experts as can have rows): each tile ends with a barrier and
+    // the warps' sums.
+    while (P.wk > 2 && (E < M ? E : M) * P.rows16 * P.wk / (2 * kWarps) >= 6 * 152) P.wk /= 2;
     const int wns = kWarps / P.wk;
     P.tiles = (P.rows16 + wns - 1) / wns;
     P.pitch = P.steps * kStepX + 64;   // rows on alternating halves of the banks
