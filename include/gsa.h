@@ -489,7 +489,8 @@ gsa_status gsa_grouped_glu_bwd(const void *dy_bf16, const gsa_qin *a, const gsa_
  * that its largest value fits (FP32 rows as the sum of two such): values are exact
  * (BF16, FP16) or within 2^-22 (FP32) of themselves down to 2^-29 of the row's
  * largest, and within 2^-39 of that largest below.
- * Errors: INVALID_ARG, UNSUPPORTED (E > 256, K % 64, K > 32768, sizes past 2^31),
+ * Errors: INVALID_ARG, UNSUPPORTED (E > 256, K % 64, K > 32768 (FP32 x: 16384), sizes past
+ * 2^31),
  * ALIGNMENT, CUDA. */
 gsa_status gsa_grouped_gemv(const void *x, int32_t x_dtype, const gsa_qin *b, const int64_t *split_sizes_dev, int64_t E,
                             int64_t M, int64_t N, int64_t K, int32_t recipe_kind, void *out, int32_t out_dtype,

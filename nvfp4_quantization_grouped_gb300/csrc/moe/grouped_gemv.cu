@@ -36,8 +36,8 @@ constexpr int kMaxE = 256, kWarps = 16, kThreads = 32 * kWarps, kScaleTile = 512
 constexpr int kStep = 128;                  // k of a step
 constexpr int kStepX = kStep * 2;           // bytes of a step of a row of x in shared memory
 constexpr int kMaxRows = 16;                // rows of x a pass
-constexpr int kSpace = 150 * 1024;          // bytes of x a block holds, at most
-constexpr int64_t kMaxK = 32768;
+constexpr int kSpace = (227 - 3) * 1024;    // bytes that a block has beside its static ones
+constexpr int64_t kMaxK = 32768;            // a row of x beside the rest (FP32: half of it)
 
 struct GemvParams {
     const void *x;
@@ -211,7 +211,7 @@ template <bool NV, int kPieces> __device__ void stage_rows(const GemvParams &P, 
 
 // A lane's part of a step: weight rows a (its low row of the tile) and b = a + 64.
 template <bool NV> struct Item;
-template <> struct Item<true> {    // 32 codes and 2 scales of each row
+template <> struct Item<true> {    // 32 codes of each row, and words of scales, 2 of which are theirs
     uint4 a, b;
     uint32_t sa, sb;
 };
@@ -220,7 +220,35 @@ template <> struct Item<false> {   // 8 codes of each of 4 blocks, and their sca
     uint32_t sa, sb;
 };
 
-template <typename T> __device__ __forceinline__ T load_stream(const void *p) { return __ldcs(static_cast<const T *>(p)); }
+// Weights on their way: each warp has kDepth steps in shared memory, where a lane's copies are its own, so that nothing but
+// its own copies' arrival is waited for.  (In registers, slots of several steps share the few scoreboards, and any use waits
+// for the newest load: @@ us instead of @@.)  Words of 16 (or 8) and 4 bytes, 32 lanes side by side.
+template <bool NV> constexpr int kSlot = 32 * (NV ? 40 : 72);
+template <bool NV, int kG> constexpr int kDepth = NV ? (kG == 1 ? 6 : 4) : (kG == 1 ? 3 : 2);
+
+template <int kBytes> __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+}
+
+template <bool NV> __device__ __forceinline__ Item<NV> item_at(uint32_t slot, int lane) {
+    Item<NV> it;
+    if constexpr (NV) {
+        it.a = tc::ld_shared(slot + 16 * lane);
+        it.b = tc::ld_shared(slot + 512 + 16 * lane);
+        it.sa = __float_as_uint(tc::ld_shared1(slot + 1024 + 4 * lane)) >> (lane & 1 ? 16 : 0);
+        it.sb = __float_as_uint(tc::ld_shared1(slot + 1152 + 4 * lane)) >> (lane & 1 ? 16 : 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(it.a[j].x), "=r"(it.a[j].y) : "r"(slot + 512 * j + 8 * lane) : "memory");
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(it.b[j].x), "=r"(it.b[j].y) : "r"(slot + 512 * j + 256 + 8 * lane) : "memory");
+        }
+        it.sa = __float_as_uint(tc::ld_shared1(slot + 2048 + 4 * lane));
+        it.sb = __float_as_uint(tc::ld_shared1(slot + 2176 + 4 * lane));
+    }
+    return it;
+}
 
 // Where a lane reads one side of a tile.  The tile i of 16 weight rows holds rows 4 (i mod 8) .. + 3 of each quarter of scale
 // tile i / 8, whose scales are 64 bytes in a row.  Nothing is predicated: rows past the last read the last (their results are
@@ -228,34 +256,33 @@ template <typename T> __device__ __forceinline__ T load_stream(const void *p) { 
 struct Aim {
     const uint8_t *a, *b, *s;
     template <bool NV> __device__ __forceinline__ void at(const GemvParams &P, int e, int side, int sides, int i, int lane) {
-        const int g = lane >> 2, t = lane & 3;
+        const int g = lane >> 2;
         const int inside = 4 * (i & 7) + (g & 3), row = 128 * (i >> 3) + inside + 32 * (g >> 2), last = static_cast<int>(P.N) - 1;
         const int64_t pitch = NV ? P.K / 2 : P.K, first = static_cast<int64_t>(e * sides + side) * P.N;
         a = P.codes + (first + min(row, last)) * pitch;
         b = P.codes + (first + min(row + 64, last)) * pitch;
-        s = P.scales + static_cast<int64_t>(e * P.scale_rows + side * P.up_tiles + (i >> 3)) * P.scale_cols * kScaleTile + 16 * inside + 4 * (g >> 2) +
-            (NV ? 2 * (t & 1) : 0);
+        s = P.scales + static_cast<int64_t>(e * P.scale_rows + side * P.up_tiles + (i >> 3)) * P.scale_cols * kScaleTile + 16 * inside + 4 * (g >> 2);
     }
-    template <bool NV> __device__ __forceinline__ void load(const GemvParams &P, Item<NV> &it, int step, int lane) const {
+    template <bool NV> __device__ __forceinline__ void load(const GemvParams &P, uint32_t slot, int step, int lane) const {
         const int t = lane & 3, K = static_cast<int>(P.K);
         if constexpr (NV) {
             const uint32_t c = min(step * (kStep / 2) + 16 * t, K / 2 - 32 + 16 * (t & 1));
             const uint32_t q = min(2 * step + (t >> 1), K / 64 - 1) * kScaleTile;
-            it.a = load_stream<uint4>(a + c);
-            it.b = load_stream<uint4>(b + c);
-            it.sa = load_stream<uint16_t>(s + q);
-            it.sb = load_stream<uint16_t>(s + q + 8);
+            copy_async<16>(slot + 16 * lane, a + c);
+            copy_async<16>(slot + 512 + 16 * lane, b + c);
+            copy_async<4>(slot + 1024 + 4 * lane, s + q);
+            copy_async<4>(slot + 1152 + 4 * lane, s + q + 8);
         } else {
             step = min(step, P.steps - 1);
             const uint32_t c = step * kStep + 8 * t, half = c + 64 < K ? 64 : 0, q = step * kScaleTile;
-            it.sa = load_stream<uint32_t>(s + q);
-            it.sb = load_stream<uint32_t>(s + q + 8);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t from = c + 32 * (j & 1) + (j & 2 ? half : 0);
-                it.a[j] = load_stream<uint2>(a + from);
-                it.b[j] = load_stream<uint2>(b + from);
+                copy_async<8>(slot + 512 * j + 8 * lane, a + from);
+                copy_async<8>(slot + 512 * j + 256 + 8 * lane, b + from);
             }
+            copy_async<4>(slot + 2048 + 4 * lane, s + q);
+            copy_async<4>(slot + 2176 + 4 * lane, s + q + 8);
         }
     }
 };
@@ -367,8 +394,15 @@ struct Cursor {
     __device__ __forceinline__ void next(const GemvParams &P, const Shared &sh) {
         if (++tile < P.tiles) return;
         tile = 0;
-        if (++pass < sh.pass0[e + 1]) return;
-        while (sh.pass0[e + 1] <= pass) ++e;   // (only asked for where there is a next tile)
+        if (++pass >= sh.pass0[e + 1]) find(P, sh);   // (only asked for where there is a next tile)
+    }
+    __device__ __forceinline__ void find(const GemvParams &P, const Shared &sh) {   // the expert of the pass
+        e = 0;
+        for (int end = P.E; end - e > 1;) {   // the last that starts at or before it
+            const int mid = (e + end) >> 1;
+            if (sh.pass0[mid] <= pass) e = mid;
+            else end = mid;
+        }
     }
 };
 
@@ -385,12 +419,12 @@ __device__ __forceinline__ float scaled(float v, float unit, float unscale) {
 
 template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_bounds__(kThreads, 1) gemv(const __grid_constant__ GemvParams P) {
     constexpr int kSides = kGlu ? 2 : 1;
-    constexpr int kDepth = NV ? 4 : 2;
+    constexpr int kAhead = kDepth<NV, kG>;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ Shared sh;
     float *const sums = reinterpret_cast<float *>(dyn);   // [2][warp][kSlab]
     constexpr int kSlab = slab(kSides * kG);
-    uint8_t *xs = dyn + 2 * kWarps * kSlab * sizeof(float);
+    uint8_t *ring = dyn + 2 * kWarps * kSlab * sizeof(float), *xs = ring + kWarps * kAhead * kSlot<NV>;
     tc::allow_next();
     tc::wait_for_previous();
     scan_rows(P, sh);
@@ -405,17 +439,18 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         Cursor ahead;   // of the loads
         ahead.pass = static_cast<int>(first / P.tiles);
         ahead.tile = static_cast<int>(first - static_cast<int64_t>(ahead.pass) * P.tiles);
-        ahead.e = 0;
-        while (sh.pass0[ahead.e + 1] <= ahead.pass) ++ahead.e;
+        ahead.find(P, sh);
         Cursor at = ahead;
         const int rounds = (P.steps + P.wk - 1) / P.wk;   // a warp's steps of a side of a tile
         int64_t to_ask = left, to_do = left;              // tiles
         Aim aim;
         int ask_side = 0, ask_round = 0;
         auto take_aim = [&] { aim.at<NV>(P, ahead.e, ask_side, kSides, min(ahead.tile * wns + wn, P.rows16 - 1), lane); };
-        auto ask = [&](Item<NV> &it) {
+        const uint32_t slots = tc::smem_u32(ring) + warp * (kAhead * kSlot<NV>);
+        auto ask = [&](int slot) {   // the next step's weights; one group of copies a call
+            if (to_ask > 0) aim.load<NV>(P, slots + slot * kSlot<NV>, ask_round * P.wk + wk, lane);
+            asm volatile("cp.async.commit_group;" ::: "memory");
             if (to_ask == 0) return;
-            aim.load<NV>(P, it, ask_round * P.wk + wk, lane);
             if (++ask_round < rounds) return;
             ask_round = 0;
             if (kGlu && ask_side == 0) {
@@ -428,9 +463,7 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
             take_aim();
         };
         take_aim();
-        Item<NV> ring[kDepth];
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) ask(ring[d]);
+        for (int d = 0; d < kAhead; ++d) ask(d);
 
         float acc[kG][4] = {};
         const uint8_t *place_of[kG];
@@ -496,31 +529,29 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
             }
             buffer ^= 1;
         };
-        while (to_do > 0) {
+        for (int slot = 0; to_do > 0; slot = slot + 1 < kAhead ? slot + 1 : 0) {
+            if (staged != at.pass) stage();
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            const int step = round * P.wk + wk;
+            if (step < P.steps) {
+                const uint8_t *from[kG];
 #pragma unroll
-            for (int d = 0; d < kDepth; ++d) {
-                if (to_do == 0) break;
-                if (staged != at.pass) stage();
-                const int step = round * P.wk + wk;
-                if (step < P.steps) {
-                    const uint8_t *from[kG];
-#pragma unroll
-                    for (int q = 0; q < kG; ++q) from[q] = place_of[q] + step * kStepX;
-                    multiply<NV, kG, kPieces>(ring[d], acc, from, groups, piece_bytes, static_cast<int>(P.K) - step * kStep);
-                }
-                ask(ring[d]);
-                if (++round < rounds) continue;
-                round = 0;
-                hand_in();
-                if (kGlu && side == 0) {
-                    side = 1;
-                    continue;
-                }
-                side = 0;
-                finish();
-                if (--to_do > 0) at.next(P, sh);
+                for (int q = 0; q < kG; ++q) from[q] = place_of[q] + step * kStepX;
+                multiply<NV, kG, kPieces>(item_at<NV>(slots + slot * kSlot<NV>, lane), acc, from, groups, piece_bytes, static_cast<int>(P.K) - step * kStep);
             }
+            ask(slot);
+            if (++round < rounds) continue;
+            round = 0;
+            hand_in();
+            if (kGlu && side == 0) {
+                side = 1;
+                continue;
+            }
+            side = 0;
+            finish();
+            if (--to_do > 0) at.next(P, sh);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     // rows that no expert has
     const int64_t tail = sh.row0[P.E] * P.N;
@@ -550,10 +581,15 @@ int sm_count() {
     return known[dev];
 }
 
+// Shared memory but for x: sums and weights under way.
+template <bool NV, bool kGlu, int kG> constexpr int own_bytes() {
+    return 2 * kWarps * slab((kGlu ? 2 : 1) * kG) * static_cast<int>(sizeof(float)) + kWarps * kDepth<NV, kG> * kSlot<NV>;
+}
+
 template <bool NV, bool kGlu, int kG, int kPieces> gsa_status launch_gemv(const GemvParams &P, cudaStream_t s) {
     const int sms = sm_count();
     if (!sms) return cuda_error();
-    const int smem = P.pass_rows * P.pitch * kPieces + 2 * kWarps * slab((kGlu ? 2 : 1) * kG) * static_cast<int>(sizeof(float));
+    const int smem = P.pass_rows * P.pitch * kPieces + own_bytes<NV, kGlu, kG>();
     auto kernel = gemv<NV, kGlu, kG, kPieces>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return cuda_error();
     cudaLaunchConfig_t cfg = {};
@@ -576,7 +612,7 @@ gsa_status run_gemv(GemvParams &P, bool glu, const void *x, int32_t x_dtype, con
     if (!known_type(x_dtype) || !known_type(out_dtype) || (b_groups != 1 && b_groups != 2)) return GSA_ERR_INVALID_ARG;
     const bool nv = recipe_kind == GSA_NVFP4;
     const int64_t sides = glu ? 2 : 1;
-    if (E > kMaxE || K % 64 != 0 || K > kMaxK || M >= (int64_t(1) << 31) - 256 || N >= (int64_t(1) << 30) / E - 256) return GSA_ERR_UNSUPPORTED;
+    if (E > kMaxE || K % 64 != 0 || K > (x_dtype == GSA_FP32 ? kMaxK / 2 : kMaxK) || M >= (int64_t(1) << 31) - 256 || N >= (int64_t(1) << 30) / E - 256) return GSA_ERR_UNSUPPORTED;
     if (glu && b_groups == 1 && N % 128 != 0) return GSA_ERR_UNSUPPORTED;
     if (M == 0) return GSA_OK;
     if (!x || !b->data || !b->scale || !out || (!split && E != 1) || (nv && !b->amax)) return GSA_ERR_INVALID_ARG;
@@ -612,18 +648,27 @@ gsa_status run_gemv(GemvParams &P, bool glu, const void *x, int32_t x_dtype, con
     P.tiles = (P.rows16 + wns - 1) / wns;
     P.pitch = P.steps * kStepX + 64;   // rows on alternating halves of the banks
     const int pieces = x_dtype == GSA_FP32 ? 2 : 1;
-    int64_t rows = kSpace / (P.pitch * pieces);
-    if (rows > kMaxRows) rows = kMaxRows;
-    if (rows > 8) rows = rows / 8 * 8;
+    auto space = [&](int groups) {   // of x, with 8 rows or 16 a pass
+        auto own = [&](auto fmt, auto gated) {
+            constexpr bool NV = decltype(fmt)::value, kGlu = decltype(gated)::value;
+            return groups == 1 ? own_bytes<NV, kGlu, 1>() : own_bytes<NV, kGlu, 2>();
+        };
+        return kSpace - (nv ? (glu ? own(std::true_type(), std::true_type()) : own(std::true_type(), std::false_type()))
+                            : (glu ? own(std::false_type(), std::true_type()) : own(std::false_type(), std::false_type())));
+    };
+    int64_t rows = space(2) / (P.pitch * pieces);
+    int groups = 2;
+    if (M <= 8 || rows <= 8) rows = space(groups = 1) / (P.pitch * pieces);
+    if (rows > 8 * groups) rows = 8 * groups;
     P.pass_rows = static_cast<int>(rows < M ? rows : M);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    auto go = [&](auto fmt, auto gated, auto groups) {
+    auto go = [&](auto fmt, auto gated, auto many) {
         constexpr bool NV = decltype(fmt)::value, kGlu = decltype(gated)::value;
-        constexpr int kG = decltype(groups)::value;
+        constexpr int kG = decltype(many)::value;
         return pieces == 2 ? launch_gemv<NV, kGlu, kG, 2>(P, s) : launch_gemv<NV, kGlu, kG, 1>(P, s);
     };
     auto grouped = [&](auto fmt, auto gated) {
-        return P.pass_rows <= 8 ? go(fmt, gated, std::integral_constant<int, 1>()) : go(fmt, gated, std::integral_constant<int, kMaxRows / 8>());
+        return groups == 1 ? go(fmt, gated, std::integral_constant<int, 1>()) : go(fmt, gated, std::integral_constant<int, 2>());
     };
     auto sided = [&](auto fmt) { return glu ? grouped(fmt, std::true_type()) : grouped(fmt, std::false_type()); };
     return nv ? sided(std::true_type()) : sided(std::false_type());
