@@ -58,8 +58,10 @@ struct GemvParams {
     glu::Act act;
 };
 
-// A warp's sums of `n` groups of 128.  Two floats more, so that four slabs further on lie eight banks on.
-__host__ __device__ constexpr int slab(int n) { return 128 * n + 2; }
+// A warp's sums: `n` groups of 8 rows of x, 16 weight rows each, 20 floats apart (the lanes' values of a product then meet no
+// bank twice); two floats more, so that four slabs further on lie eight banks on.
+constexpr int kRowSums = 20, kGroupSums = 8 * kRowSums;
+__host__ __device__ constexpr int slab(int n) { return kGroupSums * n + 2; }
 
 struct Shared {
     int row0[kMaxE + 1];     // first row of each expert
@@ -107,28 +109,34 @@ __device__ __forceinline__ void put(void *p, int type, int64_t i, float v) {
 
 // -------------------------------------------------------------- rows of x
 
-// Eight consecutive values (i a multiple of 8) in FP32.
-__device__ __forceinline__ void load8(const void *x, int type, int64_t i, float (&v)[8]) {
-    if (type == GSA_FP32) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i));
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i + 4));
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        return;
-    }
-    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight consecutive values (i a multiple of 8), and what they are in FP32.
+template <int kPieces> struct Raw {   // 2: FP32
+    uint4 r[kPieces];
+    __device__ __forceinline__ void load(const void *x, int64_t i) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(x) + i * (2 * kPieces));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (type == GSA_BF16) {
-            v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        } else {
-            __half2 h;
-            memcpy(&h, &w[j], 4);
-            const float2 f = __half22float2(h);
-            v[2 * j] = f.x, v[2 * j + 1] = f.y;
+        for (int k = 0; k < kPieces; ++k) r[k] = __ldg(p + k);
+    }
+    __device__ __forceinline__ void values(bool bf16, float (&v)[8]) const {
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (kPieces == 2) {
+                    v[4 * k + j] = __uint_as_float(w[j]);
+                } else if (bf16) {
+                    v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                } else {
+                    __half2 h;
+                    memcpy(&h, &w[j], 4);
+                    const float2 f = __half22float2(h);
+                    v[2 * j] = f.x, v[2 * j + 1] = f.y;
+                }
+            }
         }
     }
-}
+};
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
@@ -154,17 +162,25 @@ template <bool NV, int kPieces> __device__ void stage_rows(const GemvParams &P, 
     if (threadIdx.x < kMaxRows) sh.largest[threadIdx.x] = 0;
     __syncthreads();   // also: nobody reads the rows before any more
     if (threadIdx.x < sides) sh.unit[threadIdx.x] = unit;
+    const bool bf16 = P.x_type == GSA_BF16;
+    const int live = static_cast<int>(P.K) / 8;
+    constexpr int kBatch = 4;   // words asked for at once
     if (P.x_type != GSA_FP16) {
         uint32_t most = 0;
         if (row < rows)
-            for (int c = t; c < words; c += threads) {
-                if (8 * c >= P.K) break;
-                float v[8];
-                load8(P.x, P.x_type, at + 8 * c, v);
+            for (int c0 = t; c0 < live; c0 += kBatch * threads) {
+                Raw<kPieces> raw[kBatch];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-                    if (a < 0x7F800000u && a > most) most = a;
+                for (int b = 0; b < kBatch; ++b) raw[b].load(P.x, at + 8 * static_cast<int64_t>(min(c0 + b * threads, live - 1)));
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    float v[8];
+                    raw[b].values(bf16, v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+                        if (a < 0x7F800000u && a > most) most = a;
+                    }
                 }
             }
 #pragma unroll
@@ -185,23 +201,31 @@ template <bool NV, int kPieces> __device__ void stage_rows(const GemvParams &P, 
             sh.unscale[row] = 1.0f;
         }
         if (t == 0) sh.probs[row] = P.probs ? P.probs[r0 + row] : 1.0f;
-        for (int c = t; c < words; c += threads) {
-            float v[8] = {};
-            if (8 * c < P.K) load8(P.x, P.x_type, at + 8 * c, v);
-            uint32_t hi[4], lo[4];
+        for (int c0 = t; c0 < words; c0 += kBatch * threads) {
+            Raw<kPieces> raw[kBatch];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float a = v[2 * j] * scale, b = v[2 * j + 1] * scale;
-                hi[j] = half2_bits(a, b);
-                if (kPieces == 2) {
-                    const float ha = __half2float(__float2half_rn(a)), hb = __half2float(__float2half_rn(b));
-                    // an infinite value's rest would be NaN
-                    lo[j] = half2_bits(fabsf(a) <= 65504.0f ? a - ha : 0.0f, fabsf(b) <= 65504.0f ? b - hb : 0.0f);
+            for (int b = 0; b < kBatch; ++b) raw[b].load(P.x, at + 8 * static_cast<int64_t>(min(c0 + b * threads, live - 1)));
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int c = c0 + b * threads;
+                if (c >= words) break;
+                float v[8];
+                raw[b].values(bf16, v);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = c < live ? v[2 * j] * scale : 0.0f, q = c < live ? v[2 * j + 1] * scale : 0.0f;
+                    hi[j] = half2_bits(p, q);
+                    if (kPieces == 2) {
+                        const float hp = __half2float(__float2half_rn(p)), hq = __half2float(__float2half_rn(q));
+                        // an infinite value's rest would be NaN
+                        lo[j] = half2_bits(fabsf(p) <= 65504.0f ? p - hp : 0.0f, fabsf(q) <= 65504.0f ? q - hq : 0.0f);
+                    }
                 }
+                uint8_t *to = xs + row * P.pitch + place<NV>(8 * c);
+                *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if (kPieces == 2) *reinterpret_cast<uint4 *>(to + P.pass_rows * P.pitch) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
-            uint8_t *to = xs + row * P.pitch + place<NV>(8 * c);
-            *reinterpret_cast<uint4 *>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if (kPieces == 2) *reinterpret_cast<uint4 *>(to + P.pass_rows * P.pitch) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
     }
     __syncthreads();
@@ -220,69 +244,74 @@ template <> struct Item<false> {   // 8 codes of each of 4 blocks, and their sca
     uint32_t sa, sb;
 };
 
-// Weights on their way: each warp has kDepth steps in shared memory, where a lane's copies are its own, so that nothing but
-// its own copies' arrival is waited for.  (In registers, slots of several steps share the few scoreboards, and any use waits
-// for the newest load: @@ us instead of @@.)  Words of 16 (or 8) and 4 bytes, 32 lanes side by side.
-template <bool NV> constexpr int kSlot = 32 * (NV ? 40 : 72);
+// Weights on their way: each warp has kDepth steps in shared memory.  (In registers, slots of several steps share the few
+// scoreboards, and any use waits for the newest load: 55 us where this took 41, 32 rows over 128 experts, 2048 x 4096 NVFP4.)
+// Copies are 16 bytes, of whole lines where a weight row has them.  A slot:
+//   NVFP4: rows a, rows b (32 lanes x 16 bytes each), scales of two tiles (4 rows x 4 quarters x 4, twice);
+//   MXFP8: 16 rows of 128 bytes, whose four blocks are swapped by row (two rows of four lanes then meet no bank twice), scales.
+template <bool NV> constexpr int kSlot = NV ? 1024 + 128 : 2048 + 64;
 template <bool NV, int kG> constexpr int kDepth = NV ? (kG == 1 ? 6 : 4) : (kG == 1 ? 3 : 2);
 
-template <int kBytes> __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
-    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+
+__device__ __forceinline__ uint32_t block_at(int row, int block) { return row * 128 + ((block ^ (row & 3)) << 5); }
 
 template <bool NV> __device__ __forceinline__ Item<NV> item_at(uint32_t slot, int lane) {
     Item<NV> it;
+    const int g = lane >> 2, t = lane & 3, word = 16 * (g & 3) + 4 * (g >> 2);
     if constexpr (NV) {
         it.a = tc::ld_shared(slot + 16 * lane);
         it.b = tc::ld_shared(slot + 512 + 16 * lane);
-        it.sa = __float_as_uint(tc::ld_shared1(slot + 1024 + 4 * lane)) >> (lane & 1 ? 16 : 0);
-        it.sb = __float_as_uint(tc::ld_shared1(slot + 1152 + 4 * lane)) >> (lane & 1 ? 16 : 0);
+        const uint32_t s = slot + 1024 + 64 * (t >> 1) + word;
+        it.sa = __float_as_uint(tc::ld_shared1(s)) >> (16 * (t & 1));
+        it.sb = __float_as_uint(tc::ld_shared1(s + 8)) >> (16 * (t & 1));
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(it.a[j].x), "=r"(it.a[j].y) : "r"(slot + 512 * j + 8 * lane) : "memory");
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(it.b[j].x), "=r"(it.b[j].y) : "r"(slot + 512 * j + 256 + 8 * lane) : "memory");
+            const uint32_t c = slot + block_at(g, j) + 8 * t;   // (row g + 8 is swapped alike)
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(it.a[j].x), "=r"(it.a[j].y) : "r"(c) : "memory");
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(it.b[j].x), "=r"(it.b[j].y) : "r"(c + 8 * 128) : "memory");
         }
-        it.sa = __float_as_uint(tc::ld_shared1(slot + 2048 + 4 * lane));
-        it.sb = __float_as_uint(tc::ld_shared1(slot + 2176 + 4 * lane));
+        it.sa = __float_as_uint(tc::ld_shared1(slot + 2048 + word));
+        it.sb = __float_as_uint(tc::ld_shared1(slot + 2048 + word + 8));
     }
     return it;
 }
 
-// Where a lane reads one side of a tile.  The tile i of 16 weight rows holds rows 4 (i mod 8) .. + 3 of each quarter of scale
-// tile i / 8, whose scales are 64 bytes in a row.  Nothing is predicated: rows past the last read the last (their results are
-// not stored), and what lies past the end of k reads the step's first half again (x is zero there).
-struct Aim {
-    const uint8_t *a, *b, *s;
-    template <bool NV> __device__ __forceinline__ void at(const GemvParams &P, int e, int side, int sides, int i, int lane) {
-        const int g = lane >> 2;
-        const int inside = 4 * (i & 7) + (g & 3), row = 128 * (i >> 3) + inside + 32 * (g >> 2), last = static_cast<int>(P.N) - 1;
+// Where a lane copies one side of a tile from.  The tile i of 16 weight rows holds rows 4 (i mod 8) .. + 3 of each quarter of
+// scale tile i / 8 (row r of the tile: r mod 4 of quarter r / 4), whose scales are 64 bytes in a row.  Nothing is predicated:
+// rows past the last read the last (their results are not stored), and what lies past the end of k reads the step's first half
+// again (x is zero there).
+template <bool NV> struct Aim {
+    const uint8_t *row[NV ? 2 : 4], *s;
+    __device__ __forceinline__ void at(const GemvParams &P, int e, int side, int sides, int i, int lane) {
+        const int last = static_cast<int>(P.N) - 1, inside = 128 * (i >> 3) + 4 * (i & 7);
         const int64_t pitch = NV ? P.K / 2 : P.K, first = static_cast<int64_t>(e * sides + side) * P.N;
-        a = P.codes + (first + min(row, last)) * pitch;
-        b = P.codes + (first + min(row + 64, last)) * pitch;
-        s = P.scales + static_cast<int64_t>(e * P.scale_rows + side * P.up_tiles + (i >> 3)) * P.scale_cols * kScaleTile + 16 * inside + 4 * (g >> 2);
+#pragma unroll
+        for (int k = 0; k < (NV ? 2 : 4); ++k) {   // NVFP4: four lanes a row, rows g and g + 8; MXFP8: eight, rows lane / 8 + 4 k
+            const int r = NV ? (lane >> 2) + 8 * k : (lane >> 3) + 4 * k;
+            row[k] = P.codes + (first + min(inside + (r & 3) + 32 * (r >> 2), last)) * pitch;
+        }
+        s = P.scales + static_cast<int64_t>(e * P.scale_rows + side * P.up_tiles + (i >> 3)) * P.scale_cols * kScaleTile +
+            16 * (4 * (i & 7) + (lane & 3));
     }
-    template <bool NV> __device__ __forceinline__ void load(const GemvParams &P, uint32_t slot, int step, int lane) const {
-        const int t = lane & 3, K = static_cast<int>(P.K);
+    __device__ __forceinline__ void load(const GemvParams &P, uint32_t slot, int step, int lane) const {
+        const int K = static_cast<int>(P.K);
         if constexpr (NV) {
+            const int t = lane & 3;
             const uint32_t c = min(step * (kStep / 2) + 16 * t, K / 2 - 32 + 16 * (t & 1));
-            const uint32_t q = min(2 * step + (t >> 1), K / 64 - 1) * kScaleTile;
-            copy_async<16>(slot + 16 * lane, a + c);
-            copy_async<16>(slot + 512 + 16 * lane, b + c);
-            copy_async<4>(slot + 1024 + 4 * lane, s + q);
-            copy_async<4>(slot + 1152 + 4 * lane, s + q + 8);
+            copy_async(slot + 16 * lane, row[0] + c);
+            copy_async(slot + 512 + 16 * lane, row[1] + c);
+            if (lane < 8) copy_async(slot + 1024 + 16 * lane, s + min(2 * step + (lane >> 2), K / 64 - 1) * kScaleTile);
         } else {
             step = min(step, P.steps - 1);
-            const uint32_t c = step * kStep + 8 * t, half = c + 64 < K ? 64 : 0, q = step * kScaleTile;
+            const int c8 = lane & 7;
+            const uint32_t c = step * kStep + 16 * c8, from = c < K ? c : c - 64;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t from = c + 32 * (j & 1) + (j & 2 ? half : 0);
-                copy_async<8>(slot + 512 * j + 8 * lane, a + from);
-                copy_async<8>(slot + 512 * j + 256 + 8 * lane, b + from);
-            }
-            copy_async<4>(slot + 2048 + 4 * lane, s + q);
-            copy_async<4>(slot + 2176 + 4 * lane, s + q + 8);
+            for (int k = 0; k < 4; ++k) copy_async(slot + block_at((lane >> 3) + 4 * k, c8 >> 1) + 16 * (c8 & 1), row[k] + from);
+            if (lane < 4) copy_async(slot + 2048 + 16 * lane, s + step * kScaleTile);
         }
     }
 };
@@ -345,17 +374,17 @@ __device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4]
 #pragma unroll
         for (int q = 0; q < kG; ++q) {
             if (q >= groups) break;
-            float d[4] = {};
+            float d[2][4] = {};   // two chains: a product waits for the one before it in its chain
 #pragma unroll
             for (int p = 0; p < kPieces; ++p)
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
                     const uint4 b = *reinterpret_cast<const uint4 *>(xs[q] + p * piece_bytes + 64 * jj);
-                    mma(d, A[2 * jj], b.x, b.y);
-                    mma(d, A[2 * jj + 1], b.z, b.w);
+                    mma(d[0], A[2 * jj], b.x, b.y);
+                    mma(d[1], A[2 * jj + 1], b.z, b.w);
                 }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[q][i] += d[i];
+            for (int i = 0; i < 4; ++i) acc[q][i] += d[0][i] + d[1][i];
         }
     } else {
         const uint32_t keep = left > 64 ? 0xFFFFFFFFu : 0xFFFFu;   // K is a multiple of 64
@@ -433,22 +462,25 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         return;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wk = warp & (P.wk - 1), wn = warp / P.wk, wns = kWarps / P.wk;
+    // the block's run of tiles: `all` in equal parts, the first `more` one longer
     const int64_t all = static_cast<int64_t>(sh.pass0[P.E]) * P.tiles;
-    const int64_t first = all * blockIdx.x / gridDim.x, left = all * (blockIdx.x + 1) / gridDim.x - first;
+    const bool small = all >> 32 == 0;   // divisions of 64 bits take hundreds of cycles
+    const int64_t part = small ? static_cast<uint32_t>(all) / gridDim.x : all / gridDim.x, more = all - part * gridDim.x;
+    const int64_t first = part * blockIdx.x + (blockIdx.x < more ? blockIdx.x : more), left = part + (blockIdx.x < more);
     if (left > 0) {
         Cursor ahead;   // of the loads
-        ahead.pass = static_cast<int>(first / P.tiles);
+        ahead.pass = static_cast<int>(small ? static_cast<uint32_t>(first) / static_cast<uint32_t>(P.tiles) : first / P.tiles);
         ahead.tile = static_cast<int>(first - static_cast<int64_t>(ahead.pass) * P.tiles);
         ahead.find(P, sh);
         Cursor at = ahead;
         const int rounds = (P.steps + P.wk - 1) / P.wk;   // a warp's steps of a side of a tile
         int64_t to_ask = left, to_do = left;              // tiles
-        Aim aim;
+        Aim<NV> aim;
         int ask_side = 0, ask_round = 0;
-        auto take_aim = [&] { aim.at<NV>(P, ahead.e, ask_side, kSides, min(ahead.tile * wns + wn, P.rows16 - 1), lane); };
+        auto take_aim = [&] { aim.at(P, ahead.e, ask_side, kSides, min(ahead.tile * wns + wn, P.rows16 - 1), lane); };
         const uint32_t slots = tc::smem_u32(ring) + warp * (kAhead * kSlot<NV>);
         auto ask = [&](int slot) {   // the next step's weights; one group of copies a call
-            if (to_ask > 0) aim.load<NV>(P, slots + slot * kSlot<NV>, ask_round * P.wk + wk, lane);
+            if (to_ask > 0) aim.load(P, slots + slot * kSlot<NV>, ask_round * P.wk + wk, lane);
             asm volatile("cp.async.commit_group;" ::: "memory");
             if (to_ask == 0) return;
             if (++ask_round < rounds) return;
@@ -468,7 +500,7 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         float acc[kG][4] = {};
         const uint8_t *place_of[kG];
         const int piece_bytes = P.pass_rows * P.pitch;
-        const int parts = min(4, P.wk), parts_log = parts >> 1, each = P.wk / parts;
+        const int parts = min(4, P.wk), parts_log = parts >> 1, each = P.wk / parts, wns_log = 31 - __clz(wns);
         int staged = -1, rows = 0, groups = 0, r0 = 0, side = 0, round = 0, buffer = 0;
         auto stage = [&] {
             staged = at.pass;
@@ -485,43 +517,45 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         };
         // A warp's sums of a side of the tile to shared memory.
         auto hand_in = [&] {
-            float *mine = sums + (buffer * kWarps + warp) * kSlab + side * kG * 128;
+            float *mine = sums + (buffer * kWarps + warp) * kSlab + side * kG * kGroupSums + 2 * (lane & 3) * kRowSums + (lane >> 2);
 #pragma unroll
             for (int q = 0; q < kG; ++q) {
                 if (q >= groups) break;
-                float2 *to = reinterpret_cast<float2 *>(mine + q * 128);
-                to[lane] = make_float2(acc[q][0], acc[q][1]);
-                to[32 + lane] = make_float2(acc[q][2], acc[q][3]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[q][k] = 0.0f;
+                for (int k = 0; k < 4; ++k) {
+                    mine[q * kGroupSums + (k & 1) * kRowSums + (k >> 1) * 8] = acc[q][k];
+                    acc[q][k] = 0.0f;
+                }
             }
         };
-        // The tile's sums over the warps, and its results.
+        // The tile's sums over the warps, and its results: up to four lanes a result, up to four warps' sums each, first one after
+        // the other, then across the lanes.
         auto finish = [&] {
             __syncthreads();
-            // up to four lanes a result, up to four warps' sums each: first one after the other, then across the lanes
-            const int part = threadIdx.x & (parts - 1);
-            for (int base = 0; base < wns * groups * 128 * parts; base += kThreads) {
-                const int o = (base + static_cast<int>(threadIdx.x)) >> parts_log;
-                const int j = o & 7, a = (o >> 3) & 15, q = (o >> 7) & (groups - 1), b = (o >> 7) >> (groups - 1);   // row of x, weight row, group, warp row
-                const float *from = sums + (buffer * kWarps + min(b, wns - 1) * P.wk + part * each) * kSlab + q * 128 + a * 8 + j;
+            const int part = threadIdx.x & (parts - 1), total = (16 * wns * rows) << parts_log;
+            for (int base = 0; base < total; base += kThreads) {
+                const int x = base + static_cast<int>(threadIdx.x), o = x >> parts_log;
+                const int a = o & 15, b = (o >> 4) & (wns - 1), r = (o >> 4) >> wns_log;   // weight row, warp row, row of x
+                const bool on = x < total;
+                const float *from = sums + (buffer * kWarps + b * P.wk + part * each) * kSlab + (on ? r >> 3 : 0) * kGroupSums + (r & 7) * kRowSums + a;
                 float v[kSides];
 #pragma unroll
                 for (int s = 0; s < kSides; ++s) {
                     v[s] = 0.0f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (k < each) v[s] += from[s * kG * 128 + k * kSlab];
+                        if (k < each) v[s] += from[s * kG * kGroupSums + k * kSlab];
                 }
+                if (parts > 1) {
 #pragma unroll
-                for (int d = 1; d < 4; d <<= 1)
-                    if (d < parts) {
+                    for (int s = 0; s < kSides; ++s) v[s] += __shfl_xor_sync(0xFFFFFFFFu, v[s], 1);
+                }
+                if (parts > 2) {
 #pragma unroll
-                        for (int s = 0; s < kSides; ++s) v[s] += __shfl_xor_sync(0xFFFFFFFFu, v[s], d);
-                    }
-                const int i = at.tile * wns + b, r = 8 * q + j;
-                const int n = 128 * (i >> 3) + 4 * (i & 7) + (a & 3) + 32 * (a >> 2);
-                if (part != 0 || b >= wns || r >= rows || i >= P.rows16 || n >= P.N) continue;
+                    for (int s = 0; s < kSides; ++s) v[s] += __shfl_xor_sync(0xFFFFFFFFu, v[s], 2);
+                }
+                const int i = at.tile * wns + b, n = 128 * (i >> 3) + 4 * (i & 7) + (a & 3) + 32 * (a >> 2);
+                if (part != 0 || !on || i >= P.rows16 || n >= P.N) continue;
                 const float unscale = sh.unscale[r];
                 float y = scaled(v[0], sh.unit[0], unscale);
                 if constexpr (kGlu) y = sh.probs[r] * gated(P.act, y, scaled(v[kSides - 1], sh.unit[1], unscale));
@@ -532,6 +566,7 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         for (int slot = 0; to_do > 0; slot = slot + 1 < kAhead ? slot + 1 : 0) {
             if (staged != at.pass) stage();
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            __syncwarp();   // the other lanes' copies
             const int step = round * P.wk + wk;
             if (step < P.steps) {
                 const uint8_t *from[kG];
@@ -539,6 +574,7 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
                 for (int q = 0; q < kG; ++q) from[q] = place_of[q] + step * kStepX;
                 multiply<NV, kG, kPieces>(item_at<NV>(slots + slot * kSlot<NV>, lane), acc, from, groups, piece_bytes, static_cast<int>(P.K) - step * kStep);
             }
+            __syncwarp();   // all lanes have what the slot held
             ask(slot);
             if (++round < rounds) continue;
             round = 0;
