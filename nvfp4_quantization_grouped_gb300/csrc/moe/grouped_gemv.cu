@@ -12,7 +12,7 @@
 // applied to the block's sums in FP32.  x is brought to FP16 too: scaled by a power of two to
 // [2^14, 2^15), FP32 rows as the sum of two.
 //   A block holds the rows of x of one expert in shared memory (up to 16, a pass) and walks
-// a run of tiles of 16 weight rows, its 16 warps sharing out the steps of 128 k of each; their
+// a run of tiles of 16 weight rows, its 16 warps sharing out the steps of 128 bytes of each; their
 // sums meet in shared memory.  Loads run kDepth steps ahead, over the ends of tiles, passes and
 // experts.  How a sum is split goes by K alone: a row's result has the same bits whatever rows it
 // comes with.
@@ -33,8 +33,7 @@
 namespace {
 
 constexpr int kMaxE = 256, kWarps = 16, kThreads = 32 * kWarps, kScaleTile = 512;
-constexpr int kStep = 128;                  // k of a step
-constexpr int kStepX = kStep * 2;           // bytes of a step of a row of x in shared memory
+template <bool NV> constexpr int kStep = NV ? 256 : 128;   // k of a step: 128 bytes of a weight row
 constexpr int kMaxRows = 16;                // rows of x a pass
 constexpr int kSpace = (227 - 3) * 1024;    // bytes that a block has beside its static ones
 constexpr int64_t kMaxK = 32768;            // a row of x beside the rest (FP32: half of it)
@@ -49,6 +48,7 @@ struct GemvParams {
     uint32_t *status;
     int64_t M, N, K;
     int E, x_type, out_type;
+    int row_bytes;          // of a weight row's codes
     int scale_cols, scale_rows, up_tiles;   // scale tiles along k; of an expert along its rows; from a gate row to its linear row
     int b_groups;
     int steps, wk;          // steps of k; warps that share them out (a power of two)
@@ -146,18 +146,18 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
 }
 
 // Where the eight values from k on (a multiple of 8) lie in a row: in order (MXFP8: a lane's eight codes of a block of 32
-// meet them in one 16-byte load), or with the 16-byte words of a step transposed, 4 x 4 (NVFP4: a lane has 32 codes in a
+// meet them in one 16-byte load), or with the 16-byte words of 128 values transposed, 4 x 4 (NVFP4: a lane has 32 codes in a
 // row, and the four lanes of a weight row meet the words jj of theirs at once).
 template <bool NV> __device__ __forceinline__ int place(int k) {
-    const int step = k / kStep, c = k % kStep / 8;
-    return step * kStepX + 16 * (NV ? (c & 3) * 4 + (c >> 2) : c);
+    const int c = k % 128 / 8;
+    return k / 128 * 256 + 16 * (NV ? (c & 3) * 4 + (c >> 2) : c);
 }
 
 // Rows r0 .. r0 + rows of x to shared memory (kPieces 2: the FP16 halves of FP32 values, `rows` rows apart); every thread.
 template <bool NV, int kPieces> __device__ void stage_rows(const GemvParams &P, Shared &sh, uint8_t *xs, int r0, int rows, float unit, int sides) {
     int threads = kThreads;   // a row: whole warps
     for (int r = 1; r < rows; r *= 2) threads /= 2;
-    const int row = threadIdx.x / threads, t = threadIdx.x % threads, words = P.steps * (kStep / 8);
+    const int row = threadIdx.x / threads, t = threadIdx.x % threads, words = P.steps * (kStep<NV> / 8);
     const int64_t at = (r0 + static_cast<int64_t>(row)) * P.K;
     if (threadIdx.x < kMaxRows) sh.largest[threadIdx.x] = 0;
     __syncthreads();   // also: nobody reads the rows before any more
@@ -233,9 +233,9 @@ template <bool NV, int kPieces> __device__ void stage_rows(const GemvParams &P, 
 
 // ---------------------------------------------------------------- weights
 
-// A lane's part of a step: weight rows a (its low row of the tile) and b = a + 64.
+// A lane's part of 128 k (a step, NVFP4: half of one): weight rows a (its low row of the tile) and b.
 template <bool NV> struct Item;
-template <> struct Item<true> {    // 32 codes of each row, and words of scales, 2 of which are theirs
+template <> struct Item<true> {    // 32 codes of each row, and their scales (two, in the low half)
     uint4 a, b;
     uint32_t sa, sb;
 };
@@ -246,31 +246,32 @@ template <> struct Item<false> {   // 8 codes of each of 4 blocks, and their sca
 
 // Weights on their way: each warp has kDepth steps in shared memory.  (In registers, slots of several steps share the few
 // scoreboards, and any use waits for the newest load: 55 us where this took 41, 32 rows over 128 experts, 2048 x 4096 NVFP4.)
-// Copies are 16 bytes, of whole lines where a weight row has them.  A slot:
-//   NVFP4: rows a, rows b (32 lanes x 16 bytes each), scales of two tiles (4 rows x 4 quarters x 4, twice);
-//   MXFP8: 16 rows of 128 bytes, whose four blocks are swapped by row (two rows of four lanes then meet no bank twice), scales.
-template <bool NV> constexpr int kSlot = NV ? 1024 + 128 : 2048 + 64;
-template <bool NV, int kG> constexpr int kDepth = NV ? (kG == 1 ? 6 : 4) : (kG == 1 ? 3 : 2);
+// Copies are 16 bytes, eight lanes a row.  A slot has the 16 rows' 128 bytes, with their halves (NVFP4) or their four blocks
+// (MXFP8) swapped by row, so that the lanes of a load meet no bank twice, and the scales: 64 bytes a scale tile (4 rows of 4
+// quarters of 4), four of them or one.
+template <bool NV> constexpr int kSlot = 2048 + (NV ? 256 : 64);
+template <int kG> constexpr int kDepth = kG == 1 ? 3 : 2;
 
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ uint32_t block_at(int row, int block) { return row * 128 + ((block ^ (row & 3)) << 5); }
+// 16-byte word c of row r of a slot.
+template <bool NV> __device__ __forceinline__ uint32_t word_at(int r, int c) { return r * 128 + 16 * (NV ? c ^ (4 * (r & 1)) : c ^ (2 * (r & 3))); }
 
-template <bool NV> __device__ __forceinline__ Item<NV> item_at(uint32_t slot, int lane) {
+template <bool NV> __device__ __forceinline__ Item<NV> item_at(uint32_t slot, int half, int lane) {
     Item<NV> it;
     const int g = lane >> 2, t = lane & 3, word = 16 * (g & 3) + 4 * (g >> 2);
     if constexpr (NV) {
-        it.a = tc::ld_shared(slot + 16 * lane);
-        it.b = tc::ld_shared(slot + 512 + 16 * lane);
-        const uint32_t s = slot + 1024 + 64 * (t >> 1) + word;
+        const uint32_t c = slot + word_at<NV>(g, 4 * half + t), s = slot + 2048 + 64 * (2 * half + (t >> 1)) + word;
+        it.a = tc::ld_shared(c);
+        it.b = tc::ld_shared(c + 8 * 128);   // row g + 8 is swapped alike
         it.sa = __float_as_uint(tc::ld_shared1(s)) >> (16 * (t & 1));
         it.sb = __float_as_uint(tc::ld_shared1(s + 8)) >> (16 * (t & 1));
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t c = slot + block_at(g, j) + 8 * t;   // (row g + 8 is swapped alike)
+            const uint32_t c = slot + word_at<NV>(g, 2 * j) + 8 * t;
             asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(it.a[j].x), "=r"(it.a[j].y) : "r"(c) : "memory");
             asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(it.b[j].x), "=r"(it.b[j].y) : "r"(c + 8 * 128) : "memory");
         }
@@ -281,38 +282,26 @@ template <bool NV> __device__ __forceinline__ Item<NV> item_at(uint32_t slot, in
 }
 
 // Where a lane copies one side of a tile from.  The tile i of 16 weight rows holds rows 4 (i mod 8) .. + 3 of each quarter of
-// scale tile i / 8 (row r of the tile: r mod 4 of quarter r / 4), whose scales are 64 bytes in a row.  Nothing is predicated:
-// rows past the last read the last (their results are not stored), and what lies past the end of k reads the step's first half
-// again (x is zero there).
+// scale tile i / 8 (row r of the tile: r mod 4 of quarter r / 4), whose scales are 64 bytes in a row.  A lane has 16 bytes of
+// four rows, one of each quarter.  Nothing is predicated: rows past the last read the last (their results are not stored), and
+// what lies past the end of k reads the row's last word again (x is zero there).
 template <bool NV> struct Aim {
-    const uint8_t *row[NV ? 2 : 4], *s;
+    const uint8_t *row[4], *s;
     __device__ __forceinline__ void at(const GemvParams &P, int e, int side, int sides, int i, int lane) {
-        const int last = static_cast<int>(P.N) - 1, inside = 128 * (i >> 3) + 4 * (i & 7);
-        const int64_t pitch = NV ? P.K / 2 : P.K, first = static_cast<int64_t>(e * sides + side) * P.N;
+        const int last = static_cast<int>(P.N) - 1, inside = 128 * (i >> 3) + 4 * (i & 7) + (lane >> 3);
+        const int64_t pitch = NV ? P.K / 2 : P.K;
+        const uint8_t *first = P.codes + static_cast<int64_t>(e * sides + side) * P.N * pitch;
 #pragma unroll
-        for (int k = 0; k < (NV ? 2 : 4); ++k) {   // NVFP4: four lanes a row, rows g and g + 8; MXFP8: eight, rows lane / 8 + 4 k
-            const int r = NV ? (lane >> 2) + 8 * k : (lane >> 3) + 4 * k;
-            row[k] = P.codes + (first + min(inside + (r & 3) + 32 * (r >> 2), last)) * pitch;
-        }
+        for (int k = 0; k < 4; ++k) row[k] = first + min(inside + 32 * k, last) * pitch;
         s = P.scales + static_cast<int64_t>(e * P.scale_rows + side * P.up_tiles + (i >> 3)) * P.scale_cols * kScaleTile +
             16 * (4 * (i & 7) + (lane & 3));
     }
     __device__ __forceinline__ void load(const GemvParams &P, uint32_t slot, int step, int lane) const {
-        const int K = static_cast<int>(P.K);
-        if constexpr (NV) {
-            const int t = lane & 3;
-            const uint32_t c = min(step * (kStep / 2) + 16 * t, K / 2 - 32 + 16 * (t & 1));
-            copy_async(slot + 16 * lane, row[0] + c);
-            copy_async(slot + 512 + 16 * lane, row[1] + c);
-            if (lane < 8) copy_async(slot + 1024 + 16 * lane, s + min(2 * step + (lane >> 2), K / 64 - 1) * kScaleTile);
-        } else {
-            step = min(step, P.steps - 1);
-            const int c8 = lane & 7;
-            const uint32_t c = step * kStep + 16 * c8, from = c < K ? c : c - 64;
+        const uint32_t c = min(step * 128 + 16 * (lane & 7), P.row_bytes - 16);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) copy_async(slot + block_at((lane >> 3) + 4 * k, c8 >> 1) + 16 * (c8 & 1), row[k] + from);
-            if (lane < 4) copy_async(slot + 2048 + 16 * lane, s + step * kScaleTile);
-        }
+        for (int k = 0; k < 4; ++k) copy_async(slot + word_at<NV>((lane >> 3) + 4 * k, lane & 7), row[k] + c);
+        const int tile = NV ? 4 * step + (lane >> 2) : step;
+        if (lane < (NV ? 16 : 4)) copy_async(slot + 2048 + 16 * lane, s + min(tile, P.scale_cols - 1) * kScaleTile);
     }
 };
 
@@ -349,12 +338,12 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The products of one step with `groups` groups of 8 rows of x (xs: the lane's place in the step, by group 8 rows apart;
-// left: k from the step's first on, MXFP8: a word of scales holds padding behind the last block, maybe NaN).  The
+// The products of 128 k with `groups` groups of 8 rows of x (xs: the lane's place there, by group 8 rows apart;
+// left: k from the first on, MXFP8: a word of scales holds padding behind the last block, maybe NaN).  The
 // sums of a step start from zero and are added in FP32: the tensor core cuts off what it adds to (about 2^-24 of it a step of
 // 16), which would grow with the length.
 template <bool NV, int kG, int kPieces>
-__device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4], const uint8_t *const (&xs)[kG], int groups, int piece_bytes, int left) {
+__device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4], const uint32_t (&xs)[kG], int groups, int piece_bytes, int left) {
     if constexpr (NV) {
         const uint32_t sa = e4m3x2(it.sa), sb = e4m3x2(it.sb);
         const uint32_t wa[4] = {it.a.x, it.a.y, it.a.z, it.a.w}, wb[4] = {it.b.x, it.b.y, it.b.z, it.b.w};
@@ -379,7 +368,7 @@ __device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4]
             for (int p = 0; p < kPieces; ++p)
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
-                    const uint4 b = *reinterpret_cast<const uint4 *>(xs[q] + p * piece_bytes + 64 * jj);
+                    const uint4 b = tc::ld_shared(xs[q] + p * piece_bytes + 64 * jj);
                     mma(d[0], A[2 * jj], b.x, b.y);
                     mma(d[1], A[2 * jj + 1], b.z, b.w);
                 }
@@ -404,7 +393,7 @@ __device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4]
                 float d[4] = {};
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(xs[q] + p * piece_bytes + 64 * b);
+                    const uint4 x = tc::ld_shared(xs[q] + p * piece_bytes + 64 * b);
                     mma(d, A0, x.x, x.y);
                     mma(d, A1, x.z, x.w);
                 }
@@ -448,7 +437,7 @@ __device__ __forceinline__ float scaled(float v, float unit, float unscale) {
 
 template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_bounds__(kThreads, 1) gemv(const __grid_constant__ GemvParams P) {
     constexpr int kSides = kGlu ? 2 : 1;
-    constexpr int kAhead = kDepth<NV, kG>;
+    constexpr int kAhead = kDepth<kG>;
     extern __shared__ __align__(16) uint8_t dyn[];
     __shared__ Shared sh;
     float *const sums = reinterpret_cast<float *>(dyn);   // [2][warp][kSlab]
@@ -498,7 +487,7 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         for (int d = 0; d < kAhead; ++d) ask(d);
 
         float acc[kG][4] = {};
-        const uint8_t *place_of[kG];
+        uint32_t place_of[kG];
         const int piece_bytes = P.pass_rows * P.pitch;
         const int parts = min(4, P.wk), parts_log = parts >> 1, each = P.wk / parts, wns_log = 31 - __clz(wns);
         int staged = -1, rows = 0, groups = 0, r0 = 0, side = 0, round = 0, buffer = 0;
@@ -513,7 +502,7 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
             stage_rows<NV, kPieces>(P, sh, xs, r0, rows, unit, kSides);
 #pragma unroll
             for (int q = 0; q < kG; ++q)   // lanes past the last row read it again: their columns are not stored
-                place_of[q] = xs + min(8 * q + (lane >> 2), rows - 1) * P.pitch + 16 * (lane & 3);
+                place_of[q] = tc::smem_u32(xs) + min(8 * q + (lane >> 2), rows - 1) * P.pitch + 16 * (lane & 3);
         };
         // A warp's sums of a side of the tile to shared memory.
         auto hand_in = [&] {
@@ -569,10 +558,13 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
             __syncwarp();   // the other lanes' copies
             const int step = round * P.wk + wk;
             if (step < P.steps) {
-                const uint8_t *from[kG];
 #pragma unroll
-                for (int q = 0; q < kG; ++q) from[q] = place_of[q] + step * kStepX;
-                multiply<NV, kG, kPieces>(item_at<NV>(slots + slot * kSlot<NV>, lane), acc, from, groups, piece_bytes, static_cast<int>(P.K) - step * kStep);
+                for (int half = 0; half < kStep<NV> / 128; ++half) {
+                    uint32_t from[kG];
+#pragma unroll
+                    for (int q = 0; q < kG; ++q) from[q] = place_of[q] + step * (kStep<NV> * 2) + half * 256;
+                    multiply<NV, kG, kPieces>(item_at<NV>(slots + slot * kSlot<NV>, half, lane), acc, from, groups, piece_bytes, static_cast<int>(P.K) - step * kStep<NV>);
+                }
             }
             __syncwarp();   // all lanes have what the slot held
             ask(slot);
@@ -619,7 +611,7 @@ int sm_count() {
 
 // Shared memory but for x: sums and weights under way.
 template <bool NV, bool kGlu, int kG> constexpr int own_bytes() {
-    return 2 * kWarps * slab((kGlu ? 2 : 1) * kG) * static_cast<int>(sizeof(float)) + kWarps * kDepth<NV, kG> * kSlot<NV>;
+    return 2 * kWarps * slab((kGlu ? 2 : 1) * kG) * static_cast<int>(sizeof(float)) + kWarps * kDepth<kG> * kSlot<NV>;
 }
 
 template <bool NV, bool kGlu, int kG, int kPieces> gsa_status launch_gemv(const GemvParams &P, cudaStream_t s) {
@@ -672,7 +664,9 @@ gsa_status run_gemv(GemvParams &P, bool glu, const void *x, int32_t x_dtype, con
     P.b_groups = b_groups;
     P.status = gemm_status::word();
     if (!P.status) return cuda_error();
-    P.steps = static_cast<int>((K + kStep - 1) / kStep);
+    const int step = nv ? kStep<true> : kStep<false>;
+    P.steps = static_cast<int>((K + step - 1) / step);
+    P.row_bytes = static_cast<int>(nv ? K / 2 : K);
     P.wk = 1;
     while (P.wk < kWarps && P.wk < P.steps) P.wk *= 2;
     const int64_t rest = N % 128;
@@ -682,7 +676,7 @@ gsa_status run_gemv(GemvParams &P, bool glu, const void *x, int32_t x_dtype, con
     while (P.wk > 2 && (E < M ? E : M) * P.rows16 * P.wk / (2 * kWarps) >= 6 * 152) P.wk /= 2;
     const int wns = kWarps / P.wk;
     P.tiles = (P.rows16 + wns - 1) / wns;
-    P.pitch = P.steps * kStepX + 64;   // rows on alternating halves of the banks
+    P.pitch = P.steps * step * 2 + 64;   // rows on alternating halves of the banks
     const int pieces = x_dtype == GSA_FP32 ? 2 : 1;
     auto space = [&](int groups) {   // of x, with 8 rows or 16 a pass
         auto own = [&](auto fmt, auto gated) {
