@@ -48,6 +48,7 @@ struct GemvParams {
     uint32_t *status;
     int64_t M, N, K;
     int E, x_type, out_type;
+    int64_t expert_bytes, side_bytes;   // of codes: of an expert, of its gate rows
     int row_bytes;          // of a weight row's codes
     int scale_cols, scale_rows, up_tiles;   // scale tiles along k; of an expert along its rows; from a gate row to its linear row
     int b_groups;
@@ -109,13 +110,38 @@ __device__ __forceinline__ void put(void *p, int type, int64_t i, float v) {
 
 // -------------------------------------------------------------- rows of x
 
-// Eight consecutive values (i a multiple of 8), and what they are in FP32.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Eight consecutive values (i a multiple of 8).
 template <int kPieces> struct Raw {   // 2: FP32
     uint4 r[kPieces];
     __device__ __forceinline__ void load(const void *x, int64_t i) {
         const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(x) + i * (2 * kPieces));
 #pragma unroll
         for (int k = 0; k < kPieces; ++k) r[k] = __ldg(p + k);
+    }
+    // Bits of the largest magnitudes so far, in halves for BF16 (`kFinite`: of finite values).
+    template <bool kFinite> __device__ __forceinline__ uint32_t largest(uint32_t most) const {
+        constexpr uint32_t kAbs = kPieces == 2 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+            const uint32_t w[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t a = w[j] & kAbs;
+                if constexpr (kPieces == 2) {
+                    if (!kFinite || a < 0x7F800000u) most = max(most, a);
+                } else {
+                    if (kFinite) a = ((a >> 16) < 0x7F80u ? a & 0xFFFF0000u : 0) | ((a & 0xFFFFu) < 0x7F80u ? a & 0xFFFFu : 0);
+                    most = max_u16x2(most, a);
+                }
+            }
+        }
+        return most;
     }
     __device__ __forceinline__ void values(bool bf16, float (&v)[8]) const {
 #pragma unroll
@@ -164,28 +190,25 @@ template <bool NV, int kPieces> __device__ void stage_rows(const GemvParams &P, 
     if (threadIdx.x < sides) sh.unit[threadIdx.x] = unit;
     const bool bf16 = P.x_type == GSA_BF16;
     const int live = static_cast<int>(P.K) / 8;
-    constexpr int kBatch = 4;   // words asked for at once
-    if (P.x_type != GSA_FP16) {
-        uint32_t most = 0;
-        if (row < rows)
+    constexpr int kBatch = kPieces == 2 ? 4 : 8;   // words asked for at once
+    if (P.x_type != GSA_FP16 && row < rows) {
+        auto over = [&](auto finite) {
+            uint32_t most = 0;
             for (int c0 = t; c0 < live; c0 += kBatch * threads) {
                 Raw<kPieces> raw[kBatch];
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) raw[b].load(P.x, at + 8 * static_cast<int64_t>(min(c0 + b * threads, live - 1)));
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    float v[8];
-                    raw[b].values(bf16, v);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t a = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-                        if (a < 0x7F800000u && a > most) most = a;
-                    }
-                }
+                for (int b = 0; b < kBatch; ++b) most = raw[b].template largest<decltype(finite)::value>(most);
             }
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-        if (row < rows && threadIdx.x % 32 == 0) atomicMax(&sh.largest[row], most);
+            if (kPieces == 1) most = max(most & 0xFFFF0000u, most << 16);   // a BF16 is the high half of its FP32
+            return __reduce_max_sync(0xFFFFFFFFu, most);
+        };
+        uint32_t most = over(std::false_type());
+        if (most >= 0x7F800000u) most = over(std::true_type());   // infinities and NaN keep their place but set no scale
+        if (threadIdx.x % 32 == 0) atomicMax(&sh.largest[row], most);
+    }
+    if (P.x_type != GSA_FP16) {
         __syncthreads();
     }
     if (row < rows) {
@@ -286,15 +309,18 @@ template <bool NV> __device__ __forceinline__ Item<NV> item_at(uint32_t slot, in
 // four rows, one of each quarter.  Nothing is predicated: rows past the last read the last (their results are not stored), and
 // what lies past the end of k reads the row's last word again (x is zero there).
 template <bool NV> struct Aim {
+    const uint8_t *codes, *scales;   // of the expert
     const uint8_t *row[4], *s;
-    __device__ __forceinline__ void at(const GemvParams &P, int e, int side, int sides, int i, int lane) {
+    __device__ __forceinline__ void expert(const GemvParams &P, int e, int lane) {
+        codes = P.codes + e * P.expert_bytes;
+        scales = P.scales + static_cast<int64_t>(e * P.scale_rows) * P.scale_cols * kScaleTile + 16 * (lane & 3);
+    }
+    __device__ __forceinline__ void at(const GemvParams &P, bool linear, int i, int lane) {
         const int last = static_cast<int>(P.N) - 1, inside = 128 * (i >> 3) + 4 * (i & 7) + (lane >> 3);
-        const int64_t pitch = NV ? P.K / 2 : P.K;
-        const uint8_t *first = P.codes + static_cast<int64_t>(e * sides + side) * P.N * pitch;
+        const uint8_t *first = linear ? codes + P.side_bytes : codes;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) row[k] = first + min(inside + 32 * k, last) * pitch;
-        s = P.scales + static_cast<int64_t>(e * P.scale_rows + side * P.up_tiles + (i >> 3)) * P.scale_cols * kScaleTile +
-            16 * (4 * (i & 7) + (lane & 3));
+        for (int k = 0; k < 4; ++k) row[k] = first + static_cast<int64_t>(min(inside + 32 * k, last)) * P.row_bytes;
+        s = scales + static_cast<int64_t>((linear ? P.up_tiles : 0) + (i >> 3)) * (P.scale_cols * kScaleTile) + 64 * (i & 7);
     }
     __device__ __forceinline__ void load(const GemvParams &P, uint32_t slot, int step, int lane) const {
         const uint32_t c = min(step * 128 + 16 * (lane & 7), P.row_bytes - 16);
@@ -466,7 +492,7 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         int64_t to_ask = left, to_do = left;              // tiles
         Aim<NV> aim;
         int ask_side = 0, ask_round = 0;
-        auto take_aim = [&] { aim.at(P, ahead.e, ask_side, kSides, min(ahead.tile * wns + wn, P.rows16 - 1), lane); };
+        auto take_aim = [&] { aim.at(P, kGlu && ask_side, min(ahead.tile * wns + wn, P.rows16 - 1), lane); };
         const uint32_t slots = tc::smem_u32(ring) + warp * (kAhead * kSlot<NV>);
         auto ask = [&](int slot) {   // the next step's weights; one group of copies a call
             if (to_ask > 0) aim.load(P, slots + slot * kSlot<NV>, ask_round * P.wk + wk, lane);
@@ -479,17 +505,20 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
             } else {
                 ask_side = 0;
                 if (--to_ask == 0) return;
+                const int before = ahead.e;
                 ahead.next(P, sh);
+                if (ahead.e != before) aim.expert(P, ahead.e, lane);
             }
             take_aim();
         };
+        aim.expert(P, ahead.e, lane);
         take_aim();
         for (int d = 0; d < kAhead; ++d) ask(d);
 
         float acc[kG][4] = {};
         uint32_t place_of[kG];
         const int piece_bytes = P.pass_rows * P.pitch;
-        const int parts = min(4, P.wk), parts_log = parts >> 1, each = P.wk / parts, wns_log = 31 - __clz(wns);
+        const int runs = min(4, P.wk), runs_log = runs >> 1, each = P.wk / runs, wns_log = 31 - __clz(wns);
         int staged = -1, rows = 0, groups = 0, r0 = 0, side = 0, round = 0, buffer = 0;
         auto stage = [&] {
             staged = at.pass;
@@ -517,32 +546,38 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
                 }
             }
         };
-        // The tile's sums over the warps, and its results: up to four lanes a result, up to four warps' sums each, first one after
-        // the other, then across the lanes.
+        // The tile's sums over the warps, and its results.  Of each result up to four runs of warps' sums, each in order, then
+        // pairs of runs: by one lane, or by two or four where there are lanes enough, in the same order.
         auto finish = [&] {
             __syncthreads();
-            const int part = threadIdx.x & (parts - 1), total = (16 * wns * rows) << parts_log;
-            for (int base = 0; base < total; base += kThreads) {
-                const int x = base + static_cast<int>(threadIdx.x), o = x >> parts_log;
+            const int results = 16 * wns * rows, lanes_log = results * 4 <= kThreads ? runs_log : results * 2 <= kThreads ? min(1, runs_log) : 0;
+            const int mine = runs >> lanes_log, lanes = 1 << lanes_log, part = threadIdx.x & (lanes - 1);
+            for (int base = 0; base < results << lanes_log; base += kThreads) {
+                const int o = (base + static_cast<int>(threadIdx.x)) >> lanes_log;
                 const int a = o & 15, b = (o >> 4) & (wns - 1), r = (o >> 4) >> wns_log;   // weight row, warp row, row of x
-                const bool on = x < total;
-                const float *from = sums + (buffer * kWarps + b * P.wk + part * each) * kSlab + (on ? r >> 3 : 0) * kGroupSums + (r & 7) * kRowSums + a;
+                const bool on = o < results;
+                const float *from = sums + (buffer * kWarps + b * P.wk + part * mine * each) * kSlab + (on ? r >> 3 : 0) * kGroupSums + (r & 7) * kRowSums + a;
                 float v[kSides];
 #pragma unroll
                 for (int s = 0; s < kSides; ++s) {
-                    v[s] = 0.0f;
+                    float run[4] = {};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < each) v[s] += from[s * kG * kGroupSums + k * kSlab];
-                }
-                if (parts > 1) {
+                    for (int p = 0; p < 4; ++p)
+                        if (p < mine) {
 #pragma unroll
-                    for (int s = 0; s < kSides; ++s) v[s] += __shfl_xor_sync(0xFFFFFFFFu, v[s], 1);
+                            for (int k = 0; k < 4; ++k)
+                                if (k < each) run[p] += from[s * kG * kGroupSums + (p * each + k) * kSlab];
+                        }
+                    v[s] = run[0];
+                    if (mine > 1) v[s] += run[1];
+                    if (mine > 2) v[s] += run[2] + run[3];
                 }
-                if (parts > 2) {
 #pragma unroll
-                    for (int s = 0; s < kSides; ++s) v[s] += __shfl_xor_sync(0xFFFFFFFFu, v[s], 2);
-                }
+                for (int d = 1; d < 4; d <<= 1)
+                    if (d < lanes) {
+#pragma unroll
+                        for (int s = 0; s < kSides; ++s) v[s] += __shfl_xor_sync(0xFFFFFFFFu, v[s], d);
+                    }
                 const int i = at.tile * wns + b, n = 128 * (i >> 3) + 4 * (i & 7) + (a & 3) + 32 * (a >> 2);
                 if (part != 0 || !on || i >= P.rows16 || n >= P.N) continue;
                 const float unscale = sh.unscale[r];
@@ -667,6 +702,8 @@ gsa_status run_gemv(GemvParams &P, bool glu, const void *x, int32_t x_dtype, con
     const int step = nv ? kStep<true> : kStep<false>;
     P.steps = static_cast<int>((K + step - 1) / step);
     P.row_bytes = static_cast<int>(nv ? K / 2 : K);
+    P.side_bytes = N * P.row_bytes;
+    P.expert_bytes = sides * P.side_bytes;
     P.wk = 1;
     while (P.wk < kWarps && P.wk < P.steps) P.wk *= 2;
     const int64_t rest = N % 128;
