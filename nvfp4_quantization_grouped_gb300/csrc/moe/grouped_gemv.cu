@@ -282,24 +282,27 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
 // 16-byte word c of row r of a slot.
 template <bool NV> __device__ __forceinline__ uint32_t word_at(int r, int c) { return r * 128 + 16 * (NV ? c ^ (4 * (r & 1)) : c ^ (2 * (r & 3))); }
 
-template <bool NV> __device__ __forceinline__ Item<NV> item_at(uint32_t slot, int half, int lane) {
+// (Plain loads: as volatile statements they would keep their order among the products, each waiting for the one before.)
+template <typename T> __device__ __forceinline__ T at_byte(const uint8_t *p, int at) { return *reinterpret_cast<const T *>(p + at); }
+
+template <bool NV> __device__ __forceinline__ Item<NV> item_at(const uint8_t *slot, int half, int lane) {
     Item<NV> it;
     const int g = lane >> 2, t = lane & 3, word = 16 * (g & 3) + 4 * (g >> 2);
     if constexpr (NV) {
-        const uint32_t c = slot + word_at<NV>(g, 4 * half + t), s = slot + 2048 + 64 * (2 * half + (t >> 1)) + word;
-        it.a = tc::ld_shared(c);
-        it.b = tc::ld_shared(c + 8 * 128);   // row g + 8 is swapped alike
-        it.sa = __float_as_uint(tc::ld_shared1(s)) >> (16 * (t & 1));
-        it.sb = __float_as_uint(tc::ld_shared1(s + 8)) >> (16 * (t & 1));
+        const int c = word_at<NV>(g, 4 * half + t), s = 2048 + 64 * (2 * half + (t >> 1)) + word;
+        it.a = at_byte<uint4>(slot, c);
+        it.b = at_byte<uint4>(slot, c + 8 * 128);   // row g + 8 is swapped alike
+        it.sa = at_byte<uint32_t>(slot, s) >> (16 * (t & 1));
+        it.sb = at_byte<uint32_t>(slot, s + 8) >> (16 * (t & 1));
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t c = slot + word_at<NV>(g, 2 * j) + 8 * t;
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(it.a[j].x), "=r"(it.a[j].y) : "r"(c) : "memory");
-            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(it.b[j].x), "=r"(it.b[j].y) : "r"(c + 8 * 128) : "memory");
+            const int c = word_at<NV>(g, 2 * j) + 8 * t;
+            it.a[j] = at_byte<uint2>(slot, c);
+            it.b[j] = at_byte<uint2>(slot, c + 8 * 128);
         }
-        it.sa = __float_as_uint(tc::ld_shared1(slot + 2048 + word));
-        it.sb = __float_as_uint(tc::ld_shared1(slot + 2048 + word + 8));
+        it.sa = at_byte<uint32_t>(slot, 2048 + word);
+        it.sb = at_byte<uint32_t>(slot, 2048 + word + 8);
     }
     return it;
 }
@@ -359,7 +362,7 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -369,7 +372,7 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 // sums of a step start from zero and are added in FP32: the tensor core cuts off what it adds to (about 2^-24 of it a step of
 // 16), which would grow with the length.
 template <bool NV, int kG, int kPieces>
-__device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4], const uint32_t (&xs)[kG], int groups, int piece_bytes, int left) {
+__device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4], const uint8_t *const (&xs)[kG], int groups, int piece_bytes, int left) {
     if constexpr (NV) {
         const uint32_t sa = e4m3x2(it.sa), sb = e4m3x2(it.sb);
         const uint32_t wa[4] = {it.a.x, it.a.y, it.a.z, it.a.w}, wb[4] = {it.b.x, it.b.y, it.b.z, it.b.w};
@@ -394,7 +397,7 @@ __device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4]
             for (int p = 0; p < kPieces; ++p)
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
-                    const uint4 b = tc::ld_shared(xs[q] + p * piece_bytes + 64 * jj);
+                    const uint4 b = at_byte<uint4>(xs[q], p * piece_bytes + 64 * jj);
                     mma(d[0], A[2 * jj], b.x, b.y);
                     mma(d[1], A[2 * jj + 1], b.z, b.w);
                 }
@@ -419,7 +422,7 @@ __device__ __forceinline__ void multiply(const Item<NV> &it, float (&acc)[kG][4]
                 float d[4] = {};
 #pragma unroll
                 for (int p = 0; p < kPieces; ++p) {
-                    const uint4 x = tc::ld_shared(xs[q] + p * piece_bytes + 64 * b);
+                    const uint4 x = at_byte<uint4>(xs[q], p * piece_bytes + 64 * b);
                     mma(d, A0, x.x, x.y);
                     mma(d, A1, x.z, x.w);
                 }
@@ -493,7 +496,8 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         Aim<NV> aim;
         int ask_side = 0, ask_round = 0;
         auto take_aim = [&] { aim.at(P, kGlu && ask_side, min(ahead.tile * wns + wn, P.rows16 - 1), lane); };
-        const uint32_t slots = tc::smem_u32(ring) + warp * (kAhead * kSlot<NV>);
+        const uint8_t *own = ring + warp * (kAhead * kSlot<NV>);
+        const uint32_t slots = tc::smem_u32(own);
         auto ask = [&](int slot) {   // the next step's weights; one group of copies a call
             if (to_ask > 0) aim.load(P, slots + slot * kSlot<NV>, ask_round * P.wk + wk, lane);
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -516,7 +520,7 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
         for (int d = 0; d < kAhead; ++d) ask(d);
 
         float acc[kG][4] = {};
-        uint32_t place_of[kG];
+        const uint8_t *place_of[kG];
         const int piece_bytes = P.pass_rows * P.pitch;
         const int runs = min(4, P.wk), runs_log = runs >> 1, each = P.wk / runs, wns_log = 31 - __clz(wns);
         int staged = -1, rows = 0, groups = 0, r0 = 0, side = 0, round = 0, buffer = 0;
@@ -531,7 +535,7 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
             stage_rows<NV, kPieces>(P, sh, xs, r0, rows, unit, kSides);
 #pragma unroll
             for (int q = 0; q < kG; ++q)   // lanes past the last row read it again: their columns are not stored
-                place_of[q] = tc::smem_u32(xs) + min(8 * q + (lane >> 2), rows - 1) * P.pitch + 16 * (lane & 3);
+                place_of[q] = xs + min(8 * q + (lane >> 2), rows - 1) * P.pitch + 16 * (lane & 3);
         };
         // A warp's sums of a side of the tile to shared memory.
         auto hand_in = [&] {
@@ -595,10 +599,10 @@ template <bool NV, bool kGlu, int kG, int kPieces> __global__ void __launch_boun
             if (step < P.steps) {
 #pragma unroll
                 for (int half = 0; half < kStep<NV> / 128; ++half) {
-                    uint32_t from[kG];
+                    const uint8_t *from[kG];
 #pragma unroll
                     for (int q = 0; q < kG; ++q) from[q] = place_of[q] + step * (kStep<NV> * 2) + half * 256;
-                    multiply<NV, kG, kPieces>(item_at<NV>(slots + slot * kSlot<NV>, half, lane), acc, from, groups, piece_bytes, static_cast<int>(P.K) - step * kStep<NV>);
+                    multiply<NV, kG, kPieces>(item_at<NV>(own + slot * kSlot<NV>, half, lane), acc, from, groups, piece_bytes, static_cast<int>(P.K) - step * kStep<NV>);
                 }
             }
             __syncwarp();   // all lanes have what the slot held
