@@ -485,23 +485,28 @@ gsa_status gsa_grouped_glu_bwd(const void *dy_bf16, const gsa_qin *a, const gsa_
  * is reported by gsa_grouped_gemm_status).  With E = 1 split_sizes_dev may be NULL: all
  * rows.  Right for any number of rows, made for up to about 16 an expert: the weights
  * are read once for 16.  out_dtype: any of the three, rounded once from FP32 sums.
- * K is a multiple of 64.  A row's x is multiplied in FP16, scaled by a power of two so
- * that its largest value fits (FP32 rows as the sum of two such): values are exact
- * (BF16, FP16) or within 2^-22 (FP32) of themselves down to 2^-29 of the row's
- * largest, and within 2^-39 of that largest below.
- * Errors: INVALID_ARG, UNSUPPORTED (E > 256, K % 64, K > 32768 (FP32 x: 16384), sizes past
- * 2^31),
- * ALIGNMENT, CUDA. */
+ * K is a multiple of 64.  x takes part as eight digits in the weights' own format, whose
+ * blocks (of 32 or 16 values) have scales of their own: a value is within 2^-22 of its
+ * block's largest, BF16 and FP16 values down to 2^-10 of it are exact, and blocks below
+ * 2^-16 (NVFP4; MXFP8 2^-120) of the row's largest value are within 2^-37 of that.
+ * Infinite values count as products with them do; a row with more than eight is NaN.
+ * Two launches.
+ * Errors: INVALID_ARG, UNSUPPORTED (E > 256, K % 64, M >= 2^28, sizes past 2^31),
+ * ALIGNMENT (workspace 256), WORKSPACE, CUDA. */
 gsa_status gsa_grouped_gemv(const void *x, int32_t x_dtype, const gsa_qin *b, const int64_t *split_sizes_dev, int64_t E,
                             int64_t M, int64_t N, int64_t K, int32_t recipe_kind, void *out, int32_t out_dtype,
-                            gsa_stream_t stream);
+                            void *workspace, size_t workspace_bytes, gsa_stream_t stream);
+
+/* Workspace bytes of gsa_grouped_gemv and gsa_grouped_glu_gemv (256-byte aligned; any
+ * content).  0 on invalid arguments and without rows. */
+size_t gsa_grouped_gemv_workspace_size(int64_t E, int64_t M, int64_t K, int32_t recipe_kind);
 
 /* gsa_grouped_glu for such rows: y[r, n] = p_r act(sum_k x[r, k] B_e[n, k],
  * sum_k x[r, k] B_e[N + n, k]), b and b_groups as there, the rest as gsa_grouped_gemv. */
 gsa_status gsa_grouped_glu_gemv(const void *x, int32_t x_dtype, const gsa_qin *b, const int64_t *split_sizes_dev,
                                 int64_t E, int64_t M, int64_t N, int64_t K, int32_t recipe_kind, int32_t act_kind,
                                 const gsa_act_params *act_params, const float *probs, int32_t b_groups, void *y,
-                                int32_t out_dtype, gsa_stream_t stream);
+                                int32_t out_dtype, void *workspace, size_t workspace_bytes, gsa_stream_t stream);
 
 /* Takes one report out of the current device's word and synchronizes `stream`:
  * GSA_ERR_DEVICE_TIMEOUT (a bounded wait ran out), GSA_ERR_INVALID_ARG (a device

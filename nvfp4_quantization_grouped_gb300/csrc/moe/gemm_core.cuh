@@ -91,12 +91,14 @@ struct GemmShared : Barriers {
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // Group bounds from the device split: rows, scale tiles and row tiles of kRows before each group.  Every thread
-// of the block.  A negative size, a sum above M or more scale tiles than A's buffer holds sets sh.bad.
-template <int kRows> __device__ void scan_split(const GemmParams &P, GemmShared &sh) {
+// of the block.  A negative size, a sum above M or more scale tiles than A's buffer holds sets sh.bad.  kTimes: rows of A for
+// each that the split counts.  Without a split the one group has all rows.
+template <int kRows, int kTimes = 1> __device__ void scan_split(const GemmParams &P, GemmShared &sh) {
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    int64_t m = t < P.E ? P.split[t] : 0;
+    int64_t m = t < P.E ? (P.split ? P.split[t] : P.M / kTimes) : 0;
     const bool neg = m < 0 || m > P.M;
     if (neg) m = 0;
+    m *= kTimes;
     int64_t rows = m, scales = (m + 127) / 128, tiles = (m + kRows - 1) / kRows;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -152,6 +154,38 @@ template <int kRows> __device__ __forceinline__ Tile tile_at(const GemmParams &P
     t.rows = min(kRows, sh.row0[g + 1] - t.row);
     return t;
 }
+
+// The same value of all lanes as one that the compiler knows to be the same: it then lives in a uniform register, of which
+// the draining warps have plenty, while their accumulators leave them few others.
+__device__ __forceinline__ int known_uniform(int v) { return __reduce_min_sync(0xFFFFFFFFu, v); }
+
+// The tiles of a unit, without divisions: q counts row tiles over all groups (n_tiles column tiles each, one after another).
+struct Walk {
+    int q, nt, g, dq, dn;
+    __device__ __forceinline__ Walk(const GemmParams &P, int unit, int units)
+        : q(unit / P.n_tiles), nt(unit % P.n_tiles), g(0), dq(units / P.n_tiles), dn(units % P.n_tiles) {}
+    __device__ __forceinline__ void next(const GemmParams &P) {
+        q += dq, nt += dn;
+        if (nt >= P.n_tiles) nt -= P.n_tiles, ++q;
+    }
+    // Its tile, by a whole warp; the group that q is in is this one or a later one.
+    template <int kRows> __device__ __forceinline__ Tile tile(const GemmParams &P, const GemmShared &sh) {
+        if (known_uniform(sh.tile0[g + 1]) <= q) {
+            ++g;
+            for (int end = P.E + 1; end - g > 1;) {   // the last group that starts at or before q: most may be empty
+                const int mid = (g + end) >> 1;
+                if (known_uniform(sh.tile0[mid]) <= q) g = mid;
+                else end = mid;
+            }
+        }
+        Tile t;
+        t.g = g, t.nt = nt;
+        t.mt = q - known_uniform(sh.tile0[g]);
+        t.row = known_uniform(sh.row0[g]) + t.mt * kRows;
+        t.rows = min(kRows, known_uniform(sh.row0[g + 1]) - t.row);
+        return t;
+    }
+};
 
 // Where a stage's parts lie in shared memory.
 template <bool NV, int BN, bool kPair> struct Stages {

@@ -134,38 +134,6 @@ __device__ __forceinline__ float unit_of(float amax_a, float amax_b) {
     return u > 3.402823466e38f ? 3.402823466e38f : u;
 }
 
-// The same value of all lanes as one that the compiler knows to be the same: it then lives in a uniform register, of which
-// the draining warps have plenty, while their accumulators leave them few others.
-__device__ __forceinline__ int known_uniform(int v) { return __reduce_min_sync(0xFFFFFFFFu, v); }
-
-// The tiles of a unit, without divisions: q counts row tiles over all groups (n_tiles column tiles each, one after another).
-struct Walk {
-    int q, nt, g, dq, dn;
-    __device__ __forceinline__ Walk(const GluParams &P, int unit, int units)
-        : q(unit / P.n_tiles), nt(unit % P.n_tiles), g(0), dq(units / P.n_tiles), dn(units % P.n_tiles) {}
-    __device__ __forceinline__ void next(const GluParams &P) {
-        q += dq, nt += dn;
-        if (nt >= P.n_tiles) nt -= P.n_tiles, ++q;
-    }
-    // Its tile, by a whole warp; the group that q is in is this one or a later one.
-    template <int kRows> __device__ __forceinline__ Tile tile(const GluParams &P, const GemmShared &sh) {
-        if (known_uniform(sh.tile0[g + 1]) <= q) {
-            ++g;
-            for (int end = P.E + 1; end - g > 1;) {   // the last group that starts at or before q: most may be empty
-                const int mid = (g + end) >> 1;
-                if (known_uniform(sh.tile0[mid]) <= q) g = mid;
-                else end = mid;
-            }
-        }
-        Tile t;
-        t.g = g, t.nt = nt;
-        t.mt = q - known_uniform(sh.tile0[g]);
-        t.row = known_uniform(sh.row0[g]) + t.mt * kRows;
-        t.rows = min(kRows, known_uniform(sh.row0[g + 1]) - t.row);
-        return t;
-    }
-};
-
 // What a draining warp has in shared memory: a buffer for results, or (gradient) two for dy of this tile, whose place dx
 // takes, and of the next; probs of the rows of both.
 constexpr int kProbs = 32 * 4;

@@ -31,7 +31,7 @@ EXPORTED = ["gsa_layout", "gsa_workspace_size", "grouped_scaled_act_fwd", "group
             "gsa_moe_permute_bwd", "gsa_moe_unpermute", "gsa_moe_unpermute_bwd", "gsa_grouped_gemm",
             "gsa_grouped_gemm_wgrad", "gsa_grouped_gemm_wgrad_workspace_size",
             "gsa_grouped_gemm_status", "gsa_grouped_glu", "gsa_grouped_glu_bwd", "gsa_grouped_glu_bwd_workspace_size",
-            "gsa_grouped_gemv", "gsa_grouped_glu_gemv"]
+            "gsa_grouped_gemv", "gsa_grouped_gemv_workspace_size", "gsa_grouped_glu_gemv"]
 
 
 class GsaError(RuntimeError):
@@ -146,10 +146,12 @@ def load():
         gated = [i32, ctypes.POINTER(ActParams), _P, i32]             # activation, its parameters, probs, b_groups
         for name, args in (("gsa_grouped_glu", [q, q, *shape, *gated, _P, i32, _P]),
                            ("gsa_grouped_glu_bwd", [_P, q, q, *shape, *gated, _P, i32, _P, _P, ctypes.c_size_t, _P]),
-                           ("gsa_grouped_gemv", [_P, i32, q, *shape, _P, i32, _P]),
-                           ("gsa_grouped_glu_gemv", [_P, i32, q, *shape, *gated, _P, i32, _P])):
+                           ("gsa_grouped_gemv", [_P, i32, q, *shape, _P, i32, _P, ctypes.c_size_t, _P]),
+                           ("gsa_grouped_glu_gemv", [_P, i32, q, *shape, *gated, _P, i32, _P, ctypes.c_size_t, _P])):
             getattr(L, name).restype = ctypes.c_int
             getattr(L, name).argtypes = args
+        L.gsa_grouped_gemv_workspace_size.restype = ctypes.c_size_t
+        L.gsa_grouped_gemv_workspace_size.argtypes = [_I64, _I64, _I64, i32]
         L.gsa_grouped_glu_bwd_workspace_size.restype = ctypes.c_size_t
         L.gsa_grouped_glu_bwd_workspace_size.argtypes = [_I64, _I64]
         L.gsa_version.restype = ctypes.c_int32
@@ -876,7 +878,8 @@ def grouped_glu_bwd(dy, a: dict, b: dict, split, m: int, n: int, k: int, recipe_
 
 
 def _few_rows(what, x, b, split, b_groups, recipe_kind, n, out_dtype, out, stream):
-    """(QIn of b, its tensors, split's pointer, experts, out) of a product of unquantized rows."""
+    """(QIn of b, its tensors, split's pointer, experts, out, its type's code, workspace, its bytes) of a product of
+    unquantized rows."""
     torch = _torch or _setup()
     if x.dim() != 2 or x.dtype not in _DTYPES:
         raise GsaError(1, f"{what}: x must be bfloat16, float16 or float32 [rows, k], got {x.dtype} {list(x.shape)}")
@@ -893,16 +896,17 @@ def _few_rows(what, x, b, split, b_groups, recipe_kind, n, out_dtype, out, strea
     if out_dtype not in _DTYPES:
         raise GsaError(1, f"{what}: output type {out_dtype} (bfloat16, float16 or float32 expected)")
     out = _out(out, what + ": out", (x.shape[0], n), out_dtype, dev, stream)
-    return qb, tb, sp, experts, out, _DTYPES[out_dtype]
+    nbytes = _lib.gsa_grouped_gemv_workspace_size(experts, x.shape[0], x.shape[1], recipe_kind)
+    return qb, tb, sp, experts, out, _DTYPES[out_dtype], _out(None, "", (max(256, nbytes),), torch.uint8, dev, stream), nbytes
 
 
 def grouped_gemv(x, b: dict, split, n: int, recipe_kind: int, out_dtype=None, out=None, stream=None):
     """out [rows, n] = x B_e^T over the rows of each expert, for a few unquantized rows an expert (decoding): x [rows, k]
     bfloat16, float16 or float32; b, split as for grouped_gemm (split None: one matrix takes all rows).  out_dtype: any
     of the three (default: x's)."""
-    qb, tb, sp, experts, out, code = _few_rows("grouped_gemv", x, b, split, 1, recipe_kind, n, out_dtype, out, stream)
+    qb, tb, sp, experts, out, code, ws, nbytes = _few_rows("grouped_gemv", x, b, split, 1, recipe_kind, n, out_dtype, out, stream)
     st = _lib.gsa_grouped_gemv(x.data_ptr(), _DTYPES[x.dtype], qb, sp, experts, x.shape[0], n, x.shape[1], recipe_kind,
-                               out.data_ptr(), code, _stream_of(stream, x.device, x, split, *tb))
+                               out.data_ptr(), code, ws.data_ptr(), nbytes, _stream_of(stream, x.device, x, split, *tb))
     if st:
         _check(st, "gsa_grouped_gemv")
     return out
@@ -914,9 +918,10 @@ def grouped_glu_gemv(x, b: dict, split, n: int, recipe_kind: int, act="swiglu", 
     grouped_gemv, the rest as for grouped_glu."""
     _torch or _setup()
     kind, prm, pp = _gated("grouped_glu_gemv", act, params, probs, x.shape[0], b_groups, x.device)
-    qb, tb, sp, experts, out, code = _few_rows("grouped_glu_gemv", x, b, split, b_groups, recipe_kind, n, out_dtype, out, stream)
+    qb, tb, sp, experts, out, code, ws, nbytes = _few_rows("grouped_glu_gemv", x, b, split, b_groups, recipe_kind, n, out_dtype, out, stream)
     st = _lib.gsa_grouped_glu_gemv(x.data_ptr(), _DTYPES[x.dtype], qb, sp, experts, x.shape[0], n, x.shape[1], recipe_kind, kind, prm,
-                                   pp, b_groups, out.data_ptr(), code, _stream_of(stream, x.device, x, split, probs, *tb))
+                                   pp, b_groups, out.data_ptr(), code, ws.data_ptr(), nbytes,
+                                   _stream_of(stream, x.device, x, split, probs, *tb))
     if st:
         _check(st, "gsa_grouped_glu_gemv")
     return out

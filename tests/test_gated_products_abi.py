@@ -63,18 +63,19 @@ def test_gradient_refusals():
     assert bwd(dy=None) == INVALID and bwd(dx=None, dp=None) == INVALID and bwd(dtype=1) == INVALID
     assert bwd(dy=A + 8) == ALIGN and bwd(dx=A + 8) == ALIGN and bwd(dp=A + 2) == ALIGN and bwd(ws=A + 128) == ALIGN
     size = gsa.load().gsa_grouped_glu_bwd_workspace_size
-    # the word of the split and two partial sums of a row for each 128 columns
-    assert size(100, 128) == 256 + (2 * 100 * 4 + 255) // 256 * 256 and size(1, 129) == 256 + 256
+    # the word of the split and four partial sums of a row for each 128 columns
+    assert size(100, 128) == 256 + (4 * 100 * 4 + 255) // 256 * 256 and size(1, 129) == 256 + 256
     assert size(0, 128) == 0 and size(-1, 128) == 0 and size(5, 0) == 0 and size(1 << 31, 128) == 0
     assert bwd(ws_bytes=size(100, 128) - 1) == WS and bwd(ws=None) == WS
 
 
-def gemv(x=A, xt=0, b=None, split=A, e=4, m=100, n=128, k=128, recipe=1, out=A, dtype=0):
-    return gsa.load().gsa_grouped_gemv(x, xt, b or qin(), split, e, m, n, k, recipe, out, dtype, None)
+def gemv(x=A, xt=0, b=None, split=A, e=4, m=100, n=128, k=128, recipe=1, out=A, dtype=0, ws=A, ws_bytes=BIG):
+    return gsa.load().gsa_grouped_gemv(x, xt, b or qin(), split, e, m, n, k, recipe, out, dtype, ws, ws_bytes, None)
 
 
-def glu_gemv(x=A, xt=0, b=None, split=A, e=4, m=100, n=128, k=128, recipe=1, act=2, params=None, probs=A, groups=1, out=A, dtype=0):
-    return gsa.load().gsa_grouped_glu_gemv(x, xt, b or qin(), split, e, m, n, k, recipe, act, params, probs, groups, out, dtype, None)
+def glu_gemv(x=A, xt=0, b=None, split=A, e=4, m=100, n=128, k=128, recipe=1, act=2, params=None, probs=A, groups=1, out=A, dtype=0,
+             ws=A, ws_bytes=BIG):
+    return gsa.load().gsa_grouped_glu_gemv(x, xt, b or qin(), split, e, m, n, k, recipe, act, params, probs, groups, out, dtype, ws, ws_bytes, None)
 
 
 def test_products_of_unquantized_rows_refusals():
@@ -82,5 +83,10 @@ def test_products_of_unquantized_rows_refusals():
     common(glu_gemv)
     for call in (gemv, glu_gemv):
         assert call(x=None) == INVALID and call(out=None) == INVALID and call(xt=3) == INVALID and call(xt=-1) == INVALID
-        assert call(x=A + 8) == ALIGN and call(out=A + 8) == ALIGN and call(k=65600) == UNSUP
+        assert call(x=A + 8) == ALIGN and call(out=A + 8) == ALIGN and call(ws=A + 128) == ALIGN
+        assert call(ws=None) == WS and call(ws_bytes=100) == WS and call(m=1 << 28) == UNSUP and call(k=(1 << 30) + 64) == UNSUP
+    size = gsa.load().gsa_grouped_gemv_workspace_size
+    # 8 bytes a row, 8 rows of K / 2 bytes of codes each, scale tiles of 7 + 4 row tiles x 2
+    assert size(4, 100, 128, 1) == 1024 + 800 * 64 + 11 * 2 * 512 and gemv(ws_bytes=size(4, 100, 128, 1) - 1) == WS
+    assert size(0, 1, 64, 0) == 0 and size(257, 1, 64, 0) == 0 and size(1, 0, 64, 0) == 0 and size(1, 1, 32, 0) == 0 and size(1, 1, 64, 2) == 0
     assert gemv(b=qin(data_bytes=4 * 128 * 64 - 1)) == INVALID and gemv(b=qin(scale_bytes=4 * 2 * 512 - 1)) == INVALID

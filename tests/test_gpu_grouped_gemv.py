@@ -1,10 +1,12 @@
 """Products of a few unquantized rows with quantized weights, plain and gated, against their formulas in 64 bits.
 
 Rows of small integers give sums that are exact in FP32 in any order: FP32 results must be equal, others equal to their one
-rounding.  Rows of any values: a result is off by at most (K / 16 + 16) units of 2^-23 of the sum of magnitudes (a unit a
-step of 16 products and for each of the last sums), and by what FP32 rows lose in two FP16 halves: 2^-22 of each term, and
-2^-39 of the row's largest value (half a step of FP16 below 2^-14, with the largest brought to 2^14 at least) times the
-weights'."""
+rounding.  Rows of any values: a row's eight digits are sums of their own, each off by at most (K / 16 + 16) units of 2^-23 of
+its sum of magnitudes (a unit a step, and for each of the last sums).  A digit is the code nearest to what the one before
+leaves, which is at most a third of the block's largest value, then an eighth of that and so on: the digits' magnitudes are
+at most |x| and the block's largest value together.  What eight digits leave is half of 2^-20 in a unit in which the
+largest value of the block is 3 at least: 2^-22 of it; and for blocks so far below the row's largest value that their scale
+stops at 2^-17 of its, 2^-39 of that value."""
 import numpy as np
 import pytest
 import torch
@@ -31,11 +33,12 @@ def ids(v):
     return str(v) if len(str(v)) < 40 else "%d experts" % len(v)
 
 
-def mass_bound(x, w, k):
+def mass_bound(x, w, k, recipe):
     """Of x w^T before the last rounding (x [m, k], w [n, k] in FP64)."""
-    ax, aw = np.abs(x), np.abs(w)
+    ax, aw, b = np.abs(x), np.abs(w), 32 if recipe == MX else 16
+    top = np.repeat(ax.reshape(len(x), -1, b).max(2), b, 1)
     largest = ax.max(1, initial=0.0)[:, None] * aw.max(1, initial=0.0)[None, :]
-    return ((k / 16 + 16) * 2.0 ** -23 + 2.0 ** -22) * (ax @ aw.T) + k * 2.0 ** -39 * largest
+    return (k / 16 + 16) * 2.0 ** -23 * ((ax + top) @ aw.T) + 2.0 ** -22 * (top @ aw.T) + k * 2.0 ** -39 * largest
 
 
 # from here on rounding to the nearest gives infinity: half a step above the type's largest value
@@ -97,7 +100,7 @@ def test_any_values(recipe, dtype, split, n, k):
     x = torch.from_numpy(v).cuda().to(dtype)
     v = x.double().cpu().numpy()
     ref = by_expert(v, split, lambda e, w: w @ b.values[e].T, n)
-    bound = by_expert(v, split, lambda e, w: mass_bound(w, b.values[e], k) + 3 * 2.0 ** -23 * np.abs(w @ b.values[e].T), n)
+    bound = by_expert(v, split, lambda e, w: mass_bound(w, b.values[e], k, recipe) + 3 * 2.0 ** -23 * np.abs(w @ b.values[e].T), n)
     for out in {dtype, torch.float32}:
         got = gsa.grouped_gemv(x, b.dev(), dev_split(split), n, recipe, out_dtype=out).double().cpu().numpy()
         assert close(got, ref, bound, out)
@@ -121,7 +124,7 @@ def test_gated(recipe, act, dtype, split, n, k, groups):
     p = rng.uniform(-1, 1, rows).astype(np.float32)
     weights = [np.concatenate(b.values[e * groups:(e + 1) * groups]) for e in range(len(split))]
     h = by_expert(v, split, lambda e, w: w @ weights[e].T, 2 * n)
-    off = by_expert(v, split, lambda e, w: mass_bound(w, weights[e], k) + 3 * 2.0 ** -23 * np.abs(w @ weights[e].T), 2 * n)
+    off = by_expert(v, split, lambda e, w: mass_bound(w, weights[e], k, recipe) + 3 * 2.0 ** -23 * np.abs(w @ weights[e].T), 2 * n)
     limit, alpha, add = PARAMS[act]
     a, lin = np.minimum(h[:, :n], limit), np.clip(h[:, n:], -limit, limit) + add
     z = alpha * a
@@ -153,7 +156,7 @@ def test_rows_across_the_range(recipe, dtype):
     v = x.double().cpu().numpy()
     ref, w = v @ b.values[0].T, b.values[0]
     got = gsa.grouped_gemv(x, b.dev(), None, n, recipe, out_dtype=torch.float32).double().cpu().numpy()
-    bound = mass_bound(v, w, k) + U * np.abs(ref) + 2.0 ** -126 * (np.abs(ref) < 2.0 ** -125)
+    bound = mass_bound(v, w, k, recipe) + U * np.abs(ref) + 2.0 ** -126 * (np.abs(ref) < 2.0 ** -125)
     assert np.all(np.abs(got - ref) <= bound)
 
 
@@ -196,6 +199,14 @@ def test_infinities_and_nan(recipe, dtype):
     assert np.array_equal(np.isnan(got), np.isnan(ref))
     fine = ~np.isnan(ref)
     assert np.array_equal(got[fine], ref[fine])
+    many = torch.ones((3, k), dtype=dtype, device="cuda")
+    many[1, :9] = float("inf")    # more than eight: NaN, whatever the weights
+    many[2, 10:18] = float("-inf")
+    got = gsa.grouped_gemv(many, b.dev(), None, n, recipe, out_dtype=torch.float32).double().cpu().numpy()
+    assert np.isfinite(got[0][np.arange(n) != 73]).all() and np.isnan(got[1]).all()
+    with np.errstate(invalid="ignore"):
+        ref = (many[2].double().cpu().numpy() * w).sum(1)
+    assert np.array_equal(np.isnan(got[2]), np.isnan(ref)) and np.array_equal(got[2][~np.isnan(ref)], ref[~np.isnan(ref)])
 
 
 @pytest.mark.parametrize("recipe", [MX, NV])
