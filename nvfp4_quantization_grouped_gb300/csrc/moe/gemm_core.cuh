@@ -427,12 +427,14 @@ struct StageAt {
     int b_row_step;                                     // between B's 128-row boxes, where a block has two
     int a_boxes;                                        // single blocks: boxes of 32 rows of A that the tile has
 };
-template <bool NV, int BN, bool kPair, typename R>
+// kParts: both operands' (3), or for single blocks A's (1) or B's (2) alone, of which B's come first.
+template <bool NV, int BN, bool kPair, int kParts = 3, typename R>
 __device__ __forceinline__ void load_stage(Barriers &sh, const Stages<NV, BN, kPair> &st, int half, R &ring, const StageAt &w,
                                            bool &ok) {
     using C = Cfg<NV, BN, kPair>;
     const int s = ring.s;
-    ok = ok && tc::bar_wait(tc::smem_u32(&sh.empty[s]), ring.round ^ 1, &sh.dead);   // the first round passes
+    static_assert(kParts == 3 || !kPair, "");
+    if (kParts & 2) ok = ok && tc::bar_wait(tc::smem_u32(&sh.empty[s]), ring.round ^ 1, &sh.dead);   // the first round passes
     __syncwarp();
     const uint32_t own = tc::smem_u32(&sh.full[s]), bar = kPair ? tc::map_to(own, 0) : own;
     auto load = [&](uint32_t dst, const CUtensorMap *tm, int x, int y) {
@@ -444,14 +446,19 @@ __device__ __forceinline__ void load_stage(Barriers &sh, const Stages<NV, BN, kP
             if (half == 0) tc::bar_expect(own, 2 * C::kStageBytes);
             load(st.a(s), w.a, w.x, w.a_row);
         } else {   // the rows of a short tile only: the others' products go nowhere
-            tc::bar_expect(own, C::kStageBytes - (kRowsT / kBoxA - w.a_boxes) * kBoxA * kStageK);
-            for (int b = 0; b < w.a_boxes; ++b) load(st.a(s) + b * kBoxA * kStageK, w.a, w.x, w.a_row + b * kBoxA);
+            if (kParts & 2) tc::bar_expect(own, C::kStageBytes - (kRowsT / kBoxA - w.a_boxes) * kBoxA * kStageK);
+            if (kParts & 1)
+                for (int b = 0; b < w.a_boxes; ++b) load(st.a(s) + b * kBoxA * kStageK, w.a, w.x, w.a_row + b * kBoxA);
         }
+        if (kParts & 2) {
 #pragma unroll
-        for (int b = 0; b < C::kRowsB / 128; ++b) load(st.b(s) + b * 128 * kStageK, w.b, w.x, w.b_row + b * w.b_row_step);
-        load(st.sa(s), w.sa, 0, w.a_tile);
+            for (int b = 0; b < C::kRowsB / 128; ++b) load(st.b(s) + b * 128 * kStageK, w.b, w.x, w.b_row + b * w.b_row_step);
+        }
+        if (kParts & 1) load(st.sa(s), w.sa, 0, w.a_tile);
+        if (kParts & 2) {
 #pragma unroll
-        for (int b = 0; b < C::kGroupsB; ++b) load(st.sb(s) + b * C::kSc * kScaleTile, w.sb, 0, w.b_tile + b * w.b_tile_step);
+            for (int b = 0; b < C::kGroupsB; ++b) load(st.sb(s) + b * C::kSc * kScaleTile, w.sb, 0, w.b_tile + b * w.b_tile_step);
+        }
     }
     __syncwarp();
     ring.issued += ok;

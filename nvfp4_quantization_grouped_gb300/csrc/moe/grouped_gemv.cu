@@ -122,9 +122,15 @@ template <bool NV> __global__ void __launch_bounds__(kDigitThreads) split_digits
     __shared__ int tiles_of[kDigitThreads / 32], first_row, first_tile, most_t, infinite, nan, placed;
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     const int64_t r = blockIdx.x;
-    tc::allow_next();
+    // In this order: once the product's blocks run, everything before this kernel is done, and they read the split and the
+    // weights without waiting for the digits.
     tc::wait_for_previous();
+    tc::allow_next();
     if (t == 0) first_row = -1, most_t = kNone, infinite = 0, nan = 0, placed = 0;
+    const int blocks = P.K / B;
+    const bool once = blocks <= kDigitThreads;   // a block a thread: read once
+    float v[B];
+    if (once && t < blocks) load_block<B>(P.x, P.x_type, r * P.K + static_cast<int64_t>(t) * B, v);
     // the expert that has the row: its first row and scale tile
     int64_t m = t < P.E ? (P.split ? P.split[t] : P.M) : 0;
     if (m < 0 || m > P.M) m = 0;   // (a bad split: the product reports it and writes nothing)
@@ -142,10 +148,8 @@ template <bool NV> __global__ void __launch_bounds__(kDigitThreads) split_digits
     for (int k = 0; k < w; ++k) rows += rows_of[k], tiles += tiles_of[k];
     if (r < rows && r >= rows - m) first_row = static_cast<int>(rows - m), first_tile = tiles - own_tiles;
 
-    const int blocks = P.K / B;
-    float v[B];
     auto load = [&](int b, bool &finite) {   // -> the block's largest magnitude
-        load_block<B>(P.x, P.x_type, r * P.K + static_cast<int64_t>(b) * B, v);
+        if (!once) load_block<B>(P.x, P.x_type, r * P.K + static_cast<int64_t>(b) * B, v);
         float most = 0.0f;
         finite = true;
 #pragma unroll
@@ -218,9 +222,6 @@ template <bool NV> __global__ void __launch_bounds__(kDigitThreads) split_digits
     if (!special || is_nan) return;
     __syncthreads();   // the zeros are there
     for (int b = t; b < blocks; b += kDigitThreads) {
-        bool finite;
-        load(b, finite);
-        if (finite) continue;
         for (int i = 0; i < B; ++i) {
             const float x = P.x_type == GSA_FP32 ? static_cast<const float *>(P.x)[r * P.K + b * B + i]
                             : P.x_type == GSA_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(P.x)[r * P.K + b * B + i])
@@ -295,7 +296,6 @@ template <bool NV, bool kGlu, bool kClamp> __global__ void __launch_bounds__(kTh
     const Stages<NV, BN, false> st(dyn);
     open_block<C::kStages, false>(sh, warp, 1, C::kCols);
     tc::allow_next();
-    tc::wait_for_previous();
     scan_split<kRowsT, kDigits>(P, sh);
     if (sh.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(P.status, ERR_SPLIT);
     const int total = known_uniform(sh.bad ? 0 : sh.tile0[P.E + 1]), used = known_uniform(sh.bad ? 0 : sh.tile0[P.E]);   // row tiles; the rest is zeros
@@ -308,8 +308,7 @@ template <bool NV, bool kGlu, bool kClamp> __global__ void __launch_bounds__(kTh
         }
         Ring<C::kStages> ring;
         bool ok = true;
-        for (; walk.q < used; walk.next(P)) {
-            const Tile t = walk.tile<kRowsT>(P, sh);
+        auto at = [&](const Tile &t) {
             StageAt w{&P.tm_a, &P.tm_b, &P.tm_sa, &P.tm_sb};
             w.x = 0;
             w.a_row = t.row;
@@ -319,13 +318,35 @@ template <bool NV, bool kGlu, bool kClamp> __global__ void __launch_bounds__(kTh
             w.b_row_step = static_cast<int>(P.N);
             w.b_tile = (t.g * P.b_scale_rows + t.nt) * P.scale_cols;
             w.b_tile_step = P.up_tiles * P.scale_cols;
+            return w;
+        };
+        // While the digits are written: the first stages' weights.  (Further ones into L2 as well gained nothing.)
+        Walk ahead = walk;
+        int early = 0;
+        for (; ahead.q < used && early < C::kStages; ahead.next(P)) {
+            StageAt w = at(ahead.tile<kRowsT>(P, sh));
+            for (int k = 0; k < P.kt && early < C::kStages; ++k, ++early) {
+                load_stage<NV, BN, false, 2>(sh, st, 0, ring, w, ok);
+                w.x += kStageK, w.b_tile += C::kSc;
+            }
+        }
+        tc::wait_for_previous();
+        ring = Ring<C::kStages>();
+        for (; walk.q < used; walk.next(P)) {
+            StageAt w = at(walk.tile<kRowsT>(P, sh));
             for (int k = 0; k < P.kt; ++k) {
-                load_stage(sh, st, 0, ring, w, ok);
+                if (early > 0) {
+                    --early;
+                    load_stage<NV, BN, false, 1>(sh, st, 0, ring, w, ok);
+                } else {
+                    load_stage(sh, st, 0, ring, w, ok);
+                }
                 w.x += kStageK, w.a_tile += C::kSc, w.b_tile += C::kSc;
             }
         }
         end_loads<C::kStages>(sh, 0, ring.issued, ok);
     } else if (warp == 1) {
+        tc::wait_for_previous();   // (all of the block's warps, that it does not end before the digits' kernel)
         Ring<C::kStages> ring;
         int n = 0;
         bool ok = true;
@@ -335,6 +356,7 @@ template <bool NV, bool kGlu, bool kClamp> __global__ void __launch_bounds__(kTh
         const int q = warp & 3, h = (warp - kDrain) >> 2, digit = lane & (kDigits - 1);   // lanes 32 q .., columns from 64 h
         int n = 0, last = -1;
         Scale gate, linear;
+        tc::wait_for_previous();
         for (; walk.q < total; walk.next(P)) {
             const Tile t = walk.tile<kRowsT>(P, sh);
             const int rows = t.rows - 32 * q;   // of digits
