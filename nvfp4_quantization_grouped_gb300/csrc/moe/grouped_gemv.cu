@@ -45,32 +45,25 @@ struct DigitParams {
     int scale_cols;
 };
 
-// Sixteen (NVFP4) or thirty-two values of a block, in FP32.
-template <int B> __device__ __forceinline__ void load_block(const void *x, int type, int64_t i, float (&v)[B]) {
+// Eight values, in FP32.
+__device__ __forceinline__ void load8(const void *x, int type, int64_t i, float (&v)[8]) {
     if (type == GSA_FP32) {
         const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i);
-#pragma unroll
-        for (int j = 0; j < B / 4; ++j) {
-            const float4 a = __ldg(p + j);
-            v[4 * j] = a.x, v[4 * j + 1] = a.y, v[4 * j + 2] = a.z, v[4 * j + 3] = a.w;
-        }
+        const float4 a = __ldg(p), b = __ldg(p + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         return;
     }
-    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i);
+    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int j = 0; j < B / 8; ++j) {
-        const uint4 a = __ldg(p + j);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (type == GSA_BF16) {
-                v[8 * j + 2 * k] = __uint_as_float(w[k] << 16), v[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-            } else {
-                __half2 h;
-                memcpy(&h, &w[k], 4);
-                const float2 f = __half22float2(h);
-                v[8 * j + 2 * k] = f.x, v[8 * j + 2 * k + 1] = f.y;
-            }
+    for (int k = 0; k < 4; ++k) {
+        if (type == GSA_BF16) {
+            v[2 * k] = __uint_as_float(w[k] << 16), v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        } else {
+            __half2 h;
+            memcpy(&h, &w[k], 4);
+            const float2 f = __half22float2(h);
+            v[2 * k] = f.x, v[2 * k + 1] = f.y;
         }
     }
 }
@@ -111,13 +104,13 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi, float &a, float &
     return c;
 }
 
-constexpr int kDigitThreads = 256, kNone = -100000;
+constexpr int kDigitThreads = 512, kNone = -100000;
 
-// Digits of row blockIdx.x.  Infinite values get digits of their own (one each, the first eight; finite values are nothing
+// Digits of row blockIdx.x, eight values a thread: two (NVFP4) or four lanes a block.  Infinite values get digits of their own (one each, the first eight; finite values are nothing
 // beside them): products with them have the sign or, of zero weights, the NaN that the weights give.  A NaN, or more infinities,
 // makes the row NaN by a NaN scale.
 template <bool NV> __global__ void __launch_bounds__(kDigitThreads) split_digits(const __grid_constant__ DigitParams P) {
-    constexpr int B = NV ? 16 : 32, kWord = NV ? 8 : 4;   // values of a block, codes of a 32-bit word
+    constexpr int kLanes = NV ? 2 : 4;   // of a block
     __shared__ int64_t rows_of[kDigitThreads / 32];
     __shared__ int tiles_of[kDigitThreads / 32], first_row, first_tile, most_t, infinite, nan, placed;
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
@@ -127,10 +120,13 @@ template <bool NV> __global__ void __launch_bounds__(kDigitThreads) split_digits
     tc::wait_for_previous();
     tc::allow_next();
     if (t == 0) first_row = -1, most_t = kNone, infinite = 0, nan = 0, placed = 0;
-    const int blocks = P.K / B;
-    const bool once = blocks <= kDigitThreads;   // a block a thread: read once
-    float v[B];
-    if (once && t < blocks) load_block<B>(P.x, P.x_type, r * P.K + static_cast<int64_t>(t) * B, v);
+    const int parts = P.K / 8, rounded = (parts + 31) & ~31;   // of eight values; whole warps go round
+    const bool once = parts <= kDigitThreads;                  // a part a thread: read once
+    float v[8] = {};
+    auto load = [&](int i) {
+        if (i < parts) load8(P.x, P.x_type, r * P.K + static_cast<int64_t>(i) * 8, v);
+    };
+    load(t);
     // the expert that has the row: its first row and scale tile
     int64_t m = t < P.E ? (P.split ? P.split[t] : P.M) : 0;
     if (m < 0 || m > P.M) m = 0;   // (a bad split: the product reports it and writes nothing)
@@ -148,29 +144,30 @@ template <bool NV> __global__ void __launch_bounds__(kDigitThreads) split_digits
     for (int k = 0; k < w; ++k) rows += rows_of[k], tiles += tiles_of[k];
     if (r < rows && r >= rows - m) first_row = static_cast<int>(rows - m), first_tile = tiles - own_tiles;
 
-    auto load = [&](int b, bool &finite) {   // -> the block's largest magnitude
-        if (!once) load_block<B>(P.x, P.x_type, r * P.K + static_cast<int64_t>(b) * B, v);
+    auto largest = [&](int i, bool &finite) {   // of the block that part i is in; its other lanes are here too
+        if (!once) load(i);
         float most = 0.0f;
         finite = true;
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            finite &= fabsf(v[i]) <= 3.402823466e38f;
-            most = fmaxf(most, fabsf(v[i]));
+        for (int k = 0; k < 8; ++k) {
+            finite &= fabsf(v[k]) <= 3.402823466e38f;
+            most = fmaxf(most, fabsf(v[k]));
         }
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
         return most;
     };
     int mine = kNone;
-    for (int b = t; b < blocks; b += kDigitThreads) {
+    for (int i = t; i < rounded; i += kDigitThreads) {
         bool finite;
-        const float most = load(b, finite);
-        if (finite) {
-            if (most > 0.0f) mine = max(mine, block_exponent<NV>(most));
-            continue;
-        }
+        const float most = largest(i, finite);
+        if (i >= parts) continue;
+        if (most > 0.0f && most <= 3.402823466e38f) mine = max(mine, block_exponent<NV>(most));
+        if (finite) continue;
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            if (v[i] != v[i]) nan = 1;
-            else if (isinf(v[i])) atomicAdd(&infinite, 1);
+        for (int k = 0; k < 8; ++k) {
+            if (v[k] != v[k]) nan = 1;
+            else if (isinf(v[k])) atomicAdd(&infinite, 1);
         }
     }
     mine = __reduce_max_sync(0xFFFFFFFFu, mine);
@@ -186,54 +183,51 @@ template <bool NV> __global__ void __launch_bounds__(kDigitThreads) split_digits
     if (first_row < 0 || tile < 0 || tile >= P.tiles) return;
     const int64_t pitch = NV ? P.K / 2 : P.K;
     uint8_t *codes = P.codes + r * kDigits * pitch, *scales = P.scales + tile * P.scale_cols * kScaleTile + 16 * (lr & 31) + 4 * (lr >> 5);
-    for (int b = t; b < blocks; b += kDigitThreads) {
+    for (int i = t; i < rounded; i += kDigitThreads) {
         bool finite;
-        const float most = load(b, finite);
+        const float most = largest(i, finite);
+        if (i >= parts) continue;
+        const int b = i / kLanes;
         int q = kLow;
         if (most > 0.0f && !special) q = max(kLow, block_exponent<NV>(most) - row_t);
         uint8_t scale = NV ? (q >= -6 ? (q + 7) << 3 : 1 << (q + 9)) : q + 127;
         if (special) scale = is_nan ? (NV ? 0x7F : 0xFF) : (NV ? 7 << 3 : 127);
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < B; ++i) v[i] = special ? 0.0f : times_power(v[i], -row_t - q);
+        for (int k = 0; k < 8; ++k) x[k] = special ? 0.0f : times_power(v[k], -row_t - q);
 #pragma unroll
         for (int d = 0; d < kDigits; ++d) {
-            uint32_t c[B / kWord];
+            uint32_t c[NV ? 1 : 2] = {};
             const float next = NV ? (d == 0 ? 4.0f : 8.0f) : (d == 0 ? 16.0f : 32.0f);
 #pragma unroll
-            for (int i = 0; i < B; i += kWord) {
-                c[i / kWord] = 0;
-#pragma unroll
-                for (int j = i; j < i + kWord; j += 2) {
-                    float lo, hi;
-                    c[i / kWord] |= (NV ? e2m1x2(v[j], v[j + 1], lo, hi) : e4m3x2(v[j], v[j + 1], lo, hi)) << (NV ? 4 : 8) * (j - i);
-                    v[j] = (v[j] - lo) * next, v[j + 1] = (v[j + 1] - hi) * next;
-                }
+            for (int k = 0; k < 8; k += 2) {
+                float lo, hi;
+                if (NV) c[0] |= e2m1x2(x[k], x[k + 1], lo, hi) << 4 * k;
+                else c[k / 4] |= e4m3x2(x[k], x[k + 1], lo, hi) << 8 * (k % 4);
+                x[k] = (x[k] - lo) * next, x[k + 1] = (x[k + 1] - hi) * next;
             }
-            uint8_t *to = codes + d * pitch + b * (NV ? 8 : 32);
-            if constexpr (NV) {
-                *reinterpret_cast<uint2 *>(to) = make_uint2(c[0], c[1]);
-            } else {
-                *reinterpret_cast<uint4 *>(to) = make_uint4(c[0], c[1], c[2], c[3]);
-                *reinterpret_cast<uint4 *>(to + 16) = make_uint4(c[4], c[5], c[6], c[7]);
-            }
-            scales[static_cast<int64_t>(b >> 2) * kScaleTile + 16 * d + (b & 3)] = scale;
+            uint8_t *to = codes + d * pitch + static_cast<int64_t>(i) * (NV ? 4 : 8);
+            if constexpr (NV) *reinterpret_cast<uint32_t *>(to) = c[0];
+            else *reinterpret_cast<uint2 *>(to) = make_uint2(c[0], c[1]);
         }
+        // the block's scale, the same for its eight digits: a few of them by each of its lanes
+#pragma unroll
+        for (int d = 0; d < kDigits / kLanes; ++d)
+            scales[static_cast<int64_t>(b >> 2) * kScaleTile + 16 * (i % kLanes * (kDigits / kLanes) + d) + (b & 3)] = scale;
     }
     if (!special || is_nan) return;
     __syncthreads();   // the zeros are there
-    for (int b = t; b < blocks; b += kDigitThreads) {
-        for (int i = 0; i < B; ++i) {
-            const float x = P.x_type == GSA_FP32 ? static_cast<const float *>(P.x)[r * P.K + b * B + i]
-                            : P.x_type == GSA_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(P.x)[r * P.K + b * B + i])
-                                                   : __half2float(static_cast<const __half *>(P.x)[r * P.K + b * B + i]);
-            if (!isinf(x)) continue;
-            float a, z;
-            const int k = b * B + i;
-            uint8_t *row = codes + atomicAdd(&placed, 1) * pitch;   // whichever digit: sums of infinities have no order
-            const float s = copysignf(1.0f, x);
-            if (NV) row[k / 2] = static_cast<uint8_t>(k & 1 ? e2m1x2(0.0f, s, a, z) : e2m1x2(s, 0.0f, a, z));
-            else row[k] = static_cast<uint8_t>(e4m3x2(s, 0.0f, a, z));
-        }
+    for (int k = t; k < P.K; k += kDigitThreads) {
+        const int64_t i = r * P.K + k;
+        const float x = P.x_type == GSA_FP32   ? static_cast<const float *>(P.x)[i]
+                        : P.x_type == GSA_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(P.x)[i])
+                                               : __half2float(static_cast<const __half *>(P.x)[i]);
+        if (!isinf(x)) continue;
+        float a, z;
+        uint8_t *row = codes + atomicAdd(&placed, 1) * pitch;   // whichever digit: sums of infinities have no order
+        const float s = copysignf(1.0f, x);
+        if (NV) row[k / 2] = static_cast<uint8_t>(k & 1 ? e2m1x2(0.0f, s, a, z) : e2m1x2(s, 0.0f, a, z));
+        else row[k] = static_cast<uint8_t>(e4m3x2(s, 0.0f, a, z));
     }
 }
 

@@ -812,18 +812,24 @@ def grouped_gemm_wgrad(a: dict, b: dict, split, m: int, n: int, k: int, recipe_k
     return out
 
 
-def _gated(what, act, params, probs, m, b_groups, dev):
-    """(activation code, its parameters or None, pointer of probs [m]) of a gated projection."""
+def _activation(what, act, params, b_groups):
+    """(activation code, its parameters) of a gated projection."""
     kind = ACT.get(act) if isinstance(act, str) else int(act)
     if kind not in GLU_ACTS:
         raise GsaError(1, f"{what}: activation {act} (swiglu or clamped_swiglu expected)")
     if b_groups != 1 and b_groups != 2:
         raise GsaError(1, f"{what}: b_groups {b_groups} (1 or 2 expected)")
+    return kind, params or act_params(kind)
+
+
+def _gated(what, act, params, probs, m, b_groups, dev):
+    """The same, and the pointer of probs [m] or None."""
+    kind, prm = _activation(what, act, params, b_groups)
     if probs is None:
-        return kind, params or act_params(kind), None
-    _require(probs, what + ": probs", (m,), _torch.float32)
+        return kind, prm, None
+    _require(probs, what, (m,), _torch.float32)
     _same_device(what, dev, probs)
-    return kind, params or act_params(kind), probs.data_ptr()
+    return kind, prm, probs.data_ptr()
 
 
 def grouped_glu(a: dict, b: dict, split, m: int, n: int, k: int, recipe_kind: int, act="swiglu", probs=None,
@@ -877,39 +883,64 @@ def grouped_glu_bwd(dy, a: dict, b: dict, split, m: int, n: int, k: int, recipe_
     return dx, dprobs if want_dprobs else None
 
 
-def _few_rows(what, x, b, split, b_groups, recipe_kind, n, out_dtype, out, stream):
-    """(QIn of b, its tensors, split's pointer, experts, out, its type's code, workspace, its bytes) of a product of
-    unquantized rows."""
-    torch = _torch or _setup()
-    if x.dim() != 2 or x.dtype not in _DTYPES:
-        raise GsaError(1, f"{what}: x must be bfloat16, float16 or float32 [rows, k], got {x.dtype} {list(x.shape)}")
-    _require(x, what + ": x", x.shape, x.dtype)
-    dev, sp, experts = x.device, None, 1
+_few_bytes: dict = {}   # workspace bytes by sizes
+
+
+def _few_rows(what, x, b, split, b_groups, recipe_kind, n, out_dtype, out, stream, act=None):
+    """A product of unquantized rows.  act: (activation code, parameters, probs) of a gated one."""
+    dt, dev = x.dtype, x.device
+    x_code = _DTYPES.get(dt)
+    if x_code is None or x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise GsaError(1, f"{what}: x must be contiguous CUDA bfloat16, float16 or float32 [rows, k], got {x.device} {dt} "
+                          f"{list(x.shape)}{'' if x.is_contiguous() else ' (not contiguous)'}")
+    m, k = x.shape
+    sp, experts = None, 1
     if split is not None:
-        if split.dim() != 1:
-            raise GsaError(1, f"{what}: split must be [experts]")
-        _require(split, what + ": split", split.shape, torch.int64)
-        _same_device(what, dev, split)
-        sp, experts = split.data_ptr(), split.shape[0]
-    qb, *tb = _operand(b, "row", recipe_kind, experts * b_groups, what + ": b", dev)
-    out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
-    if out_dtype not in _DTYPES:
+        if split.dtype is not _torch.int64 or split.dim() != 1 or not split.is_cuda or not split.is_contiguous():
+            raise GsaError(1, f"{what}: contiguous CUDA int64 [experts] split expected, got {split.device} {split.dtype} {list(split.shape)}")
+        if split.device != dev:
+            _same_device(what, dev, split)
+        sp, experts = split.data_ptr(), split.numel()
+    kind = prm = probs = pp = None
+    if act is not None:
+        kind, prm, probs = act
+        if probs is not None:
+            _require(probs, what, (m,), _torch.float32)
+            _same_device(what, dev, probs)
+            pp = probs.data_ptr()
+    qb, data, scale, amax = _operand(b, "row", recipe_kind, experts * b_groups, what, dev)
+    if out_dtype is None:
+        out_dtype, code = (dt, x_code) if out is None else (out.dtype, _DTYPES.get(out.dtype))
+    else:
+        code = _DTYPES.get(out_dtype)
+    if code is None:
         raise GsaError(1, f"{what}: output type {out_dtype} (bfloat16, float16 or float32 expected)")
-    out = _out(out, what + ": out", (x.shape[0], n), out_dtype, dev, stream)
-    nbytes = _lib.gsa_grouped_gemv_workspace_size(experts, x.shape[0], x.shape[1], recipe_kind)
-    return qb, tb, sp, experts, out, _DTYPES[out_dtype], _out(None, "", (max(256, nbytes),), torch.uint8, dev, stream), nbytes
+    key = (experts, m, k, recipe_kind)
+    nbytes = _few_bytes.get(key)
+    if nbytes is None:
+        if len(_few_bytes) > 4096:
+            _few_bytes.clear()
+        nbytes = _few_bytes[key] = _lib.gsa_grouped_gemv_workspace_size(*key)
+    out = _out(out, what, (m, n), out_dtype, dev, stream)
+    ws = _out(None, "", (nbytes or 256,), _torch.uint8, dev, stream)
+    s = _stream_of(stream, dev, x, split, probs, data, scale, amax)
+    if act is None:
+        st = _lib.gsa_grouped_gemv(x.data_ptr(), x_code, qb, sp, experts, m, n, k, recipe_kind, out.data_ptr(), code, ws.data_ptr(), nbytes, s)
+    else:
+        st = _lib.gsa_grouped_glu_gemv(x.data_ptr(), x_code, qb, sp, experts, m, n, k, recipe_kind, kind, prm, pp, b_groups,
+                                       out.data_ptr(), code, ws.data_ptr(), nbytes, s)
+    if st:
+        _check(st, "gsa_" + what)
+    return out
 
 
 def grouped_gemv(x, b: dict, split, n: int, recipe_kind: int, out_dtype=None, out=None, stream=None):
     """out [rows, n] = x B_e^T over the rows of each expert, for a few unquantized rows an expert (decoding): x [rows, k]
     bfloat16, float16 or float32; b, split as for grouped_gemm (split None: one matrix takes all rows).  out_dtype: any
-    of the three (default: x's)."""
-    qb, tb, sp, experts, out, code, ws, nbytes = _few_rows("grouped_gemv", x, b, split, 1, recipe_kind, n, out_dtype, out, stream)
-    st = _lib.gsa_grouped_gemv(x.data_ptr(), _DTYPES[x.dtype], qb, sp, experts, x.shape[0], n, x.shape[1], recipe_kind,
-                               out.data_ptr(), code, ws.data_ptr(), nbytes, _stream_of(stream, x.device, x, split, *tb))
-    if st:
-        _check(st, "gsa_grouped_gemv")
-    return out
+    of the three (default: x's).  x keeps its precision: within 2^-22 of the largest value of its block of 16 (NVFP4) or
+    32 (MXFP8)."""
+    _torch or _setup()
+    return _few_rows("grouped_gemv", x, b, split, 1, recipe_kind, n, out_dtype, out, stream)
 
 
 def grouped_glu_gemv(x, b: dict, split, n: int, recipe_kind: int, act="swiglu", probs=None, params: ActParams | None = None,
@@ -917,14 +948,8 @@ def grouped_glu_gemv(x, b: dict, split, n: int, recipe_kind: int, act="swiglu", 
     """grouped_glu for a few unquantized rows an expert: y [rows, n] = probs * act(x Bg_e^T, x Bl_e^T), x as for
     grouped_gemv, the rest as for grouped_glu."""
     _torch or _setup()
-    kind, prm, pp = _gated("grouped_glu_gemv", act, params, probs, x.shape[0], b_groups, x.device)
-    qb, tb, sp, experts, out, code, ws, nbytes = _few_rows("grouped_glu_gemv", x, b, split, b_groups, recipe_kind, n, out_dtype, out, stream)
-    st = _lib.gsa_grouped_glu_gemv(x.data_ptr(), _DTYPES[x.dtype], qb, sp, experts, x.shape[0], n, x.shape[1], recipe_kind, kind, prm,
-                                   pp, b_groups, out.data_ptr(), code, ws.data_ptr(), nbytes,
-                                   _stream_of(stream, x.device, x, split, probs, *tb))
-    if st:
-        _check(st, "gsa_grouped_glu_gemv")
-    return out
+    kind, prm = _activation("grouped_glu_gemv", act, params, b_groups)
+    return _few_rows("grouped_glu_gemv", x, b, split, b_groups, recipe_kind, n, out_dtype, out, stream, (kind, prm, probs))
 
 
 def grouped_gemm_status(stream=None) -> int:
