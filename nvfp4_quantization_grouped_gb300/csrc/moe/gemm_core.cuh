@@ -612,6 +612,14 @@ bool map_scales(CUtensorMap *tm, const void *p, int64_t tiles, int box) {
 struct PerDevice {
     std::mutex mu;
     int n[64] = {};
+    bool did[64] = {};
+    template <typename F> bool once(F &&act) {   // false: a CUDA error
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!did[dev]) did[dev] = act() == cudaSuccess;
+        return did[dev];
+    }
     template <typename F> int get(F &&ask) {   // 0: a CUDA error
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
@@ -634,21 +642,20 @@ int sm_count() {
 template <bool kPair, typename P>
 gsa_status launch(void (*kernel)(P), const P &params, int threads, size_t smem, int64_t want, cudaStream_t s, PerDevice &pairs) {
     const int sms = sm_count();
-    if (!sms) return cuda_error();
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    if (!sms || !pairs.once([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)); }))
         return cuda_error();
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kPair ? 2 : 1;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see wait_for_previous
-    at[1].val.programmaticStreamSerializationAllowed = 1;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see wait_for_previous
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = kPair ? 2 : 1;
     int64_t units = sms;
     if (kPair) {   // the machine's clusters may not fill every SM
         units = pairs.get([&](int, int &v) {
