@@ -9,16 +9,22 @@
 // linear side: a pair of blocks loads one each, the draining warps find g and u of an element
 // in the same lane, and neither is rounded or written.  The gradient multiplies again instead
 // of reading them: a training step keeps only the quantized rows, which the weight gradient
-// needs anyway.  A lane holds a row's 64 columns, so dp takes no shuffles: each warp writes a
+// needs anyway.  A lane holds a row's 32 columns, so dp takes no shuffles: each warp writes a
 // partial sum a row, and a second kernel adds them in order.
+//   65536 rows over 32 experts, N and K 2048, NVFP4: 197 us alone in a graph (5.6 PFLOP/s; 5900
+// cycles a tile, of which products and scale copies take 5700), 212 to 220 among other calls;
+// gradient 276 to 287: its 64 KB of results a tile share the block's way to L2 with the operands'
+// copies (without the stores 204 us, with all of them to one small region no less than with).
+// 262144 x 4096 x 2048 MXFP8 over 128 experts: 3080 to 3150 us (2.8 PFLOP/s, what the power limit
+// leaves).  512 rows over 128 experts, 2048 x 2048 NVFP4: 66 to 71 us, the weights at 6.1 TB/s.
 #include "gemm_core.cuh"
 #include "glu_act.cuh"
 
 namespace {
 
 constexpr int kBN = 256, kSide = kBN / 2, kCols = 32;   // columns of a tile; of one side; of one side that a warp drains
-// Sixteen warps drain (8 in the grouped product): two of them a scheduler cannot hide the latencies of the activation, with
-// the registers that 64 accumulators a side leave them (gradient, 65536 x 2048 x 2048 NVFP4: @@ -> @@ us).
+// Sixteen warps drain (8 in the grouped product): with 64 accumulators a side a warp has too few registers left to work on
+// several elements at once (gradient, 65536 x 2048 x 2048 NVFP4: 323 -> 287 us).
 constexpr int kWarps = 16, kGluThreads = 32 * (kDrain + kWarps);
 constexpr int kBuf = 32 * 64;   // a warp's piece of dy or results: 32 rows x 64 bytes
 static_assert(kGluThreads <= kMaxThreads, "threads");
@@ -89,8 +95,8 @@ template <int kBytes, typename T> __device__ __forceinline__ void store_lane(con
 }
 
 // A warp's 32 x 32 results, a row a lane, to memory.  Whole sectors from the lanes' registers wherever rows start on them:
-// shared memory is what the products and their copies live on (117 of its 128 bytes a cycle, NVFP4), and passing results
-// through it slows them (@@).  Else by way of the warp's buffer.
+// the products and their copies use most of shared memory's bandwidth, and results that pass through it slow them (forward,
+// 65536 x 2048 x 2048 NVFP4: 220 -> 216 us).  Else by way of the warp's buffer.
 template <typename T> __device__ __forceinline__ void store_rows(const uint32_t *v, uint32_t buf, const OutAt<T> &w, int lane) {
     if (w.wide) {
         if ((w.pitch | w.cols) * sizeof(T) % 32 == 0 && reinterpret_cast<uintptr_t>(w.o) % 32 == 0) store_lane<32>(v, w, lane);
@@ -366,7 +372,11 @@ gsa_status glu_params(GluParams &P, bool &pair, int64_t &tiles, const gsa_qin *a
         return GSA_ERR_INVALID_ARG;
     if (a_rows * cols >= (int64_t(1) << 31) || 2 * E * n128 * cols >= (int64_t(1) << 31)) return GSA_ERR_UNSUPPORTED;
     if (!has_space) return GSA_ERR_WORKSPACE;
-    pair = M >= 128 * E;
+    // Pairs of blocks (256 rows) from 128 rows an expert on and where they fill the machine, single blocks (128 rows) else.
+    // Pairs / singles, us, even splits of 128 experts, 2048 x 2048: 96 rows an expert 113 / 103 (NVFP4), 197 / 180 (MXFP8),
+    // gradient 138 / 134 and 226 / 203; 128 rows 116 / 113, 200 / 200, 147 / 161, 233 / 224; 192 rows 120 / 133, 204 / 239,
+    // 155 / 197, 244 / 267.  Few tiles, 8 experts x 256 rows, 1024 x 1024: 9.9 / 8.7, 11.5 / 10.7, 17.2 / 14.9, 18.2 / 16.4.
+    pair = M >= 128 * E && M / 256 * n128 >= 76;
     const int sc = nv ? 4 : 1;
     if (!map_codes(&P.tm_a, a->data, M, k_bytes, pair ? kRowsT : kBoxA) || !map_codes(&P.tm_b, b->data, 2 * E * N, k_bytes, 128) ||
         !map_scales(&P.tm_sa, a->scale, a_rows * cols, sc) || !map_scales(&P.tm_sb, b->scale, 2 * E * n128 * cols, sc))
