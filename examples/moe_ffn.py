@@ -1,11 +1,14 @@
 """A mixture-of-experts FFN on quantized operands, forward and backward, from this library's calls alone.
 
     python examples/moe_ffn.py [--recipe mxfp8|nvfp4] [--tokens 4096] [--experts 16] [--topk 4] [--hidden 1024]
-                               [--width 1024] [--act srelu]
+                               [--width 1024] [--act srelu|identity|swiglu]
 
 Forward:  sort the routed tokens by expert -> gather their rows -> quantize -> first projection -> scaled activation
 fused with the quantization of its result -> second projection -> sum each token's expert rows.
 Backward: the same way back, with both input gradients, both weight gradients and the router probabilities' gradient.
+Gated activations of widths that are multiples of 128 are the first projection's epilogue: its result is not written in
+front of the activation, and the backward multiplies again instead of keeping it.
+Decoding: both projections of a few rows an expert without quantizing them (gated activations).
 The split stays on the device throughout: nothing waits for the host, and a step can be captured in a CUDA graph.
 """
 import argparse
@@ -30,6 +33,8 @@ class MoeFfn:
         self.experts, self.w_in, self.hidden = w1.shape
         self.width = w2.shape[2]
         self.act, self.recipe, self.rht, self.mask = act, recipe, recipe == gsa.NVFP4, rht_mask
+        self.gated = act in ("swiglu", "clamped_swiglu")
+        self.fused = self.gated and self.width % 128 == 0
         self.w1, self.w2 = self._weights(w1), self._weights(w2)
 
     def _weights(self, w):
@@ -48,8 +53,12 @@ class MoeFfn:
         xs, ps = gsa.moe_permute(x, row, probs)
         m, used = xs.shape[0], split[:e]
         qx = self._quantize(xs, split)
-        h = gsa.grouped_gemm(qx, self.w1, used, m, self.w_in, self.hidden, r)
-        qy = gsa.fwd_graph_safe(h, ps, split, self.act, r, self.rht, self.mask, scale_layout=T)
+        if self.fused:
+            h = None
+            qy = self._quantize(gsa.grouped_glu(qx, self.w1, used, m, self.width, self.hidden, r, self.act, ps), split)
+        else:
+            h = gsa.grouped_gemm(qx, self.w1, used, m, self.w_in, self.hidden, r)
+            qy = gsa.fwd_graph_safe(h, ps, split, self.act, r, self.rht, self.mask, scale_layout=T)
         ys = gsa.grouped_gemm(qy, self.w2, used, m, self.hidden, self.width, r)
         return gsa.moe_unpermute(ys, row), (row, split, ps, qx, h, qy)   # the activation applied the probabilities
 
@@ -57,27 +66,40 @@ class MoeFfn:
         """-> dx [tokens, H] BF16, dprobs [tokens, topk] FP32, dw1 and dw2 FP32."""
         row, split, ps, qx, h, qy = saved
         r, e = self.recipe, self.experts
-        m, used = h.shape[0], split[:e]
+        m, used = ps.shape[0], split[:e]
         dys, _ = gsa.moe_unpermute_bwd(dout, None, row)
         qd = self._quantize(dys, split)
         dy = gsa.grouped_gemm(qd, self.w2, used, m, self.width, self.hidden, r, b_columnwise=True)
         dw2 = gsa.grouped_gemm_wgrad(qd, qy, used, m, self.hidden, self.width, r)
-        g = gsa.bwd_graph_safe(dy, h, ps, split, self.act, r, self.rht, self.mask, scale_layout=T)
+        if self.fused:
+            dh, dps = gsa.grouped_glu_bwd(dy, qx, self.w1, used, m, self.width, self.hidden, r, self.act, ps)
+            g = dict(self._quantize(dh, split), dprobs=dps)
+        else:
+            g = gsa.bwd_graph_safe(dy, h, ps, split, self.act, r, self.rht, self.mask, scale_layout=T)
         dxs = gsa.grouped_gemm(g, self.w1, used, m, self.hidden, self.w_in, r, b_columnwise=True)
         dw1 = gsa.grouped_gemm_wgrad(g, qx, used, m, self.w_in, self.hidden, r)
         dx, dprobs = gsa.moe_permute_bwd(dxs, row, g["dprobs"])
         return dx, dprobs, dw1, dw2
 
+    def decode(self, x, expert_idx, probs):
+        """The forward of a few tokens [tokens, H] (BF16, FP16 or FP32), rows as they are against the quantized weights."""
+        row, split = gsa.moe_sort(expert_idx, self.experts)
+        xs, ps = gsa.moe_permute(x, row, probs)
+        used = split[:self.experts]
+        y = gsa.grouped_glu_gemv(xs, self.w1, used, self.width, self.recipe, self.act, ps)
+        return gsa.moe_unpermute(gsa.grouped_gemv(y, self.w2, used, self.hidden, self.recipe), row)
+
 
 def reference(x, idx, probs, w1, w2, dout, act):
-    """The same step in FP32 autograd on unquantized operands, expert by expert (srelu or identity)."""
+    """The same step in FP32 autograd on unquantized operands, expert by expert (srelu, identity or swiglu)."""
     x, probs, w1, w2 = (t.float().requires_grad_() for t in (x, probs, w1, w2))
     out = torch.zeros_like(x)
     for e in range(w1.shape[0]):
         tok, slot = torch.nonzero(idx == e, as_tuple=True)
         if tok.numel():
             h = x[tok] @ w1[e].t()
-            a = torch.relu(h) ** 2 if act == "srelu" else h
+            gate, linear = h.chunk(2, 1)
+            a = torch.relu(h) ** 2 if act == "srelu" else gate * torch.sigmoid(gate) * linear if act == "swiglu" else h
             out = out.index_add(0, tok, (probs[tok, slot][:, None] * a) @ w2[e].t())
     out.backward(dout.float())
     return out.detach(), x.grad, probs.grad, w1.grad, w2.grad
@@ -86,7 +108,7 @@ def reference(x, idx, probs, w1, w2, dout, act):
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--recipe", choices=("mxfp8", "nvfp4"), default="mxfp8")
-    ap.add_argument("--act", default="srelu", choices=("srelu", "identity"))
+    ap.add_argument("--act", default="srelu", choices=("srelu", "identity", "swiglu"))
     for name, value in (("tokens", 4096), ("experts", 16), ("topk", 4), ("hidden", 1024), ("width", 1024)):
         ap.add_argument("--" + name, type=int, default=value)
     a = ap.parse_args()
@@ -96,7 +118,7 @@ def main():
     def normal(*shape, scale=1.0):
         return (torch.randn(shape, generator=g, device="cuda") * scale).to(torch.bfloat16)
 
-    w1 = normal(a.experts, a.width, a.hidden, scale=a.hidden ** -0.5)
+    w1 = normal(a.experts, a.width * (2 if a.act == "swiglu" else 1), a.hidden, scale=a.hidden ** -0.5)
     w2 = normal(a.experts, a.hidden, a.width, scale=a.width ** -0.5)
     x, dout = normal(a.tokens, a.hidden), normal(a.tokens, a.hidden)
     logits = torch.randn((a.tokens, a.experts), generator=g, device="cuda")
@@ -120,6 +142,10 @@ def main():
     end.record()
     torch.cuda.synchronize()
     print("forward + backward: %.1f us" % (start.elapsed_time(end) * 100))
+    if ffn.gated:
+        few = slice(0, 4)
+        u, v = ffn.decode(x[few], idx[few].contiguous(), probs[few].contiguous()), got[0][few]
+        print("decode  against the forward's rows: %.3f" % float((u.float() - v.float()).norm() / v.float().norm()))
 
 
 if __name__ == "__main__":
