@@ -24,7 +24,7 @@ constexpr int kRowsT = 128;          // rows of a tile: the lanes of tensor memo
 constexpr int kStageK = 128;         // bytes of k per stage: one 128-byte swizzled row
 constexpr int kScaleTile = 512;      // bytes of one 128 x 4 scale tile
 constexpr int kThreads = 384;        // warp 0 loads, warp 1 multiplies, warps 4-11 drain
-constexpr int kMaxThreads = 640;     // of the kernels that share the split's scan
+constexpr int kMaxThreads = 576;     // of the kernels that share the split's scan
 constexpr int kEpiWarps = 8, kDrain = 4;   // the draining warps, the first of them
 constexpr int kBoxA = 32;            // rows of A that single blocks load at a time
 constexpr int kOutBuf = 32 * 128;    // a draining warp's piece of results: 32 rows x 128 bytes

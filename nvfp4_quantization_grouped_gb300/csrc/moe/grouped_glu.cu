@@ -11,10 +11,13 @@
 // of reading them: a training step keeps only the quantized rows, which the weight gradient
 // needs anyway.  A lane holds a row's 32 columns, so dp takes no shuffles: each warp writes a
 // partial sum a row, and a second kernel adds them in order.
-//   65536 rows over 32 experts, N and K 2048, NVFP4: 197 us alone in a graph (5.6 PFLOP/s; 5900
+//   65536 rows over 32 experts, N and K 2048, NVFP4: 192 to 198 us alone in a graph (5.6 PFLOP/s; 5900
 // cycles a tile, of which products and scale copies take 5700), 212 to 220 among other calls;
-// gradient 276 to 287: its 64 KB of results a tile share the block's way to L2 with the operands'
-// copies (without the stores 204 us, with all of them to one small region no less than with).
+// gradient 262 to 270, 9500 cycles a tile: the draining warps' round, of which the mathematics
+// take 2400 and 64 KB of results, in whose time the load/store unit serves nothing else, 4000 (without
+// the stores 204 us).  The same with half or all of the results as TMA stores (265), with a third
+// buffer for them (268), and with the rows' operand shared by two pairs of a cluster through
+// multicast (269; forward 201).
 // 262144 x 4096 x 2048 MXFP8 over 128 experts: 3080 to 3150 us (2.8 PFLOP/s, what the power limit
 // leaves).  512 rows over 128 experts, 2048 x 2048 NVFP4: 66 to 71 us, the weights at 6.1 TB/s.
 #include "gemm_core.cuh"
@@ -25,7 +28,7 @@ namespace {
 constexpr int kBN = 256, kSide = kBN / 2, kCols = 32;   // columns of a tile; of one side; of one side that a warp drains
 // Sixteen warps drain (8 in the grouped product): with 64 accumulators a side a warp has too few registers left to work on
 // several elements at once (gradient, 65536 x 2048 x 2048 NVFP4: 323 -> 287 us).
-constexpr int kWarps = 16, kGluThreads = 32 * (kDrain + kWarps);
+constexpr int kWarps = 16, kFirst = 2, kGluThreads = 32 * (kFirst + kWarps);   // (the first of them)
 constexpr int kBuf = 32 * 64;   // a warp's piece of dy or results: 32 rows x 64 bytes
 static_assert(kGluThreads <= kMaxThreads, "threads");
 
@@ -70,56 +73,88 @@ __device__ __forceinline__ void load_dy(uint32_t buf, const OutAt<const __nv_bfl
     }
 }
 
-// 32 bytes of results to memory in one instruction, or 16.
-template <int kBytes> __device__ __forceinline__ void store_chunk(void *p, const uint32_t *x) {
-    if constexpr (kBytes == 32)
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]),
-                     "r"(x[5]), "r"(x[6]), "r"(x[7])
-                     : "memory");
-    else
-        *static_cast<uint4 *>(p) = make_uint4(x[0], x[1], x[2], x[3]);
+__device__ __forceinline__ float ld_result(uint32_t at, float) { return tc::ld_shared1(at); }
+__device__ __forceinline__ __nv_bfloat16 ld_result(uint32_t at, __nv_bfloat16) {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+    return __ushort_as_bfloat16(x);
 }
 
-// A lane's row of 32 results, straight from its registers.
-template <int kBytes, typename T> __device__ __forceinline__ void store_lane(const uint32_t *v, const OutAt<T> &w, int lane) {
-    constexpr int kPer = kBytes / sizeof(T);
-    if (lane >= w.rows) return;
-    T *o = w.o + lane * w.pitch;
+// 32 bytes of results to memory.
+__device__ __forceinline__ void store_sector(void *p, const uint32_t *x) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]),
+                 "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
+// A lane's results: a row's 32 columns, rounded to T as soon as there are eight (they then take half of the registers).
+constexpr int kPieceWords = 16;                                        // 64 bytes
+template <typename T> constexpr int kPerPiece = 64 / sizeof(T);       // columns of them
+template <typename T> struct Results {
+    uint32_t w[kCols * sizeof(T) / 4];
+    __device__ __forceinline__ void put(int j, const uint32_t *v) {   // columns j .. j + 7
+        constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
-    for (int j = 0; j < kCols; j += kPer) {
-        uint32_t x[kBytes / 4];
+        for (int i = 0; i < 8 / kPer; ++i) finish<false>(v + i * kPer, 1.0f, 1.0f, reinterpret_cast<uint32_t(&)[4]>(w[(j + i * kPer) / kPer * 4]), T());
+    }
+};
+
+// A warp's 32 x 32 results, straight from the registers: 64 bytes of an even lane's row by it and the next, then of the odd
+// one's.  (A row a lane, an instruction meets 32 lines: gradient, 65536 x 2048 x 2048 NVFP4, 278 -> 268 us.)
+template <typename T> __device__ __forceinline__ void store_pairs(const Results<T> &v, const OutAt<T> &w, int lane) {
+    constexpr int kPer = kPerPiece<T> / 2;
+    const bool odd = lane & 1;
+    const int even = lane & ~1, c = odd ? kPer : 0;
+    T *o = w.o + even * w.pitch + c;
 #pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i) finish<false>(v + j + i * (kPer / (kBytes / 16)), 1.0f, 1.0f, reinterpret_cast<uint32_t(&)[4]>(x[4 * i]), T());
-        if (j < w.cols) store_chunk<kBytes>(o + j, x);
+    for (int j = 0; j < kCols; j += 2 * kPer) {
+        const uint32_t *x = v.w + j / (2 * kPer) * kPieceWords;
+        uint32_t first[8], second[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? x[i] : x[8 + i], 1);
+            first[i] = odd ? got : x[i];
+            second[i] = odd ? x[8 + i] : got;
+        }
+        if (j + c < w.cols && even < w.rows) store_sector(o + j, first);
+        if (j + c < w.cols && even + 1 < w.rows) store_sector(o + w.pitch + j, second);
     }
 }
 
-// A warp's 32 x 32 results, a row a lane, to memory.  Whole sectors from the lanes' registers wherever rows start on them:
-// the products and their copies use most of shared memory's bandwidth, and results that pass through it slow them (forward,
-// 65536 x 2048 x 2048 NVFP4: 220 -> 216 us).  Else by way of the warp's buffer.
-template <typename T> __device__ __forceinline__ void store_rows(const uint32_t *v, uint32_t buf, const OutAt<T> &w, int lane) {
-    if (w.wide) {
-        if ((w.pitch | w.cols) * sizeof(T) % 32 == 0 && reinterpret_cast<uintptr_t>(w.o) % 32 == 0) store_lane<32>(v, w, lane);
-        else store_lane<16>(v, w, lane);
-    } else {   // rows that do not start on 16 bytes: 16 columns at a time in FP32, a column a lane, two rows at once
+// A warp's 32 x 32 results to memory.  Whole sectors from the lanes' registers wherever rows start on them: the products and
+// their copies use most of shared memory's bandwidth, and results that pass through it slow them (forward, 65536 x 2048 x 2048
+// NVFP4: 220 -> 216 us).  Else by way of the warp's buffer, 64 bytes of a row at a time.
+template <typename T> __device__ __forceinline__ void store_rows(const Results<T> &v, uint32_t buf, const OutAt<T> &w, int lane) {
+    constexpr int kPer = 16 / sizeof(T), kPiece = kPerPiece<T>;
+    if (w.wide && (w.pitch | w.cols) * sizeof(T) % 32 == 0 && reinterpret_cast<uintptr_t>(w.o) % 32 == 0) {
+        store_pairs(v, w, lane);
+        return;
+    }
 #pragma unroll
-        for (int j = 0; j < kCols; j += 16) {
-            if (j >= w.cols) break;
+    for (int j = 0; j < kCols; j += kPiece) {
+        if (j >= w.cols) break;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t x[4];
-                finish<false>(v + j + 4 * c, 1.0f, 1.0f, x, float());
-                tc::st_shared(chunk(buf, lane, c), x);
+        for (int c = 0; c < 4; ++c) tc::st_shared(chunk(buf, lane, c), v.w + j / kPiece * kPieceWords + 4 * c);
+        __syncwarp();
+        if (w.wide) {   // (16 bytes a lane straight from the registers: gradient of 4999 x 1000 x 1024 MXFP8 30 us, this way 27)
+            const int c = lane & 3;
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 8) {
+                const int r = r0 + (lane >> 2);
+                const uint4 x = tc::ld_shared(chunk(buf, r, c));
+                if (r < w.rows && j + c * kPer < w.cols) *reinterpret_cast<uint4 *>(w.o + r * w.pitch + j + c * kPer) = x;
             }
-            __syncwarp();
-            const int c = lane & 15;
+        } else {   // rows that do not start on 16 bytes: a column a lane
+            const int c = lane & (kPiece - 1);
             if (j + c < w.cols) {
 #pragma unroll 8
-                for (int r = lane >> 4; r < 32; r += 2)
-                    if (r < w.rows) w.o[r * w.pitch + j + c] = static_cast<T>(tc::ld_shared1(chunk(buf, r, c >> 2) + 4 * (c & 3)));
+                for (int r = lane / kPiece; r < 32; r += 32 / kPiece) {
+                    const uint32_t at = chunk(buf, r, c / kPer) + sizeof(T) * (c % kPer);
+                    if (r < w.rows) w.o[r * w.pitch + j + c] = ld_result(at, T());
+                }
             }
-            __syncwarp();
         }
+        __syncwarp();
     }
 }
 
@@ -212,10 +247,10 @@ __global__ void __launch_bounds__(kGluThreads, 1) grouped_glu(const __grid_const
         bool ok = true;
         for (; walk.q < used; walk.next(P)) multiply_tile<kLen>(sh, st, n, ring, P.k_bytes, ok);
         if (!ok || *static_cast<volatile uint32_t *>(&sh.dead)) settle<C::kStages>(sh.empty, ring.issued);
-    } else if (warp >= kDrain) {
-        const int q = warp & 3, h = (warp - kDrain) >> 2;   // lanes 32 q .., 32 columns of both sides from 32 h
+    } else if (warp >= kFirst) {
+        const int q = warp & 3, h = (warp - kFirst) >> 2;   // lanes 32 q .., 32 columns of both sides from 32 h
         const int r0 = half * kRowsT + 32 * q, c0 = h * kCols;
-        const uint32_t own = st.a(C::kStages) + (warp - kDrain) * kOwn<kBwd>;
+        const uint32_t own = st.a(C::kStages) + (warp - kFirst) * kOwn<kBwd>;
         uint32_t turn = 0;   // 0 or 1: which dy buffer and probs are this tile's
         auto buf = [&](uint32_t i) { return own + 2 * kProbs + (kBwd ? i * kBuf : 0); };
         int n = 0, last = -1;
@@ -283,6 +318,7 @@ __global__ void __launch_bounds__(kGluThreads, 1) grouped_glu(const __grid_const
                         if (j >= cols) v[j] = v[kCols + j] = 0;
                 }
                 float2 dp = make_float2(0.0f, 0.0f);
+                Results<T> of_gate, of_linear;
 #pragma unroll
                 for (int j = 0; j < kCols; j += 8) {
                     const uint4 x = tc::ld_shared(chunk(buf(turn), lane, j >> 3));
@@ -297,22 +333,29 @@ __global__ void __launch_bounds__(kGluThreads, 1) grouped_glu(const __grid_const
                         g[0] = __float_as_uint(dg.x), g[1] = __float_as_uint(dg.y);
                         u[0] = __float_as_uint(du.x), u[1] = __float_as_uint(du.y);
                     }
+                    of_gate.put(j, v + j);
+                    of_linear.put(j, v + kCols + j);
                 }
                 __syncwarp();
                 partial(dp.x + dp.y);
                 if (P.out) {
                     OutAt<T> w = out_at(row, nt, rows, cols);
-                    store_rows(v, buf(turn), w, lane);
+                    store_rows(of_gate, buf(turn), w, lane);
                     w.o += P.N;
-                    store_rows(v + kCols, buf(turn), w, lane);
+                    store_rows(of_linear, buf(turn), w, lane);
                 }
             } else {
+                Results<T> of_y;
 #pragma unroll
-                for (int j = 0; j < kCols; j += 2) {
-                    const float2 y = glu::mul2(glu::value<kClamp>(P.act, pair_of<NV>(v + j, ug), pair_of<NV>(v + kCols + j, uu)), p);
-                    v[j] = __float_as_uint(y.x), v[j + 1] = __float_as_uint(y.y);
+                for (int j = 0; j < kCols; j += 8) {
+#pragma unroll
+                    for (int k = j; k < j + 8; k += 2) {
+                        const float2 y = glu::mul2(glu::value<kClamp>(P.act, pair_of<NV>(v + k, ug), pair_of<NV>(v + kCols + k, uu)), p);
+                        v[k] = __float_as_uint(y.x), v[k + 1] = __float_as_uint(y.y);
+                    }
+                    of_y.put(j, v + j);
                 }
-                store_rows(v, buf(0), out_at(row, nt, rows, cols), lane);
+                store_rows(of_y, buf(0), out_at(row, nt, rows, cols), lane);
             }
             turn ^= 1;
         }
