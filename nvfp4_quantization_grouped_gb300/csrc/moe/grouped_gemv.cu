@@ -21,8 +21,10 @@
 // the digits are written.  GPU time in a graph: 32 rows over 128 experts, 2048 x 4096 NVFP4
 // 20 to 21 us (11 of them the weights' stream at the memory's rate, 4 the start and the digits,
 // 3 the end); one row, 4096 x 4096 NVFP4 10; 64 rows over 8, 4096 x 4096 MXFP8 30; gated, 8 rows
-// over 128 experts, 4096 x 2048 NVFP4 18 to 20; 64 over 128, 2048 x 2048 MXFP8 49.  The host takes
-// 17 to 23 a call (two launches), which is what small calls cost outside of graphs.
+// over 128 experts, 4096 x 2048 NVFP4 17 to 18; 64 over 128, 2048 x 2048 MXFP8 48.  The host takes
+// 17 to 23 a call (two launches and two allocations), which is what small calls cost outside of
+// graphs.  In one launch, with every block making the digits of its rows in its own stages, the
+// same calls took 46, 10, 83, 22 and 71: a row's digits are made again for each column tile.
 #include "gemm_core.cuh"
 #include "glu_act.cuh"
 
@@ -50,15 +52,15 @@ struct DigitParams {
     int scale_cols;
 };
 
-// Eight values, in FP32.
+// Eight values, in FP32.  (Plain loads: the kernel may have started before x was written, see tc::wait_for_previous.)
 __device__ __forceinline__ void load8(const void *x, int type, int64_t i, float (&v)[8]) {
     if (type == GSA_FP32) {
         const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
+        const float4 a = p[0], b = p[1];
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         return;
     }
-    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i));
+    const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + i);
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -284,10 +286,11 @@ struct Scale {
 };
 
 constexpr int kCols = 64;   // columns of a side that a warp drains
+template <bool NV, bool kGlu> using FewCfg = Cfg<NV, kGlu ? 256 : 128, false, 0>;   // results go straight from the registers
 
 template <bool NV, bool kGlu, bool kClamp> __global__ void __launch_bounds__(kThreads, 1) grouped_few(const __grid_constant__ FewParams P) {
     constexpr int BN = kGlu ? 256 : 128, kLen = kPiece<float>;
-    using C = Cfg<NV, BN, false>;
+    using C = FewCfg<NV, kGlu>;
     extern __shared__ uint8_t dyn[];
     __shared__ GemmShared sh;
     static_assert(sizeof(GemmShared) <= kStatic, "shared memory");
@@ -396,7 +399,7 @@ template <bool NV, bool kGlu, bool kClamp> __global__ void __launch_bounds__(kTh
 
 template <bool NV, bool kGlu, bool kClamp> gsa_status launch_few(const FewParams &P, int64_t tiles, cudaStream_t s) {
     static PerDevice pairs;
-    return launch<false, FewParams>(grouped_few<NV, kGlu, kClamp>, P, kThreads, Cfg<NV, kGlu ? 256 : 128, false>::kSmem, tiles * P.n_tiles, s, pairs);
+    return launch<false, FewParams>(grouped_few<NV, kGlu, kClamp>, P, kThreads, FewCfg<NV, kGlu>::kSmem, tiles * P.n_tiles, s, pairs);
 }
 
 template <bool NV> gsa_status launch_digits(const DigitParams &P, cudaStream_t s) {
