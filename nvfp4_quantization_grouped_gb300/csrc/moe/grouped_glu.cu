@@ -13,11 +13,13 @@
 // partial sum a row, and a second kernel adds them in order.
 //   65536 rows over 32 experts, N and K 2048, NVFP4: 192 to 198 us alone in a graph (5.6 PFLOP/s; 5900
 // cycles a tile, of which products and scale copies take 5700), 212 to 220 among other calls;
-// gradient 262 to 270, 9500 cycles a tile: the draining warps' round, of which the mathematics
-// take 2400 and 64 KB of results, in whose time the load/store unit serves nothing else, 4000 (without
-// the stores 204 us).  The same with half or all of the results as TMA stores (265), with a third
-// buffer for them (268), and with the rows' operand shared by two pairs of a cluster through
-// multicast (269; forward 201).
+// gradient 260 to 270, 9500 cycles a tile: the draining warps' round, of which the mathematics take
+// 2400 and 64 KB of results, which leave the block at 16 to 20 bytes a cycle, 3500 to 4000, during which
+// its load/store unit serves nothing else (without the stores 204 us; a pair that alone of all stores
+// takes as long as all do).  The same with half or all of the results as TMA stores, behind which the
+// operands' copies then wait (260 to 265), with a third buffer for them (268), with units that start
+// up to a tile apart (no change), and with the rows' operand shared by two pairs of a cluster
+// through multicast (269; forward 201).
 // 262144 x 4096 x 2048 MXFP8 over 128 experts: 3080 to 3150 us (2.8 PFLOP/s, what the power limit
 // leaves).  512 rows over 128 experts, 2048 x 2048 NVFP4: 66 to 71 us, the weights at 6.1 TB/s.
 #include "gemm_core.cuh"
