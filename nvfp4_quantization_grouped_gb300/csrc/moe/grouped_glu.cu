@@ -65,8 +65,8 @@ __device__ __forceinline__ void load_dy(uint32_t buf, const OutAt<const __nv_bfl
             const bool in = r < w.rows && 8 * c < w.cols;
             copy_async(chunk(buf, r, c), in ? w.o + r * w.pitch + 8 * c : any, in ? 16 : 0);
         }
-    } else {   // a column a lane
-#pragma unroll 8
+    } else {   // a column a lane; all rows asked for before the first is there (gradient, 167450 x 1071 x 64 NVFP4: 650 -> 550 us)
+#pragma unroll
         for (int r = 0; r < 32; ++r) {
             uint16_t x = 0;
             if (r < w.rows && lane < w.cols) x = __ldcs(reinterpret_cast<const uint16_t *>(w.o + r * w.pitch + lane));
@@ -149,7 +149,7 @@ template <typename T> __device__ __forceinline__ void store_rows(const Results<T
         } else {   // rows that do not start on 16 bytes: a column a lane
             const int c = lane & (kPiece - 1);
             if (j + c < w.cols) {
-#pragma unroll 8
+#pragma unroll 16
                 for (int r = lane / kPiece; r < 32; r += 32 / kPiece) {
                     const uint32_t at = chunk(buf, r, c / kPer) + sizeof(T) * (c % kPer);
                     if (r < w.rows) w.o[r * w.pitch + j + c] = ld_result(at, T());
