@@ -79,3 +79,27 @@ def test_a_bad_split_writes_nothing(recipe):
         gsa.grouped_glu_bwd(c.dy_dev, a, b, dev_split(split), m, n, k, recipe, out=(dx, dp))
         assert gsa.grouped_gemm_status() != 0
         assert all(bool((t == 3.0).all()) for t in (y, dx, dp))
+
+
+@pytest.mark.parametrize("recipe", [MX, NV])
+@pytest.mark.parametrize("n", [258, 260, 264, 259])
+def test_widths_that_rows_of_other_alignments_have(recipe, n):
+    """Rows that start on 4, 8, 16 and 2 bytes, with a last tile of a few columns: the columns of a width of 272 (a multiple
+    of 16, on 32 bytes) that has the same weights in front."""
+    k, wide, split = 128, 272, [5000, 37, 5600]
+    c = Case(72, recipe, split, wide, k, 2)
+    m, e = c.m, len(split)
+    kb = k if recipe == MX else k // 2
+    rows = c.qb["row_data"][:2 * e * wide * kb].view(2 * e, wide, kb)
+    b = dict(c.qb, row_data=rows[:, :n].contiguous().view(-1))   # (scale tiles: 3 of 128 rows for either width)
+    dy = c.dy_dev[:, :n].contiguous()
+    for dtype in (torch.bfloat16, torch.float32):
+        y = gsa.grouped_glu(c.qa, c.qb, c.dev, m, wide, k, recipe, "swiglu", c.probs, b_groups=2, out_dtype=dtype)
+        got = gsa.grouped_glu(c.qa, b, c.dev, m, n, k, recipe, "swiglu", c.probs, b_groups=2, out_dtype=dtype)
+        assert torch.equal(got, y[:, :n])
+        padded = torch.zeros((m, wide), dtype=torch.bfloat16, device="cuda")
+        padded[:, :n] = dy
+        dx, dp = gsa.grouped_glu_bwd(padded, c.qa, c.qb, c.dev, m, wide, k, recipe, "swiglu", c.probs, b_groups=2, out_dtype=dtype)
+        du, dpu = gsa.grouped_glu_bwd(dy, c.qa, b, c.dev, m, n, k, recipe, "swiglu", c.probs, b_groups=2, out_dtype=dtype)
+        assert torch.equal(du[:, :n], dx[:, :n]) and torch.equal(du[:, n:], dx[:, wide:wide + n]) and torch.equal(dpu, dp)
+    assert gsa.grouped_gemm_status() == 0
