@@ -192,11 +192,21 @@ template <bool NV> __device__ __forceinline__ float2 pair_of(const uint32_t *v, 
     return NV ? glu::mul2(f, u) : f;
 }
 
-// 1 / (S_A S_B).  Past FP32's end (every sum but 0 is then past it too) it stays finite: 0 times it is 0.
-__device__ __forceinline__ float unit_of(float amax_a, float amax_b) {
-    const float u = __fdiv_rn(1.0f, tensor_scale(amax_a)) * __fdiv_rn(1.0f, tensor_scale(amax_b));
-    return u > 3.402823466e38f ? 3.402823466e38f : u;
+// 1 / (S_A S_B) of a side's sums, where FP32 holds it to full precision (nearly always).  Where the product is subnormal, past
+// FP32's end, infinite or NaN: minus the smaller factor, and sums are multiplied by minus the larger one (*first) before.
+// Sums are 0 or 2^-20 to 2^53, so that this first step leaves FP32's range only where the result does, and what an infinite
+// amax makes of its zero sums is NaN.
+__device__ __forceinline__ float unit_of(float amax_a, float amax_b, float *first) {
+    const float a = __fdiv_rn(1.0f, tensor_scale(amax_a)), b = __fdiv_rn(1.0f, tensor_scale(amax_b)), u = a * b;
+    const bool near = u >= 0x1p-126f && u <= 3.402823466e38f;
+    *first = near ? 1.0f : -fmaxf(a, b);
+    return near ? u : -fminf(a, b);
 }
+
+struct GluShared : GemmShared {
+    float first[kWarps][2];   // of a warp's gate and linear sums: read where it is not 1 alone (kept in registers, of which the
+                              // gradient has too few: 269 -> 293 us, 65536 x 2048 x 2048)
+};
 
 // What a draining warp has in shared memory: a buffer for results, or (gradient) two for dy of this tile, whose place dx
 // takes, and of the next; probs of the rows of both.
@@ -210,8 +220,8 @@ __global__ void __launch_bounds__(kGluThreads, 1) grouped_glu(const __grid_const
     // Sums of the gradient in short pieces: dp is an FP32 result, and adds up what the tensor core cuts off of both sides.
     constexpr int kLen = kBwd ? kPiece<float> : kPiece<T>;
     extern __shared__ uint8_t dyn[];
-    __shared__ GemmShared sh;
-    static_assert(sizeof(GemmShared) <= kStatic, "shared memory");
+    __shared__ GluShared sh;
+    static_assert(sizeof(GluShared) <= kStatic, "shared memory");
     constexpr int kRows = kPair ? 2 * kRowsT : kRowsT;
     const int warp = known_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int unit = kPair ? blockIdx.x >> 1 : blockIdx.x, units = kPair ? gridDim.x >> 1 : gridDim.x;
@@ -325,14 +335,25 @@ __global__ void __launch_bounds__(kGluThreads, 1) grouped_glu(const __grid_const
             }
             if (NV && t.g != last) {
                 const float a = P.amax_a[t.g];
-                ug = uu = unit_of(a, P.amax_b[t.g * P.b_groups]);
-                if (P.b_groups == 2) uu = unit_of(a, P.amax_b[2 * t.g + 1]);
+                float fg, fu;
+                ug = unit_of(a, P.amax_b[t.g * P.b_groups], &fg);
+                uu = unit_of(a, P.amax_b[(t.g + 1) * P.b_groups - 1], &fu);
+                __syncwarp();
+                if (lane == 0) sh.first[warp - kFirst][0] = fg, sh.first[warp - kFirst][1] = fu;
                 last = t.g;
             }
             wait_copies();
             ask(turn ^ 1);
             uint32_t v[2 * kCols];   // columns of g, and of u
             if (!take_tile<kBN, C::kAcc, kPair, kLen, 2>(sh, n, P.kt, q, lane, c0, kSide + c0, v)) break;
+            if (NV && fminf(ug, uu) < 0.0f) {
+                const float fg = sh.first[warp - kFirst][0], fu = sh.first[warp - kFirst][1];
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) {
+                    v[j] = __float_as_uint(__uint_as_float(v[j]) * fg);
+                    v[kCols + j] = __float_as_uint(__uint_as_float(v[kCols + j]) * fu);
+                }
+            }
             const float p = P.probs ? tc::ld_shared1(own + turn * kProbs + 4 * lane) : 1.0f;
             if (kBwd) {
                 if (cols < kCols) {   // past the last column: whatever the next rows and the scales' padding give, NaN too
