@@ -36,10 +36,25 @@ class MoeFfn:
         self.gated = act in ("swiglu", "clamped_swiglu")
         self.fused = self.gated and self.width % 128 == 0
         self.w1, self.w2 = self._weights(w1), self._weights(w2)
+        self.w1_sides = self._by_side(self.w1) if self.gated and not self.fused else None
 
     def _weights(self, w):
         e, n, k = w.shape
         return gsa.fwd(w.reshape(e * n, k), None, [n] * e, "identity", self.recipe, scale_layout=T)
+
+    def _by_side(self, q):
+        """The rowwise copy of w1 as gate rows and linear rows of their own (b_groups = 2), for widths that are no multiple of
+        128: the same codes, block scales and units; the linear rows' scales start on a tile."""
+        e, w = self.experts, self.width
+        before, after = -(-2 * w // 128), -(-w // 128)
+        c4 = q["row_scale"].numel() // (e * before * 512)
+        rows = q["row_scale"].view(e, before, c4, 32, 4, 4).permute(0, 1, 4, 3, 2, 5).reshape(e, before * 128, 4 * c4)
+        scale = rows.new_zeros((2 * e, after * 128, 4 * c4))
+        scale[:, :w] = rows[:, :2 * w].reshape(2 * e, w, 4 * c4)
+        sides = {"row_data": q["row_data"], "row_scale": scale.view(2 * e, after, 4, 32, c4, 4).permute(0, 1, 4, 3, 2, 5).reshape(-1)}
+        if self.recipe == gsa.NVFP4:
+            sides["amax_row"] = q["amax_row"].repeat_interleave(2)
+        return sides
 
     def _quantize(self, rows, split):
         return gsa.fwd_graph_safe(rows, None, split, "identity", self.recipe, self.rht, self.mask, scale_layout=T)
@@ -86,7 +101,8 @@ class MoeFfn:
         row, split = gsa.moe_sort(expert_idx, self.experts)
         xs, ps = gsa.moe_permute(x, row, probs)
         used = split[:self.experts]
-        y = gsa.grouped_glu_gemv(xs, self.w1, used, self.width, self.recipe, self.act, ps)
+        w1, groups = (self.w1, 1) if self.fused else (self.w1_sides, 2)
+        y = gsa.grouped_glu_gemv(xs, w1, used, self.width, self.recipe, self.act, ps, b_groups=groups)
         return gsa.moe_unpermute(gsa.grouped_gemv(y, self.w2, used, self.hidden, self.recipe), row)
 
 
