@@ -6,8 +6,10 @@
 Forward:  sort the routed tokens by expert -> gather their rows -> quantize -> first projection -> scaled activation
 fused with the quantization of its result -> second projection -> sum each token's expert rows.
 Backward: the same way back, with both input gradients, both weight gradients and the router probabilities' gradient.
-Gated activations of widths that are multiples of 128 are the first projection's epilogue: its result is not written in
-front of the activation, and the backward multiplies again instead of keeping it.
+Gated activations of widths that are multiples of 128 can be the first projection's epilogue: its result is then not written
+in front of the activation, and the backward multiplies again instead of keeping it.  NVFP4 steps and forwards that no
+backward follows do so; MXFP8 steps, in which the second multiplication costs more than the writing, are made of the
+separate calls unless the memory matters more (recompute=True).
 Decoding: both projections of a few rows an expert without quantizing them (gated activations).
 The split stays on the device throughout: nothing waits for the host, and a step can be captured in a CUDA graph.
 """
@@ -27,14 +29,20 @@ class MoeFfn:
     """Expert weights w1 [E, W_in, H] and w2 [E, H, W] (BF16; W_in = 2 W for the GLU activations), quantized once.
 
     NVFP4 takes the random Hadamard transform on the columnwise copies of activations and gradients (they meet only
-    in weight gradients, where it cancels) and none on the weights' (they meet untransformed rows)."""
+    in weight gradients, where it cancels) and none on the weights' (they meet untransformed rows).
 
-    def __init__(self, w1, w2, act="srelu", recipe=gsa.MXFP8, rht_mask=0xBEEF):
+    recompute: whether the step of a gated FFN keeps no pre-activations (4 W bytes a row less) and multiplies again in the
+    backward.  None: where that is faster.  Steps in a graph with and without, ms, 8192 tokens to 8 of 32 experts, H and W
+    2048, and 32768 to 8 of 128, W 4096: NVFP4 2.59 / 2.71 and 16.7 / 17.9, MXFP8 2.96 to 3.02 / 2.87 to 2.89 and 22.7 to
+    23.2 / 21.1 to 21.3 (4096 tokens to 4 of 16, H and W 1024: 0.45 / 0.47 and 0.415 / 0.42)."""
+
+    def __init__(self, w1, w2, act="srelu", recipe=gsa.MXFP8, rht_mask=0xBEEF, recompute=None):
         self.experts, self.w_in, self.hidden = w1.shape
         self.width = w2.shape[2]
         self.act, self.recipe, self.rht, self.mask = act, recipe, recipe == gsa.NVFP4, rht_mask
         self.gated = act in ("swiglu", "clamped_swiglu")
-        self.fused = self.gated and self.width % 128 == 0
+        self.fused = self.gated and self.width % 128 == 0   # the activation may be the first projection's epilogue
+        self.recompute = recipe == gsa.NVFP4 if recompute is None else recompute
         self.w1, self.w2 = self._weights(w1), self._weights(w2)
         self.w1_sides = self._by_side(self.w1) if self.gated and not self.fused else None
 
@@ -59,16 +67,17 @@ class MoeFfn:
     def _quantize(self, rows, split):
         return gsa.fwd_graph_safe(rows, None, split, "identity", self.recipe, self.rht, self.mask, scale_layout=T)
 
-    def forward(self, x, expert_idx, probs):
+    def forward(self, x, expert_idx, probs, train=True):
         """x [tokens, H] BF16, expert_idx [tokens, topk] (outside [0, E): dropped), probs [tokens, topk] FP32
-        -> out [tokens, H] and what the backward needs."""
+        -> out [tokens, H] and what the backward needs.  train=False: no backward follows, whose needs then do not decide
+        how the activation is made (a backward that does follow multiplies again)."""
         r, e = self.recipe, self.experts
         row, split = gsa.moe_sort(expert_idx, e)
         split = gsa.moe_groups(split)                        # the dropped rows are the last group (or the last expert's)
         xs, ps = gsa.moe_permute(x, row, probs)
         m, used = xs.shape[0], split[:e]
         qx = self._quantize(xs, split)
-        if self.fused:
+        if self.fused and (self.recompute or not train):
             h = None
             qy = self._quantize(gsa.grouped_glu(qx, self.w1, used, m, self.width, self.hidden, r, self.act, ps), split)
         else:
@@ -86,7 +95,7 @@ class MoeFfn:
         qd = self._quantize(dys, split)
         dy = gsa.grouped_gemm(qd, self.w2, used, m, self.width, self.hidden, r, b_columnwise=True)
         dw2 = gsa.grouped_gemm_wgrad(qd, qy, used, m, self.hidden, self.width, r)
-        if self.fused:
+        if h is None:
             dh, dps = gsa.grouped_glu_bwd(dy, qx, self.w1, used, m, self.width, self.hidden, r, self.act, ps)
             g = dict(self._quantize(dh, split), dprobs=dps)
         else:
