@@ -572,16 +572,28 @@ gsa_status cuda_error() {
     return GSA_ERR_CUDA;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
-    PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_relaxed);
+// A function of the driver (nullptr: a CUDA error).
+template <typename F> F driver_fn(const char *name, std::atomic<F> &known) {
+    F fn = known.load(std::memory_order_relaxed);
     if (fn) return fn;
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-        known.store(fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p), std::memory_order_relaxed);
+    if (cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q) == cudaSuccess && q == cudaDriverEntryPointSuccess)
+        known.store(fn = reinterpret_cast<F>(p), std::memory_order_relaxed);
     return fn;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+    return driver_fn("cuTensorMapEncodeTiled", known);
+}
+
+// The current context's number, which no other context of the process has had (0: none is current yet).
+uint64_t context_id() {
+    static std::atomic<PFN_cuCtxGetId_v12000> known{nullptr};
+    auto fn = driver_fn("cuCtxGetId", known);
+    unsigned long long id = 0;
+    return fn && fn(nullptr, &id) == CUDA_SUCCESS ? id : 0;
 }
 
 // Codes [rows, bytes]: boxes of 128 bytes x `box` rows in the 128-byte swizzle, zeros outside.
@@ -608,17 +620,22 @@ bool map_scales(CUtensorMap *tm, const void *p, int64_t tiles, int box) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// What is asked once per device: only answers are kept, a failed query is made again.
+// What is asked once per device: only answers are kept, a failed query is made again.  What is set up (once()) is so in a
+// context: in another one, or after the device's has been reset, it is set up again (asking which one is current takes 0.01 us,
+// the shared memory of a kernel 0.2).
 struct PerDevice {
     std::mutex mu;
     int n[64] = {};
-    bool did[64] = {};
+    uint64_t did[64] = {};   // the context that it was last done in
     template <typename F> bool once(F &&act) {   // false: a CUDA error
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+        const uint64_t here = context_id();
         std::lock_guard<std::mutex> lock(mu);
-        if (!did[dev]) did[dev] = act() == cudaSuccess;
-        return did[dev];
+        if (here && did[dev] == here) return true;
+        if (act() != cudaSuccess) return false;
+        did[dev] = here;
+        return true;
     }
     template <typename F> int get(F &&ask) {   // 0: a CUDA error
         int dev = 0;

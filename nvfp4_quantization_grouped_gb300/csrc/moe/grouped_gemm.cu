@@ -464,20 +464,24 @@ struct WgradSpace {
 
 uint32_t *gemm_status::word() {
     static std::mutex mu;
-    static uint32_t *known[64];
+    static struct {
+        uint64_t context;   // whose address it is
+        uint32_t *at;
+    } known[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    const uint64_t here = context_id();
     std::lock_guard<std::mutex> lock(mu);
-    if (!known[dev]) {
-        // a first call may be inside a capture, which this does not touch
-        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
-        void *p = nullptr;
-        const bool ok = cudaGetSymbolAddress(&p, g_status) == cudaSuccess;
-        cudaThreadExchangeStreamCaptureMode(&mode);
-        if (ok) known[dev] = static_cast<uint32_t *>(p);
-    }
-    return known[dev];
+    if (here && known[dev].context == here) return known[dev].at;
+    // a first call may be inside a capture, which this does not touch
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return nullptr;
+    void *p = nullptr;
+    const bool ok = cudaGetSymbolAddress(&p, g_status) == cudaSuccess;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (!ok) return nullptr;
+    known[dev] = {here, static_cast<uint32_t *>(p)};
+    return known[dev].at;
 }
 
 extern "C" {
