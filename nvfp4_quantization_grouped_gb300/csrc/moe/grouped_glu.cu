@@ -537,8 +537,15 @@ gsa_status gsa_grouped_glu_bwd(const void *dy_bf16, const gsa_qin *a, const gsa_
     st = launch_glu<true>(P, recipe_kind == GSA_NVFP4, pair, out_dtype, tiles, s);
     if (st != GSA_OK || !dprobs_opt) return st;
     // (As a programmatic dependent: 4999 x 1000 x 1024 MXFP8 28.5 us, this way 26.4.)
-    sum_partials<<<static_cast<unsigned>((M + 255) / 256), 256, 0, s>>>(P.part, P.bad, kParts * P.n_tiles, M, dprobs_opt);
-    return cudaGetLastError() == cudaSuccess ? GSA_OK : GSA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((M + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    // the launch's own status: an error that another call left in the runtime is not this one's
+    return cudaLaunchKernelEx(&cfg, sum_partials, static_cast<const float *>(P.part), static_cast<const uint32_t *>(P.bad), kParts * P.n_tiles, M,
+                              dprobs_opt) == cudaSuccess
+               ? GSA_OK
+               : cuda_error();
 }
 
 }  // extern "C"
