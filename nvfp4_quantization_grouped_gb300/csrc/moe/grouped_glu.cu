@@ -459,11 +459,14 @@ gsa_status glu_params(GluParams &P, bool &pair, int64_t &tiles, const gsa_qin *a
         return GSA_ERR_INVALID_ARG;
     if (a_rows * cols >= (int64_t(1) << 31) || 2 * E * n128 * cols >= (int64_t(1) << 31)) return GSA_ERR_UNSUPPORTED;
     if (!has_space) return GSA_ERR_WORKSPACE;
-    // Pairs of blocks (256 rows) from 128 rows an expert on and where they fill the machine, single blocks (128 rows) else.
+    // Pairs of blocks (256 rows) from 128 rows an expert on and where there is a tile of theirs for every two SMs (76 pairs on
+    // 152), single blocks (128 rows) else.  By M and E: the split is on the device.
     // Pairs / singles, us, even splits of 128 experts, 2048 x 2048: 96 rows an expert 113 / 103 (NVFP4), 197 / 180 (MXFP8),
     // gradient 138 / 134 and 226 / 203; 128 rows 116 / 113, 200 / 200, 147 / 161, 233 / 224; 192 rows 120 / 133, 204 / 239,
     // 155 / 197, 244 / 267.  Few tiles, 8 experts x 256 rows, 1024 x 1024: 9.9 / 8.7, 11.5 / 10.7, 17.2 / 14.9, 18.2 / 16.4.
-    pair = M >= 128 * E && M / 256 * n128 >= 76;
+    const int sms = sm_count();
+    if (!sms) return cuda_error();
+    pair = M >= 128 * E && M / 256 * n128 >= sms / 2;
     const int sc = nv ? 4 : 1;
     if (!map_codes(&P.tm_a, a->data, M, k_bytes, pair ? kRowsT : kBoxA) || !map_codes(&P.tm_b, b->data, 2 * E * N, k_bytes, 128) ||
         !map_scales(&P.tm_sa, a->scale, a_rows * cols, sc) || !map_scales(&P.tm_sb, b->scale, 2 * E * n128 * cols, sc))
