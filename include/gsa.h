@@ -23,6 +23,9 @@
  *     array.  The caller owns every buffer, including the workspace; the
  *     library never allocates, frees or synchronizes (except
  *     gsa_workspace_status, which synchronizes the given stream).
+ *   - The activation calls set their kernels and scratch up once a device and
+ *     process: they are for one context of a device, until it is reset.  The
+ *     gsa_grouped_* products may be called in any context.
  *   - Rows are grouped by expert in expert order: expert e owns rows
  *     [o_e, o_e + M_e), o_e = sum of split_sizes before e.  M = sum M_e.
  *   - W_in = width of X.  W = width of Y: W_in for the unary activations,
@@ -443,7 +446,8 @@ gsa_status gsa_grouped_gemm_wgrad(const gsa_qin *a, const gsa_qin *b, const int6
  * with act GSA_ACT_SWIGLU or GSA_ACT_CLAMPED_SWIGLU (act_params as for the
  * activation step, may be NULL for SwiGLU) and p = probs ([M] FP32, NULL: 1).  g and u
  * stay in FP32 and are not written; y is rounded once.  (The activation step reads
- * BF16 pre-activations: results differ by their rounding.)  A NaN g or u gives NaN.
+ * BF16 pre-activations: results differ by their rounding.)  A NaN g or u gives NaN, and so does
+ * an infinite amax of either side (S is 0 then and so are the sums), as in gsa_grouped_gemm.
  *   a    rowwise copy of the [M, K] rows grouped by split_sizes_dev, as for
  *        gsa_grouped_gemm, with the same rules for the split; rows of y past its sum
  *        are zero.
@@ -510,7 +514,7 @@ gsa_status gsa_grouped_glu_gemv(const void *x, int32_t x_dtype, const gsa_qin *b
 
 /* Takes one report out of the current device's word and synchronizes `stream`:
  * GSA_ERR_DEVICE_TIMEOUT (a bounded wait ran out), GSA_ERR_INVALID_ARG (a device
- * split) or GSA_OK when there is none left.  The word is one a device: it collects
+ * split) or GSA_OK when there is none left.  The word is one a device (and context): it collects
  * what products report on any stream, each kind once until it is taken, so a
  * program that runs them on several streams joins them first.  Queries may run
  * on several threads; none loses a report.  Errors: CUDA (also on a stream that

@@ -14,7 +14,9 @@
 // so on: eight rows of one block-scaled operand, which go through the block-scaled product
 // (tcgen05) with the weights as they lie in memory.  An E2M1 code leaves an eighth of its
 // unit's half, an E4M3 code less: eight leave 2^-22 of the block's largest value, and nothing of
-// BF16 and FP16 values down to 2^-10 of it.  A lane of tensor memory holds a digit's sum, so the eight
+// BF16 and FP16 values down to 2^-10 of it.  That is as far as block scales reach below the row's largest
+// value: E4M3's to 2^-17 of it, E8M0's to 2^-127.  Blocks below 2^-16 (2^-120) have digits in that
+// last unit, which leave 2^-37 of the row's largest value at most.  A lane of tensor memory holds a digit's sum, so the eight
 // lanes of a row are added on the way out.
 //   The rest is the grouped product's kernel with 16 rows of x to a tile of 128 x 128 (gated: 128
 // of both sides), whose loads leave the absent rows out, and which starts on the weights while

@@ -837,8 +837,9 @@ def grouped_glu(a: dict, b: dict, split, m: int, n: int, k: int, recipe_kind: in
     """The gated first projection in one product: y [m, n] = probs * act(A Bg_e^T, A Bl_e^T) over the rows of each expert,
     act "swiglu" or "clamped_swiglu", probs [m] FP32 (None: 1).  a, split as for grouped_gemm.  b: the rowwise copy of the
     experts' weights [E * 2 n, k], n gate rows and then n linear rows an expert, quantized in E groups of 2 n rows
-    (b_groups 1, n a multiple of 128) or 2 E groups of n rows (b_groups 2).  out_dtype: torch.bfloat16 (default) or
-    torch.float32.  The pre-activations stay in FP32 and are not written: grouped_glu_bwd multiplies again."""
+    (b_groups 1, n a multiple of 128) or 2 E groups of n rows (b_groups 2; fwd takes 256 groups, but a copy made in E groups
+    becomes one of 2 E with its scale tiles laid out anew and each amax twice, as in examples/moe_ffn.py).  out_dtype:
+    torch.bfloat16 (default) or torch.float32.  The pre-activations stay in FP32 and are not written: grouped_glu_bwd multiplies again."""
     torch = _torch or _setup()
     out_dtype = out_dtype or (out.dtype if out is not None else torch.bfloat16)
     dev, experts, code = _product_args("grouped_glu", split, out_dtype)
@@ -937,8 +938,9 @@ def _few_rows(what, x, b, split, b_groups, recipe_kind, n, out_dtype, out, strea
 def grouped_gemv(x, b: dict, split, n: int, recipe_kind: int, out_dtype=None, out=None, stream=None):
     """out [rows, n] = x B_e^T over the rows of each expert, for a few unquantized rows an expert (decoding): x [rows, k]
     bfloat16, float16 or float32; b, split as for grouped_gemm (split None: one matrix takes all rows).  out_dtype: any
-    of the three (default: x's).  x keeps its precision: within 2^-22 of the largest value of its block of 16 (NVFP4) or
-    32 (MXFP8)."""
+    of the three (default: x's).  x keeps its precision: values within 2^-22 of the largest one of their block of 16 (NVFP4)
+    or 32 (MXFP8); blocks whose largest value is less than 2^-16 (NVFP4; MXFP8 2^-120) of the row's within 2^-37 of the row's.
+    A row with a NaN or with more than eight infinite values gives NaN."""
     _torch or _setup()
     return _few_rows("grouped_gemv", x, b, split, 1, recipe_kind, n, out_dtype, out, stream)
 
