@@ -492,7 +492,7 @@ gsa_status gsa_grouped_glu_bwd(const void *dy_bf16, const gsa_qin *a, const gsa_
  * K is a multiple of 64.  x takes part as eight digits in the weights' own format, whose
  * blocks (of 32 or 16 values) have scales of their own: a value is within 2^-22 of its
  * block's largest, BF16 and FP16 values down to 2^-10 of it are exact, and blocks below
- * 2^-16 (NVFP4; MXFP8 2^-120) of the row's largest value are within 2^-37 of that.
+ * 2^-16 (NVFP4; MXFP8 2^-80) of the row's largest value are within 2^-37 of that.
  * Infinite values count as products with them do; a row with more than eight is NaN.
  * Two launches.
  * Errors: INVALID_ARG, UNSUPPORTED (E > 256, K % 64, M >= 2^28, sizes past 2^31),

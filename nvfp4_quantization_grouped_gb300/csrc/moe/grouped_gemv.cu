@@ -15,7 +15,7 @@
 // (tcgen05) with the weights as they lie in memory.  An E2M1 code leaves an eighth of its
 // unit's half, an E4M3 code less: eight leave 2^-22 of the block's largest value, and nothing of
 // BF16 and FP16 values down to 2^-10 of it.  That is as far as block scales reach below the row's largest
-// value: E4M3's to 2^-17 of it, E8M0's to 2^-127.  Blocks below 2^-16 (2^-120) have digits in that
+// value: E4M3's to 2^-17 of it, E8M0's to 2^-87 or further.  Blocks below 2^-16 (2^-80) have digits in that
 // last unit, which leave 2^-37 of the row's largest value at most.  A lane of tensor memory holds a digit's sum, so the eight
 // lanes of a row are added on the way out.
 //   The rest is the grouped product's kernel with 16 rows of x to a tile of 128 x 128 (gated: 128
@@ -183,8 +183,12 @@ template <bool NV> __global__ void __launch_bounds__(kDigitThreads) split_digits
     if (lane == 0 && mine != kNone) atomicMax(&most_t, mine);
     __syncthreads();
     const bool is_nan = nan || infinite > kDigits, special = nan || infinite;
-    constexpr int kTop = NV ? 8 : 0, kLow = NV ? -9 : -127;   // exponents of the largest block's scale (E4M3's largest power of two) and of the least
-    const int row_t = (most_t == kNone ? 0 : most_t) - kTop;
+    // Exponents of the largest block's scale and of the least.  E4M3's largest power of two; E8M0 has room for x's own size, from
+    // 2^-40 to 1: a small row against large weights (up to 2^136) then has sums of its results' size, where a row scaled to the
+    // top took them through infinity, and below 2^-40 no sum can get there.
+    const int most = most_t == kNone ? 0 : most_t, top = NV ? 8 : max(-40, min(0, most));
+    constexpr int kLow = NV ? -9 : -127;
+    const int row_t = most - top;
     if (t == 0) P.info[r] = {special ? 0 : row_t, is_nan ? 0 : infinite};
     // A bad split may leave the row, or room for its scales, to no expert.
     const int at = static_cast<int>(r - first_row) * kDigits, lr = at & 127;

@@ -939,7 +939,7 @@ def grouped_gemv(x, b: dict, split, n: int, recipe_kind: int, out_dtype=None, ou
     """out [rows, n] = x B_e^T over the rows of each expert, for a few unquantized rows an expert (decoding): x [rows, k]
     bfloat16, float16 or float32; b, split as for grouped_gemm (split None: one matrix takes all rows).  out_dtype: any
     of the three (default: x's).  x keeps its precision: values within 2^-22 of the largest one of their block of 16 (NVFP4)
-    or 32 (MXFP8); blocks whose largest value is less than 2^-16 (NVFP4; MXFP8 2^-120) of the row's within 2^-37 of the row's.
+    or 32 (MXFP8); blocks whose largest value is less than 2^-16 (NVFP4; MXFP8 2^-80) of the row's within 2^-37 of the row's.
     A row with a NaN or with more than eight infinite values gives NaN."""
     _torch or _setup()
     return _few_rows("grouped_gemv", x, b, split, 1, recipe_kind, n, out_dtype, out, stream)
