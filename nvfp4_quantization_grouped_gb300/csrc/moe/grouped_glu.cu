@@ -11,9 +11,9 @@
 // of reading them: a training step keeps only the quantized rows, which the weight gradient
 // needs anyway.  A lane holds a row's 32 columns, so dp takes no shuffles: each warp writes a
 // partial sum a row, and a second kernel adds them in order.
-//   65536 rows over 32 experts, N and K 2048, NVFP4: 192 to 198 us alone in a graph (5.6 PFLOP/s; 5900
+//   65536 rows over 32 experts, N and K 2048, NVFP4: 188 to 202 us alone in a graph (5.6 PFLOP/s; 5900
 // cycles a tile, of which products and scale copies take 5700), 212 to 220 among other calls;
-// gradient 260 to 270, 9500 cycles a tile: the draining warps' round, of which the mathematics take
+// gradient 258 to 270, 9500 cycles a tile: the draining warps' round, of which the mathematics take
 // 2400 and 64 KB of results, which leave the block at 16 to 20 bytes a cycle, 3500 to 4000, during which
 // its load/store unit serves nothing else (without the stores 204 us; a pair that alone of all stores
 // takes as long as all do).  The same with half or all of the results as TMA stores, behind which the
